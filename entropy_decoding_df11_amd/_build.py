@@ -8,6 +8,7 @@ streams and allocations are valid inside the library.
 
 from __future__ import annotations
 
+import concurrent.futures
 import importlib.util
 import os
 import shutil
@@ -38,6 +39,10 @@ HIP_FLAGS = [
 ]
 
 
+HOST_SOURCES = ("df11_host.cpp", "df11_rans_host.cpp")
+DEVICE_SOURCES = ("df11_decode.hip", "df11_rans_decode.hip", "df11_norm.hip")
+
+
 def _torch_lib_dir() -> str:
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.origin:
@@ -53,24 +58,29 @@ def _run(cmd: List[str], verbose: bool) -> None:
         raise RuntimeError(f"build step failed ({res.returncode}): {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
 
 
+def _run_all(cmds: List[List[str]], verbose: bool) -> None:
+    """Independent build steps, at the same time (the device sources take
+    most of a build each); the first failure is raised once all have ended."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(cmds)) as pool:
+        for step in [pool.submit(_run, cmd, verbose) for cmd in cmds]:
+            step.result()
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source of the library and return the path of libdf11.so."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     hipcc = shutil.which("hipcc") or os.path.join(ROCM, "bin", "hipcc")
-    host_objs = []
-    for src in ("df11_host.cpp", "df11_rans_host.cpp"):
-        obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
-        _run(["g++", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{INCLUDE}", f"-I{CSRC}",
-              "-c", os.path.join(CSRC, src), "-o", obj], verbose)
-        host_objs.append(obj)
-    dev_objs = []
-    for src in ("df11_decode.hip", "df11_rans_decode.hip"):
-        obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
-        _run([hipcc, *HIP_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", os.path.join(CSRC, src), "-o", obj], verbose)
-        dev_objs.append(obj)
+    objs, cmds = [], []
+    for src in (*HOST_SOURCES, *DEVICE_SOURCES):
+        obj = os.path.join(BUILD_DIR, src.split(".")[0] + ".o")
+        compiler = ["g++", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra"] if src in HOST_SOURCES else \
+            [hipcc, *HIP_FLAGS]
+        cmds.append([*compiler, f"-I{INCLUDE}", f"-I{CSRC}", "-c", os.path.join(CSRC, src), "-o", obj])
+        objs.append(obj)
+    _run_all(cmds, verbose)
     rpaths = [p for p in (_torch_lib_dir(), os.path.join(ROCM, "lib")) if p]
     tmp = LIB_PATH + ".tmp"
-    _run([hipcc, f"--offload-arch={OFFLOAD_ARCH}", "-shared", "-fPIC", "-o", tmp, *host_objs, *dev_objs,
+    _run([hipcc, f"--offload-arch={OFFLOAD_ARCH}", "-shared", "-fPIC", "-o", tmp, *objs,
           *[f"-Wl,-rpath,{p}" for p in rpaths]], verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
@@ -102,13 +112,14 @@ def build_sanitized(out_path: str, verbose: bool = False) -> str:
     work = os.path.join(BUILD_DIR, "sanitized")
     os.makedirs(work, exist_ok=True)
     hipcc = shutil.which("hipcc") or os.path.join(ROCM, "bin", "hipcc")
-    objs = []
-    for src in ("df11_host.cpp", "df11_rans_host.cpp", "df11_decode.hip", "df11_rans_decode.hip"):
+    objs, cmds = [], []
+    for src in (*HOST_SOURCES, *DEVICE_SOURCES):
         obj = os.path.join(work, src.split(".")[0] + ".o")
         lang = [] if src.endswith(".hip") else ["-x", "hip"]
-        _run([hipcc, *HIP_FLAGS, *SAN_HOST, "-O1", f"-I{INCLUDE}", f"-I{CSRC}", *lang, "-c",
-              os.path.join(CSRC, src), "-o", obj], verbose)
+        cmds.append([hipcc, *HIP_FLAGS, *SAN_HOST, "-O1", f"-I{INCLUDE}", f"-I{CSRC}", *lang, "-c",
+                     os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
+    _run_all(cmds, verbose)
     rpaths = [p for p in (_torch_lib_dir(), os.path.join(ROCM, "lib")) if p]
     _run([hipcc, f"--offload-arch={OFFLOAD_ARCH}", "-shared", "-fPIC", "-shared-libasan", *SAN_HOST, "-o", out_path,
           *objs, *[f"-Wl,-rpath,{p}" for p in rpaths]], verbose)

@@ -31,6 +31,7 @@ MAX_BATCH = 16  # DF11_MAX_BATCH
 MAX_ELEMENTS = (1 << 32) - (1 << 16)  # DF11_MAX_ELEMENTS
 LINEAR_MAX_TOKENS = 8  # DF11_LINEAR_MAX_TOKENS
 LINEAR_MIN_IN_FEATURES = 512  # DF11_LINEAR_MIN_IN_FEATURES
+BF16, FP16, FP32 = 0, 1, 2  # DF11_BF16, DF11_FP16, DF11_FP32
 RANS_PROB_BITS = 12  # DF11_RANS_PROB_BITS
 RANS_LANES = 64  # DF11_RANS_LANES
 RANS_STEPS = 512  # DF11_RANS_STEPS
@@ -60,6 +61,9 @@ EXPORTED = [
     "df11_linear_batch",
     "df11_linear_acc",
     "df11_linear_batch_acc",
+    "df11_rms_norm",
+    "df11_rms_norm_grad_workspace",
+    "df11_rms_norm_grad",
     "df11_rans_quantize",
     "df11_rans_encode",
     "df11_rans_build_table",
@@ -171,6 +175,7 @@ def load() -> ctypes.CDLL:
     u16p = ctypes.POINTER(ctypes.c_uint16)
     u32p = ctypes.POINTER(ctypes.c_uint32)
     u64p = ctypes.POINTER(ctypes.c_uint64)
+    vp, u32, u64 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64
     sig = {
         "df11_histogram": (ctypes.c_int, [u16p, ctypes.c_uint64, u64p]),
         "df11_build_codebook": (ctypes.c_int, [u64p, ctypes.POINTER(Codebook)]),
@@ -220,6 +225,11 @@ def load() -> ctypes.CDLL:
                                                  ctypes.c_uint32, ctypes.c_uint32, u32p,
                                                  ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p, ctypes.c_void_p,
                                                  ctypes.c_void_p]),
+        "df11_rms_norm": (ctypes.c_int, [vp, u64, vp, u64, vp, u32, u32, u32, u32, ctypes.c_float, vp, u64, vp, u64,
+                                         vp, vp]),
+        "df11_rms_norm_grad_workspace": (u64, [u32, u32]),
+        "df11_rms_norm_grad": (ctypes.c_int, [vp, u64, vp, u32, vp, vp, u64, vp, u64, u32, u32, u32, vp, u64, vp, vp,
+                                              u64, vp]),
         "df11_rans_quantize": (ctypes.c_int, [u64p, u32p]),
         "df11_rans_encode": (ctypes.c_int, [u32p, u16p, ctypes.c_uint64, u32p, u32p, u16p, ctypes.c_uint64, u8p,
                                             ctypes.POINTER(RansHeader)]),

@@ -82,18 +82,18 @@ __device__ __forceinline__ void store_chunk_at(uint16_t *out, uint32_t dst, uint
     }
 }
 
-uint64_t round_up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
+[[maybe_unused]] uint64_t round_up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+[[maybe_unused]] bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-bool overlaps(const void *a, uint64_t an, const void *b, uint64_t bn) {
+[[maybe_unused]] bool overlaps(const void *a, uint64_t an, const void *b, uint64_t bn) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return an && bn && a0 < b0 + bn && b0 < a0 + an;
 }
 
 // Workgroups of kernel fn (with `threads` threads and `lds` bytes of dynamic
 // LDS) that fit on one CU of device dev, cached per (kernel, device, LDS).
-int resident_per_cu(const void *fn, uint32_t threads, int dev, size_t lds) {
+[[maybe_unused]] int resident_per_cu(const void *fn, uint32_t threads, int dev, size_t lds) {
     struct Entry {
         const void *fn;
         int dev;
@@ -117,7 +117,7 @@ int resident_per_cu(const void *fn, uint32_t threads, int dev, size_t lds) {
 // Launch fn.  With both events null this is a plain hipLaunchKernel, which a
 // caller may capture into a HIP graph; with either event given,
 // hipExtLaunchKernel records it at the kernel's own start or end.
-int launch_kernel(const void *fn, dim3 grid, dim3 block, void **params, size_t lds, hipStream_t stream,
+[[maybe_unused]] int launch_kernel(const void *fn, dim3 grid, dim3 block, void **params, size_t lds, hipStream_t stream,
                   hipEvent_t start, hipEvent_t stop) {
     const hipError_t e = (start || stop)
                              ? hipExtLaunchKernel(fn, grid, block, params, lds, stream, start, stop, 0)
@@ -126,7 +126,7 @@ int launch_kernel(const void *fn, dim3 grid, dim3 block, void **params, size_t l
     return hipGetLastError() == hipSuccess ? DF11_OK : DF11_E_HIP;
 }
 
-int device_cus(int &dev, int &cus) {
+[[maybe_unused]] int device_cus(int &dev, int &cus) {
     if (hipGetDevice(&dev) != hipSuccess) return DF11_E_HIP;
     if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return DF11_E_HIP;
     return DF11_OK;

@@ -877,3 +877,7 @@ def rans_compress(tensor: ArrayLike, shape: Optional[Sequence[int]] = None, devi
     if shape is None:
         shape = tuple(tensor.shape)
     return DF11RansTensor(rans_encode(tensor), shape, device=device)
+
+
+# The operators around the products, under the same roof as the products.
+from .operators import rms_norm  # noqa: E402,F401

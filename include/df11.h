@@ -69,6 +69,11 @@ typedef enum df11_status {
 #define DF11_LINEAR_MAX_TOKENS 8
 #define DF11_LINEAR_MIN_IN_FEATURES 512
 
+/* Element types of the operators around the products. */
+#define DF11_BF16 0
+#define DF11_FP16 1
+#define DF11_FP32 2
+
 /* The codebook shared by all tensors of one stream (host, plain data).
  *   code_lengths[e]: Huffman code length of exponent e, 0 if unused
  *                    (the page's CodeLengths table).
@@ -470,6 +475,62 @@ int df11_matmul_timed(const df11_device_stream *w, const uint16_t *x, uint32_t n
 int df11_matmul_batch(const df11_device_stream *ws, uint32_t n_streams, const uint16_t *const *xs, uint32_t n_tokens,
                       const uint32_t *in_features, const uint32_t *out_features, float *const *ys, int accumulate,
                       void *hip_stream, void *start_event, void *stop_event);
+
+/* ---------------------------------------------------------------------------
+ * Operators around the products of a transformer block.  Not on the page,
+ * which leaves everything but the weights to the framework that runs the
+ * model: what a forward through compressed weights computes between one
+ * product and the next.  Strides are in elements.  A buffer of elements is
+ * aligned to one element unless stated otherwise; 16-byte aligned rows are
+ * read and written in 16-byte vectors.  Every sum is taken in float in an
+ * order that the shapes alone fix, so that a call's results do not change
+ * from run to run, and every result is rounded once.  None of these calls
+ * uses memory of the library's own: calls that share no output or workspace
+ * may overlap in time.
+ * ------------------------------------------------------------------------- */
+
+/* RMS norm with the residual's addition:
+ *   s = round(x + residual), or x without a residual
+ *   y = s * rstd * weight, rstd = 1 / sqrt(mean(s^2) + eps)
+ * with s rounded to the rows' type first, so that y is the norm of the very
+ * values that the residual stream carries on.
+ *   x          device, rows x cols of dtype (DF11_BF16, DF11_FP16, DF11_FP32),
+ *              x_stride from row to row
+ *   residual   device, rows x cols of dtype, or NULL
+ *   weight     device, cols of weight_dtype (dtype or DF11_FP32), or NULL (ones)
+ *   rows       0 .. 2^30; with 0 nothing is launched
+ *   cols       1 .. 2^30
+ *   sum        device, rows x cols, receives s; or NULL.  Only with a residual
+ *   y          device, rows x cols
+ *   rstd       device, rows floats, or NULL; kept for df11_rms_norm_grad
+ * sum and y may each lie exactly on x or on residual (same address and
+ * stride), but not on each other.  A row with an infinity or a NaN gives NaN
+ * in that row alone.  Errors: DF11_E_INVALID_ARG (types, sizes, alignment,
+ * output rows that overlap, other overlaps), DF11_E_HIP. */
+int df11_rms_norm(const void *x, uint64_t x_stride, const void *residual, uint64_t residual_stride,
+                  const void *weight, uint32_t weight_dtype, uint32_t rows, uint32_t cols, uint32_t dtype, float eps,
+                  void *sum, uint64_t sum_stride, void *y, uint64_t y_stride, float *rstd, void *hip_stream);
+
+/* Bytes of df11_rms_norm_grad's workspace when it computes dweight. */
+uint64_t df11_rms_norm_grad_workspace(uint32_t rows, uint32_t cols);
+
+/* Gradients of df11_rms_norm, with h = s * rstd:
+ *   dx = rstd * (dy * weight - h * mean(dy * weight * h)) + dsum
+ *   dweight = sum over the rows of dy * h
+ * dx is the gradient of x and of residual alike.
+ *   s, rstd      the forward call's sum (x itself without a residual) and rstd
+ *   dy, dsum     device, rows x cols of dtype: the gradients of y and, or
+ *                NULL, of sum
+ *   dx           device, rows x cols of dtype; may lie exactly on s, dy or dsum
+ *   dweight      device, cols of weight_dtype, or NULL; needs weight.  With no
+ *                rows it is zero
+ *   workspace    device, 16-byte aligned, df11_rms_norm_grad_workspace bytes
+ *                (with dweight; else it may be NULL)
+ * Errors: as for df11_rms_norm, DF11_E_BUFFER_TOO_SMALL. */
+int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uint32_t weight_dtype, const float *rstd,
+                       const void *dy, uint64_t dy_stride, const void *dsum, uint64_t dsum_stride, uint32_t rows,
+                       uint32_t cols, uint32_t dtype, void *dx, uint64_t dx_stride, void *dweight, void *workspace,
+                       uint64_t workspace_bytes, void *hip_stream);
 
 /* ---------------------------------------------------------------------------
  * rANS exponent coder.  The discussion on the page ("Opini Hacker News")
