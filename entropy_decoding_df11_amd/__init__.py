@@ -9,11 +9,12 @@ forwards captured into HIP graphs) and the seeded synthetic workloads.
 
 from .df11 import (DF11Block, DF11BlockBatch, DF11RansTensor, DF11Tensor, HostStream, RansHostStream, build_codebook,
                    codebook_arrays, compress, compress_block, decode_table, decompress, decompress_batch, encode,
-                   histogram, linear_batch, rans_compress, rans_encode, rms_norm)
+                   gated_matmul, histogram, linear_batch, matmul_epilogue, rans_compress, rans_encode, rms_norm)
 from ._lib import Df11Error
 
 __all__ = [
     "DF11Block", "DF11BlockBatch", "DF11RansTensor", "DF11Tensor", "Df11Error", "HostStream", "RansHostStream",
     "build_codebook", "codebook_arrays", "compress", "compress_block", "decode_table", "decompress",
-    "decompress_batch", "encode", "histogram", "linear_batch", "rans_compress", "rans_encode", "rms_norm",
+    "decompress_batch", "encode", "gated_matmul", "histogram", "linear_batch", "matmul_epilogue", "rans_compress",
+    "rans_encode", "rms_norm",
 ]

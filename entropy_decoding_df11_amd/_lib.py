@@ -32,6 +32,7 @@ MAX_ELEMENTS = (1 << 32) - (1 << 16)  # DF11_MAX_ELEMENTS
 LINEAR_MAX_TOKENS = 8  # DF11_LINEAR_MAX_TOKENS
 LINEAR_MIN_IN_FEATURES = 512  # DF11_LINEAR_MIN_IN_FEATURES
 BF16, FP16, FP32 = 0, 1, 2  # DF11_BF16, DF11_FP16, DF11_FP32
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # DF11_ACT_*
 RANS_PROB_BITS = 12  # DF11_RANS_PROB_BITS
 RANS_LANES = 64  # DF11_RANS_LANES
 RANS_STEPS = 512  # DF11_RANS_STEPS
@@ -64,6 +65,9 @@ EXPORTED = [
     "df11_rms_norm",
     "df11_rms_norm_grad_workspace",
     "df11_rms_norm_grad",
+    "df11_epilogue_workspace",
+    "df11_matmul_epilogue",
+    "df11_gated_matmul",
     "df11_rans_quantize",
     "df11_rans_encode",
     "df11_rans_build_table",
@@ -129,6 +133,21 @@ class DeviceStream(ctypes.Structure):
         ("schedule", ctypes.c_void_p),
         ("max_workgroups", ctypes.c_uint32),
         ("tile_cols", ctypes.c_uint32),
+    ]
+
+
+class Epilogue(ctypes.Structure):
+    _fields_ = [
+        ("bias", ctypes.c_void_p * 2),
+        ("residual", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("pre", ctypes.c_void_p * 2),
+        ("residual_stride", ctypes.c_uint64),
+        ("out_stride", ctypes.c_uint64),
+        ("bias_dtype", ctypes.c_uint32),
+        ("residual_dtype", ctypes.c_uint32),
+        ("out_dtype", ctypes.c_uint32),
+        ("activation", ctypes.c_uint32),
     ]
 
 
@@ -230,6 +249,11 @@ def load() -> ctypes.CDLL:
         "df11_rms_norm_grad_workspace": (u64, [u32, u32]),
         "df11_rms_norm_grad": (ctypes.c_int, [vp, u64, vp, u32, vp, vp, u64, vp, u64, u32, u32, u32, vp, u64, vp, vp,
                                               u64, vp]),
+        "df11_epilogue_workspace": (u64, [ctypes.POINTER(DeviceStream), ctypes.POINTER(DeviceStream), u32]),
+        "df11_matmul_epilogue": (ctypes.c_int, [ctypes.POINTER(DeviceStream), vp, u64, u32, u32, u32,
+                                                ctypes.POINTER(Epilogue), vp, u64, vp]),
+        "df11_gated_matmul": (ctypes.c_int, [ctypes.POINTER(DeviceStream), ctypes.POINTER(DeviceStream), vp, u64, u32,
+                                             u32, u32, ctypes.POINTER(Epilogue), vp, u64, vp]),
         "df11_rans_quantize": (ctypes.c_int, [u64p, u32p]),
         "df11_rans_encode": (ctypes.c_int, [u32p, u16p, ctypes.c_uint64, u32p, u32p, u16p, ctypes.c_uint64, u8p,
                                             ctypes.POINTER(RansHeader)]),

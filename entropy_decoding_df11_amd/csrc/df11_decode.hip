@@ -44,6 +44,7 @@
 #include "df11_internal.h"
 #include "df11_launch.h"
 #include "df11_pairs.h"
+#include "df11_partials.h"
 
 namespace {
 
@@ -87,8 +88,15 @@ struct DecodeArgs {
     uint32_t *sched;         // work counters (dynamic schedule) or null
     uint32_t pools;          // dynamic schedule: counters in use, dividing the workgroup count
     uint32_t tile_ks;        // C / 32: k-steps per 64-row panel of a tiled matrix
-    uint64_t tile_magic;     // floor(2^64 / tile_ks) + 1: umulhi64(i, tile_magic) == i / tile_ks, i < 2^32
+    uint64_t tile_magic;     // floor(2^64 / tile_ks) + 1, or 0 for tile_ks = 1 (panel_of_step)
 };
+
+// Panel of global k-step g of a tiled matrix, g / tile_ks: umulhi64(g,
+// tile_magic) for all g < 2^32, but a magic number of 2^64 (one k-step per
+// panel) does not fit its word.
+__device__ __forceinline__ uint32_t panel_of_step(const DecodeArgs &a, uint32_t g) {
+    return a.tile_magic ? static_cast<uint32_t>(__umul64hi(g, a.tile_magic)) : g;
+}
 
 // MFMA tile order (df11_tile_order): 512-element blocks, each the operand
 // of one 16 x 16 x 32 bf16 matrix instruction; block b is n-tile b mod 4 of
@@ -98,7 +106,7 @@ struct DecodeArgs {
 // the row-major matrix of the first element of chunk c (8 elements):
 __device__ __forceinline__ uint32_t tiled_chunk_origin(const DecodeArgs &a, uint32_t c) {
     const uint32_t l = c & 63u, nt = (c >> 6) & 3u, g = c >> 8;
-    const uint32_t panel = static_cast<uint32_t>(__umul64hi(g, a.tile_magic));
+    const uint32_t panel = panel_of_step(a, g);
     const uint32_t ks = g - panel * a.tile_ks;
     return (64u * panel + 16u * nt + (l & 15u)) * a.tile_cols + 32u * ks + 8u * (l >> 4);
 }
@@ -115,6 +123,12 @@ struct MatmulArgs {
     uint32_t yacc_rows;    // rows of W that one group's outputs can touch
     uint32_t passes;       // matrix-core product: sweeps of the stream, 16 MT tokens each
     uint32_t fixed_len;    // matrix-core product with a dealt tail: super-groups of each fixed range
+    // Matrix-core product into slots (flush_slot); y is the stream's first slot.
+    uint32_t x_stride;     // elements from one row of x to the next, a multiple of 8
+    uint32_t wg_panels;    // slots of one group slot of a workgroup's fixed range
+    uint32_t group_panels; // slots of one group of the dealt tail
+    uint32_t tail_group0;  // first group of the dealt tail
+    uint64_t tail_slots;   // floats before the dealt tail's first slot
 };
 
 __device__ __forceinline__ uint32_t bswap32(uint32_t x) { return __builtin_amdgcn_perm(x, x, 0x00010203u); }
@@ -748,7 +762,41 @@ struct PanelSums {
     floatx4 d[MT];   // lane l, entry r: token 16 mt + 4 (l / 16) + r, row 16 wave + (l mod 16)
     uint32_t panel;  // 64-row panel of the sums (wave-uniform), ~0 when empty
     uint32_t pass;   // pass of the sums (wave-uniform)
+    // Into slots (all wave-uniform): the region's first slot, panel and slot
+    // count, the panel after its last one, and its group (~0: a fixed range).
+    float *region;
+    uint32_t first, panels, panel_end, group;
 };
+
+// The slots' form of the product: in place of float atomics, whose order
+// changes the sums' last bits, every region of the stream (a workgroup's
+// fixed range, once for each of its group slots, or one group of the dealt
+// tail) has one slot of n_tokens x 64 floats for each panel it touches, and
+// writes each of them exactly once: the sums of the panels it holds, zeros
+// for a panel that only the range's other group slot reached.  A second
+// kernel adds a panel's slots in the order of the stream.  Writes the sums to
+// their slot and zeros up to panel `upto`; slot numbers past the region's
+// (a corrupt stream) are dropped.
+template <int MT>
+__device__ __forceinline__ void flush_slot(const MatmulArgs &m, PanelSums<MT> &ps, uint32_t upto, uint32_t wave,
+                                           uint32_t lane) {
+    const uint32_t j0 = ps.panel - ps.first, j1 = min(upto - ps.first, ps.panels);
+    const uint32_t row = 16u * wave + (lane & 15u);
+    for (uint32_t j = j0; j < j1; ++j) {
+        float *slot = ps.region + static_cast<size_t>(j) * m.n_tokens * 64u;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t t = mt * 16u + 4u * (lane >> 4) + r;
+                if (t < m.n_tokens) slot[t * 64u + row] = ps.d[mt][r];
+                ps.d[mt][r] = 0.0f;
+            }
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) ps.d[mt] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+}
 
 template <int MT>
 __device__ __forceinline__ void flush_panel(const MatmulArgs &m, PanelSums<MT> &ps, uint32_t wave, uint32_t lane) {
@@ -768,16 +816,16 @@ __device__ __forceinline__ void flush_panel(const MatmulArgs &m, PanelSums<MT> &
 
 // x operands of one round: token tiles mt of the pass, the 8 columns of the
 // lane at global k-step g (tokens past n_tokens read as zero).
-template <int MT>
+template <int MT, bool kSlots>
 __device__ __forceinline__ void load_xa(const DecodeArgs &a, const MatmulArgs &m, uint32_t g, uint32_t pass,
                                         uint32_t lane, uint4 (&xa)[MT]) {
-    const uint32_t panel = static_cast<uint32_t>(__umul64hi(g, a.tile_magic));
+    const uint32_t panel = panel_of_step(a, g);
     const uint32_t col = 32u * (g - panel * a.tile_ks) + 8u * (lane >> 4);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const uint32_t t = (pass * MT + mt) * 16u + (lane & 15u);
         const uint4 v = *reinterpret_cast<const uint4 *>(m.x + static_cast<size_t>(min(t, m.n_tokens - 1u)) *
-                                                                   m.in_features + col);
+                                                                   (kSlots ? m.x_stride : m.in_features) + col);
         xa[mt] = t < m.n_tokens ? v : make_uint4(0, 0, 0, 0);
     }
 }
@@ -795,7 +843,7 @@ __device__ __forceinline__ void load_xa(const DecodeArgs &a, const MatmulArgs &m
 template <int MT>
 constexpr int kXTiles = MT <= 2 ? 4 : 2;
 
-template <int MT>
+template <int MT, bool kSlots>
 __device__ __forceinline__ void stage_x(const DecodeArgs &a, const MatmulArgs &m, uint32_t base, uint32_t pass,
                                         uint32_t wave, uint32_t lane, uint8_t *s_x) {
     // (global_load_lds writes lane l's 16 bytes at the wave-uniform LDS
@@ -807,20 +855,22 @@ __device__ __forceinline__ void stage_x(const DecodeArgs &a, const MatmulArgs &m
         const uint32_t tile = q + wave;  // (round tile / MT, token tile tile % MT)
         if (tile < static_cast<uint32_t>(kXTiles<MT> * MT)) {
             const uint32_t g = g0 + tile / MT, mt = tile % MT;
-            const uint32_t panel = static_cast<uint32_t>(__umul64hi(g, a.tile_magic));
+            const uint32_t panel = panel_of_step(a, g);
             const uint32_t col = 32u * (g - panel * a.tile_ks) + 8u * (lane >> 4);
             const uint32_t t = min((pass * MT + mt) * 16u + (lane & 15u), m.n_tokens - 1u);
             __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void *)(m.x + static_cast<size_t>(t) * m.in_features + col),
+                (const __attribute__((address_space(1))) void *)(
+                    m.x + static_cast<size_t>(t) * (kSlots ? m.x_stride : m.in_features) + col),
                 (__attribute__((address_space(3))) void *)(s_x + 1024u * tile), 16, 0, 0);
         }
     }
 }
 
-template <int MT>
+template <int MT, bool kSlots, bool kTail>
 __device__ __forceinline__ void merge_mfma(const DecodeArgs &a, const MatmulArgs &m, uint8_t *ebuf,
                                            const uint64_t (&sm)[kPrefetchChunks], uint32_t base, uint32_t end,
-                                           uint32_t pass, uint32_t ltid, PanelSums<MT> &ps, const uint8_t *s_x) {
+                                           uint32_t pass, uint32_t group, uint32_t ltid, PanelSums<MT> &ps,
+                                           const uint8_t *s_x) {
     const uint32_t c0 = base >> 3;
     const uint32_t n_chunks = min(group_chunks(base, end), a.ebuf_cap / 8u);
     const uint32_t lead = c0 & 255u;
@@ -835,6 +885,16 @@ __device__ __forceinline__ void merge_mfma(const DecodeArgs &a, const MatmulArgs
     if (ltid == 0 && 8u * (n_chunks + 1u) <= a.ebuf_cap) *reinterpret_cast<uint64_t *>(ebuf + 8u * n_chunks) = 0;
     if (n_chunks == 0) return;
     const uint32_t g0 = c0 >> 8;
+    if constexpr (kSlots && kTail) {
+        if (group >= m.tail_group0 && group < a.n_groups) {  // a region of its own
+            flush_slot<MT>(m, ps, ps.group == ~0u ? ps.panel_end : ps.panel + 1u, wave, lane);
+            ps.group = group;
+            ps.region = m.y + m.tail_slots +
+                        static_cast<size_t>(group - m.tail_group0) * m.group_panels * m.n_tokens * 64u;
+            ps.first = ps.panel = panel_of_step(a, g0);
+            ps.panels = m.group_panels;
+        }
+    }
     auto round = [&](uint32_t j, const uint4 (&xa)[MT], uint64_t s8) {
         const uint32_t kk = ltid + 256u * j;
         const uint32_t k = kk - lead;
@@ -856,8 +916,13 @@ __device__ __forceinline__ void merge_mfma(const DecodeArgs &a, const MatmulArgs
                 if (e0 + e < base || e0 + e >= end) w[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
         }
         const uint32_t g = g0 + j;
-        const uint32_t panel = static_cast<uint32_t>(__umul64hi(g, a.tile_magic));
-        if (panel != ps.panel || pass != ps.pass) {
+        const uint32_t panel = panel_of_step(a, g);
+        if constexpr (kSlots) {
+            if (panel != ps.panel) {
+                flush_slot<MT>(m, ps, panel, wave, lane);
+                ps.panel = panel;
+            }
+        } else if (panel != ps.panel || pass != ps.pass) {
             flush_panel<MT>(m, ps, wave, lane);
             ps.panel = panel;
             ps.pass = pass;
@@ -884,7 +949,7 @@ __device__ __forceinline__ void merge_mfma(const DecodeArgs &a, const MatmulArgs
     }
     for (uint32_t j = kXTiles<MT>; j < rounds; ++j) {
         uint4 xa[MT];
-        load_xa<MT>(a, m, g0 + j, pass, lane, xa);
+        load_xa<MT, kSlots>(a, m, g0 + j, pass, lane, xa);
         uint64_t s8 = 0;
         const uint32_t kk = ltid + 256u * j;
         if (j < static_cast<uint32_t>(kPrefetchChunks)) {
@@ -1085,7 +1150,10 @@ __device__ __forceinline__ void decode_half(uint64_t pair, uint32_t end, uint32_
 // kPairs (decompression of a tile-ordered stream with an even number of
 // k-steps per panel): the merge writes whole row-major lines
 // (merge_group_pairs) through a per-wave LDS stage after the dynamic LDS.
-template <int K, int GPW, int TB, bool kTail = false, bool kPairs = false>
+//
+// kSlots (matrix-core product, one pass): the sums go to slots (flush_slot)
+// instead of being added into y.
+template <int K, int GPW, int TB, bool kTail = false, bool kPairs = false, bool kSlots = false>
 __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulArgs &m, const uint32_t wg,
                                               const uint32_t n_wg) {
     // Static LDS: the first-level table (2^K (lo, aux) word pairs, then 2^K
@@ -1165,7 +1233,19 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
         ps.panel = ~0u;
         ps.pass = 0;
     }
-    uint32_t prev_pass = 0;
+    uint32_t prev_pass = 0, prev_group = 0;
+    if constexpr (kSlots) {
+        // The fixed range's panels, from its first and last element (as the
+        // kernel that adds the slots finds them: df11::range_panels).
+        const uint32_t last = a.n_elements - 1u;
+        const uint32_t e0 = min(out_pos_at(a, r0 * GPW), last);
+        const uint32_t e1 = min(max(out_pos_at(a, min((r0 + len) * GPW, a.n_groups)), 1u) - 1u, last);
+        ps.first = ps.panel = panel_of_step(a, e0 >> 11);
+        ps.panel_end = panel_of_step(a, e1 >> 11) + 1u;
+        ps.panels = m.wg_panels;
+        ps.group = ~0u;
+        ps.region = m.y + static_cast<size_t>(wg * GPW + slot) * m.wg_panels * m.n_tokens * 64u;
+    }
 
     // Pipeline state: the group's output range (scalar) and thread inputs one
     // super-group ahead; the sign/mantissa chunks of the group waiting to be
@@ -1261,7 +1341,9 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
                 merge_matmul<TB>(a, m, s_ebuf, sm, prev_base, prev_end, ltid, s_edge[0] != 0, s_edge[1] != 0, s_yacc,
                                  y_row0, y_rows);
         } else if constexpr (kMfma) {
-            if (it > 0) merge_mfma<MT>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, ltid, ps, s_x);
+            if (it > 0)
+                merge_mfma<MT, kSlots, kTail>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, prev_group, ltid, ps,
+                                              s_x);
         }
         const GroupLoad nx = load_group(a, g_nx, ltid);
         uint32_t fetched = 0;
@@ -1346,7 +1428,7 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
             y_rows = 0;
         } else if constexpr (kMfma) {
             // Every wave's merge has read the staged tiles: stage this group's.
-            stage_x<MT>(a, m, base, kTail ? 0u : s_cur / len, wave, lane, s_x);
+            stage_x<MT, kSlots>(a, m, base, kTail ? 0u : s_cur / len, wave, lane, s_x);
         }
         __builtin_amdgcn_s_setprio(1);
         uint32_t wave_off = 0;
@@ -1414,6 +1496,7 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
         prev_base = base;
         prev_end = end;
         if constexpr (kMfma) prev_pass = kTail ? 0u : s_cur / len;
+        if constexpr (kSlots && kTail) prev_group = g;
         cur = nx;
         cur_base = nx_base;
         cur_end = nx_end;
@@ -1424,8 +1507,12 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
     } else if constexpr (TB == 0) {
         merge_group(a, s_ebuf, sm, prev_base, prev_end, ltid, s_edge[0] != 0, s_edge[1] != 0);
     } else if constexpr (kMfma) {
-        merge_mfma<MT>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, ltid, ps, s_x);
-        flush_panel<MT>(m, ps, wave, lane);
+        merge_mfma<MT, kSlots, kTail>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, prev_group, ltid, ps, s_x);
+        if constexpr (kSlots) {
+            flush_slot<MT>(m, ps, ps.group == ~0u ? ps.panel_end : ps.panel + 1u, wave, lane);
+        } else {
+            flush_panel<MT>(m, ps, wave, lane);
+        }
     } else {
         merge_matmul<TB>(a, m, s_ebuf, sm, prev_base, prev_end, ltid, s_edge[0] != 0, s_edge[1] != 0, s_yacc, y_row0,
                          y_rows);
@@ -1544,6 +1631,31 @@ void df11_gemm_batch_kernel(LinearBatchArgs b) {
     uint32_t i = 0;
     while (i + 1u < b.n && id >= b.wg_begin[i + 1]) ++i;
     decode_stream<K, kGemmGPW, -MT, kTail>(b.s[i], b.m[i], id - b.wg_begin[i], b.wg_begin[i + 1] - b.wg_begin[i]);
+}
+
+// The matrix-core product of one or two matrices with the same x into slots
+// (df11_partials.h), the grid split between the two as for
+// df11_decode_batch_kernel.
+struct PartialArgs {
+    DecodeArgs s[2];
+    MatmulArgs m[2];
+    uint32_t wg_begin[3];
+    uint32_t stride;  // coprime to the grid size
+};
+
+template <int K, int MT, bool kTail>
+__global__ __launch_bounds__(kThreadsPerGroup *kGemmGPW) __attribute__((amdgpu_waves_per_eu(kGemmWaves<MT>)))
+void df11_partial_kernel(DecodeArgs a, MatmulArgs m) {
+    decode_stream<K, kGemmGPW, -MT, kTail, false, true>(a, m, blockIdx.x, gridDim.x);
+}
+
+template <int K, int MT, bool kTail>
+__global__ __launch_bounds__(kThreadsPerGroup *kGemmGPW) __attribute__((amdgpu_waves_per_eu(kGemmWaves<MT>)))
+void df11_partial_pair_kernel(PartialArgs b) {
+    const uint32_t id = static_cast<uint32_t>((static_cast<uint64_t>(blockIdx.x) * b.stride) % gridDim.x);
+    const uint32_t i = id >= b.wg_begin[1];
+    decode_stream<K, kGemmGPW, -MT, kTail, false, true>(b.s[i], b.m[i], id - b.wg_begin[i],
+                                                        b.wg_begin[i + 1] - b.wg_begin[i]);
 }
 
 // Zero several outputs: y[i] has end[i] - end[i - 1] floats (end[-1] = 0).
@@ -1766,7 +1878,7 @@ void fill_args(const df11_device_stream *s, DecodeArgs &a) {
     a.tile_cols = s->tile_cols;
     if (s->tile_cols) {
         a.tile_ks = s->tile_cols / 32u;
-        a.tile_magic = ~0ull / a.tile_ks + 1ull;  // umulhi64(i, tile_magic) == i / tile_ks for all i < 2^32
+        a.tile_magic = ~0ull / a.tile_ks + 1ull;  // (0 for tile_ks = 1)
     }
 }
 
@@ -2342,6 +2454,89 @@ int gemm_batch_impl(const df11_device_stream *ws, uint32_t n, const uint16_t *co
 #undef DF11_GEMM_BATCH_CASE
 }
 
+// Products into slots (df11_partials.h): one launch for one matrix, or two
+// that multiply the same x.  Fills p for the kernel that adds the slots;
+// with no workspace that is all (a query of p.slot_bytes).
+template <int K, int MT>
+int launch_partials(PartialArgs &b, uint32_t n, uint32_t max_wg, df11::Partials &p, float *slots,
+                    hipStream_t stream) {
+    size_t lds = 0;
+    for (uint32_t i = 0; i < n; ++i) lds = std::max(lds, dynamic_lds<K, kGemmGPW>(b.s[i], kGemmXBytes<MT>));
+    int dev = 0, cus = 0;
+    if (device_cus(dev, cus)) return DF11_E_HIP;
+    const auto pick = [n](bool tail) {
+        constexpr bool kCan = MT == 1;
+        if (n == 1)
+            return tail ? reinterpret_cast<const void *>(&df11_partial_kernel<K, MT, kCan>)
+                        : reinterpret_cast<const void *>(&df11_partial_kernel<K, MT, false>);
+        return tail ? reinterpret_cast<const void *>(&df11_partial_pair_kernel<K, MT, kCan>)
+                    : reinterpret_cast<const void *>(&df11_partial_pair_kernel<K, MT, false>);
+    };
+    // (the persistent grid must fit whichever instance launches)
+    int per_cu = resident_per_cu(pick(false), kThreadsPerGroup * kGemmGPW, dev, lds);
+    if (MT == 1) per_cu = std::min(per_cu, resident_per_cu(pick(true), kThreadsPerGroup * kGemmGPW, dev, lds));
+    if (per_cu < 1) return DF11_E_HIP;
+    uint64_t resident = static_cast<uint64_t>(per_cu) * static_cast<uint64_t>(cus);
+    if (max_wg) resident = std::min<uint64_t>(resident, std::max<uint32_t>(max_wg, n));
+    uint64_t sup[2], want[2];
+    for (uint32_t i = 0; i < n; ++i) sup[i] = (b.s[i].n_groups + kGemmGPW - 1) / kGemmGPW;
+    df11::split_grid(sup, n, resident, want);
+    // The dealt tail when every stream qualifies (as in launch_gemm_batch).
+    bool tail = MT == 1;
+    uint32_t share[2] = {};
+    for (uint32_t i = 0; i < n; ++i) {
+        DecodeArgs s = b.s[i];
+        share[i] = tail ? tail_schedule(s, b.m[i], sup[i], want[i]) : 0u;
+        tail = tail && share[i] != 0;
+        if (share[i]) b.s[i].pools = s.pools;
+    }
+    uint32_t next = 0;
+    uint64_t floats = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+        DecodeArgs &a = b.s[i];
+        MatmulArgs &m = b.m[i];
+        const uint32_t n_wg = tail ? share[i] : static_cast<uint32_t>(want[i]);
+        if (!tail) {
+            a.sched = nullptr;
+            m.fixed_len = 0;
+        }
+        m.passes = 1;
+        b.wg_begin[i] = next;
+        next += n_wg;
+        // Panels that a run of e elements touches: at most e / panel + 2.
+        const uint64_t panel = 64ull * a.tile_cols, group = p.max_group[i];
+        const uint64_t longest = tail ? m.fixed_len : (sup[i] + n_wg - 1) / n_wg;
+        m.wg_panels = static_cast<uint32_t>(std::min<uint64_t>(longest * kGemmGPW * group / panel + 2, a.n_elements / panel));
+        m.group_panels = static_cast<uint32_t>(std::min<uint64_t>(group / panel + 2, a.n_elements / panel));
+        m.tail_group0 = tail ? std::min<uint32_t>(n_wg * m.fixed_len * kGemmGPW, a.n_groups) : a.n_groups;
+        const uint64_t slot = 64ull * m.n_tokens;
+        m.tail_slots = static_cast<uint64_t>(n_wg) * kGemmGPW * m.wg_panels * slot;
+        df11::PartialStream &q = p.s[i];
+        q.out_pos = a.out_pos;
+        q.tile_magic = a.tile_magic;
+        q.base = floats;
+        q.tail = floats + m.tail_slots;
+        q.n_elements = a.n_elements;
+        q.n_groups = a.n_groups;
+        q.n_super = static_cast<uint32_t>(sup[i]);
+        q.n_wg = n_wg;
+        q.fixed_len = m.fixed_len;
+        q.wg_panels = m.wg_panels;
+        q.group_panels = m.group_panels;
+        q.tail_group0 = m.tail_group0;
+        m.y = slots + floats;
+        floats += m.tail_slots + static_cast<uint64_t>(a.n_groups - m.tail_group0) * m.group_panels * slot;
+    }
+    b.wg_begin[n] = next;
+    p.slot_bytes = 4 * floats;
+    if (!slots) return DF11_OK;
+    b.stride = df11::coprime_stride(next);
+    (void)hipGetLastError();
+    void *one[] = {&b.s[0], &b.m[0]}, *pair[] = {&b};
+    return launch_kernel(pick(tail), dim3(next), dim3(kThreadsPerGroup * kGemmGPW), n == 1 ? one : pair, lds, stream,
+                         nullptr, nullptr);
+}
+
 // The allocation-free batched decode's work counters: one set of
 // DF11_SCHEDULE_WORDS words per stream of a call, in a file-scope device
 // array that every call on a GPU shares (each GPU holds its own copy until
@@ -2369,6 +2564,63 @@ int scratch_address(uint32_t **ptr) {
 }
 
 }  // namespace
+
+namespace df11 {
+
+static_assert(kPartialGroups == kGemmGPW, "the kernel that adds the slots counts the group slots of a workgroup");
+
+int check_stream(const df11_device_stream *s) { return validate(s); }
+
+bool stream_overlaps(const df11_device_stream *s, const void *p, uint64_t bytes) {
+    const df11_header &h = s->h;
+    return h.n_elements && (overlaps(p, bytes, s->enc, h.enc_bytes) || overlaps(p, bytes, s->sm, h.sm_bytes) ||
+                            overlaps(p, bytes, s->gaps, h.gaps_bytes) || overlaps(p, bytes, s->out_pos, h.out_pos_bytes) ||
+                            overlaps(p, bytes, s->luts, 256ull * h.n_luts) || overlaps(p, bytes, s->code_lengths, 256) ||
+                            overlaps(p, bytes, s->decode_table, df11_decode_table_bytes(table_bits(s))) ||
+                            overlaps(p, bytes, s->schedule, s->schedule ? 4 * DF11_SCHEDULE_WORDS : 0));
+}
+
+bool same_table_bits(const df11_device_stream *a, const df11_device_stream *b) {
+    return table_bits(a) == table_bits(b);
+}
+
+int partial_products(const df11_device_stream *const *ws, uint32_t n, const uint16_t *x, uint64_t x_stride,
+                     uint32_t n_tokens, float *slots, hipStream_t stream, Partials &p) {
+    PartialArgs b{};
+    uint32_t max_wg = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+        fill_args(ws[i], b.s[i]);
+        MatmulArgs &m = b.m[i];
+        m.x = x;
+        m.x_stride = static_cast<uint32_t>(x_stride);
+        m.in_features = ws[i]->tile_cols;
+        m.out_features = static_cast<uint32_t>(ws[i]->h.n_elements / ws[i]->tile_cols);
+        m.n_tokens = n_tokens;
+        p.max_group[i] = ws[i]->h.max_group_elems;
+        const uint32_t cap = ws[i]->max_workgroups;
+        if (cap) max_wg = max_wg ? std::min(max_wg, cap) : cap;
+    }
+    // (the same tensor twice, say)
+    if (n == 2 && ws[0]->schedule && ws[1]->schedule &&
+        overlaps(ws[0]->schedule, 4 * DF11_SCHEDULE_WORDS, ws[1]->schedule, 4 * DF11_SCHEDULE_WORDS))
+        b.s[1].sched = nullptr;
+#define DF11_PARTIAL_CASE(KB)                                                   \
+    case KB:                                                                    \
+        switch (gemm_tiles(n_tokens)) {                                         \
+        case 1: return launch_partials<KB, 1>(b, n, max_wg, p, slots, stream);  \
+        case 2: return launch_partials<KB, 2>(b, n, max_wg, p, slots, stream);  \
+        default: return launch_partials<KB, 4>(b, n, max_wg, p, slots, stream); \
+        }
+    switch (table_bits(ws[0])) {
+        DF11_PARTIAL_CASE(10)
+        DF11_PARTIAL_CASE(11)
+        DF11_PARTIAL_CASE(12)
+    default: return DF11_E_INVALID_ARG;
+    }
+#undef DF11_PARTIAL_CASE
+}
+
+}  // namespace df11
 
 extern "C" {
 

@@ -880,4 +880,4 @@ def rans_compress(tensor: ArrayLike, shape: Optional[Sequence[int]] = None, devi
 
 
 # The operators around the products, under the same roof as the products.
-from .operators import rms_norm  # noqa: E402,F401
+from .operators import gated_matmul, matmul_epilogue, rms_norm  # noqa: E402,F401

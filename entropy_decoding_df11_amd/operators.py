@@ -8,6 +8,8 @@ and the norm's weight.  (The compressed weights are frozen: they have none.)
 
     y = rms_norm(x, weight)                       # norm
     y, s = rms_norm(x, weight, residual=r)        # s = x + r, y = norm of s
+    y = matmul_epilogue(w, x, bias, "gelu", r)    # act(x W^T + bias) + r
+    h = gated_matmul(gate, up, x)                 # silu(x Wg^T) * (x Wu^T)
 
 As in df11.py every step runs in libdf11.so on torch's current stream, or on
 the stream given; this module checks and passes arguments.
@@ -231,3 +233,113 @@ def rms_norm(x: "torch.Tensor", weight: Optional["torch.Tensor"] = None,  # noqa
         return _function("norm").apply(x, weight, residual, eps)
     y, s, _ = _norm_forward(x, weight, residual, eps, out, sum_out, stream, False)
     return y if residual is None else (y, s)
+
+
+# ---------------------------------------------------------------------------
+# Products with an epilogue.
+# ---------------------------------------------------------------------------
+
+def _check_product(ws, x, biases, activation, residual, out, out_dtype):
+    """Checks a product's arguments; (x as rows, its stride, activation code,
+    out's dtype)."""
+    import torch
+    for w in ws:
+        if len(w.shape) != 2 or not w.tile_cols:
+            raise ValueError("weights must be 2-D and compressed with layout='mfma_tiles'")
+    out_f, in_f = ws[0].shape
+    dev = ws[0]._bufs["enc"].device
+    if len(ws) == 2:
+        if ws[1].shape != ws[0].shape or ws[1].decode_table_bits != ws[0].decode_table_bits:
+            raise ValueError("gate and up must have the same shape and decode-table width")
+        if ws[1]._bufs["enc"].device != dev:
+            raise ValueError("gate and up must be on one device")
+    if x.dtype != torch.bfloat16 or x.dim() == 0 or x.shape[-1] != in_f:
+        raise ValueError("x must be a bfloat16 (..., in_features) tensor")
+    x2, xs = _rows(x, in_f, "x")
+    if x2.numel() and (x2.data_ptr() % 16 or xs % 8):
+        raise ValueError("x's rows must be 16-byte aligned")
+    act = _lib.ACTIVATIONS.get(activation if activation is not None else "none")
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(_lib.ACTIVATIONS)} or None")
+    floats = (torch.bfloat16, torch.float32)
+    for b in biases:
+        if b is not None and (b.shape != (out_f,) or b.dtype not in floats or not b.is_contiguous()):
+            raise ValueError("a bias must be contiguous bfloat16 or float32, one element per output feature")
+    if len({b.dtype for b in biases if b is not None}) > 1:
+        raise ValueError("both biases must have one dtype")
+    shape = x.shape[:-1] + (out_f,)
+    if residual is not None and (residual.shape != shape or residual.dtype not in floats):
+        raise ValueError("residual must be a bfloat16 or float32 (..., out_features) tensor")
+    if out is not None and (out.shape != shape or out.dtype not in floats):
+        raise ValueError("out must be a bfloat16 or float32 (..., out_features) tensor")
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out_dtype must be out's dtype")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in floats:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    _same_device(dev, x=x, residual=residual, out=out, bias=biases[0], up_bias=biases[-1])
+    return dev, x2, xs, act, out_dtype
+
+
+def _product_forward(ws, x, biases, activation, residual, out, out_dtype, stream, keep):
+    """act(x W^T + b) [* (x Wu^T + bu)] + residual; with keep, also the sums
+    before the activation, float32."""
+    import torch
+    dev, x2, xs, act, out_dtype = _check_product(ws, x, biases, activation, residual, out, out_dtype)
+    out_f, in_f = ws[0].shape
+    tokens = x2.shape[0]
+    lib = _lib.load()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(x.shape[:-1] + (out_f,), dtype=out_dtype, device=dev)
+        pre = [torch.empty((tokens, out_f), dtype=torch.float32, device=dev) for _ in ws] if keep else []
+        if out.numel() == 0:
+            return out, pre
+        e = _lib.Epilogue()
+        y2, e.out_stride = _rows(out, out_f, "out")
+        e.out, e.out_dtype, e.activation = y2.data_ptr(), _dtype(out, "out"), act
+        for i, b in enumerate(biases):
+            if b is not None:
+                e.bias[i], e.bias_dtype = b.data_ptr(), _dtype(b, "bias")
+        if residual is not None:
+            r2, e.residual_stride = _rows(residual, out_f, "residual")
+            e.residual, e.residual_dtype = r2.data_ptr(), _dtype(residual, "residual")
+        for i, p in enumerate(pre):
+            e.pre[i] = p.data_ptr()
+        structs = [ctypes.byref(w._stream_struct) for w in ws]
+        nbytes = lib.df11_epilogue_workspace(structs[0], structs[1] if len(ws) == 2 else None, tokens)
+        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        st = [w._claim(stream) for w in ws][0]
+        name = "df11_matmul_epilogue" if len(ws) == 1 else "df11_gated_matmul"
+        _lib.check(getattr(lib, name)(*structs, x2.data_ptr(), xs, tokens, in_f, out_f, ctypes.byref(e),
+                                      work.data_ptr(), nbytes, st), name)
+    return out, pre
+
+
+def matmul_epilogue(w, x: "torch.Tensor", bias: Optional["torch.Tensor"] = None,  # noqa: F821
+                    activation: Optional[str] = None, residual: Optional["torch.Tensor"] = None,  # noqa: F821
+                    out: Optional["torch.Tensor"] = None, out_dtype=None, stream=None) -> "torch.Tensor":  # noqa: F821
+    """act(x W^T + bias) + residual on the matrix cores with W compressed
+    (df11_matmul_epilogue), for any number of tokens.
+
+    w: a DF11Tensor compressed with layout="mfma_tiles"; x: bfloat16 (...,
+    in_features), rows at one stride and 16-byte aligned; bias: bfloat16 or
+    float32, one element per output feature; activation: None, "relu", "silu",
+    "gelu" or "gelu_tanh"; residual: bfloat16 or float32 (..., out_features).
+    Returns out, bfloat16 unless out or out_dtype says float32; out may be the
+    residual itself.  Everything before out is float32, and the same call gives
+    the same bits again."""
+    return _product_forward((w,), x, (bias,), activation, residual, out, out_dtype, stream, False)[0]
+
+
+def gated_matmul(gate, up, x: "torch.Tensor", gate_bias: Optional["torch.Tensor"] = None,  # noqa: F821
+                 up_bias: Optional["torch.Tensor"] = None, activation: Optional[str] = "silu",  # noqa: F821
+                 residual: Optional["torch.Tensor"] = None, out: Optional["torch.Tensor"] = None,  # noqa: F821
+                 out_dtype=None, stream=None) -> "torch.Tensor":  # noqa: F821
+    """act(x Wg^T + gate_bias) * (x Wu^T + up_bias) + residual, both
+    projections in one launch (df11_gated_matmul): the first half of a gated
+    feed-forward block.  gate and up have the same shape; otherwise as
+    matmul_epilogue."""
+    return _product_forward((gate, up), x, (gate_bias, up_bias), activation, residual, out, out_dtype, stream,
+                            False)[0]

@@ -73,6 +73,13 @@ typedef enum df11_status {
 #define DF11_BF16 0
 #define DF11_FP16 1
 #define DF11_FP32 2
+/* Activations of the products' epilogues: none, max(z, 0), z / (1 + exp(-z)),
+ * z Phi(z), and the tanh approximation of the last. */
+#define DF11_ACT_NONE 0
+#define DF11_ACT_RELU 1
+#define DF11_ACT_SILU 2
+#define DF11_ACT_GELU 3
+#define DF11_ACT_GELU_TANH 4
 
 /* The codebook shared by all tensors of one stream (host, plain data).
  *   code_lengths[e]: Huffman code length of exponent e, 0 if unused
@@ -531,6 +538,69 @@ int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uin
                        const void *dy, uint64_t dy_stride, const void *dsum, uint64_t dsum_stride, uint32_t rows,
                        uint32_t cols, uint32_t dtype, void *dx, uint64_t dx_stride, void *dweight, void *workspace,
                        uint64_t workspace_bytes, void *hip_stream);
+
+/* What a product does with its sums z before it writes them (host struct of
+ * device pointers):
+ *   df11_matmul_epilogue   out = act(z + bias[0]) + residual
+ *   df11_gated_matmul      out = act(z0 + bias[0]) * (z1 + bias[1]) + residual
+ *   bias             device, out_features of bias_dtype, or NULL; bias[1] only
+ *                    for a gated product
+ *   residual         device, n_tokens x out_features of residual_dtype,
+ *                    residual_stride elements from row to row, or NULL
+ *   out              device, n_tokens x out_features of out_dtype; may lie
+ *                    exactly on residual (same address, stride and type)
+ *   pre              device, n_tokens x out_features floats each, row-major:
+ *                    receive z + bias (both or neither for a gated product),
+ *                    for df11_matmul_grad; or NULL
+ *   activation       one of DF11_ACT_*
+ * Types are DF11_BF16 or DF11_FP32.  Everything up to out is float; out is
+ * rounded once. */
+typedef struct df11_epilogue {
+    const void *bias[2];
+    const void *residual;
+    void *out;
+    float *pre[2];
+    uint64_t residual_stride;
+    uint64_t out_stride;
+    uint32_t bias_dtype;
+    uint32_t residual_dtype;
+    uint32_t out_dtype;
+    uint32_t activation;
+} df11_epilogue;
+
+/* Bytes of the workspace of df11_matmul_epilogue (up NULL) or
+ * df11_gated_matmul for n_tokens tokens on the current device; 0 for streams
+ * that those calls refuse, or where nothing needs computing. */
+uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_stream *up, uint32_t n_tokens);
+
+/* y = act(x W^T + bias) + residual with W compressed, for any number of
+ * tokens: df11_matmul with its epilogue.
+ *   w             device stream in MFMA tile order, as for df11_matmul
+ *   x             device, n_tokens x in_features BF16, 16-byte aligned, x_stride
+ *                 elements (a multiple of 8) from row to row
+ *   in_features   a multiple of 32;  out_features a multiple of 64
+ *   workspace     device, 256-byte aligned, df11_epilogue_workspace bytes; holds
+ *                 nothing between calls, but calls that overlap in time need
+ *                 one each
+ * Sums are taken in float in an order fixed by the stream, the shapes and the
+ * device, not by timing.  A token whose x holds an infinity or a NaN gives
+ * infinities or NaN in its own outputs alone (0 * inf included: a weight of
+ * zero does not hide it).  Uses the stream's schedule counters like df11_decompress: calls
+ * that share a stream's counters must not overlap in time.  With no tokens or
+ * no outputs nothing is launched.  Errors: DF11_E_INVALID_ARG,
+ * DF11_E_BAD_STREAM, DF11_E_TOO_LARGE (n_tokens * features >= 2^32),
+ * DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
+int df11_matmul_epilogue(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t n_tokens,
+                         uint32_t in_features, uint32_t out_features, const df11_epilogue *e, void *workspace,
+                         uint64_t workspace_bytes, void *hip_stream);
+
+/* The gated product of a feed-forward block, both projections in one launch:
+ *   out = act(x Wg^T + bias[0]) * (x Wu^T + bias[1]) + residual
+ * gate and up have the same shape and decode_table_bits and may be the same
+ * stream.  Otherwise as df11_matmul_epilogue. */
+int df11_gated_matmul(const df11_device_stream *gate, const df11_device_stream *up, const uint16_t *x,
+                      uint64_t x_stride, uint32_t n_tokens, uint32_t in_features, uint32_t out_features,
+                      const df11_epilogue *e, void *workspace, uint64_t workspace_bytes, void *hip_stream);
 
 /* ---------------------------------------------------------------------------
  * rANS exponent coder.  The discussion on the page ("Opini Hacker News")

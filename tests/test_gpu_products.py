@@ -1,0 +1,286 @@
+"""GPU parity of the compressed products with an epilogue (matmul_epilogue,
+gated_matmul) against their formulas in float64 on the original weights.
+
+Tolerances.  u = 2^-24 and h half a step of the output's type.  Every product
+of two BF16 is exact in float32; a sum of C of them is added in float32 in
+some order, so z is off by at most dz = 1.01 C u sum |x w|, plus u |z| for
+the bias (its addition rounds once).  The activations have a slope of at most
+1.13 and are computed to 8 u of their value (expf and erfcf to 2 ulp, a
+quotient and two products); in a gated product each factor's error meets the
+other's size; the residual's addition rounds once and the output once."""
+
+import sys
+
+import numpy as np
+import pytest
+
+from entropy_decoding_df11_amd import df11, workloads
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+SLOPE = 1.13  # the largest slope of any activation here (GELU's)
+
+
+@pytest.fixture(scope="module")
+def torch_cuda():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a visible AMD GPU"
+    return torch
+
+
+def _note(msg):
+    print(f"[gpu-case] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+_WEIGHTS = {}
+
+
+def _weight(rows, cols, kind="normal", seed=0):
+    """(compressed weight, its float64 values on the GPU), kept for the module."""
+    import torch
+    key = (rows, cols, kind, seed)
+    if key not in _WEIGHTS:
+        rng = np.random.default_rng(seed)
+        n = rows * cols
+        bits = np.zeros(n, np.uint16) if kind == "zeros" else workloads.gen_stress(seed=seed, n=n) if kind == "stress" \
+            else workloads.f32_to_bf16_bits(rng.standard_normal(n) * 0.05)
+        w = torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16).view(rows, cols).double()
+        _WEIGHTS[key] = (df11.compress(bits, shape=(rows, cols), layout="mfma_tiles"), w)
+    return _WEIGHTS[key]
+
+
+def _act64(torch, name, z):
+    import torch.nn.functional as F
+    return {None: lambda v: v, "none": lambda v: v, "relu": F.relu, "silu": F.silu, "gelu": F.gelu,
+            "gelu_tanh": lambda v: F.gelu(v, approximate="tanh")}[name](z)
+
+
+def _half_step(torch, t, v):
+    f = torch.finfo(t)
+    return torch.clamp(v.abs() * (f.eps / 2), min=f.smallest_normal * f.eps / 2)
+
+
+def _linear64(x, w64, bias):
+    x64 = x.double().reshape(-1, w64.shape[1])
+    z = x64 @ w64.t()
+    dz = 1.01 * w64.shape[1] * U * (x64.abs() @ w64.abs().t())
+    if bias is not None:
+        z = z + bias.double()
+        dz = dz + U * (z.abs() + dz)
+    return z, dz
+
+
+def _expected(torch, x, ws, biases, act, residual, out_dtype):
+    """(value, bound) in float64."""
+    z, dz = _linear64(x, ws[0], biases[0])
+    y = _act64(torch, act, z)
+    dy = SLOPE * dz + 8 * U * (y.abs() + dz)
+    if len(ws) == 2:
+        z1, dz1 = _linear64(x, ws[1], biases[1])
+        dy = dy * (z1.abs() + dz1) + (y.abs() + dy) * dz1
+        y = y * z1
+        dy = dy + U * y.abs()
+    if residual is not None:
+        y = y + residual.double().reshape(y.shape)
+        dy = dy + U * (y.abs() + dy)
+    return y, dy + _half_step(torch, out_dtype, y.abs() + dy)
+
+
+def _assert_close(y, y64, bound):
+    err = (y.double().reshape(y64.shape) - y64).abs()
+    ok, worst = bool((err <= bound).all()), float((err / bound).max())
+    assert ok, worst
+
+
+def _x(torch, tokens, cols, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(tokens, cols, device="cuda", generator=g).bfloat16()
+
+
+def _side(torch, shape, dt, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, device="cuda", generator=g).to(dt)
+
+
+# one k-step; odd k-steps; panels smaller than a group, so that a range's
+# group slots skip panels; panels over many workgroups; long codes; one-bit
+# codes (groups of 2048 chunks)
+SHAPES = [(64, 32, "normal"), (192, 96, "normal"), (4096, 32, "normal"), (1024, 64, "zeros"), (128, 4096, "normal"),
+          (64, 14336, "stress"), (640, 1056, "normal"), (64, 8192, "zeros")]
+TOKENS = [1, 2, 8, 9, 16, 17, 33, 64, 65, 130, 300]
+
+
+@pytest.mark.parametrize("rows,cols,kind", SHAPES)
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_product(torch_cuda, rows, cols, kind, tokens):
+    torch = torch_cuda
+    _note(f"product {tokens} x {cols} -> {rows} {kind}")
+    w, w64 = _weight(rows, cols, kind)
+    u, u64 = _weight(rows, cols, kind, 1)
+    x = _x(torch, tokens, cols, seed=tokens)
+    for i, (act, bdt, rdt, odt) in enumerate([
+            (None, None, None, torch.float32), ("gelu", torch.bfloat16, None, torch.bfloat16),
+            ("silu", None, torch.bfloat16, torch.bfloat16), ("gelu_tanh", torch.float32, torch.float32, torch.float32),
+            ("relu", torch.bfloat16, torch.float32, torch.bfloat16)]):
+        bias = None if bdt is None else _side(torch, (rows,), bdt, 3)
+        bias2 = None if bdt is None or i == 3 else _side(torch, (rows,), bdt, 4)
+        res = None if rdt is None else _side(torch, (tokens, rows), rdt, 5)
+        y = df11.matmul_epilogue(w, x, bias=bias, activation=act, residual=res, out_dtype=odt)
+        assert y.dtype == odt and y.shape == (tokens, rows)
+        _assert_close(y, *_expected(torch, x, (w64,), (bias,), act, res, odt))
+        assert torch.equal(y, df11.matmul_epilogue(w, x, bias=bias, activation=act, residual=res, out_dtype=odt))
+        h = df11.gated_matmul(w, u, x, gate_bias=bias, up_bias=bias2, activation=act, residual=res, out_dtype=odt)
+        _assert_close(h, *_expected(torch, x, (w64, u64), (bias, bias2), act, res, odt))
+        assert torch.equal(h, df11.gated_matmul(w, u, x, gate_bias=bias, up_bias=bias2, activation=act, residual=res,
+                                                out_dtype=odt))
+
+
+@pytest.mark.parametrize("rows,cols", [(4096, 4096), (1024, 8192)])
+def test_product_long_streams(torch_cuda, rows, cols):
+    """Streams long enough for the dealt tail at 1 to 8 tokens, and every
+    launch shape: the schedule on and off, a capped grid."""
+    torch = torch_cuda
+    w, w64 = _weight(rows, cols)
+    u, u64 = _weight(rows, cols, "normal", 1)
+    for tokens in (1, 5, 8, 16, 40, 64, 100):
+        _note(f"long product {tokens} x {cols} -> {rows}")
+        x = _x(torch, tokens, cols, seed=tokens)
+        for t in (w, u):
+            t.set_dynamic_schedule(True)
+            t.set_max_workgroups(0)
+        y = df11.matmul_epilogue(w, x, activation="silu", out_dtype=torch.float32)
+        _assert_close(y, *_expected(torch, x, (w64,), (None,), "silu", None, torch.float32))
+        h = df11.gated_matmul(w, u, x, out_dtype=torch.float32)
+        want = _expected(torch, x, (w64, u64), (None, None), "silu", None, torch.float32)
+        _assert_close(h, *want)
+        # the same stream as gate and up
+        _assert_close(df11.gated_matmul(w, w, x, out_dtype=torch.float32),
+                      *_expected(torch, x, (w64, w64), (None, None), "silu", None, torch.float32))
+        for dynamic, cap in ((False, 0), (True, 37), (True, 3)):
+            for t in (w, u):
+                t.set_dynamic_schedule(dynamic)
+                t.set_max_workgroups(cap)
+            _assert_close(df11.gated_matmul(w, u, x, out_dtype=torch.float32), *want)
+            assert torch.equal(df11.gated_matmul(w, u, x), df11.gated_matmul(w, u, x))
+    for t in (w, u):
+        t.set_dynamic_schedule(True)
+        t.set_max_workgroups(0)
+
+
+@pytest.mark.parametrize("bits", [10, 12])
+def test_product_table_widths(torch_cuda, bits):
+    torch = torch_cuda
+    rng = np.random.default_rng(8)
+    raw = workloads.f32_to_bf16_bits(rng.standard_normal(256 * 512) * 0.05)
+    w64 = torch.from_numpy(raw.view(np.int16)).cuda().view(torch.bfloat16).view(256, 512).double()
+    w = df11.compress(raw, shape=(256, 512), layout="mfma_tiles", decode_table_bits=bits)
+    for tokens in (1, 20, 50, 90):
+        _note(f"product table {bits} {tokens}")
+        x = _x(torch, tokens, 512)
+        for table in (True, False):
+            w.use_decode_table(table)
+            _assert_close(df11.matmul_epilogue(w, x), *_expected(torch, x, (w64,), (None,), None, None, torch.bfloat16))
+            _assert_close(df11.gated_matmul(w, w, x),
+                          *_expected(torch, x, (w64, w64), (None, None), "silu", None, torch.bfloat16))
+
+
+@pytest.mark.parametrize("tokens", [1, 7, 40, 150])
+def test_product_strides_and_places(torch_cuda, tokens):
+    torch = torch_cuda
+    _note(f"product strides {tokens}")
+    w, w64 = _weight(640, 1056)
+    u, u64 = _weight(640, 1056, "normal", 1)
+    big = _x(torch, tokens * 3, 1056 + 40, seed=1).view(tokens, 3, 1096)
+    x = big[:, 1, 16:1072]  # 16-byte aligned rows, 3288 elements apart
+    res = _side(torch, (640,), torch.bfloat16, 2).expand(tokens, 640)  # one row for all
+    y = torch.full((tokens, 700), 5.0, device="cuda", dtype=torch.bfloat16)
+    got = df11.matmul_epilogue(w, x, activation="gelu", residual=res, out=y[:, 3:643])
+    _assert_close(got, *_expected(torch, x, (w64,), (None,), "gelu", res, torch.bfloat16))
+    assert bool((y[:, :3] == 5).all()) and bool((y[:, 643:] == 5).all())
+    # the residual stream updated in place, on a side stream
+    r = res.clone().contiguous()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    h = df11.gated_matmul(w, u, x, residual=r, out=r, stream=side)
+    side.synchronize()
+    assert h is r
+    _assert_close(r, *_expected(torch, x, (w64, u64), (None, None), "silu", res, torch.bfloat16))
+    torch.cuda.current_stream().wait_stream(side)
+    # three dimensions, one dimension, no tokens
+    x3 = _x(torch, tokens * 2, 1056).view(2, tokens, 1056)
+    y3 = df11.matmul_epilogue(w, x3)
+    assert y3.shape == (2, tokens, 640)
+    _assert_close(y3, *_expected(torch, x3, (w64,), (None,), None, None, torch.bfloat16))
+    assert df11.matmul_epilogue(w, x3[0, 0]).shape == (640,)
+    assert df11.gated_matmul(w, u, x3[:, :0]).shape == (2, 0, 640)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 100])
+def test_product_nonfinite_tokens_stay_alone(torch_cuda, tokens):
+    torch = torch_cuda
+    _note(f"product nonfinite {tokens}")
+    w, w64 = _weight(640, 1056)
+    u, u64 = _weight(640, 1056, "normal", 1)
+    x = _x(torch, tokens, 1056, seed=6)
+    x[1, 3] = float("inf")
+    x[tokens - 1, 1000] = float("nan")
+    keep = [t for t in range(tokens) if t not in (1, tokens - 1)]
+    for y, want in ((df11.matmul_epilogue(w, x), _expected(torch, x, (w64,), (None,), None, None, torch.bfloat16)),
+                    (df11.gated_matmul(w, u, x),
+                     _expected(torch, x, (w64, u64), (None, None), "silu", None, torch.bfloat16))):
+        _assert_close(y[keep], want[0][keep], want[1][keep])
+        assert not bool(torch.isfinite(y[tokens - 1]).any()) and bool(torch.isnan(y[tokens - 1]).all())
+    assert not bool(torch.isfinite(df11.matmul_epilogue(w, x)[1]).any())
+
+
+@pytest.mark.parametrize("tokens", [1, 24, 64, 200])
+def test_product_replays(torch_cuda, tokens):
+    """Two captured graphs of the same weights, replayed on new inputs with
+    eager calls between them."""
+    torch = torch_cuda
+    _note(f"product graph {tokens}")
+    w, _ = _weight(4096, 4096)
+    u, _ = _weight(4096, 4096, "normal", 1)
+    x = _x(torch, tokens, 4096)
+
+    def step():
+        h = df11.gated_matmul(w, u, x)
+        return h, df11.matmul_epilogue(w, h, activation="gelu", residual=x)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = step()
+        graphs.append((g, held))
+    for seed in (1, 2, 3):
+        x.copy_(_x(torch, tokens, 4096, seed=seed))
+        for g, held in graphs:
+            g.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in held]
+            assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def test_one_step_panels(torch_cuda):
+    """A matrix of 32 columns has one k-step per panel: its product and its
+    decompression must still tell its panels apart."""
+    torch = torch_cuda
+    _note("32 columns")
+    w, w64 = _weight(4096, 32)
+    same = torch.equal(w.decompress().double(), w64)
+    assert same
+    for tokens in (1, 20, 70):
+        x = _x(torch, tokens, 32)
+        z, dz = _linear64(x, w64, None)
+        _assert_close(w.matmul(x), z, dz)

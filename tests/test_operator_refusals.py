@@ -79,3 +79,109 @@ def test_norm_binding_refuses():
                 dict(x=x, out=torch.zeros(4, 8).half()), dict(x=x.clone().requires_grad_(), out=x)):
         with pytest.raises(ValueError):
             df11.rms_norm(**bad)
+
+
+def _stream(rows=128, cols=64, bits=11, at=0x200000000, tile=True):
+    """A device stream whose header is sound and whose addresses are never read."""
+    import numpy as np
+    from entropy_decoding_df11_amd import df11, workloads
+    w = workloads.f32_to_bf16_bits(np.random.default_rng(0).standard_normal(rows * cols) * 0.02)
+    host = df11.encode(w)
+    s = _lib.DeviceStream()
+    s.h = host.header
+    for i, name in enumerate(("enc", "sm", "gaps", "out_pos", "luts", "code_lengths", "decode_table")):
+        setattr(s, name, at + i * 0x1000000)
+    s.decode_table_bits = bits
+    s.tile_cols = cols if tile else 0
+    return s
+
+
+def _product(gated=False, **k):
+    import ctypes
+    lib = _lib_or_skip()
+    a = dict(w=_stream(), u=_stream(at=0x300000000), x=A, xs=64, t=4, inf=64, outf=128, ws=G, wb=0, bias=(None, None),
+             bt=0, res=None, rs=128, rt=0, out=B, os=128, ot=0, pre=(None, None), act=0, e=True)
+    a.update(k)
+    e = _lib.Epilogue()
+    for i in range(2):
+        e.bias[i], e.pre[i] = a["bias"][i], a["pre"][i]
+    e.residual, e.residual_stride, e.residual_dtype = a["res"], a["rs"], a["rt"]
+    e.out, e.out_stride, e.out_dtype = a["out"], a["os"], a["ot"]
+    e.bias_dtype, e.activation = a["bt"], a["act"]
+    ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
+    tail = (a["x"], a["xs"], a["t"], a["inf"], a["outf"], ctypes.byref(e) if a["e"] else None, a["ws"], a["wb"], None)
+    if gated:
+        return lib.df11_gated_matmul(ref(a["w"]), ref(a["u"]), *tail)
+    return lib.df11_matmul_epilogue(ref(a["w"]), *tail)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("bad", [
+    dict(w=None), dict(inf=32), dict(outf=64), dict(inf=60), dict(outf=100), dict(e=False), dict(act=5),
+    dict(ot=1), dict(ot=3), dict(res=C, rt=1), dict(bias=(C, None), bt=1), dict(bias=(C, None), bt=9),
+    dict(x=None), dict(x=A + 8), dict(xs=68), dict(xs=(1 << 31) + 8), dict(out=None), dict(out=B + 1),
+    dict(ot=2, out=B + 2), dict(os=127), dict(os=(1 << 31) + 1), dict(res=C + 1), dict(rt=2, res=C + 2),
+    dict(rs=(1 << 31) + 1, res=C), dict(bias=(C + 1, None)), dict(pre=(C + 2, D)), dict(out=A), dict(out=A + 128),
+    dict(res=B + 2), dict(res=B, rs=256), dict(res=B, rt=2), dict(bias=(B, None)), dict(pre=(B, D)), dict(pre=(A, D)),
+    dict(out=0x200000000), dict(out=0x201000000), dict(ws=G + 128),
+])
+def test_product_refuses(gated, bad):
+    assert _product(gated, **bad) == INVALID
+
+
+def test_product_refuses_streams():
+    assert _product(w=_stream(tile=False)) == INVALID       # not in tile order
+    assert _product(bias=(None, C)) == INVALID              # a second bias without a second matrix
+    assert _product(pre=(C, D)) == INVALID
+    assert _product(True, pre=(C, None)) == INVALID         # both or neither
+    assert _product(True, u=None) == INVALID
+    assert _product(True, u=_stream(rows=64, at=0x300000000)) == INVALID
+    assert _product(True, u=_stream(bits=10, at=0x300000000)) == INVALID
+    broken = _stream()
+    broken.h.n_groups += 1
+    assert _product(w=broken) == -6
+    assert _product(t=1 << 26) == TOO_LARGE
+
+
+def test_product_takes_nothing():
+    assert _product(t=0, x=None, out=None, ws=None) == 0
+    assert _product(True, t=0) == 0
+    import ctypes
+    lib = _lib_or_skip()
+    s, plain = _stream(), _stream(tile=False)
+    assert lib.df11_epilogue_workspace(None, None, 4) == 0
+    assert lib.df11_epilogue_workspace(ctypes.byref(s), None, 0) == 0
+    assert lib.df11_epilogue_workspace(ctypes.byref(plain), None, 4) == 0
+
+
+class _FakeWeight:
+    shape, tile_cols, decode_table_bits = (128, 64), 64, 11
+
+    def __init__(self, **k):
+        import torch
+        self._bufs = {"enc": torch.zeros(4)}
+        self.__dict__.update(k)
+
+
+def test_product_binding_refuses():
+    import torch
+    from entropy_decoding_df11_amd import df11
+    w, x = _FakeWeight(), torch.zeros(4, 64, dtype=torch.bfloat16)
+    bf = torch.bfloat16
+    for bad in (dict(x=x.float()), dict(x=x[:, :32]), dict(x=torch.zeros(64, 4, dtype=bf).t()),
+                dict(x=torch.zeros(4, 68, dtype=bf)[:, 4:]), dict(x=torch.zeros(4, 68, dtype=bf)[:, :64]),
+                dict(x=x, bias=torch.zeros(64)), dict(x=x, bias=torch.zeros(128).half()),
+                dict(x=x, bias=torch.zeros(256)[::2]), dict(x=x, activation="tanh"),
+                dict(x=x, residual=torch.zeros(4, 64)), dict(x=x, residual=torch.zeros(4, 128).half()),
+                dict(x=x, out=torch.zeros(3, 128)), dict(x=x, out=torch.zeros(4, 128).half()),
+                dict(x=x, out=torch.zeros(4, 128), out_dtype=bf), dict(x=x, out_dtype=torch.float16), dict(x=x)):
+        with pytest.raises(ValueError):
+            df11.matmul_epilogue(w, **bad)
+    for fake in (_FakeWeight(tile_cols=0), _FakeWeight(shape=(128,))):
+        with pytest.raises(ValueError):
+            df11.matmul_epilogue(fake, x)
+    for u in (_FakeWeight(shape=(64, 64)), _FakeWeight(decode_table_bits=12)):
+        with pytest.raises(ValueError):
+            df11.gated_matmul(w, u, x)
+    with pytest.raises(ValueError):
+        df11.gated_matmul(w, w, x, gate_bias=torch.zeros(128), up_bias=torch.zeros(128, dtype=bf))
