@@ -40,7 +40,8 @@ HIP_FLAGS = [
 
 
 HOST_SOURCES = ("df11_host.cpp", "df11_rans_host.cpp")
-DEVICE_SOURCES = ("df11_decode.hip", "df11_rans_decode.hip", "df11_norm.hip", "df11_product.hip")
+DEVICE_SOURCES = ("df11_decode.hip", "df11_rans_decode.hip", "df11_norm.hip", "df11_product.hip",
+                  "df11_dense.hip")
 
 
 def _torch_lib_dir() -> str:

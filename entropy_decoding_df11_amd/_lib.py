@@ -68,6 +68,8 @@ EXPORTED = [
     "df11_epilogue_workspace",
     "df11_matmul_epilogue",
     "df11_gated_matmul",
+    "df11_epilogue_grad_workspace",
+    "df11_matmul_epilogue_grad",
     "df11_rans_quantize",
     "df11_rans_encode",
     "df11_rans_build_table",
@@ -147,6 +149,21 @@ class Epilogue(ctypes.Structure):
         ("bias_dtype", ctypes.c_uint32),
         ("residual_dtype", ctypes.c_uint32),
         ("out_dtype", ctypes.c_uint32),
+        ("activation", ctypes.c_uint32),
+    ]
+
+
+class ProductGrad(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("pre", ctypes.c_void_p * 2),
+        ("dx", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p * 2),
+        ("dy_stride", ctypes.c_uint64),
+        ("dx_stride", ctypes.c_uint64),
+        ("dy_dtype", ctypes.c_uint32),
+        ("dx_dtype", ctypes.c_uint32),
+        ("bias_dtype", ctypes.c_uint32),
         ("activation", ctypes.c_uint32),
     ]
 
@@ -254,6 +271,10 @@ def load() -> ctypes.CDLL:
                                                 ctypes.POINTER(Epilogue), vp, u64, vp]),
         "df11_gated_matmul": (ctypes.c_int, [ctypes.POINTER(DeviceStream), ctypes.POINTER(DeviceStream), vp, u64, u32,
                                              u32, u32, ctypes.POINTER(Epilogue), vp, u64, vp]),
+        "df11_epilogue_grad_workspace": (u64, [ctypes.POINTER(DeviceStream), ctypes.POINTER(DeviceStream), u32,
+                                               ctypes.POINTER(ProductGrad)]),
+        "df11_matmul_epilogue_grad": (ctypes.c_int, [ctypes.POINTER(DeviceStream), ctypes.POINTER(DeviceStream), u32,
+                                                     u32, u32, ctypes.POINTER(ProductGrad), vp, u64, vp]),
         "df11_rans_quantize": (ctypes.c_int, [u64p, u32p]),
         "df11_rans_encode": (ctypes.c_int, [u32p, u16p, ctypes.c_uint64, u32p, u32p, u16p, ctypes.c_uint64, u8p,
                                             ctypes.POINTER(RansHeader)]),

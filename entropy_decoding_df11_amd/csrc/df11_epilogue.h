@@ -9,7 +9,23 @@
 #include "df11.h"
 #include "df11_types.h"
 
+namespace df11 {
+
+// Kernel arguments of an epilogue (df11_epilogue with its checks done).
+struct Epilogue {
+    const void *bias[2];
+    const void *residual;
+    void *out;
+    float *pre[2];
+    uint64_t residual_stride, out_stride;
+    uint32_t bias_dtype, residual_dtype, out_dtype, act;
+};
+
+}  // namespace df11
+
 namespace {
+
+using df11::Epilogue;
 
 // act(z) in float.  Each form keeps its relative accuracy where the value is
 // small (erfc and the logistic in place of 1 + erf and 1 + tanh, which cancel
@@ -47,16 +63,6 @@ __device__ __forceinline__ float slope(uint32_t act, float z) {
     default: return 1.0f;
     }
 }
-
-// Kernel arguments of an epilogue (df11_epilogue with its checks done).
-struct Epilogue {
-    const void *bias[2];
-    const void *residual;
-    void *out;
-    float *pre[2];
-    uint64_t residual_stride, out_stride;
-    uint32_t bias_dtype, residual_dtype, out_dtype, act;
-};
 
 // Sums of one output element (the second of a gated product) to its place.
 // row: token, col: output feature, features: outputs per token.

@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include "df11.h"
+#include "df11_columns.h"
 #include "df11_device.h"
 #include "df11_types.h"
 
@@ -398,6 +399,16 @@ constexpr uint64_t kMaxRowElements = 1ull << 40;  // keeps row * stride * bytes 
 
 }  // namespace
 
+namespace df11 {
+
+int column_sums(const float *p, uint32_t rows, uint32_t cols, void *out, uint32_t dtype, hipStream_t stream) {
+    void *params[] = {&p, &rows, &cols, &out, &dtype};
+    return launch_kernel(reinterpret_cast<const void *>(&df11_column_sum_kernel),
+                         dim3((cols + kWaveSize - 1) / kWaveSize), dim3(1024), params, 0, stream, nullptr, nullptr);
+}
+
+}  // namespace df11
+
 extern "C" {
 
 int df11_rms_norm(const void *x, uint64_t x_stride, const void *residual, uint64_t residual_stride,
@@ -508,13 +519,7 @@ int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uin
                                      dim3(block), params, 0, stream, nullptr, nullptr);
         if (rc) return rc;
     }
-    if (dweight) {
-        void *params[] = {&partial, &groups, &cols, &dweight, &weight_dtype};
-        return launch_kernel(reinterpret_cast<const void *>(&df11_column_sum_kernel),
-                             dim3((cols + kWaveSize - 1) / kWaveSize), dim3(1024), params, 0, stream, nullptr,
-                             nullptr);
-    }
-    return DF11_OK;
+    return dweight ? df11::column_sums(partial, groups, cols, dweight, weight_dtype, stream) : DF11_OK;
 }
 
 }  // extern "C"

@@ -4,10 +4,21 @@
 //   y = act(x Wg^T + bias0) * (x Wu^T + bias1) + residual   df11_gated_matmul
 //
 // The weights are DF11 streams in MFMA tile order.  Up to kPartialTokens
-// tokens at a time the decode is fused into the product
-// (df11::partial_products): partial sums go to slots, and one kernel adds a
-// panel's slots in the order of the stream, applies the epilogue and rounds
-// once.
+// tokens the decode is fused into the product (df11::partial_products):
+// partial sums go to slots, and one kernel adds a panel's slots in the order
+// of the stream, applies the epilogue and rounds once.  Beyond that the
+// stream is decoded once into the workspace, in tile order as it is stored,
+// and multiplied from there (df11::dense_product): every further sweep of the
+// fused product would decode it again.
+//
+// The gradients go through the dense product too:
+//
+//   dz = dy * act'(z)   or   dzg = dy * zu * act'(zg), dzu = dy * act(zg)
+//   dx = dz W           or   dx = dzg Wg + dzu Wu
+//   dbias = sum over the tokens of dz
+//
+// with dz rounded to BF16, the matrix cores' operand type, for dx and kept in
+// float for dbias.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -15,6 +26,8 @@
 #include <stdint.h>
 
 #include "df11.h"
+#include "df11_columns.h"
+#include "df11_dense.h"
 #include "df11_device.h"
 #include "df11_epilogue.h"
 #include "df11_partials.h"
@@ -135,6 +148,70 @@ __global__ __launch_bounds__(256) void df11_sum_slots_kernel(SumArgs a) {
     }
 }
 
+// dz of every output, from dy and the sums before the activation.
+struct SlopeArgs {
+    const void *dy;
+    const float *pre[2];
+    uint16_t *dz[2];     // BF16, tokens x features; or null
+    float *partial[2];   // [chunk][features]: sums of dz over the chunk's tokens; or null
+    uint64_t dy_stride;
+    uint32_t dy_dtype, dy_vec, act, tokens, features, chunk;
+};
+
+// A wave takes four columns per lane of every fourth token of the block's
+// chunk of tokens (blockIdx.y); the four waves' column sums meet in LDS.
+template <bool kGated>
+__global__ __launch_bounds__(256) void df11_slope_kernel(SlopeArgs a) {
+    __shared__ float s_sum[2][3][256];
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), wave = threadIdx.x / kWaveSize;
+    const uint32_t col = 256u * blockIdx.x + 4u * lane;
+    const uint32_t end = min((blockIdx.y + 1u) * a.chunk, a.tokens);
+    constexpr int kMats = kGated ? 2 : 1;
+    float sum[2][4] = {};
+    for (uint32_t t = blockIdx.y * a.chunk + wave; t < end && col < a.features; t += 4u) {
+        float dy[4], z0[4], z1[4], d[2][4];
+        const uint64_t at = t * a.dy_stride + col, in = static_cast<uint64_t>(t) * a.features + col;
+        if (a.dy_vec && a.dy_dtype == DF11_BF16) {
+            load_vec<bf16_t, 4>(static_cast<const bf16_t *>(a.dy) + at, dy);
+        } else if (a.dy_vec) {
+            load_vec<float, 4>(static_cast<const float *>(a.dy) + at, dy);
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) dy[e] = load_as(a.dy, at + e, a.dy_dtype);
+        }
+        if (a.pre[0]) load_vec<float, 4>(a.pre[0] + in, z0);
+        if constexpr (kGated) load_vec<float, 4>(a.pre[1] + in, z1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (kGated) {
+                d[0][e] = dy[e] * z1[e] * slope(a.act, z0[e]);
+                d[1][e] = dy[e] * activate(a.act, z0[e]);
+            } else {
+                d[0][e] = a.act == DF11_ACT_NONE ? dy[e] : dy[e] * slope(a.act, z0[e]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kMats; ++m) {
+            if (a.dz[m]) store_vec<bf16_t, 4>(reinterpret_cast<bf16_t *>(a.dz[m]) + in, d[m]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[m][e] += d[m][e];
+        }
+    }
+    if (!a.partial[0] && !a.partial[1]) return;
+    for (int m = 0; m < kMats; ++m)
+        for (int e = 0; e < 4 && wave; ++e) s_sum[m][wave - 1u][4u * lane + e] = sum[m][e];
+    __syncthreads();
+    if (wave || col >= a.features) return;
+    for (int m = 0; m < kMats; ++m) {
+        if (!a.partial[m]) continue;
+        for (uint32_t e = 0; e < 4; ++e) {
+            float v = sum[m][e];
+            for (int w = 0; w < 3; ++w) v += s_sum[m][w][4u * lane + e];
+            a.partial[m][static_cast<uint64_t>(blockIdx.y) * a.features + col + e] = v;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host.
 
@@ -235,56 +312,237 @@ bool workspace_clear(const Call &c, const void *ws, uint64_t bytes) {
     return !bad;
 }
 
-int slots_impl(const Call &c, uint32_t t0, uint32_t tokens, void *workspace, hipStream_t stream) {
+int slots_impl(const Call &c, void *workspace, hipStream_t stream) {
     SumArgs a{};
     Partials p{};
-    float *slots = static_cast<float *>(workspace);
-    int rc = df11::partial_products(c.w, c.n, c.x + t0 * c.x_stride, c.x_stride, tokens, slots, stream, p);
+    a.slots = static_cast<float *>(workspace);
+    const int rc = df11::partial_products(c.w, c.n, c.x, c.x_stride, c.n_tokens, static_cast<float *>(workspace), stream, p);
     if (rc) return rc;
     a.s[0] = p.s[0];
     a.s[1] = p.s[1];
-    a.slots = slots;
     a.e = c.e;
-    const uint64_t done = static_cast<uint64_t>(t0) * c.out_features;
-    a.e.out = static_cast<uint8_t *>(a.e.out) + t0 * a.e.out_stride * dtype_bytes(a.e.out_dtype);
-    if (a.e.residual)
-        a.e.residual = static_cast<const uint8_t *>(a.e.residual) +
-                       t0 * a.e.residual_stride * dtype_bytes(a.e.residual_dtype);
-    for (int i = 0; i < 2; ++i)
-        if (a.e.pre[i]) a.e.pre[i] += done;
-    a.n_tokens = tokens;
+    a.n_tokens = c.n_tokens;
     a.features = c.out_features;
     void *params[] = {&a};
     return launch_kernel(c.n == 2 ? reinterpret_cast<const void *>(&df11_sum_slots_kernel<true>)
                                   : reinterpret_cast<const void *>(&df11_sum_slots_kernel<false>),
-                         dim3(c.out_features / kPanelRows, (tokens + kSumTokens - 1) / kSumTokens), dim3(256), params,
-                         0, stream, nullptr, nullptr);
+                         dim3(c.out_features / kPanelRows, (c.n_tokens + kSumTokens - 1) / kSumTokens), dim3(256),
+                         params, 0, stream, nullptr, nullptr);
 }
 
 uint64_t slots_bytes(const df11_device_stream *const *ws, uint32_t n, uint32_t n_tokens) {
     Partials p{};
-    if (df11::partial_products(ws, n, nullptr, 0, std::min(n_tokens, kPartialTokens), nullptr, nullptr, p)) return 0;
+    if (df11::partial_products(ws, n, nullptr, 0, n_tokens, nullptr, nullptr, p)) return 0;
     return p.slot_bytes;
 }
 
-uint64_t forward_workspace(const df11_device_stream *const *ws, uint32_t n, uint32_t n_tokens) {
-    return slots_bytes(ws, n, n_tokens);
+// Bytes of the decoded weights (one copy of a stream given twice).
+uint64_t decoded_bytes(const df11_device_stream *const *ws, uint32_t n) {
+    const uint64_t one = round_up(2 * ws[0]->h.n_elements, 256);
+    return n == 2 && ws[1]->enc != ws[0]->enc ? 2 * one : one;
+}
+
+// Decodes the streams into the workspace in tile order, as they are stored;
+// out[i] receives where.
+int decode_weights(const df11_device_stream *const *ws, uint32_t n, void *workspace, const uint16_t **out,
+                   hipStream_t stream) {
+    const uint64_t one = round_up(2 * ws[0]->h.n_elements, 256);
+    df11_device_stream flat[2];
+    uint16_t *to[2];
+    const bool both = n == 2 && ws[1]->enc != ws[0]->enc;
+    for (uint32_t i = 0; i < n; ++i) {
+        flat[i] = *ws[i];
+        flat[i].tile_cols = 0;
+        to[i] = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + (both ? i * one : 0));
+        out[i] = to[i];
+    }
+    if (both && flat[0].groups_per_workgroup == flat[1].groups_per_workgroup)
+        return df11_decompress_batch(flat, 2, to, stream);
+    int rc = df11_decompress(&flat[0], to[0], stream);
+    if (!rc && both) rc = df11_decompress(&flat[1], to[1], stream);
+    return rc;
+}
+
+uint64_t forward_workspace(const df11_device_stream *const *ws, uint32_t n, uint32_t n_tokens, uint32_t cols) {
+    if (n_tokens <= kPartialTokens) return slots_bytes(ws, n, n_tokens);
+    const uint32_t rows = static_cast<uint32_t>(ws[0]->h.n_elements / cols);
+    const uint64_t more = df11::dense_workspace(n == 2 ? df11::kDenseGated : df11::kDensePlain, n, n_tokens, rows, cols);
+    return more == ~0ull ? 0 : decoded_bytes(ws, n) + more;
+}
+
+int dense_impl(const Call &c, void *workspace, hipStream_t stream) {
+    df11::DenseCall d{};
+    d.mode = c.n == 2 ? df11::kDenseGated : df11::kDensePlain;
+    d.left[0] = c.x;
+    d.left_stride = c.x_stride;
+    d.tokens = c.n_tokens;
+    d.rows = c.out_features;
+    d.cols = c.in_features;
+    const int rc = decode_weights(c.w, c.n, workspace, d.w, stream);
+    if (rc) return rc;
+    return df11::dense_product(d, c.e, reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + decoded_bytes(c.w, c.n)),
+                               stream);
 }
 
 int forward(Call &c, const df11_epilogue *e, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {
     bool empty = false;
     int rc = check_call(c, e, workspace, empty);
     if (rc || empty) return rc;
-    const uint64_t need = forward_workspace(c.w, c.n, c.n_tokens);
+    const uint64_t need = forward_workspace(c.w, c.n, c.n_tokens, c.in_features);
     if (!need) return DF11_E_HIP;
     if (!workspace) return DF11_E_INVALID_ARG;
     if (workspace_bytes < need) return DF11_E_BUFFER_TOO_SMALL;
     if (!workspace_clear(c, workspace, need)) return DF11_E_INVALID_ARG;
-    for (uint32_t t0 = 0; t0 < c.n_tokens; t0 += kPartialTokens) {
-        rc = slots_impl(c, t0, std::min(kPartialTokens, c.n_tokens - t0), workspace, stream);
+    return c.n_tokens <= kPartialTokens ? slots_impl(c, workspace, stream) : dense_impl(c, workspace, stream);
+}
+
+// ---- gradients
+
+constexpr uint32_t kSlopeChunk = 32;      // tokens of one block of the slopes' kernel, at least
+constexpr uint32_t kSlopeMaxChunks = 256;  // (partial rows of a bias gradient)
+
+uint32_t slope_chunk(uint32_t tokens) {
+    return std::max(kSlopeChunk, (tokens + kSlopeMaxChunks - 1) / kSlopeMaxChunks);
+}
+
+// Where a gradient call's parts of the workspace begin.
+struct GradPlan {
+    uint64_t dz[2], partial[2], weights, split, end;
+    uint32_t chunks;
+    bool own_dz;  // dz is written (not dy itself)
+};
+
+bool grad_plan(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols,
+               const df11_product_grad &g, GradPlan &p) {
+    p.own_dz = n == 2 || g.activation != DF11_ACT_NONE || g.dy_dtype != DF11_BF16 || !aligned(g.dy, 16) ||
+               g.dy_stride % 8;
+    const uint32_t chunk = slope_chunk(tokens);
+    p.chunks = (tokens + chunk - 1) / chunk;
+    uint64_t at = 0;
+    for (uint32_t i = 0; i < 2; ++i) {
+        p.dz[i] = at;
+        if (i < n && g.dx && p.own_dz) at += round_up(2ull * tokens * rows, 256);
+        p.partial[i] = at;
+        if (i < n && g.dbias[i]) at += round_up(4ull * p.chunks * rows, 256);
+    }
+    p.weights = at;
+    if (g.dx) at += decoded_bytes(ws, n);
+    p.split = at;
+    if (g.dx) {
+        const uint64_t more = df11::dense_workspace(df11::kDenseBack, n, tokens, rows, cols);
+        if (more == ~0ull) return false;
+        at += more;
+    }
+    p.end = at;
+    return true;
+}
+
+int backward(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens, uint32_t cols, uint32_t rows,
+             const df11_product_grad *g, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {
+    int rc = check_streams(ws, n, tokens, cols, rows);
+    if (rc) return rc;
+    if (!g || g->activation > DF11_ACT_GELU_TANH) return DF11_E_INVALID_ARG;
+    const auto float_bytes = [](uint32_t dtype) { return dtype == DF11_FP16 ? 0u : dtype_bytes(dtype); };
+    const uint32_t dy_bytes = float_bytes(g->dy_dtype), dx_bytes = float_bytes(g->dx_dtype);
+    const uint32_t bias_bytes = float_bytes(g->bias_dtype);
+    if (!dy_bytes || (g->dx && !dx_bytes) || ((g->dbias[0] || g->dbias[1]) && !bias_bytes)) return DF11_E_INVALID_ARG;
+    if (n == 1 && (g->dbias[1] || g->pre[1])) return DF11_E_INVALID_ARG;
+    if (rows == 0) return DF11_OK;
+    const bool needs_pre = n == 2 || g->activation != DF11_ACT_NONE;
+    if (tokens) {
+        if (!g->dy || !aligned(g->dy, dy_bytes) || g->dy_stride > kMaxStride) return DF11_E_INVALID_ARG;
+        for (uint32_t i = 0; i < n; ++i)
+            if (needs_pre && (!g->pre[i] || !aligned(g->pre[i], 16))) return DF11_E_INVALID_ARG;
+        if (g->dx && (!aligned(g->dx, dx_bytes) || g->dx_stride > kMaxStride || (tokens > 1 && g->dx_stride < cols)))
+            return DF11_E_INVALID_ARG;
+    }
+    for (int i = 0; i < 2; ++i)
+        if (g->dbias[i] && !aligned(g->dbias[i], bias_bytes)) return DF11_E_INVALID_ARG;
+    // Outputs and the workspace stay clear of the inputs and of each other.
+    const uint64_t dy_span = tokens ? rows_span(tokens, rows, g->dy_stride, dy_bytes) : 0;
+    const uint64_t elems = static_cast<uint64_t>(tokens) * rows;
+    GradPlan p{};
+    uint64_t need = 0;
+    if (tokens) {
+        // (nothing below reads a pointer, so the overlap checks can wait for the plan)
+        if (workspace && !aligned(workspace, 256)) return DF11_E_INVALID_ARG;
+    }
+    const void *outs[] = {tokens ? g->dx : nullptr, g->dbias[0], g->dbias[1], nullptr};
+    uint64_t spans[] = {tokens && g->dx ? rows_span(tokens, cols, g->dx_stride, dx_bytes) : 0,
+                        g->dbias[0] ? static_cast<uint64_t>(bias_bytes) * rows : 0,
+                        g->dbias[1] ? static_cast<uint64_t>(bias_bytes) * rows : 0, 0};
+    const auto clear = [&](int k) {
+        for (int j = 0; j < k; ++j)
+            if (overlaps(outs[k], spans[k], outs[j], spans[j])) return false;
+        if (overlaps(outs[k], spans[k], g->dy, dy_span)) return false;
+        for (int i = 0; i < 2; ++i)
+            if (g->pre[i] && overlaps(outs[k], spans[k], g->pre[i], 4 * elems)) return false;
+        for (uint32_t i = 0; i < n; ++i)
+            if (df11::stream_overlaps(ws[i], outs[k], spans[k])) return false;
+        return true;
+    };
+    for (int k = 0; k < 3; ++k)
+        if (!clear(k)) return DF11_E_INVALID_ARG;
+    if (tokens == 0) {
+        for (uint32_t i = 0; i < n; ++i) {
+            if (!g->dbias[i]) continue;
+            rc = df11::column_sums(nullptr, 0, rows, g->dbias[i], g->bias_dtype, stream);
+            if (rc) return rc;
+        }
+        return DF11_OK;
+    }
+    if (!g->dx && !g->dbias[0] && !g->dbias[1]) return DF11_OK;
+    if (!grad_plan(ws, n, tokens, rows, cols, *g, p)) return DF11_E_HIP;
+    need = p.end;
+    if (!workspace && need) return DF11_E_INVALID_ARG;
+    if (workspace_bytes < need) return DF11_E_BUFFER_TOO_SMALL;
+    outs[3] = workspace;
+    spans[3] = need;
+    if (!clear(3)) return DF11_E_INVALID_ARG;
+
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    SlopeArgs a{};
+    a.dy = g->dy;
+    a.dy_stride = g->dy_stride;
+    a.dy_dtype = g->dy_dtype;
+    a.dy_vec = aligned(g->dy, 4 * dy_bytes) && g->dy_stride % 4 == 0;
+    a.act = g->activation;
+    a.tokens = tokens;
+    a.features = rows;
+    a.chunk = slope_chunk(tokens);
+    for (uint32_t i = 0; i < n; ++i) {
+        a.pre[i] = needs_pre ? g->pre[i] : nullptr;
+        if (g->dx && p.own_dz) a.dz[i] = reinterpret_cast<uint16_t *>(base + p.dz[i]);
+        if (g->dbias[i]) a.partial[i] = reinterpret_cast<float *>(base + p.partial[i]);
+    }
+    (void)hipGetLastError();
+    if (a.dz[0] || a.partial[0] || a.partial[1]) {
+        void *params[] = {&a};
+        rc = launch_kernel(n == 2 ? reinterpret_cast<const void *>(&df11_slope_kernel<true>)
+                                  : reinterpret_cast<const void *>(&df11_slope_kernel<false>),
+                           dim3((rows + 255) / 256, p.chunks), dim3(256), params, 0, stream, nullptr, nullptr);
         if (rc) return rc;
     }
-    return DF11_OK;
+    for (uint32_t i = 0; i < n; ++i) {
+        if (!g->dbias[i]) continue;
+        rc = df11::column_sums(a.partial[i], p.chunks, rows, g->dbias[i], g->bias_dtype, stream);
+        if (rc) return rc;
+    }
+    if (!g->dx) return DF11_OK;
+    df11::DenseCall d{};
+    d.mode = df11::kDenseBack;
+    d.tokens = tokens;
+    d.rows = rows;
+    d.cols = cols;
+    rc = decode_weights(ws, n, base + p.weights, d.w, stream);
+    if (rc) return rc;
+    for (uint32_t i = 0; i < n; ++i) d.left[i] = p.own_dz ? a.dz[i] : static_cast<const uint16_t *>(g->dy);
+    d.left_stride = p.own_dz ? rows : g->dy_stride;
+    Epilogue e{};
+    e.out = g->dx;
+    e.out_stride = g->dx_stride;
+    e.out_dtype = g->dx_dtype;
+    return df11::dense_product(d, e, reinterpret_cast<float *>(base + p.split), stream);
 }
 
 }  // namespace
@@ -299,7 +557,29 @@ uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_
         if (df11::check_stream(ws[i]) || !ws[i]->h.n_elements || !ws[i]->tile_cols ||
             ws[i]->h.n_elements != w->h.n_elements || ws[i]->tile_cols != w->tile_cols)
             return 0;
-    return forward_workspace(ws, n, n_tokens);
+    return forward_workspace(ws, n, n_tokens, w->tile_cols);
+}
+
+uint64_t df11_epilogue_grad_workspace(const df11_device_stream *w, const df11_device_stream *up, uint32_t n_tokens,
+                                     const df11_product_grad *g) {
+    const df11_device_stream *ws[] = {w, up};
+    const uint32_t n = up ? 2 : 1;
+    if (!w || !n_tokens || !g) return 0;
+    for (uint32_t i = 0; i < n; ++i)
+        if (df11::check_stream(ws[i]) || !ws[i]->h.n_elements || !ws[i]->tile_cols ||
+            ws[i]->h.n_elements != w->h.n_elements || ws[i]->tile_cols != w->tile_cols)
+            return 0;
+    GradPlan p{};
+    return grad_plan(ws, n, n_tokens, static_cast<uint32_t>(w->h.n_elements / w->tile_cols), w->tile_cols, *g, p) ? p.end
+                                                                                                             : 0;
+}
+
+int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_stream *up, uint32_t n_tokens,
+                          uint32_t in_features, uint32_t out_features, const df11_product_grad *g, void *workspace,
+                          uint64_t workspace_bytes, void *hip_stream) {
+    const df11_device_stream *ws[] = {w, up};
+    return backward(ws, up ? 2 : 1, n_tokens, in_features, out_features, g, workspace, workspace_bytes,
+                    static_cast<hipStream_t>(hip_stream));
 }
 
 int df11_matmul_epilogue(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t n_tokens,

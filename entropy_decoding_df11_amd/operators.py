@@ -52,7 +52,7 @@ def _rows(t: "torch.Tensor", cols: int, what: str) -> Tuple["torch.Tensor", int]
             v = t.view(-1, cols) if t.dim() and t.numel() else t.reshape(0, cols)
         except RuntimeError:
             raise ValueError(f"{what} must have rows at one stride") from None
-    if cols > 1 and v.stride(1) != 1:
+    if cols > 1 and v.numel() and v.stride(1) != 1:
         raise ValueError(f"{what} must be contiguous along its last dimension")
     stride = v.stride(0) if v.shape[0] > 1 else cols
     if stride < 0:
@@ -206,7 +206,31 @@ def _function(name):
                                             want_w)
                 return dx if want_x else None, dw, dx if want_r else None, None
 
+        class Product(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, residual, bias0, bias1, ws, activation, out_dtype):
+                biases = (bias0, bias1)[:len(ws)]
+                keep = len(ws) == 2 or activation not in (None, "none")
+                y, pre = _product_forward(ws, x, biases, activation, residual, None, out_dtype, None, keep)
+                # (a bias is kept for its type alone)
+                ctx.save_for_backward(bias0, bias1, *pre)
+                ctx.ws, ctx.activation, ctx.x_shape = ws, activation, x.shape
+                ctx.residual_dtype = None if residual is None else residual.dtype
+                return y
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dy):
+                bias0, bias1, *pre = ctx.saved_tensors
+                want_x, want_r, want0, want1 = ctx.needs_input_grad[:4]
+                biases = [b if want else None for b, want in ((bias0, want0), (bias1, want1))][:len(ctx.ws)]
+                dx, db = _product_backward(ctx.ws, pre, dy, _lib.ACTIVATIONS[ctx.activation or "none"], ctx.x_shape,
+                                           want_x, biases)
+                dr = dy.to(ctx.residual_dtype) if want_r else None
+                return dx, dr, db[0], db[1] if len(db) == 2 else None, None, None, None
+
         _FUNCTIONS["norm"] = Norm
+        _FUNCTIONS["product"] = Product
     return _FUNCTIONS[name]
 
 
@@ -317,6 +341,48 @@ def _product_forward(ws, x, biases, activation, residual, out, out_dtype, stream
     return out, pre
 
 
+def _product_backward(ws, pre, dy, act, x_shape, want_x, biases):
+    """(dx or None, the biases' gradients): biases[i] is a tensor like the
+    bias whose gradient is wanted, or None."""
+    import torch
+    out_f, in_f = ws[0].shape
+    dev = dy.device
+    dy = _rowwise(dy)
+    dy2, dys = _rows(dy, out_f, "dy")
+    tokens = dy2.shape[0]
+    lib = _lib.load()
+    with _on(dev, None) as st:
+        dx = torch.empty(x_shape, dtype=torch.bfloat16, device=dev) if want_x else None
+        db = [None if b is None else torch.empty_like(b) for b in biases]
+        g = _lib.ProductGrad()
+        g.dy, g.dy_stride, g.dy_dtype, g.activation = dy2.data_ptr(), dys, _dtype(dy, "dy"), act
+        for i, p in enumerate(pre):
+            g.pre[i] = p.data_ptr()
+        if dx is not None:
+            g.dx, g.dx_stride, g.dx_dtype = dx.data_ptr(), in_f, _lib.BF16
+        for i, b in enumerate(db):
+            if b is not None:
+                g.dbias[i], g.bias_dtype = b.data_ptr(), _dtype(b, "bias")
+        structs = [ctypes.byref(w._stream_struct) for w in ws] + [None] * (2 - len(ws))
+        nbytes = lib.df11_epilogue_grad_workspace(*structs, tokens, ctypes.byref(g)) if tokens else 0
+        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        st = [w._claim(None) for w in ws][0]
+        _lib.check(lib.df11_matmul_epilogue_grad(*structs, tokens, in_f, out_f, ctypes.byref(g), work.data_ptr(),
+                                                 nbytes, st), "df11_matmul_epilogue_grad")
+    return dx, db
+
+
+def _product(ws, x, biases, activation, residual, out, out_dtype, stream):
+    import torch
+    inputs = (x, residual, *biases)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        if out is not None or stream is not None:
+            raise ValueError("out and stream are for calls without gradients")
+        return _function("product").apply(x, residual, biases[0], biases[1] if len(ws) == 2 else None, ws, activation,
+                                          out_dtype)
+    return _product_forward(ws, x, biases, activation, residual, out, out_dtype, stream, False)[0]
+
+
 def matmul_epilogue(w, x: "torch.Tensor", bias: Optional["torch.Tensor"] = None,  # noqa: F821
                     activation: Optional[str] = None, residual: Optional["torch.Tensor"] = None,  # noqa: F821
                     out: Optional["torch.Tensor"] = None, out_dtype=None, stream=None) -> "torch.Tensor":  # noqa: F821
@@ -329,8 +395,10 @@ def matmul_epilogue(w, x: "torch.Tensor", bias: Optional["torch.Tensor"] = None,
     "gelu" or "gelu_tanh"; residual: bfloat16 or float32 (..., out_features).
     Returns out, bfloat16 unless out or out_dtype says float32; out may be the
     residual itself.  Everything before out is float32, and the same call gives
-    the same bits again."""
-    return _product_forward((w,), x, (bias,), activation, residual, out, out_dtype, stream, False)[0]
+    the same bits again.  Where x, bias or residual require a gradient the
+    output carries it (then neither out nor stream may be given): the sums
+    before an activation are kept for it in float32, and w itself is frozen."""
+    return _product((w,), x, (bias,), activation, residual, out, out_dtype, stream)
 
 
 def gated_matmul(gate, up, x: "torch.Tensor", gate_bias: Optional["torch.Tensor"] = None,  # noqa: F821
@@ -341,5 +409,4 @@ def gated_matmul(gate, up, x: "torch.Tensor", gate_bias: Optional["torch.Tensor"
     projections in one launch (df11_gated_matmul): the first half of a gated
     feed-forward block.  gate and up have the same shape; otherwise as
     matmul_epilogue."""
-    return _product_forward((gate, up), x, (gate_bias, up_bias), activation, residual, out, out_dtype, stream,
-                            False)[0]
+    return _product((gate, up), x, (gate_bias, up_bias), activation, residual, out, out_dtype, stream)

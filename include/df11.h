@@ -602,6 +602,48 @@ int df11_gated_matmul(const df11_device_stream *gate, const df11_device_stream *
                       uint64_t x_stride, uint32_t n_tokens, uint32_t in_features, uint32_t out_features,
                       const df11_epilogue *e, void *workspace, uint64_t workspace_bytes, void *hip_stream);
 
+/* What a product's backward pass reads and writes (host struct of device
+ * pointers).  With z the sums after the bias that the forward call kept in
+ * df11_epilogue.pre, dy the gradient of its output:
+ *   one weight   dz = dy * act'(z);  dx = dz W
+ *   gated        dz0 = dy * z1 * act'(z0), dz1 = dy * act(z0);
+ *                dx = dz0 Wg + dz1 Wu
+ *   dbias[i] = sum over the tokens of dz_i
+ * (the residual's gradient is dy itself; the weights are frozen.)
+ *   dy           device, n_tokens x out_features of dy_dtype, dy_stride
+ *                elements from row to row
+ *   pre          16-byte aligned; unused (may be NULL) for one weight without
+ *                an activation
+ *   dx           device, n_tokens x in_features of dx_dtype, or NULL
+ *   dbias        device, out_features of bias_dtype each, or NULL
+ * Types are DF11_BF16 or DF11_FP32.  dz is rounded to BF16 for dx, the matrix
+ * cores' operand type, and stays float for dbias. */
+typedef struct df11_product_grad {
+    const void *dy;
+    const float *pre[2];
+    void *dx;
+    void *dbias[2];
+    uint64_t dy_stride;
+    uint64_t dx_stride;
+    uint32_t dy_dtype;
+    uint32_t dx_dtype;
+    uint32_t bias_dtype;
+    uint32_t activation;
+} df11_product_grad;
+
+/* Bytes of df11_matmul_epilogue_grad's workspace on the current device; 0 for
+ * streams that the call refuses, or where nothing needs computing. */
+uint64_t df11_epilogue_grad_workspace(const df11_device_stream *w, const df11_device_stream *up, uint32_t n_tokens,
+                                      const df11_product_grad *g);
+
+/* The backward pass of df11_matmul_epilogue (up NULL) or df11_gated_matmul,
+ * through the frozen compressed weights: the streams are decoded into the
+ * workspace.  Sizes, streams, workspace, sums and errors as for the forward
+ * calls; no output may overlap anything else.  With no tokens dbias is zero. */
+int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_stream *up, uint32_t n_tokens,
+                              uint32_t in_features, uint32_t out_features, const df11_product_grad *g,
+                              void *workspace, uint64_t workspace_bytes, void *hip_stream);
+
 /* ---------------------------------------------------------------------------
  * rANS exponent coder.  The discussion on the page ("Opini Hacker News")
  * names rANS as an entropy coder that suits SIMD-style instruction sets better

@@ -114,6 +114,11 @@ SHAPES = [(64, 32, "normal"), (192, 96, "normal"), (4096, 32, "normal"), (1024, 
 TOKENS = [1, 2, 8, 9, 16, 17, 33, 64, 65, 130, 300]
 
 
+def _slope64(torch, name, z):
+    z = z.detach().clone().requires_grad_()
+    return torch.autograd.grad(_act64(torch, name, z).sum(), z)[0]
+
+
 @pytest.mark.parametrize("rows,cols,kind", SHAPES)
 @pytest.mark.parametrize("tokens", TOKENS)
 def test_product(torch_cuda, rows, cols, kind, tokens):
@@ -284,3 +289,148 @@ def test_one_step_panels(torch_cuda):
         x = _x(torch, tokens, 32)
         z, dz = _linear64(x, w64, None)
         _assert_close(w.matmul(x), z, dz)
+
+
+# Gradients.  dz = dy act'(z) (times the other factor of a gated product) is
+# off by the error of z times the slope's own slope (at most 1 here, 1.13 for
+# the gated factor act), by 16 u of its value for computing it, and, for dx
+# alone, by 2^-9 of its value for its rounding to BF16 (2^-8 / 2 is half a
+# step: h = 2^-8 relative to the value at most); dx adds R (2 R gated) products
+# in float32 and is rounded once.
+@pytest.mark.parametrize("rows,cols,kind", [(64, 32, "normal"), (192, 96, "normal"), (128, 4096, "normal"),
+                                            (64, 1024, "stress"), (640, 1056, "normal"), (2048, 320, "normal")])
+@pytest.mark.parametrize("tokens", [1, 17, 64, 129, 300])
+def test_product_gradients(torch_cuda, rows, cols, kind, tokens):
+    torch = torch_cuda
+    _note(f"gradient {tokens} x {cols} -> {rows} {kind}")
+    w, w64 = _weight(rows, cols, kind)
+    u, u64 = _weight(rows, cols, kind, 1)
+    x = _x(torch, tokens, cols, seed=tokens)
+    for gated in (False, True):
+        for act, bdt, odt in (("none", None, torch.bfloat16), ("none", torch.bfloat16, torch.float32),
+                              ("gelu", torch.bfloat16, torch.bfloat16), ("silu", torch.float32, torch.float32),
+                              ("gelu_tanh", None, torch.bfloat16)):
+            ws = (w64, u64) if gated else (w64,)
+            biases = [None if bdt is None else _side(torch, (rows,), bdt, 3 + i) for i in range(len(ws))]
+            res = _side(torch, (tokens, rows), torch.float32, 5)
+            dy = _side(torch, (tokens, rows), odt, 6)
+            leaves = [t.clone().requires_grad_() for t in (x, res, *biases) if t is not None]
+            bl = leaves[2:] if bdt is not None else [None] * len(ws)
+            if gated:
+                y = df11.gated_matmul(w, u, leaves[0], gate_bias=bl[0], up_bias=bl[1], activation=act,
+                                      residual=leaves[1], out_dtype=odt)
+            else:
+                y = df11.matmul_epilogue(w, leaves[0], bias=bl[0], activation=act, residual=leaves[1], out_dtype=odt)
+            _assert_close(y, *_expected(torch, x, ws, biases if gated else biases, act, res, odt))
+            grads = torch.autograd.grad(y, leaves, dy)
+            assert torch.equal(grads[1], dy.float())
+            zs = [_linear64(x, m, b) for m, b in zip(ws, biases)]
+            z, dz = zs[0]
+            d64 = dy.double()
+            s64, a64 = _slope64(torch, act, z), _act64(torch, act, z)
+            curve = 0.0 if act == "none" else 1.0
+            if gated:
+                z1, dz1 = zs[1]
+                ds = [d64 * z1 * s64, d64 * a64]
+                err = [d64.abs() * (dz1 * (s64.abs() + curve * dz) + z1.abs() * curve * dz) + 16 * U * (
+                    d64 * z1).abs() * (s64.abs() + z.abs() + 1), d64.abs() * SLOPE * dz + 16 * U * ds[1].abs()]
+            else:
+                ds = [d64 * s64]
+                err = [d64.abs() * curve * dz + 16 * U * d64.abs() * (s64.abs() + z.abs() + 1)]
+            dx64 = sum(d @ m for d, m in zip(ds, ws))
+            size = sum(d.abs() @ m.abs() for d, m in zip(ds, ws))
+            bound = sum((e + 2.0 ** -8 * (d.abs() + e)) @ m.abs() for d, e, m in zip(ds, err, ws))
+            bound = bound + 1.01 * len(ws) * rows * U * (size + bound)
+            _assert_close(grads[0], dx64, bound + _half_step(torch, torch.bfloat16, dx64.abs() + bound))
+            for i, b in enumerate(biases):
+                if b is not None:
+                    b64 = ds[i].sum(0)
+                    eb = err[i].sum(0) + 1.01 * (tokens + 8) * U * (ds[i].abs().sum(0) + err[i].sum(0))
+                    assert grads[2 + i].dtype == b.dtype
+                    _assert_close(grads[2 + i], b64, eb + _half_step(torch, b.dtype, b64.abs() + eb))
+
+
+def test_product_gradient_against_differences(torch_cuda):
+    """dx along a direction against a central difference of the formula in float64."""
+    torch = torch_cuda
+    _note("gradient differences")
+    w, w64 = _weight(640, 1056)
+    u, u64 = _weight(640, 1056, "normal", 1)
+    x = _x(torch, 20, 1056, seed=3)
+    b = _side(torch, (640,), torch.float32, 4)
+    dy = _side(torch, (20, 640), torch.float32, 6)
+    for act in ("silu", "gelu", "gelu_tanh", "none"):
+        leaves = [x.clone().requires_grad_(), b.clone().requires_grad_()]
+        y = df11.gated_matmul(w, u, leaves[0], gate_bias=leaves[1], activation=act, out_dtype=torch.float32)
+        grads = torch.autograd.grad(y, leaves, dy)
+        v = _side(torch, (20, 1056), torch.float64, 8)
+        vb = _side(torch, (640,), torch.float64, 9)
+
+        def value(e):
+            x64 = x.double() + e * v
+            return (_act64(torch, act, x64 @ w64.t() + b.double() + e * vb) * (x64 @ u64.t()) * dy.double()).sum()
+
+        diff = (value(1e-5) - value(-1e-5)) / 2e-5
+        got = (grads[0].double() * v).sum() + (grads[1].double() * vb).sum()
+        # dz and dx are rounded to BF16 (2^-8 each, at most): twice that of the sum of sizes, over the
+        # root of the 20 * 1056 independent roundings, five times over
+        size = (grads[0].double().abs() * v.abs()).sum()
+        assert abs(float(diff - got)) <= 5 * 2 * 2.0 ** -8 * float(size) / (20 * 1056) ** 0.5 + 1e-6 * float(size)
+
+
+def test_product_gradient_parts(torch_cuda):
+    """Only what is asked for, expanded and strided gradients, no tokens."""
+    torch = torch_cuda
+    _note("gradient parts")
+    w, w64 = _weight(640, 1056)
+    x = _x(torch, 40, 1056, seed=3)
+    b = _side(torch, (640,), torch.bfloat16, 4).requires_grad_()
+    df11.matmul_epilogue(w, x, bias=b, activation="relu", out_dtype=torch.float32).sum().backward()
+    want = (x.double() @ w64.t() + b.detach().double() > 0).double().sum(0)
+    assert bool(((b.grad.double() - want).abs() <= want * 2.0 ** -8 + 1).all())
+    xg = x.clone().requires_grad_()
+    y = df11.matmul_epilogue(w, xg)
+    wide = _side(torch, (40, 1280), torch.bfloat16, 6)
+    for dy in (wide[:, 320:960], wide[:, 3:643], wide[:1, :640].expand(40, 640), wide[:, ::2]):
+        g, = torch.autograd.grad(y, xg, dy, retain_graph=True)
+        g2, = torch.autograd.grad(y, xg, dy.contiguous(), retain_graph=True)
+        assert torch.equal(g, g2)
+    b0 = b.detach().clone().requires_grad_()
+    x0 = x[:0].clone().requires_grad_()
+    df11.matmul_epilogue(w, x0, bias=b0, activation="silu").sum().backward()
+    assert bool((b0.grad == 0).all()) and x0.grad.shape == (0, 1056)
+
+
+def test_training_step_replays(torch_cuda):
+    """Norm, gated product and down product, forward and backward, captured
+    and replayed on new inputs with eager steps between."""
+    torch = torch_cuda
+    _note("training graph")
+    w, _ = _weight(4096, 4096)
+    u, _ = _weight(4096, 4096, "normal", 1)
+    nw = torch.ones(4096, device="cuda", dtype=torch.bfloat16)
+    x = _x(torch, 100, 4096)
+    dy = _x(torch, 100, 4096, seed=50)
+
+    def step():
+        a, n = x.detach().requires_grad_(), nw.detach().requires_grad_()
+        h = df11.gated_matmul(w, u, df11.rms_norm(a, weight=n))
+        y = df11.matmul_epilogue(u, h, residual=a)
+        return (y.detach(),) + torch.autograd.grad(y, (a, n), dy)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in (1, 2, 3):
+        x.copy_(_x(torch, 100, 4096, seed=seed))
+        dy.copy_(_x(torch, 100, 4096, seed=seed + 60))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))

@@ -185,3 +185,42 @@ def test_product_binding_refuses():
             df11.gated_matmul(w, u, x)
     with pytest.raises(ValueError):
         df11.gated_matmul(w, w, x, gate_bias=torch.zeros(128), up_bias=torch.zeros(128, dtype=bf))
+
+
+def _product_grad(gated=False, **k):
+    import ctypes
+    lib = _lib_or_skip()
+    a = dict(w=_stream(), u=_stream(at=0x300000000) if gated else None, t=4, inf=64, outf=128, ws=G, wb=0, dy=A, dys=128,
+             dyt=0, pre=(C, D if gated else None), dx=B, dxs=64, dxt=0, db=(None, None), bt=0, act=2, g=True)
+    a.update(k)
+    g = _lib.ProductGrad()
+    g.dy, g.dy_stride, g.dy_dtype, g.activation = a["dy"], a["dys"], a["dyt"], a["act"]
+    g.dx, g.dx_stride, g.dx_dtype, g.bias_dtype = a["dx"], a["dxs"], a["dxt"], a["bt"]
+    for i in range(2):
+        g.pre[i], g.dbias[i] = a["pre"][i], a["db"][i]
+    ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
+    return lib.df11_matmul_epilogue_grad(ref(a["w"]), ref(a["u"]), a["t"], a["inf"], a["outf"],
+                                         ctypes.byref(g) if a["g"] else None, a["ws"], a["wb"], None)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("bad", [
+    dict(w=None), dict(inf=32), dict(g=False), dict(act=7), dict(dyt=1), dict(dxt=1), dict(db=(E, None), bt=1),
+    dict(dy=None), dict(dy=A + 1), dict(dyt=2, dy=A + 2), dict(dys=(1 << 31) + 1), dict(pre=(None, None)),
+    dict(pre=(C + 4, D)), dict(dx=B + 1), dict(dxs=63), dict(dxs=(1 << 31) + 1), dict(db=(E + 1, None)),
+    dict(dx=A), dict(dx=C + 16), dict(dx=0x202000000), dict(db=(A, None)), dict(db=(B, None)), dict(ws=G + 8),
+])
+def test_product_grad_refuses(gated, bad):
+    if not gated and bad.get("pre") == (C + 4, D):
+        bad = dict(pre=(C + 4, None))
+    assert _product_grad(gated, **bad) == INVALID
+
+
+def test_product_grad_refuses_second_parts():
+    assert _product_grad(db=(None, E)) == INVALID
+    assert _product_grad(pre=(C, D)) == INVALID
+    assert _product_grad(True, u=_stream(rows=64, at=0x300000000)) == INVALID
+    assert _product_grad(True, db=(E, E)) == INVALID
+    assert _product_grad(t=1 << 26) == TOO_LARGE
+    assert _product_grad(dx=None) == 0  # nothing asked for, nothing launched
+    assert _product_grad(t=0, dy=None, dx=None, pre=(None, None)) == 0
