@@ -230,6 +230,10 @@ uint64_t rows_span(uint32_t rows, uint32_t cols, uint64_t stride, uint32_t bytes
 }
 
 constexpr uint64_t kMaxStride = 1ull << 31;
+// Longest row of x, of W and of an operand of the dense product, and largest
+// stride between them: 256 of them then lie within a buffer resource's 32
+// bits of offset.
+constexpr uint64_t kMaxRow = 1ull << 22;
 
 // Checks of the streams and the sizes that every entry point shares.
 int check_streams(const df11_device_stream *const *ws, uint32_t n, uint32_t n_tokens, uint32_t in_features,
@@ -244,7 +248,8 @@ int check_streams(const df11_device_stream *const *ws, uint32_t n, uint32_t n_to
             return DF11_E_INVALID_ARG;
     }
     if (n == 2 && out_features && !df11::same_table_bits(ws[0], ws[1])) return DF11_E_INVALID_ARG;
-    if (static_cast<uint64_t>(n_tokens) * std::max(in_features, out_features) >= (1ull << 32)) return DF11_E_TOO_LARGE;
+    if (in_features > kMaxRow || static_cast<uint64_t>(n_tokens) * std::max(in_features, out_features) >= (1ull << 32))
+        return DF11_E_TOO_LARGE;
     return DF11_OK;
 }
 
@@ -262,7 +267,7 @@ int check_call(Call &c, const df11_epilogue *e, void *workspace, bool &empty) {
     if (c.n == 2 && !e->pre[0] != !e->pre[1]) return DF11_E_INVALID_ARG;
     empty = c.n_tokens == 0 || c.out_features == 0;
     if (empty) return DF11_OK;
-    if (!c.x || !aligned(c.x, 16) || c.x_stride % 8 || c.x_stride > kMaxStride || !e->out ||
+    if (!c.x || !aligned(c.x, 16) || c.x_stride % 8 || c.x_stride > kMaxRow || !e->out ||
         !aligned(e->out, out_bytes) || e->out_stride > kMaxStride ||
         (c.n_tokens > 1 && e->out_stride < c.out_features))
         return DF11_E_INVALID_ARG;
@@ -415,7 +420,7 @@ struct GradPlan {
 bool grad_plan(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols,
                const df11_product_grad &g, GradPlan &p) {
     p.own_dz = n == 2 || g.activation != DF11_ACT_NONE || g.dy_dtype != DF11_BF16 || !aligned(g.dy, 16) ||
-               g.dy_stride % 8;
+               g.dy_stride % 8 || g.dy_stride > kMaxRow;
     const uint32_t chunk = slope_chunk(tokens);
     p.chunks = (tokens + chunk - 1) / chunk;
     uint64_t at = 0;
@@ -448,6 +453,7 @@ int backward(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens, u
     if (!dy_bytes || (g->dx && !dx_bytes) || ((g->dbias[0] || g->dbias[1]) && !bias_bytes)) return DF11_E_INVALID_ARG;
     if (n == 1 && (g->dbias[1] || g->pre[1])) return DF11_E_INVALID_ARG;
     if (rows == 0) return DF11_OK;
+    if (rows > kMaxRow) return DF11_E_TOO_LARGE;
     const bool needs_pre = n == 2 || g->activation != DF11_ACT_NONE;
     if (tokens) {
         if (!g->dy || !aligned(g->dy, dy_bytes) || g->dy_stride > kMaxStride) return DF11_E_INVALID_ARG;

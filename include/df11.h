@@ -578,7 +578,8 @@ uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_
  *   w             device stream in MFMA tile order, as for df11_matmul
  *   x             device, n_tokens x in_features BF16, 16-byte aligned, x_stride
  *                 elements (a multiple of 8) from row to row
- *   in_features   a multiple of 32;  out_features a multiple of 64
+ *   in_features   a multiple of 32, with x_stride at most 2^22;  out_features a
+ *                 multiple of 64
  *   workspace     device, 256-byte aligned, df11_epilogue_workspace bytes; holds
  *                 nothing between calls, but calls that overlap in time need
  *                 one each
@@ -639,7 +640,8 @@ uint64_t df11_epilogue_grad_workspace(const df11_device_stream *w, const df11_de
 /* The backward pass of df11_matmul_epilogue (up NULL) or df11_gated_matmul,
  * through the frozen compressed weights: the streams are decoded into the
  * workspace.  Sizes, streams, workspace, sums and errors as for the forward
- * calls; no output may overlap anything else.  With no tokens dbias is zero. */
+ * calls, and out_features at most 2^22; no output may overlap anything else.
+ * With no tokens dbias is zero. */
 int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_stream *up, uint32_t n_tokens,
                               uint32_t in_features, uint32_t out_features, const df11_product_grad *g,
                               void *workspace, uint64_t workspace_bytes, void *hip_stream);

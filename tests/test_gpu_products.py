@@ -321,7 +321,7 @@ def test_product_gradients(torch_cuda, rows, cols, kind, tokens):
                                       residual=leaves[1], out_dtype=odt)
             else:
                 y = df11.matmul_epilogue(w, leaves[0], bias=bl[0], activation=act, residual=leaves[1], out_dtype=odt)
-            _assert_close(y, *_expected(torch, x, ws, biases if gated else biases, act, res, odt))
+            _assert_close(y.detach(), *_expected(torch, x, ws, biases, act, res, odt))
             grads = torch.autograd.grad(y, leaves, dy)
             assert torch.equal(grads[1], dy.float())
             zs = [_linear64(x, m, b) for m, b in zip(ws, biases)]
@@ -348,6 +348,38 @@ def test_product_gradients(torch_cuda, rows, cols, kind, tokens):
                     eb = err[i].sum(0) + 1.01 * (tokens + 8) * U * (ds[i].abs().sum(0) + err[i].sum(0))
                     assert grads[2 + i].dtype == b.dtype
                     _assert_close(grads[2 + i], b64, eb + _half_step(torch, b.dtype, b64.abs() + eb))
+
+
+# Whole rounds of large tiles with a rest of small ones, large tiles alone,
+# small ones alone, splits along K of either; odd k-steps; outputs that end
+# inside a tile.
+@pytest.mark.parametrize("tokens,rows,cols", [(2000, 10304, 416), (1030, 6208, 2080), (2300, 4096, 320),
+                                              (4100, 192, 4096), (1500, 4096, 4096), (70, 4096, 4096)])
+def test_dense_plans(torch_cuda, tokens, rows, cols):
+    torch = torch_cuda
+    _note(f"dense {tokens} x {cols} -> {rows}")
+    w, w64 = _weight(rows, cols)
+    u, u64 = _weight(rows, cols, "normal", 1)
+    x = _x(torch, tokens, cols, seed=7)
+    res = _side(torch, (tokens, rows), torch.bfloat16, 5)
+    y = df11.matmul_epilogue(w, x, activation="gelu", residual=res)
+    _assert_close(y, *_expected(torch, x, (w64,), (None,), "gelu", res, torch.bfloat16))
+    del y
+    xg = x.clone().requires_grad_()
+    h = df11.gated_matmul(w, u, xg, activation="none", out_dtype=torch.float32)
+    want, bound = _expected(torch, x, (w64, u64), (None, None), "none", None, torch.float32)
+    _assert_close(h.detach(), want, bound)
+    del want, bound
+    dy = _side(torch, (tokens, rows), torch.float32, 6)
+    dx, = torch.autograd.grad(h, xg, dy)
+    del h
+    (z0, e0), (z1, e1) = _linear64(x, w64, None), _linear64(x, u64, None)
+    d = dy.double()
+    dx64 = (d * z1) @ w64 + (d * z0) @ u64
+    size = (d * z1).abs() @ w64.abs() + (d * z0).abs() @ u64.abs()
+    slack = (d.abs() * e1) @ w64.abs() + (d.abs() * e0) @ u64.abs()
+    bound = slack + (2.0 ** -8 + 16 * U + 1.01 * 2 * rows * U) * (size + slack)
+    _assert_close(dx, dx64, bound + _half_step(torch, torch.bfloat16, dx64.abs() + bound))
 
 
 def test_product_gradient_against_differences(torch_cuda):

@@ -119,7 +119,7 @@ def _product(gated=False, **k):
 @pytest.mark.parametrize("bad", [
     dict(w=None), dict(inf=32), dict(outf=64), dict(inf=60), dict(outf=100), dict(e=False), dict(act=5),
     dict(ot=1), dict(ot=3), dict(res=C, rt=1), dict(bias=(C, None), bt=1), dict(bias=(C, None), bt=9),
-    dict(x=None), dict(x=A + 8), dict(xs=68), dict(xs=(1 << 31) + 8), dict(out=None), dict(out=B + 1),
+    dict(x=None), dict(x=A + 8), dict(xs=68), dict(xs=(1 << 22) + 8), dict(out=None), dict(out=B + 1),
     dict(ot=2, out=B + 2), dict(os=127), dict(os=(1 << 31) + 1), dict(res=C + 1), dict(rt=2, res=C + 2),
     dict(rs=(1 << 31) + 1, res=C), dict(bias=(C + 1, None)), dict(pre=(C + 2, D)), dict(out=A), dict(out=A + 128),
     dict(res=B + 2), dict(res=B, rs=256), dict(res=B, rt=2), dict(bias=(B, None)), dict(pre=(B, D)), dict(pre=(A, D)),
