@@ -32,7 +32,7 @@ MAX_ELEMENTS = (1 << 32) - (1 << 16)  # DF11_MAX_ELEMENTS
 LINEAR_MAX_TOKENS = 8  # DF11_LINEAR_MAX_TOKENS
 LINEAR_MIN_IN_FEATURES = 512  # DF11_LINEAR_MIN_IN_FEATURES
 BF16, FP16, FP32 = 0, 1, 2  # DF11_BF16, DF11_FP16, DF11_FP32
-ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # DF11_ACT_*
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # DF11_ACT_*
 RANS_PROB_BITS = 12  # DF11_RANS_PROB_BITS
 RANS_LANES = 64  # DF11_RANS_LANES
 RANS_STEPS = 512  # DF11_RANS_STEPS

@@ -88,14 +88,12 @@ struct DecodeArgs {
     uint32_t *sched;         // work counters (dynamic schedule) or null
     uint32_t pools;          // dynamic schedule: counters in use, dividing the workgroup count
     uint32_t tile_ks;        // C / 32: k-steps per 64-row panel of a tiled matrix
-    uint64_t tile_magic;     // floor(2^64 / tile_ks) + 1, or 0 for tile_ks = 1 (panel_of_step)
+    uint64_t tile_magic;     // floor(2^42 / tile_ks) + 1 (df11::panel_of_step)
 };
 
-// Panel of global k-step g of a tiled matrix, g / tile_ks: umulhi64(g,
-// tile_magic) for all g < 2^32, but a magic number of 2^64 (one k-step per
-// panel) does not fit its word.
+// Panel of global k-step g of a tiled matrix.
 __device__ __forceinline__ uint32_t panel_of_step(const DecodeArgs &a, uint32_t g) {
-    return a.tile_magic ? static_cast<uint32_t>(__umul64hi(g, a.tile_magic)) : g;
+    return df11::panel_of_step(g, a.tile_magic);
 }
 
 // MFMA tile order (df11_tile_order): 512-element blocks, each the operand
@@ -125,10 +123,7 @@ struct MatmulArgs {
     uint32_t fixed_len;    // matrix-core product with a dealt tail: super-groups of each fixed range
     // Matrix-core product into slots (flush_slot); y is the stream's first slot.
     uint32_t x_stride;     // elements from one row of x to the next, a multiple of 8
-    uint32_t wg_panels;    // slots of one group slot of a workgroup's fixed range
-    uint32_t group_panels; // slots of one group of the dealt tail
-    uint32_t tail_group0;  // first group of the dealt tail
-    uint64_t tail_slots;   // floats before the dealt tail's first slot
+    uint32_t wg_panels;    // slots of one group slot of a workgroup's range
 };
 
 __device__ __forceinline__ uint32_t bswap32(uint32_t x) { return __builtin_amdgcn_perm(x, x, 0x00010203u); }
@@ -444,7 +439,7 @@ __device__ __forceinline__ void merge_group_pairs(const DecodeArgs &a, uint8_t *
     auto pair_round = [&](uint32_t p, uint64_t s0, uint64_t s1) {
         const uint32_t cb = df11::pair_chunk(c0, p, 0, ltid - lane);  // the wave's lane 0, half 0
         const uint32_t g = cb >> 8;                                    // global k-step of half 0 (even)
-        const uint32_t panel = static_cast<uint32_t>(__umul64hi(g, a.tile_magic));
+        const uint32_t panel = panel_of_step(a, g);
         const uint32_t wave_dst = df11::pair_wave_dst(panel, g - panel * a.tile_ks, a.tile_cols, wave);
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
@@ -762,20 +757,19 @@ struct PanelSums {
     floatx4 d[MT];   // lane l, entry r: token 16 mt + 4 (l / 16) + r, row 16 wave + (l mod 16)
     uint32_t panel;  // 64-row panel of the sums (wave-uniform), ~0 when empty
     uint32_t pass;   // pass of the sums (wave-uniform)
-    // Into slots (all wave-uniform): the region's first slot, panel and slot
-    // count, the panel after its last one, and its group (~0: a fixed range).
+    // Into slots (all wave-uniform): the range's first slot for this group
+    // slot, its first panel, its slots, and the panel after its last one.
     float *region;
-    uint32_t first, panels, panel_end, group;
+    uint32_t first, panels, panel_end;
 };
 
 // The slots' form of the product: in place of float atomics, whose order
-// changes the sums' last bits, every region of the stream (a workgroup's
-// fixed range, once for each of its group slots, or one group of the dealt
-// tail) has one slot of n_tokens x 64 floats for each panel it touches, and
+// changes the sums' last bits, each group slot of a workgroup has one slot of
+// n_tokens x 64 floats for each panel that the workgroup's range touches, and
 // writes each of them exactly once: the sums of the panels it holds, zeros
 // for a panel that only the range's other group slot reached.  A second
 // kernel adds a panel's slots in the order of the stream.  Writes the sums to
-// their slot and zeros up to panel `upto`; slot numbers past the region's
+// their slot and zeros up to panel `upto`; slot numbers past the range's
 // (a corrupt stream) are dropped.
 template <int MT>
 __device__ __forceinline__ void flush_slot(const MatmulArgs &m, PanelSums<MT> &ps, uint32_t upto, uint32_t wave,
@@ -866,11 +860,10 @@ __device__ __forceinline__ void stage_x(const DecodeArgs &a, const MatmulArgs &m
     }
 }
 
-template <int MT, bool kSlots, bool kTail>
+template <int MT, bool kSlots>
 __device__ __forceinline__ void merge_mfma(const DecodeArgs &a, const MatmulArgs &m, uint8_t *ebuf,
                                            const uint64_t (&sm)[kPrefetchChunks], uint32_t base, uint32_t end,
-                                           uint32_t pass, uint32_t group, uint32_t ltid, PanelSums<MT> &ps,
-                                           const uint8_t *s_x) {
+                                           uint32_t pass, uint32_t ltid, PanelSums<MT> &ps, const uint8_t *s_x) {
     const uint32_t c0 = base >> 3;
     const uint32_t n_chunks = min(group_chunks(base, end), a.ebuf_cap / 8u);
     const uint32_t lead = c0 & 255u;
@@ -885,16 +878,6 @@ __device__ __forceinline__ void merge_mfma(const DecodeArgs &a, const MatmulArgs
     if (ltid == 0 && 8u * (n_chunks + 1u) <= a.ebuf_cap) *reinterpret_cast<uint64_t *>(ebuf + 8u * n_chunks) = 0;
     if (n_chunks == 0) return;
     const uint32_t g0 = c0 >> 8;
-    if constexpr (kSlots && kTail) {
-        if (group >= m.tail_group0 && group < a.n_groups) {  // a region of its own
-            flush_slot<MT>(m, ps, ps.group == ~0u ? ps.panel_end : ps.panel + 1u, wave, lane);
-            ps.group = group;
-            ps.region = m.y + m.tail_slots +
-                        static_cast<size_t>(group - m.tail_group0) * m.group_panels * m.n_tokens * 64u;
-            ps.first = ps.panel = panel_of_step(a, g0);
-            ps.panels = m.group_panels;
-        }
-    }
     auto round = [&](uint32_t j, const uint4 (&xa)[MT], uint64_t s8) {
         const uint32_t kk = ltid + 256u * j;
         const uint32_t k = kk - lead;
@@ -1233,17 +1216,17 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
         ps.panel = ~0u;
         ps.pass = 0;
     }
-    uint32_t prev_pass = 0, prev_group = 0;
+    uint32_t prev_pass = 0;
+    static_assert(!(kSlots && kTail), "a range's slots belong to one workgroup");
     if constexpr (kSlots) {
-        // The fixed range's panels, from its first and last element (as the
-        // kernel that adds the slots finds them: df11::range_panels).
+        // The range's panels, from its first and last element (as the kernel
+        // that adds the slots finds them).
         const uint32_t last = a.n_elements - 1u;
         const uint32_t e0 = min(out_pos_at(a, r0 * GPW), last);
         const uint32_t e1 = min(max(out_pos_at(a, min((r0 + len) * GPW, a.n_groups)), 1u) - 1u, last);
         ps.first = ps.panel = panel_of_step(a, e0 >> 11);
         ps.panel_end = panel_of_step(a, e1 >> 11) + 1u;
         ps.panels = m.wg_panels;
-        ps.group = ~0u;
         ps.region = m.y + static_cast<size_t>(wg * GPW + slot) * m.wg_panels * m.n_tokens * 64u;
     }
 
@@ -1342,8 +1325,7 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
                                  y_row0, y_rows);
         } else if constexpr (kMfma) {
             if (it > 0)
-                merge_mfma<MT, kSlots, kTail>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, prev_group, ltid, ps,
-                                              s_x);
+                merge_mfma<MT, kSlots>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, ltid, ps, s_x);
         }
         const GroupLoad nx = load_group(a, g_nx, ltid);
         uint32_t fetched = 0;
@@ -1496,7 +1478,6 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
         prev_base = base;
         prev_end = end;
         if constexpr (kMfma) prev_pass = kTail ? 0u : s_cur / len;
-        if constexpr (kSlots && kTail) prev_group = g;
         cur = nx;
         cur_base = nx_base;
         cur_end = nx_end;
@@ -1507,9 +1488,9 @@ __device__ __forceinline__ void decode_stream(const DecodeArgs &a, const MatmulA
     } else if constexpr (TB == 0) {
         merge_group(a, s_ebuf, sm, prev_base, prev_end, ltid, s_edge[0] != 0, s_edge[1] != 0);
     } else if constexpr (kMfma) {
-        merge_mfma<MT, kSlots, kTail>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, prev_group, ltid, ps, s_x);
+        merge_mfma<MT, kSlots>(a, m, s_ebuf, sm, prev_base, prev_end, prev_pass, ltid, ps, s_x);
         if constexpr (kSlots) {
-            flush_slot<MT>(m, ps, ps.group == ~0u ? ps.panel_end : ps.panel + 1u, wave, lane);
+            flush_slot<MT>(m, ps, ps.panel_end, wave, lane);
         } else {
             flush_panel<MT>(m, ps, wave, lane);
         }
@@ -1643,18 +1624,18 @@ struct PartialArgs {
     uint32_t stride;  // coprime to the grid size
 };
 
-template <int K, int MT, bool kTail>
+template <int K, int MT>
 __global__ __launch_bounds__(kThreadsPerGroup *kGemmGPW) __attribute__((amdgpu_waves_per_eu(kGemmWaves<MT>)))
 void df11_partial_kernel(DecodeArgs a, MatmulArgs m) {
-    decode_stream<K, kGemmGPW, -MT, kTail, false, true>(a, m, blockIdx.x, gridDim.x);
+    decode_stream<K, kGemmGPW, -MT, false, false, true>(a, m, blockIdx.x, gridDim.x);
 }
 
-template <int K, int MT, bool kTail>
+template <int K, int MT>
 __global__ __launch_bounds__(kThreadsPerGroup *kGemmGPW) __attribute__((amdgpu_waves_per_eu(kGemmWaves<MT>)))
 void df11_partial_pair_kernel(PartialArgs b) {
     const uint32_t id = static_cast<uint32_t>((static_cast<uint64_t>(blockIdx.x) * b.stride) % gridDim.x);
     const uint32_t i = id >= b.wg_begin[1];
-    decode_stream<K, kGemmGPW, -MT, kTail, false, true>(b.s[i], b.m[i], id - b.wg_begin[i],
+    decode_stream<K, kGemmGPW, -MT, false, false, true>(b.s[i], b.m[i], id - b.wg_begin[i],
                                                         b.wg_begin[i + 1] - b.wg_begin[i]);
 }
 
@@ -1878,7 +1859,7 @@ void fill_args(const df11_device_stream *s, DecodeArgs &a) {
     a.tile_cols = s->tile_cols;
     if (s->tile_cols) {
         a.tile_ks = s->tile_cols / 32u;
-        a.tile_magic = ~0ull / a.tile_ks + 1ull;  // (0 for tile_ks = 1)
+        a.tile_magic = (1ull << 42) / a.tile_ks + 1ull;
     }
 }
 
@@ -2456,85 +2437,66 @@ int gemm_batch_impl(const df11_device_stream *ws, uint32_t n, const uint16_t *co
 
 // Products into slots (df11_partials.h): one launch for one matrix, or two
 // that multiply the same x.  Fills p for the kernel that adds the slots;
-// with no workspace that is all (a query of p.slot_bytes).
+// with no slots that is all (a query of p.slot_bytes).
+//
+// Fixed ranges alone: the dealt tail of launch_gemm gains nothing here (gate
+// and up of 14336 x 4096 at one token 83.0 against 84.7 us, at eight tokens
+// 91.3 against 86.6; 28672 x 4096 alone 81.9 against 80.4), and without it a
+// call uses no work counters.
 template <int K, int MT>
-int launch_partials(PartialArgs &b, uint32_t n, uint32_t max_wg, df11::Partials &p, float *slots,
+int launch_partials(PartialArgs &b, uint32_t n, uint32_t max_wg, df11::Partials &p, float *slots, uint64_t capacity,
                     hipStream_t stream) {
     size_t lds = 0;
     for (uint32_t i = 0; i < n; ++i) lds = std::max(lds, dynamic_lds<K, kGemmGPW>(b.s[i], kGemmXBytes<MT>));
     int dev = 0, cus = 0;
     if (device_cus(dev, cus)) return DF11_E_HIP;
-    const auto pick = [n](bool tail) {
-        constexpr bool kCan = MT == 1;
-        if (n == 1)
-            return tail ? reinterpret_cast<const void *>(&df11_partial_kernel<K, MT, kCan>)
-                        : reinterpret_cast<const void *>(&df11_partial_kernel<K, MT, false>);
-        return tail ? reinterpret_cast<const void *>(&df11_partial_pair_kernel<K, MT, kCan>)
-                    : reinterpret_cast<const void *>(&df11_partial_pair_kernel<K, MT, false>);
-    };
-    // (the persistent grid must fit whichever instance launches)
-    int per_cu = resident_per_cu(pick(false), kThreadsPerGroup * kGemmGPW, dev, lds);
-    if (MT == 1) per_cu = std::min(per_cu, resident_per_cu(pick(true), kThreadsPerGroup * kGemmGPW, dev, lds));
+    const void *fn = n == 1 ? reinterpret_cast<const void *>(&df11_partial_kernel<K, MT>)
+                            : reinterpret_cast<const void *>(&df11_partial_pair_kernel<K, MT>);
+    const int per_cu = resident_per_cu(fn, kThreadsPerGroup * kGemmGPW, dev, lds);
     if (per_cu < 1) return DF11_E_HIP;
     uint64_t resident = static_cast<uint64_t>(per_cu) * static_cast<uint64_t>(cus);
     if (max_wg) resident = std::min<uint64_t>(resident, std::max<uint32_t>(max_wg, n));
     uint64_t sup[2], want[2];
     for (uint32_t i = 0; i < n; ++i) sup[i] = (b.s[i].n_groups + kGemmGPW - 1) / kGemmGPW;
-    df11::split_grid(sup, n, resident, want);
-    // The dealt tail when every stream qualifies (as in launch_gemm_batch).
-    bool tail = MT == 1;
-    uint32_t share[2] = {};
-    for (uint32_t i = 0; i < n; ++i) {
-        DecodeArgs s = b.s[i];
-        share[i] = tail ? tail_schedule(s, b.m[i], sup[i], want[i]) : 0u;
-        tail = tail && share[i] != 0;
-        if (share[i]) b.s[i].pools = s.pools;
+    if (n == 1) {  // (what split_grid gives one stream, one workgroup at a time)
+        want[0] = std::max<uint64_t>(1, std::min(resident, sup[0]));
+    } else {
+        df11::split_grid(sup, n, resident, want);
     }
     uint32_t next = 0;
     uint64_t floats = 0;
     for (uint32_t i = 0; i < n; ++i) {
         DecodeArgs &a = b.s[i];
         MatmulArgs &m = b.m[i];
-        const uint32_t n_wg = tail ? share[i] : static_cast<uint32_t>(want[i]);
-        if (!tail) {
-            a.sched = nullptr;
-            m.fixed_len = 0;
-        }
+        a.sched = nullptr;
         m.passes = 1;
         b.wg_begin[i] = next;
-        next += n_wg;
+        next += static_cast<uint32_t>(want[i]);
         // Panels that a run of e elements touches: at most e / panel + 2.
-        const uint64_t panel = 64ull * a.tile_cols, group = p.max_group[i];
-        const uint64_t longest = tail ? m.fixed_len : (sup[i] + n_wg - 1) / n_wg;
-        m.wg_panels = static_cast<uint32_t>(std::min<uint64_t>(longest * kGemmGPW * group / panel + 2, a.n_elements / panel));
-        m.group_panels = static_cast<uint32_t>(std::min<uint64_t>(group / panel + 2, a.n_elements / panel));
-        m.tail_group0 = tail ? std::min<uint32_t>(n_wg * m.fixed_len * kGemmGPW, a.n_groups) : a.n_groups;
-        const uint64_t slot = 64ull * m.n_tokens;
-        m.tail_slots = static_cast<uint64_t>(n_wg) * kGemmGPW * m.wg_panels * slot;
+        const uint64_t panel = 64ull * a.tile_cols, longest = (sup[i] + want[i] - 1) / want[i];
+        m.wg_panels = static_cast<uint32_t>(
+            std::min<uint64_t>(longest * kGemmGPW * p.max_group[i] / panel + 2, a.n_elements / panel));
         df11::PartialStream &q = p.s[i];
         q.out_pos = a.out_pos;
         q.tile_magic = a.tile_magic;
         q.base = floats;
-        q.tail = floats + m.tail_slots;
         q.n_elements = a.n_elements;
         q.n_groups = a.n_groups;
         q.n_super = static_cast<uint32_t>(sup[i]);
-        q.n_wg = n_wg;
-        q.fixed_len = m.fixed_len;
+        q.n_wg = static_cast<uint32_t>(want[i]);
         q.wg_panels = m.wg_panels;
-        q.group_panels = m.group_panels;
-        q.tail_group0 = m.tail_group0;
         m.y = slots + floats;
-        floats += m.tail_slots + static_cast<uint64_t>(a.n_groups - m.tail_group0) * m.group_panels * slot;
+        floats += want[i] * kGemmGPW * m.wg_panels * 64ull * m.n_tokens;
     }
     b.wg_begin[n] = next;
     p.slot_bytes = 4 * floats;
     if (!slots) return DF11_OK;
+    if (capacity < p.slot_bytes) return DF11_E_BUFFER_TOO_SMALL;
     b.stride = df11::coprime_stride(next);
     (void)hipGetLastError();
     void *one[] = {&b.s[0], &b.m[0]}, *pair[] = {&b};
-    return launch_kernel(pick(tail), dim3(next), dim3(kThreadsPerGroup * kGemmGPW), n == 1 ? one : pair, lds, stream,
-                         nullptr, nullptr);
+    return launch_kernel(fn, dim3(next), dim3(kThreadsPerGroup * kGemmGPW), n == 1 ? one : pair, lds, stream, nullptr,
+                         nullptr);
 }
 
 // The allocation-free batched decode's work counters: one set of
@@ -2585,7 +2547,7 @@ bool same_table_bits(const df11_device_stream *a, const df11_device_stream *b) {
 }
 
 int partial_products(const df11_device_stream *const *ws, uint32_t n, const uint16_t *x, uint64_t x_stride,
-                     uint32_t n_tokens, float *slots, hipStream_t stream, Partials &p) {
+                     uint32_t n_tokens, float *slots, uint64_t capacity, hipStream_t stream, Partials &p) {
     PartialArgs b{};
     uint32_t max_wg = 0;
     for (uint32_t i = 0; i < n; ++i) {
@@ -2600,17 +2562,11 @@ int partial_products(const df11_device_stream *const *ws, uint32_t n, const uint
         const uint32_t cap = ws[i]->max_workgroups;
         if (cap) max_wg = max_wg ? std::min(max_wg, cap) : cap;
     }
-    // (the same tensor twice, say)
-    if (n == 2 && ws[0]->schedule && ws[1]->schedule &&
-        overlaps(ws[0]->schedule, 4 * DF11_SCHEDULE_WORDS, ws[1]->schedule, 4 * DF11_SCHEDULE_WORDS))
-        b.s[1].sched = nullptr;
-#define DF11_PARTIAL_CASE(KB)                                                   \
-    case KB:                                                                    \
-        switch (gemm_tiles(n_tokens)) {                                         \
-        case 1: return launch_partials<KB, 1>(b, n, max_wg, p, slots, stream);  \
-        case 2: return launch_partials<KB, 2>(b, n, max_wg, p, slots, stream);  \
-        default: return launch_partials<KB, 4>(b, n, max_wg, p, slots, stream); \
-        }
+    static_assert(kPartialTokens == 32, "two token tiles of 16");
+#define DF11_PARTIAL_CASE(KB)                                                                      \
+    case KB:                                                                                       \
+        return n_tokens <= 16 ? launch_partials<KB, 1>(b, n, max_wg, p, slots, capacity, stream)   \
+                              : launch_partials<KB, 2>(b, n, max_wg, p, slots, capacity, stream);
     switch (table_bits(ws[0])) {
         DF11_PARTIAL_CASE(10)
         DF11_PARTIAL_CASE(11)

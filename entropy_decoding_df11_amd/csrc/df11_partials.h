@@ -2,16 +2,11 @@
 // kernel that adds the slots needs to find them.
 //
 // A stream's super-groups (kPartialGroups consecutive groups, one per group
-// slot of a workgroup) are split into contiguous ranges, one per workgroup;
-// up to 8 tokens, a long enough stream deals the last few percent of its
-// groups out at run time instead.  Workgroup w's group slot h holds
-// wg_panels slots, one for each 64-row panel from the first to the last that
-// w's range touches, at float
+// slot of a workgroup) are split into contiguous ranges, one per workgroup.
+// Workgroup w's group slot h holds wg_panels slots, one for each 64-row panel
+// from the first to the last that w's range touches, at float
 //     base + ((w * kPartialGroups + h) * wg_panels + panel - first) * 64 n_tokens
-// and group g of the dealt tail group_panels slots likewise at
-//     tail + ((g - tail_group0) * group_panels + panel - first) * 64 n_tokens
-// A slot is n_tokens x 64 floats.  Which workgroup took a dealt group does
-// not show in the slots, so the sums do not depend on the schedule.
+// A slot is n_tokens x 64 floats.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -23,16 +18,24 @@
 namespace df11 {
 
 constexpr uint32_t kPartialGroups = 2;
-// Most tokens of one product into slots (one sweep of the stream).
-constexpr uint32_t kPartialTokens = 64;
+// Most tokens of a product into slots: one sweep with two token tiles.  Four
+// tiles leave the decoder half its waves, and decoding once and multiplying
+// the tiles (df11_dense.h) is faster: 14336 -> 4096 at 33 tokens 79 against
+// 154 us, 4096 -> 4096 36 against 56; at 32 tokens 76 against 63, 36 against 32.
+constexpr uint32_t kPartialTokens = 32;
+
+// g / d for a global k-step g < 2^21 (2^32 elements of 2048 each) and the d =
+// C / 32 k-steps of a panel, d <= 2^21, with magic = floor(2^42 / d) + 1: the
+// quotient's error g / 2^42 stays below 1 / d.
+__host__ __device__ inline uint32_t panel_of_step(uint32_t g, uint64_t magic) {
+    return static_cast<uint32_t>(g * magic >> 42);
+}
 
 struct PartialStream {
     const uint32_t *out_pos;
-    uint64_t tile_magic;  // panel of k-step i: umulhi64(i, tile_magic), or i itself with 0 (C = 32)
-    uint64_t base, tail;  // floats into the slots
-    uint32_t n_elements, n_groups, n_super, n_wg;
-    uint32_t fixed_len;   // 0: ranges over all super-groups; else the length of each, the rest dealt
-    uint32_t wg_panels, group_panels, tail_group0;
+    uint64_t tile_magic;  // floor(2^42 / (C / 32)) + 1 (panel_of_step)
+    uint64_t base;        // floats into the slots
+    uint32_t n_elements, n_groups, n_super, n_wg, wg_panels;
 };
 
 struct Partials {
@@ -46,10 +49,11 @@ bool stream_overlaps(const df11_device_stream *s, const void *p, uint64_t bytes)
 bool same_table_bits(const df11_device_stream *a, const df11_device_stream *b);
 
 // x W_i^T of n (1 or 2) checked, non-empty, tile-ordered streams of the same
-// shape and table width into slots, for at most kPartialTokens tokens.  With
-// slots null nothing is launched and p.slot_bytes says what they take on the
-// current device.
+// shape and table width into slots (capacity bytes; DF11_E_BUFFER_TOO_SMALL
+// if they take more), for at most kPartialTokens tokens.  With slots null
+// nothing is launched and p.slot_bytes says what they take on the current
+// device.
 int partial_products(const df11_device_stream *const *ws, uint32_t n, const uint16_t *x, uint64_t x_stride,
-                     uint32_t n_tokens, float *slots, hipStream_t stream, Partials &p);
+                     uint32_t n_tokens, float *slots, uint64_t capacity, hipStream_t stream, Partials &p);
 
 }  // namespace df11

@@ -22,6 +22,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include <stdint.h>
 
@@ -40,7 +41,6 @@ using df11::Partials;
 using df11::PartialStream;
 
 constexpr uint32_t kPanelRows = 64;  // output features of one panel
-constexpr int kSumTokens = 16;       // tokens of one workgroup of the slots' kernel
 
 struct SumArgs {
     PartialStream s[2];
@@ -51,97 +51,99 @@ struct SumArgs {
 
 // Panel of element e of a tile-ordered stream.
 __device__ __forceinline__ uint32_t panel_of(const PartialStream &s, uint32_t e) {
-    const uint32_t step = min(e, s.n_elements - 1u) >> 11;
-    return s.tile_magic ? static_cast<uint32_t>(__umul64hi(step, s.tile_magic)) : step;
+    return df11::panel_of_step(min(e, s.n_elements - 1u) >> 11, s.tile_magic);
 }
 
 __device__ __forceinline__ uint32_t out_pos_of(const PartialStream &s, uint32_t g) {
     return s.out_pos[min(g, s.n_groups)];
 }
 
-// First super-group of workgroup w's fixed range.
+// First super-group of workgroup w's range: floor(w n_super / n_wg), as
+// w * (n_super / n_wg) + floor(w * (n_super % n_wg) / n_wg) in 32 bits
+// (n_wg is a grid size, far below 2^16).
 __device__ __forceinline__ uint32_t range_begin(const PartialStream &s, uint32_t w) {
-    return s.fixed_len ? w * s.fixed_len
-                       : static_cast<uint32_t>(static_cast<uint64_t>(w) * s.n_super / s.n_wg);
+    return w * (s.n_super / s.n_wg) + w * (s.n_super % s.n_wg) / s.n_wg;
 }
 
-// Panels of the stream's regions that hold slots of panel p: ranges
-// [wg_lo, wg_hi) and dealt groups [g_lo, g_hi), found by all threads at once
-// (a search would wait for one load after the other).  Regions follow the
-// stream, so those of a panel are consecutive.
+// The workgroups [lo, hi) whose ranges touch a panel, and the panels that
+// the first of them holds before it.  Ranges follow the stream, so those of
+// a panel are consecutive, and every one but the first begins with it.
 struct Found {
-    uint32_t wg_lo, wg_hi, g_lo, g_hi;
+    uint32_t lo, hi, skip;
 };
 
-__device__ void find_regions(const PartialStream &s, uint32_t p, Found *f) {
-    if (threadIdx.x == 0) *f = Found{~0u, 0u, ~0u, 0u};
-    __syncthreads();
+// Finds them with all threads at once: a search would wait for one load
+// after the other.
+__device__ __forceinline__ void find_ranges(const PartialStream &s, uint32_t p, Found *f) {
     for (uint32_t w = threadIdx.x; w < s.n_wg; w += blockDim.x) {
         const uint32_t a = panel_of(s, out_pos_of(s, range_begin(s, w) * kPartialGroups));
         const uint32_t b = panel_of(s, max(out_pos_of(s, range_begin(s, w + 1u) * kPartialGroups), 1u) - 1u);
         if (a <= p && p <= b) {
-            atomicMin(&f->wg_lo, w);
-            atomicMax(&f->wg_hi, w + 1u);
+            atomicMin(&f->lo, w);
+            atomicMax(&f->hi, w + 1u);
+            atomicMax(&f->skip, p - a);
         }
     }
-    for (uint32_t g = s.tail_group0 + threadIdx.x; g < s.n_groups; g += blockDim.x) {
-        const uint32_t a = panel_of(s, out_pos_of(s, g)), b = panel_of(s, max(out_pos_of(s, g + 1u), 1u) - 1u);
-        if (a <= p && p <= b) {
-            atomicMin(&f->g_lo, g);
-            atomicMax(&f->g_hi, g + 1u);
-        }
-    }
-    __syncthreads();
 }
 
-// One workgroup adds the slots of one panel for up to kSumTokens tokens: a
-// lane per output feature, the slots split between the four waves, whose
-// sums meet in LDS in wave order.
-template <bool kGated>
+// One workgroup adds the slots of one panel for up to TOKENS tokens: a lane
+// per output feature, the slots split between the four waves, whose sums
+// meet in LDS in wave order.  Few tokens leave the loads of few slots in
+// flight at a time, so a wave then takes several slots at once.
+template <bool kGated, int TOKENS>
 __global__ __launch_bounds__(256) void df11_sum_slots_kernel(SumArgs a) {
-    __shared__ Found s_found[2];
-    __shared__ float s_sum[2][4][kSumTokens][kWaveSize];
-    const uint32_t p = blockIdx.x, t0 = blockIdx.y * kSumTokens;
-    const uint32_t lane = threadIdx.x & (kWaveSize - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
-    const uint32_t tokens = min(static_cast<uint32_t>(kSumTokens), a.n_tokens - t0);
-    const uint64_t slot = static_cast<uint64_t>(kPanelRows) * a.n_tokens;
     constexpr int kStreams = kGated ? 2 : 1;
-    for (int i = 0; i < kStreams; ++i) find_regions(a.s[i], p, &s_found[i]);
+    constexpr int kAtOnce = TOKENS >= 16 ? 2 : TOKENS >= 4 ? 4 : 8;  // slots
+    __shared__ Found s_found[kStreams];
+    __shared__ float s_sum[kStreams][4][TOKENS][kWaveSize];
+    const uint32_t p = blockIdx.x, t0 = blockIdx.y * TOKENS;
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const uint32_t tokens = min(static_cast<uint32_t>(TOKENS), a.n_tokens - t0);
+    const uint64_t slot = static_cast<uint64_t>(kPanelRows) * a.n_tokens;
+    if (threadIdx.x < kStreams) s_found[threadIdx.x] = Found{~0u, 0u, 0u};
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) find_ranges(a.s[i], p, &s_found[i]);
+    __syncthreads();
+#pragma unroll
     for (int i = 0; i < kStreams; ++i) {
         const PartialStream &s = a.s[i];
         const Found f = s_found[i];
-        const uint32_t n_fixed = f.wg_lo < f.wg_hi ? (f.wg_hi - f.wg_lo) * kPartialGroups : 0u;
-        const uint32_t n_dealt = f.g_lo < f.g_hi ? f.g_hi - f.g_lo : 0u;
-        float sum[kSumTokens];
+        const uint32_t n = f.lo < f.hi ? (f.hi - f.lo) * kPartialGroups : 0u, each = (n + 3u) / 4u;
+        const uint32_t begin = wave * each, end = min(n, begin + each);
+        const uint32_t skip = min(f.skip, s.wg_panels - 1u);
+        // Float offset of the c-th group slot's slot.
+        auto at = [&](uint32_t c) {
+            return s.base + (static_cast<uint64_t>(f.lo * kPartialGroups + c) * s.wg_panels +
+                             (c < kPartialGroups ? skip : 0u)) * slot;
+        };
+        float sum[TOKENS];
 #pragma unroll
-        for (int t = 0; t < kSumTokens; ++t) sum[t] = 0.0f;
-        const uint32_t n = n_fixed + n_dealt, each = (n + 3u) / 4u;
-        const uint32_t end = min(n, (wave + 1u) * each);
-        for (uint32_t c = wave * each; c < end; ++c) {
-            uint64_t at;
-            if (c < n_fixed) {
-                const uint32_t w = f.wg_lo + c / kPartialGroups, h = c % kPartialGroups;
-                const uint32_t first = panel_of(s, out_pos_of(s, range_begin(s, w) * kPartialGroups));
-                at = s.base + (static_cast<uint64_t>(w * kPartialGroups + h) * s.wg_panels +
-                               min(p - first, s.wg_panels - 1u)) * slot;
-            } else {
-                const uint32_t g = f.g_lo + c - n_fixed;
-                const uint32_t first = panel_of(s, out_pos_of(s, g));
-                at = s.tail + (static_cast<uint64_t>(g - s.tail_group0) * s.group_panels +
-                               min(p - first, s.group_panels - 1u)) * slot;
+        for (int t = 0; t < TOKENS; ++t) sum[t] = 0.0f;
+        const float *slots = a.slots + static_cast<uint64_t>(t0) * kPanelRows + lane;
+        for (uint32_t c = begin; c < end; c += kAtOnce) {
+            // (past the end the last slot again, not added; past the last
+            // token the first one, not written)
+            float v[kAtOnce][TOKENS];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float *q = slots + at(min(c + k, end - 1u));
+#pragma unroll
+                for (int t = 0; t < TOKENS; ++t) v[k][t] = q[t < static_cast<int>(tokens) ? t * kPanelRows : 0u];
             }
-            const float *q = a.slots + at + static_cast<uint64_t>(t0) * kPanelRows + lane;
 #pragma unroll
-            for (int t = 0; t < kSumTokens; ++t)
-                if (t < static_cast<int>(tokens)) sum[t] += q[t * kPanelRows];
+            for (int k = 0; k < kAtOnce; ++k)
+                if (c + k < end)
+#pragma unroll
+                    for (int t = 0; t < TOKENS; ++t) sum[t] += v[k][t];
         }
 #pragma unroll
-        for (int t = 0; t < kSumTokens; ++t)
-            if (t < static_cast<int>(tokens)) s_sum[i][wave][t][lane] = sum[t];
+        for (int t = 0; t < TOKENS; ++t) s_sum[i][wave][t][lane] = sum[t];
     }
     __syncthreads();
     for (uint32_t t = wave; t < tokens; t += 4u) {
         float z[2] = {};
+#pragma unroll
         for (int i = 0; i < kStreams; ++i)
             z[i] = (s_sum[i][0][t][lane] + s_sum[i][1][t][lane]) + (s_sum[i][2][t][lane] + s_sum[i][3][t][lane]);
         finish<kGated>(a.e, t0 + t, kPanelRows * p + lane, a.features, z[0], z[1]);
@@ -317,11 +319,12 @@ bool workspace_clear(const Call &c, const void *ws, uint64_t bytes) {
     return !bad;
 }
 
-int slots_impl(const Call &c, void *workspace, hipStream_t stream) {
+int slots_impl(const Call &c, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {
     SumArgs a{};
     Partials p{};
     a.slots = static_cast<float *>(workspace);
-    const int rc = df11::partial_products(c.w, c.n, c.x, c.x_stride, c.n_tokens, static_cast<float *>(workspace), stream, p);
+    const int rc = df11::partial_products(c.w, c.n, c.x, c.x_stride, c.n_tokens, static_cast<float *>(workspace),
+                                          workspace_bytes, stream, p);
     if (rc) return rc;
     a.s[0] = p.s[0];
     a.s[1] = p.s[1];
@@ -329,15 +332,21 @@ int slots_impl(const Call &c, void *workspace, hipStream_t stream) {
     a.n_tokens = c.n_tokens;
     a.features = c.out_features;
     void *params[] = {&a};
-    return launch_kernel(c.n == 2 ? reinterpret_cast<const void *>(&df11_sum_slots_kernel<true>)
-                                  : reinterpret_cast<const void *>(&df11_sum_slots_kernel<false>),
-                         dim3(c.out_features / kPanelRows, (c.n_tokens + kSumTokens - 1) / kSumTokens), dim3(256),
-                         params, 0, stream, nullptr, nullptr);
+    const uint32_t each = c.n_tokens <= 1 ? 1 : c.n_tokens <= 4 ? 4 : 16;  // tokens of a workgroup
+    const auto pick = [each](auto gated) {
+        constexpr bool kGated = decltype(gated)::value;
+        return each == 1   ? reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 1>)
+               : each == 4 ? reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 4>)
+                           : reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 16>);
+    };
+    return launch_kernel(c.n == 2 ? pick(std::true_type{}) : pick(std::false_type{}),
+                         dim3(c.out_features / kPanelRows, (c.n_tokens + each - 1) / each), dim3(256), params, 0,
+                         stream, nullptr, nullptr);
 }
 
 uint64_t slots_bytes(const df11_device_stream *const *ws, uint32_t n, uint32_t n_tokens) {
     Partials p{};
-    if (df11::partial_products(ws, n, nullptr, 0, n_tokens, nullptr, nullptr, p)) return 0;
+    if (df11::partial_products(ws, n, nullptr, 0, n_tokens, nullptr, 0, nullptr, p)) return 0;
     return p.slot_bytes;
 }
 
@@ -375,7 +384,10 @@ uint64_t forward_workspace(const df11_device_stream *const *ws, uint32_t n, uint
     return more == ~0ull ? 0 : decoded_bytes(ws, n) + more;
 }
 
-int dense_impl(const Call &c, void *workspace, hipStream_t stream) {
+int dense_impl(const Call &c, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {
+    const uint64_t need = forward_workspace(c.w, c.n, c.n_tokens, c.in_features);
+    if (!need) return DF11_E_HIP;
+    if (workspace_bytes < need) return DF11_E_BUFFER_TOO_SMALL;
     df11::DenseCall d{};
     d.mode = c.n == 2 ? df11::kDenseGated : df11::kDensePlain;
     d.left[0] = c.x;
@@ -393,12 +405,10 @@ int forward(Call &c, const df11_epilogue *e, void *workspace, uint64_t workspace
     bool empty = false;
     int rc = check_call(c, e, workspace, empty);
     if (rc || empty) return rc;
-    const uint64_t need = forward_workspace(c.w, c.n, c.n_tokens, c.in_features);
-    if (!need) return DF11_E_HIP;
     if (!workspace) return DF11_E_INVALID_ARG;
-    if (workspace_bytes < need) return DF11_E_BUFFER_TOO_SMALL;
-    if (!workspace_clear(c, workspace, need)) return DF11_E_INVALID_ARG;
-    return c.n_tokens <= kPartialTokens ? slots_impl(c, workspace, stream) : dense_impl(c, workspace, stream);
+    if (!workspace_clear(c, workspace, workspace_bytes)) return DF11_E_INVALID_ARG;
+    return c.n_tokens <= kPartialTokens ? slots_impl(c, workspace, workspace_bytes, stream)
+                                        : dense_impl(c, workspace, workspace_bytes, stream);
 }
 
 // ---- gradients

@@ -586,7 +586,8 @@ uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_
  * Sums are taken in float in an order fixed by the stream, the shapes and the
  * device, not by timing.  A token whose x holds an infinity or a NaN gives
  * infinities or NaN in its own outputs alone (0 * inf included: a weight of
- * zero does not hide it).  Uses the stream's schedule counters like df11_decompress: calls
+ * zero does not hide it).  Beyond 32 tokens the stream is decoded into the
+ * workspace, which uses its schedule counters like df11_decompress: such calls
  * that share a stream's counters must not overlap in time.  With no tokens or
  * no outputs nothing is launched.  Errors: DF11_E_INVALID_ARG,
  * DF11_E_BAD_STREAM, DF11_E_TOO_LARGE (n_tokens * features >= 2^32),

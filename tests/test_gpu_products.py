@@ -146,8 +146,8 @@ def test_product(torch_cuda, rows, cols, kind, tokens):
 
 @pytest.mark.parametrize("rows,cols", [(4096, 4096), (1024, 8192)])
 def test_product_long_streams(torch_cuda, rows, cols):
-    """Streams long enough for the dealt tail at 1 to 8 tokens, and every
-    launch shape: the schedule on and off, a capped grid."""
+    """Long streams, and every launch shape: the schedule on and off, a capped
+    grid."""
     torch = torch_cuda
     w, w64 = _weight(rows, cols)
     u, u64 = _weight(rows, cols, "normal", 1)
