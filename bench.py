@@ -554,9 +554,10 @@ def integration(args, dev) -> int:
     weights, DF11 blocks decoded in line before each block, DF11 blocks
     decoded on a side stream (capped grid) while the previous block computes,
     and, at 1..8 tokens, DF11 blocks (a stream per weight) whose projections
-    decode inside their products (runtime.fused_block_forward); at up to 16
-    tokens also the resident, in-line and fused forwards captured into HIP
-    graphs and replayed."""
+    decode inside their products (runtime.fused_block_forward); the forward
+    through the operators around the products (runtime.operator_block_forward);
+    at up to 16 tokens also the resident, in-line, fused and operator forwards
+    captured into HIP graphs and replayed."""
     import torch
     from entropy_decoding_df11_amd import df11, runtime, workloads
     blocks, resident, per_weight, tiled = [], [], [], []
@@ -583,6 +584,9 @@ def integration(args, dev) -> int:
             x = runtime.fused_block_forward(x, blk)
         return x
 
+    def operator_forward(x):
+        return runtime.operator_model_forward(x, tiled)
+
     for tokens in (1, 2, 4, 8, 16, 256, 4096):
         rng = np.random.default_rng(tokens)
         x = workloads.f32_to_bf16_bits(rng.standard_normal(tokens * 4096) * 0.5).reshape(tokens, 4096)
@@ -608,7 +612,8 @@ def integration(args, dev) -> int:
         row = {"tokens": tokens, "ms_per_forward": res,
                "df11_overlap_vs_resident": round(res["df11_overlap"] / res["resident"], 3),
                "df11_inline_vs_resident": round(res["df11_inline"] / res["resident"], 3)}
-        for name, fwd, limit in (("df11_fused", fused_forward, 8), ("df11_fused_tiles", tiled_forward, 256)):
+        for name, fwd, limit in (("df11_fused", fused_forward, 8), ("df11_fused_tiles", tiled_forward, 256),
+                                 ("df11_operators", operator_forward, 4096)):
             if tokens > limit:
                 continue
             for _ in range(3):
@@ -636,11 +641,12 @@ def integration(args, dev) -> int:
             if tokens <= 8:
                 graphs["df11_fused_graph"] = fused_forward
             graphs["df11_fused_tiles_graph"] = tiled_forward
+            graphs["df11_operators_graph"] = operator_forward
             for name, fwd in graphs.items():
                 g = runtime.CapturedForward(fwd, x)
                 y = g(x)
                 torch.cuda.synchronize()
-                if name.startswith("df11_fused"):
+                if name.startswith(("df11_fused", "df11_operators")):
                     ok = float((y.float() - ref.float()).abs().max()) <= 0.05 * float(ref.float().abs().max())
                 else:
                     ok = torch.equal(y.view(torch.int16), ref.view(torch.int16))
@@ -660,6 +666,8 @@ def integration(args, dev) -> int:
                 row["df11_fused_graph_vs_resident_graph"] = round(res["df11_fused_graph"] / res["resident_graph"], 3)
             row["df11_fused_tiles_graph_vs_resident_graph"] = round(res["df11_fused_tiles_graph"]
                                                                    / res["resident_graph"], 3)
+            row["df11_operators_graph_vs_resident_graph"] = round(res["df11_operators_graph"]
+                                                                  / res["resident_graph"], 3)
         rows.append(row)
     comp = sum(b.tensor.compressed_bytes() for b in blocks)
     raw = sum(2 * b.n_elements for b in blocks)

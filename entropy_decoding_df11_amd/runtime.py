@@ -15,6 +15,7 @@ from __future__ import annotations
 from typing import Dict, Iterator, List, Optional, Sequence, Tuple, Union
 
 from .df11 import DF11Block, DF11BlockBatch
+from .operators import gated_matmul, matmul_epilogue, rms_norm
 
 Block = Union[DF11Block, DF11BlockBatch]
 
@@ -95,25 +96,33 @@ class BlockDecoder:
             free[i % 2] = ev
 
 
-def block_forward(x, w: Dict, eps: float = 1e-5):
+def block_forward(x, w: Dict, eps: float = 1e-5, operators: bool = False):
     """A synthetic Llama-style block forward on BF16 weights (no attention
     mixing, which needs no weights): RMS-normed projections q, k, v and o
     with a residual, then the gated MLP (gate, up, down) with a residual.
-    Used to show the decompressed weights in use; shapes follow the weights."""
+    Used to show the decompressed weights in use; shapes follow the weights.
+
+    operators: the norms run as rms_norm (the second one with the residual's
+    addition), one launch each in place of torch's elementwise ones.  They
+    round once where torch's chain rounds the reciprocal root and each
+    product to x's dtype, so the last bits differ."""
     import torch
     import torch.nn.functional as F
 
     def rms(h):
         return h * torch.rsqrt(h.float().pow(2).mean(-1, keepdim=True) + eps).to(h.dtype)
 
-    h = rms(x)
+    h = rms_norm(x, eps=eps) if operators else rms(x)
     q = F.linear(h, w["q_proj"])
     k = F.linear(h, w["k_proj"])
     v = F.linear(h, w["v_proj"])
     rep = q.shape[-1] // k.shape[-1]
     a = q + (k * v).repeat_interleave(rep, dim=-1)
-    x = x + F.linear(a, w["o_proj"])
-    h = rms(x)
+    if operators:
+        h, x = rms_norm(F.linear(a, w["o_proj"]), residual=x, eps=eps)
+    else:
+        x = x + F.linear(a, w["o_proj"])
+        h = rms(x)
     x = x + F.linear(F.silu(F.linear(h, w["gate_proj"])) * F.linear(h, w["up_proj"]), w["down_proj"])
     return x
 
@@ -124,6 +133,38 @@ def block_forward(x, w: Dict, eps: float = 1e-5):
 # up to 8 tokens.
 FUSED_MAX_TOKENS_TILES = 64
 FUSED_MAX_TOKENS_ROWS = 8
+
+
+def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5):
+    """block_forward through the operators around the products, for any number
+    of tokens: rms_norm, q, k and v (one matmul_batch up to
+    FUSED_MAX_TOKENS_TILES tokens, else and under autograd matmul_epilogue),
+    o and down with the residual in their epilogue (matmul_epilogue), gate and
+    up as one gated product (gated_matmul).  blk holds one DF11 stream per
+    weight in MFMA tile order (compress_block(..., codebook="per_weight",
+    layout="mfma_tiles")).  Every operator computes in float32 and rounds its
+    output once.  Differentiable with respect to x (the weights are frozen)."""
+    import torch
+    from .df11 import matmul_batch
+
+    w = {nm: t for (nm, _, _), t in zip(blk.views, blk.tensors)}
+    qkv = [w[nm] for nm in ("q_proj", "k_proj", "v_proj")]
+    h = rms_norm(x, eps=eps)
+    if x.shape[0] > FUSED_MAX_TOKENS_TILES or (torch.is_grad_enabled() and x.requires_grad):
+        q, k, v = (matmul_epilogue(t, h) for t in qkv)
+    else:
+        q, k, v = (y.to(x.dtype) for y in matmul_batch(qkv, [h] * 3))
+    a = q + (k * v).repeat_interleave(q.shape[-1] // k.shape[-1], dim=-1)
+    x = matmul_epilogue(w["o_proj"], a, residual=x)
+    h = gated_matmul(w["gate_proj"], w["up_proj"], rms_norm(x, eps=eps))
+    return matmul_epilogue(w["down_proj"], h, residual=x)
+
+
+def operator_model_forward(x, blocks: Sequence[DF11BlockBatch]):
+    """operator_block_forward over every block in order."""
+    for blk in blocks:
+        x = operator_block_forward(x, blk)
+    return x
 
 
 def fused_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5, scratch=None):
@@ -229,10 +270,10 @@ class CapturedForward:
         return self.y
 
 
-def model_forward(x, blocks: Union[BlockDecoder, List[Dict]]):
+def model_forward(x, blocks: Union[BlockDecoder, List[Dict]], operators: bool = False):
     """Run block_forward over every block in order, taking the weights from a
     BlockDecoder (compressed) or from a list of dicts (resident BF16)."""
     items = iter(blocks) if isinstance(blocks, BlockDecoder) else enumerate(blocks)
     for _, w in items:
-        x = block_forward(x, w)
+        x = block_forward(x, w, operators=operators)
     return x
