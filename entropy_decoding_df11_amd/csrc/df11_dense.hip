@@ -21,16 +21,18 @@
 // Rows past the last token and outputs past the last row of W lie past the
 // end of their buffer resource, whose loads give zero.
 //
-// 256 x 256 tiles in eight waves (128 x 64 each) read 192 KB from LDS and
-// write 64 KB to it for 2048 cycles of MFMAs a step and SIMD, which keeps the
-// LDS busy all the time: what bounds this shape.  4096 tokens, 14336 -> 4096:
-// 410 us, 1.17 PFLOP/s; without the LDS reads 357, without the loads 379,
-// the MFMAs alone 264.  Four waves of 128 x 128 would read less, but the
-// compiler then moves accumulators between register files (520 us), and
-// operands of W straight from memory to registers double the L1's traffic
-// (445 us).  128 x 128 tiles (two workgroups a CU) reach 0.77 PFLOP/s on
-// that product and win where 256 x 256 leave CUs idle (2048 tokens, 4096 ->
-// 4096: 74 against 92 us).
+// What bounds it: on a full chip, power.  4096 tokens, 14336 -> 4096 take
+// 415 us (1.16 PFLOP/s) on random operands and 295 us (1.63 PFLOP/s) on
+// zeros, with the same instructions; the MFMAs alone, without loads or LDS
+// reads, take 264.  So every form tried ends within 3% of the same time:
+// four waves of 128 x 128 with the accumulators pinned by hand (which read a
+// third less from LDS) 411 to 418 us, half-steps of 32 in a ring of four or
+// five buffers 417 and 419, v_mfma_f32_32x32x16_bf16 416.  (Operands of W
+// straight from memory to registers double the L1's traffic: 445.)  With a
+// fifth of the CUs busy a step of 256 x 256 takes 1.2 us against 0.85 of
+// MFMAs.  128 x 128 tiles (two workgroups a CU, a quarter more LDS traffic a
+// MFMA) take 505 us on that product and win where 256 x 256 leave CUs idle
+// (2048 tokens, 4096 -> 4096: 64 against 92 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
