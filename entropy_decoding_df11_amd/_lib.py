@@ -31,6 +31,7 @@ MAX_BATCH = 16  # DF11_MAX_BATCH
 MAX_ELEMENTS = (1 << 32) - (1 << 16)  # DF11_MAX_ELEMENTS
 LINEAR_MAX_TOKENS = 8  # DF11_LINEAR_MAX_TOKENS
 LINEAR_MIN_IN_FEATURES = 512  # DF11_LINEAR_MIN_IN_FEATURES
+EPILOGUE_FUSED_TOKENS = 32  # DF11_EPILOGUE_FUSED_TOKENS
 BF16, FP16, FP32 = 0, 1, 2  # DF11_BF16, DF11_FP16, DF11_FP32
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # DF11_ACT_*
 RANS_PROB_BITS = 12  # DF11_RANS_PROB_BITS

@@ -275,7 +275,7 @@ int check_call(Call &c, const df11_epilogue *e, void *workspace, bool &empty) {
         return DF11_E_INVALID_ARG;
     if (e->residual && (!aligned(e->residual, res_bytes) || e->residual_stride > kMaxStride)) return DF11_E_INVALID_ARG;
     for (int i = 0; i < 2; ++i)
-        if ((e->bias[i] && !aligned(e->bias[i], bias_bytes)) || (e->pre[i] && !aligned(e->pre[i], 4)))
+        if ((e->bias[i] && !aligned(e->bias[i], bias_bytes)) || (e->pre[i] && !aligned(e->pre[i], 16)))
             return DF11_E_INVALID_ARG;
     // Every buffer written stays clear of everything else, but the output
     // may lie exactly on the residual (same address, stride and type).

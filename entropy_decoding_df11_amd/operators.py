@@ -286,7 +286,8 @@ def _launch_product(dev, ws, x, biases, act, residual, out, out_dtype, keep):
     first, second = ws[0]._stream_struct, ws[1]._stream_struct if len(ws) == 2 else None
     nbytes = lib.df11_epilogue_workspace(first, second, tokens)
     work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    handle = _claim(ws, dev)
+    # (only a decode uses the weights' work counters)
+    handle = _stream(dev) if tokens <= _lib.EPILOGUE_FUSED_TOKENS else _claim(ws, dev)
     if second is None:
         status = lib.df11_matmul_epilogue(first, x_ptr, xs, tokens, in_f, out_f, e, work.data_ptr(), nbytes, handle)
     else:
@@ -298,13 +299,13 @@ def _launch_product(dev, ws, x, biases, act, residual, out, out_dtype, keep):
 
 
 def _launch_product_grad(dev, ws, pre, dy, act, x_shape, want_x, biases):
-    """(dx or None, the biases' gradients): biases[i] is a tensor like the
-    bias whose gradient is wanted, or None."""
+    """(dx or None, the biases' gradients): biases[i] is the type of a bias
+    whose gradient is wanted, or None."""
     out_f, in_f = ws[0].shape
     dy2, dys = _rows(dy, out_f, "dy")
     tokens = dy2.shape[0]
     dx = torch.empty(x_shape, dtype=torch.bfloat16, device=dev) if want_x else None
-    db = [None if b is None else torch.empty_like(b) for b in biases]
+    db = [None if b is None else torch.empty(out_f, dtype=b, device=dev) for b in biases]
     g = _lib.ProductGrad(dy=dy2.data_ptr(), dy_stride=dys, dy_dtype=_DTYPES[dy.dtype], activation=act)
     for i, p in enumerate(pre):
         g.pre[i] = p.data_ptr()
@@ -399,23 +400,23 @@ def _make_functions() -> None:
             biases = (bias0, bias1)[:len(ws)]
             keep = len(ws) == 2 or act != 0
             y, pre = _run(x.device, None, _launch_product, ws, x, biases, act, residual, None, out_dtype, keep)
-            # (a bias is kept for its type alone)
-            ctx.save_for_backward(bias0, bias1, *pre)
+            ctx.save_for_backward(*pre)
             ctx.ws, ctx.act, ctx.x_shape = ws, act, x.shape
-            ctx.residual_dtype = None if residual is None else residual.dtype
+            ctx.types = [None if t is None else t.dtype for t in (residual, bias0, bias1)]
             return y
 
         @staticmethod
         @once_differentiable
         def backward(ctx, dy):
-            bias0, bias1, *pre = ctx.saved_tensors
             want_x, want_r, want0, want1 = ctx.needs_input_grad[:4]
+            residual, bias0, bias1 = ctx.types
             db = None, None
             dx = None
             if want_x or want0 or want1:
-                dx, db = _run(dy.device, None, _launch_product_grad, ctx.ws, pre, _rowwise(dy), ctx.act, ctx.x_shape,
-                              want_x, (bias0 if want0 else None, bias1 if want1 else None)[:len(ctx.ws)])
-            return (dx, dy.to(ctx.residual_dtype) if want_r else None, db[0], db[1] if len(db) == 2 else None, None,
+                dx, db = _run(dy.device, None, _launch_product_grad, ctx.ws, ctx.saved_tensors, _rowwise(dy), ctx.act,
+                              ctx.x_shape, want_x,
+                              (bias0 if want0 else None, bias1 if want1 else None)[:len(ctx.ws)])
+            return (dx, dy.to(residual) if want_r else None, db[0], db[1] if len(db) == 2 else None, None,
                     None, None)
 
     _Norm, _Product = Norm, Product

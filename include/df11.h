@@ -73,6 +73,8 @@ typedef enum df11_status {
 #define DF11_BF16 0
 #define DF11_FP16 1
 #define DF11_FP32 2
+/* Most tokens of a product with an epilogue whose decode is fused in. */
+#define DF11_EPILOGUE_FUSED_TOKENS 32
 /* Activations of the products' epilogues: none, max(z, 0), z / (1 + exp(-z)),
  * z Phi(z), and the tanh approximation of the last. */
 #define DF11_ACT_NONE 0
@@ -492,8 +494,8 @@ int df11_matmul_batch(const df11_device_stream *ws, uint32_t n_streams, const ui
  * read and written in 16-byte vectors.  Every sum is taken in float in an
  * order that the shapes alone fix, so that a call's results do not change
  * from run to run, and every result is rounded once.  None of these calls
- * uses memory of the library's own: calls that share no output or workspace
- * may overlap in time.
+ * uses memory of the library's own: calls that share no output and no
+ * workspace may overlap in time, unless stated otherwise.
  * ------------------------------------------------------------------------- */
 
 /* RMS norm with the residual's addition:
@@ -511,8 +513,9 @@ int df11_matmul_batch(const df11_device_stream *ws, uint32_t n_streams, const ui
  *   y          device, rows x cols
  *   rstd       device, rows floats, or NULL; kept for df11_rms_norm_grad
  * sum and y may each lie exactly on x or on residual (same address and
- * stride), but not on each other.  A row with an infinity or a NaN gives NaN
- * in that row alone.  Errors: DF11_E_INVALID_ARG (types, sizes, alignment,
+ * stride), but not on each other.  A row with a NaN is NaN throughout; one with
+ * an infinity is NaN there and zero elsewhere; other rows are not touched by
+ * either.  Errors: DF11_E_INVALID_ARG (types, sizes, alignment,
  * output rows that overlap, other overlaps), DF11_E_HIP. */
 int df11_rms_norm(const void *x, uint64_t x_stride, const void *residual, uint64_t residual_stride,
                   const void *weight, uint32_t weight_dtype, uint32_t rows, uint32_t cols, uint32_t dtype, float eps,
@@ -549,8 +552,8 @@ int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uin
  *                    residual_stride elements from row to row, or NULL
  *   out              device, n_tokens x out_features of out_dtype; may lie
  *                    exactly on residual (same address, stride and type)
- *   pre              device, n_tokens x out_features floats each, row-major:
- *                    receive z + bias (both or neither for a gated product),
+ *   pre              device, n_tokens x out_features floats each, row-major,
+ *                    16-byte aligned: receive z + bias (both or neither for a gated product),
  *                    for df11_matmul_grad; or NULL
  *   activation       one of DF11_ACT_*
  * Types are DF11_BF16 or DF11_FP32.  Everything up to out is float; out is
@@ -586,9 +589,10 @@ uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_
  * Sums are taken in float in an order fixed by the stream, the shapes and the
  * device, not by timing.  A token whose x holds an infinity or a NaN gives
  * infinities or NaN in its own outputs alone (0 * inf included: a weight of
- * zero does not hide it).  Beyond 32 tokens the stream is decoded into the
- * workspace, which uses its schedule counters like df11_decompress: such calls
- * that share a stream's counters must not overlap in time.  With no tokens or
+ * zero does not hide it).  Up to DF11_EPILOGUE_FUSED_TOKENS tokens the decode
+ * is fused into the product; beyond, the stream is decoded into the workspace,
+ * which uses its schedule counters like df11_decompress: such calls that share
+ * a stream's counters must not overlap in time.  With no tokens or
  * no outputs nothing is launched.  Errors: DF11_E_INVALID_ARG,
  * DF11_E_BAD_STREAM, DF11_E_TOO_LARGE (n_tokens * features >= 2^32),
  * DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */

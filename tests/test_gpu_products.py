@@ -466,3 +466,50 @@ def test_training_step_replays(torch_cuda):
         torch.cuda.synchronize()
         got = [t.clone() for t in held]
         assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@pytest.mark.parametrize("tokens", [4, 32, 33, 200])
+def test_products_on_two_streams_at_once(torch_cuda, tokens):
+    """The same weights multiplied on two streams without a wait between."""
+    torch = torch_cuda
+    _note(f"two streams {tokens}")
+    w, w64 = _weight(4096, 4096)
+    u, u64 = _weight(4096, 4096, "normal", 1)
+    xs = [_x(torch, tokens, 4096, seed=s) for s in range(6)]
+    want = [df11.gated_matmul(w, u, x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [df11.gated_matmul(w, u, x, stream=streams[i % 2]) for i, x in enumerate(xs)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for st in streams:
+        torch.cuda.current_stream().wait_stream(st)
+
+
+@pytest.mark.parametrize("tokens", [5, 80])
+def test_gradients_of_shared_and_broadcast_inputs(torch_cuda, tokens):
+    """One bias for both projections, one residual row for every token, x as
+    its own residual, the same weights as gate and up; the bias changed in
+    place between the passes."""
+    torch = torch_cuda
+    _note(f"shared gradients {tokens}")
+    w, w64 = _weight(4096, 4096)
+    x = _x(torch, tokens, 4096, seed=1).requires_grad_()
+    b = _side(torch, (4096,), torch.float32, 2).requires_grad_()
+    r = _side(torch, (1, 4096), torch.float32, 3).requires_grad_()
+    dy = _side(torch, (tokens, 4096), torch.float32, 4)
+    y = df11.gated_matmul(w, w, x, gate_bias=b, up_bias=b, residual=r.expand(tokens, 4096), out_dtype=torch.float32)
+    with torch.no_grad():
+        b += 1  # (the backward pass needs the sums, not the bias)
+    dx, db, dr = torch.autograd.grad(y, (x, b, r), dy)
+    x64, b64, d64 = x.detach().double().requires_grad_(), (b.detach().double() - 1).requires_grad_(), dy.double()
+    z = x64 @ w64.t() + b64
+    ex, eb = torch.autograd.grad(torch.nn.functional.silu(z) * z, (x64, b64), d64)
+    # (norm-wise: dz rounded to BF16, 2^-8, and dx rounded once more)
+    for got, want, part in ((dx, ex, 2.0 ** -7), (db, eb, 1e-4), (dr, d64.sum(0, keepdim=True), 1e-5)):
+        off = float((got.double() - want).norm() / want.norm())
+        assert got.shape == want.shape and off <= part
+    s, = torch.autograd.grad(df11.matmul_epilogue(w, x, residual=x), x, dy.bfloat16())
+    p, = torch.autograd.grad(df11.matmul_epilogue(w, x), x, dy.bfloat16())
+    off = float((s.double() - p.double() - dy.bfloat16().double()).norm() / s.double().norm())
+    assert off <= 2.0 ** -7

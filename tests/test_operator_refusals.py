@@ -121,7 +121,7 @@ def _product(gated=False, **k):
     dict(ot=1), dict(ot=3), dict(res=C, rt=1), dict(bias=(C, None), bt=1), dict(bias=(C, None), bt=9),
     dict(x=None), dict(x=A + 8), dict(xs=68), dict(xs=(1 << 22) + 8), dict(out=None), dict(out=B + 1),
     dict(ot=2, out=B + 2), dict(os=127), dict(os=(1 << 31) + 1), dict(res=C + 1), dict(rt=2, res=C + 2),
-    dict(rs=(1 << 31) + 1, res=C), dict(bias=(C + 1, None)), dict(pre=(C + 2, D)), dict(out=A), dict(out=A + 128),
+    dict(rs=(1 << 31) + 1, res=C), dict(bias=(C + 1, None)), dict(pre=(C + 2, D)), dict(pre=(C + 4, D)), dict(out=A), dict(out=A + 128),
     dict(res=B + 2), dict(res=B, rs=256), dict(res=B, rt=2), dict(bias=(B, None)), dict(pre=(B, D)), dict(pre=(A, D)),
     dict(out=0x200000000), dict(out=0x201000000), dict(ws=G + 128),
 ])
