@@ -380,7 +380,7 @@ bool apart_or_same(const void *out, uint64_t out_stride, const void *in, uint64_
 // Row groups of the backward pass when it sums the weight's gradient: a
 // group's partial sums cost four bytes a column written and read again, so a
 // group takes at least eight rows, and there are at most two blocks a CU.
-constexpr uint32_t kGradRowsPerGroup = 8;
+constexpr uint32_t kGradRowsPerGroup = 4;
 constexpr uint32_t kGradMaxGroups = 512;
 
 uint32_t grad_groups(uint32_t rows, uint32_t per_block) {

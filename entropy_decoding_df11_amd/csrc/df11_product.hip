@@ -413,11 +413,16 @@ int forward(Call &c, const df11_epilogue *e, void *workspace, uint64_t workspace
 
 // ---- gradients
 
-constexpr uint32_t kSlopeChunk = 32;      // tokens of one block of the slopes' kernel, at least
-constexpr uint32_t kSlopeMaxChunks = 256;  // (partial rows of a bias gradient)
+// Tokens of one block of the slopes' kernel: as many as leave about
+// kSlopeBlocks blocks, between one and eight a wave, but at most
+// kSlopeMaxChunks partial rows of a bias gradient.  (777 tokens of 1024
+// features in blocks of 32 tokens: 100 blocks, 16.6 us.)
+constexpr uint32_t kSlopeBlocks = 1024, kSlopeMaxChunks = 256;
 
-uint32_t slope_chunk(uint32_t tokens) {
-    return std::max(kSlopeChunk, (tokens + kSlopeMaxChunks - 1) / kSlopeMaxChunks);
+uint32_t slope_chunk(uint32_t tokens, uint32_t rows) {
+    const uint64_t strips = (rows + 255) / 256;
+    const uint32_t want = static_cast<uint32_t>(std::min<uint64_t>(32, tokens * strips / kSlopeBlocks));
+    return std::max((std::max(want, 1u) + 3) / 4 * 4, (tokens + kSlopeMaxChunks - 1) / kSlopeMaxChunks);
 }
 
 // Where a gradient call's parts of the workspace begin.
@@ -431,7 +436,7 @@ bool grad_plan(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens,
                const df11_product_grad &g, GradPlan &p) {
     p.own_dz = n == 2 || g.activation != DF11_ACT_NONE || g.dy_dtype != DF11_BF16 || !aligned(g.dy, 16) ||
                g.dy_stride % 8 || g.dy_stride > kMaxRow;
-    const uint32_t chunk = slope_chunk(tokens);
+    const uint32_t chunk = slope_chunk(tokens, rows);
     p.chunks = (tokens + chunk - 1) / chunk;
     uint64_t at = 0;
     for (uint32_t i = 0; i < 2; ++i) {
@@ -525,7 +530,7 @@ int backward(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens, u
     a.act = g->activation;
     a.tokens = tokens;
     a.features = rows;
-    a.chunk = slope_chunk(tokens);
+    a.chunk = slope_chunk(tokens, rows);
     for (uint32_t i = 0; i < n; ++i) {
         a.pre[i] = needs_pre ? g->pre[i] : nullptr;
         if (g->dx && p.own_dz) a.dz[i] = reinterpret_cast<uint16_t *>(base + p.dz[i]);
