@@ -14,8 +14,14 @@
 // threads hold its elements in registers between the sum and the output, so
 // the row is not read again for the second use.  Sums are float, taken lane
 // by lane, then across the wave by shuffles and across waves through LDS, in
-// an order that depends on the width alone: results do not change from call
-// to call.
+// an order that depends on the width and the type alone: results do not
+// change from call to call.  (The rows' sums of the weight's gradient depend
+// on the number of rows too.)
+//
+// What bounds them is memory.  bf16 with a residual, data not cached: forward
+// 8192 x 4096 (268 MB) 49.6 us, 5.4 TB/s; 64 rows of it 3.1 us; backward with
+// the weight's gradient 8192 x 4096 (268 MB) 53.5 us, 5.0 TB/s; 2048 rows of
+// it 18.7 us and 64 rows 6.4.  A large copy reaches 4.75 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -42,45 +48,94 @@ struct NormArgs {
     float eps;
 };
 
-// Sum of v over the TPR threads of a row, in every one of them.  One wave
-// needs no LDS; the waves of a wider row meet in s_part (one float per wave
-// of the block).
+// Rows are read and written in vectors of 16 bytes, at any alignment of their
+// elements (the card loads and stores unaligned vectors); a row's last vector
+// may be a part of one, `left` being the elements from its first to the end.
+// (8192 x 4095 bf16 forward 85 us, where no row is aligned to more than its
+// elements; one element at a time 183 us.)
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Unaligned {
+    vec_t<T, kVec<T>> v;
+};
+
+template <typename T>
+__device__ __forceinline__ vec_t<T, kVec<T>> load_row(const T *p, uint32_t left) {
+    if (left >= static_cast<uint32_t>(kVec<T>)) return reinterpret_cast<const Unaligned<T> *>(p)->v;
+    vec_t<T, kVec<T>> v = {};
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+        if (e < static_cast<int>(left)) v[e] = p[e];
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T *p, uint32_t left, const float (&f)[kVec<T>]) {
+    vec_t<T, kVec<T>> v;
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e) v[e] = static_cast<T>(f[e]);
+    if (left >= static_cast<uint32_t>(kVec<T>)) {
+        reinterpret_cast<Unaligned<T> *>(p)->v = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < kVec<T>; ++e)
+        if (e < static_cast<int>(left)) p[e] = v[e];
+}
+
+// The weights of one vector of T (float32 weights may go with any T).
+template <typename T>
+__device__ __forceinline__ void load_weight(const void *weight, uint32_t f32, uint32_t i, uint32_t left,
+                                            float (&w)[kVec<T>]) {
+    if (!weight) {
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) w[e] = 1.0f;
+    } else if (f32) {
+#pragma unroll
+        for (int q = 0; q < kVec<T>; q += 4) {
+            const vec_t<float, 4> v =
+                load_row(static_cast<const float *>(weight) + i + q, left > static_cast<uint32_t>(q) ? left - q : 0u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[q + e] = v[e];
+        }
+    } else {
+        const vec_t<T, kVec<T>> v = load_row(static_cast<const T *>(weight) + i, left);
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) w[e] = static_cast<float>(v[e]);
+    }
+}
+
+// Threads of a block: one row, or as many rows as 256 threads hold where a
+// row needs no more than a wave.
+__host__ __device__ constexpr int block_threads(int tpr) { return tpr <= static_cast<int>(kWaveSize) ? 256 : tpr; }
+
+// Sum of v over the TPR threads of a row, in every one of them.  Within a
+// wave it needs no LDS; the waves of a wider row meet in s_part.
 template <int TPR>
 __device__ __forceinline__ float row_total(float v, float *s_part) {
 #pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+    for (int m = (TPR < static_cast<int>(kWaveSize) ? TPR : static_cast<int>(kWaveSize)) / 2; m; m >>= 1)
+        v += __shfl_xor(v, m);
     if constexpr (TPR > static_cast<int>(kWaveSize)) {
-        constexpr int kRowWaves = TPR / static_cast<int>(kWaveSize);
         if ((threadIdx.x & (kWaveSize - 1)) == 0) s_part[threadIdx.x / kWaveSize] = v;
         __syncthreads();
         v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kRowWaves; ++w) v += s_part[w];
+        for (int w = 0; w < TPR / static_cast<int>(kWaveSize); ++w) v += s_part[w];
     }
     return v;
 }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_weight(const void *weight, uint32_t f32, uint32_t i, float (&w)[VEC]) {
-    if (!weight) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = 1.0f;
-    } else if (f32) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = static_cast<const float *>(weight)[i + e];
-    } else {
-        load_vec<T, VEC>(static_cast<const T *>(weight) + i, w);
-    }
-}
-
-// TPR threads per row, NV vectors of VEC elements held per thread.  kWide:
-// rows beyond TPR * NV vectors, whose elements past the held ones are read
-// a second time for the output (from the sum where one is written).
-template <typename T, int VEC, int NV, int TPR, bool kWide>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void df11_rms_norm_kernel(NormArgs a) {
-    constexpr int kBlock = TPR < 256 ? 256 : TPR;
-    constexpr int kRows = kBlock / TPR;
-    __shared__ float s_part[2][kBlock / kWaveSize];
+// TPR threads per row, NV vectors held per thread.  kWide: rows beyond TPR *
+// NV vectors, whose elements past the held ones are read a second time for
+// the output (from the sum where one is written).
+template <typename T, int NV, int TPR, bool kWide>
+__global__ __launch_bounds__(block_threads(TPR)) void df11_rms_norm_kernel(NormArgs a) {
+    constexpr int VEC = kVec<T>, kRows = block_threads(TPR) / TPR;
+    using Vec = vec_t<T, VEC>;
+    __shared__ float s_part[2][block_threads(TPR) / kWaveSize];
     const uint32_t lid = threadIdx.x % TPR;
     uint32_t turn = 0;
     // (one row per group of threads, unless the rows outnumber the largest
@@ -91,32 +146,46 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void df11_rms_norm_kernel(No
         T *sum = a.sum ? static_cast<T *>(a.sum) + row * a.sum_stride : nullptr;
         T *y = static_cast<T *>(a.y) + row * a.y_stride;
 
-        float v[NV][VEC];
-        float total = 0.0f;
-        // One vector's s, written to the sum if there is one.
-        auto take = [&](uint32_t i, float (&s)[VEC]) {
-            load_vec<T, VEC>(x + i, s);
-            if (res) {
-                float r[VEC];
-                load_vec<T, VEC>(res + i, r);
+        // One vector's s = round(x + residual).
+        auto add = [&](const Vec &vx, const Vec &vr, float (&s)[VEC]) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s[e] = static_cast<float>(static_cast<T>(s[e] + r[e]));
+            for (int e = 0; e < VEC; ++e) {
+                s[e] = static_cast<float>(vx[e]);
+                if (res) s[e] = static_cast<float>(static_cast<T>(s[e] + static_cast<float>(vr[e])));
             }
-            if (sum) store_vec<T, VEC>(sum + i, s);
         };
+        auto put = [&](uint32_t i, const float (&s)[VEC], float r) {
+            float w[VEC];
+            load_weight<T>(a.weight, a.weight_f32, i, a.cols - i, w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] *= s[e] * r;
+            store_row(y + i, a.cols - i, w);
+        };
+        Vec vx[NV], vr[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t i = (j * TPR + lid) * VEC;
+            vx[j] = vr[j] = Vec{};
             if (i < a.cols) {
-                take(i, v[j]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) total += v[j][e] * v[j][e];
+                vx[j] = load_row(x + i, a.cols - i);
+                if (res) vr[j] = load_row(res + i, a.cols - i);
             }
+        }
+        float v[NV][VEC];
+        float total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t i = (j * TPR + lid) * VEC;
+            add(vx[j], vr[j], v[j]);
+            if (sum && i < a.cols) store_row(sum + i, a.cols - i, v[j]);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) total += v[j][e] * v[j][e];
         }
         if constexpr (kWide) {
             for (uint32_t i = (NV * TPR + lid) * VEC; i < a.cols; i += TPR * VEC) {
                 float s[VEC];
-                take(i, s);
+                add(load_row(x + i, a.cols - i), res ? load_row(res + i, a.cols - i) : Vec{}, s);
+                if (sum) store_row(sum + i, a.cols - i, s);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) total += s[e] * s[e];
             }
@@ -125,31 +194,24 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void df11_rms_norm_kernel(No
         // (the quotient and the root are each rounded to float)
         const float r = 1.0f / sqrtf(total / static_cast<float>(a.cols) + a.eps);
         if (a.rstd && lid == 0) a.rstd[row] = r;
-        auto put = [&](uint32_t i, const float (&s)[VEC]) {
-            float w[VEC];
-            load_weight<T, VEC>(a.weight, a.weight_f32, i, w);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] *= s[e] * r;
-            store_vec<T, VEC>(y + i, w);
-        };
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t i = (j * TPR + lid) * VEC;
-            if (i < a.cols) put(i, v[j]);
+            if (i < a.cols) put(i, v[j], r);
         }
         if constexpr (kWide) {
             // Each thread reads back only what it wrote or read itself, so the
             // output may be x's or the residual's own buffer.
             for (uint32_t i = (NV * TPR + lid) * VEC; i < a.cols; i += TPR * VEC) {
                 float s[VEC];
-                load_vec<T, VEC>((sum ? static_cast<const T *>(sum) : x) + i, s);
-                if (res && !sum) {
-                    float q[VEC];
-                    load_vec<T, VEC>(res + i, q);
+                if (sum) {
+                    const Vec back = load_row(static_cast<const T *>(sum) + i, a.cols - i);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) s[e] = static_cast<float>(static_cast<T>(s[e] + q[e]));
+                    for (int e = 0; e < VEC; ++e) s[e] = static_cast<float>(back[e]);
+                } else {
+                    add(load_row(x + i, a.cols - i), res ? load_row(res + i, a.cols - i) : Vec{}, s);
                 }
-                put(i, s);
+                put(i, s, r);
             }
         }
     }
@@ -162,7 +224,7 @@ struct NormGradArgs {
     const void *dy;
     const void *dsum;    // or null
     void *dx;
-    float *partial;      // or null: [row groups][cols] sums of dy * h
+    float *partial;      // or null: [blocks][cols] sums of dy * h
     uint64_t s_stride, dy_stride, dsum_stride, dx_stride;
     uint32_t rows, cols;
     uint32_t weight_f32;
@@ -170,58 +232,60 @@ struct NormGradArgs {
 
 // A row group (the TPR threads of one row at a time) takes rows g, g + G,
 // g + 2 G, ... of the G groups of the launch, and keeps its sums of dy * h
-// for the columns its threads hold in registers; they leave once, at the end.
-template <typename T, int VEC, int NV, int TPR, bool kWide>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void df11_rms_norm_grad_kernel(NormGradArgs a) {
-    constexpr int kBlock = TPR < 256 ? 256 : TPR;
-    constexpr int kRows = kBlock / TPR;
-    __shared__ float s_part[2][kBlock / kWaveSize];
+// for the columns its threads hold in registers; at the end a block's groups
+// add theirs in LDS, in order, and the block's sums leave once.
+template <typename T, int NV, int TPR, bool kWide>
+__global__ __launch_bounds__(block_threads(TPR)) void df11_rms_norm_grad_kernel(NormGradArgs a) {
+    constexpr int VEC = kVec<T>, kRows = block_threads(TPR) / TPR;
+    using Vec = vec_t<T, VEC>;
+    __shared__ float s_part[2][block_threads(TPR) / kWaveSize];
     const uint32_t lid = threadIdx.x % TPR;
-    const uint32_t group = blockIdx.x * kRows + threadIdx.x / TPR;
-    const uint32_t groups = gridDim.x * kRows;
     const float inv = 1.0f / static_cast<float>(a.cols);
     float acc[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[j][e] = 0.0f;
-    float *part = a.partial ? a.partial + static_cast<uint64_t>(group) * a.cols : nullptr;
+    float *part = a.partial ? a.partial + static_cast<uint64_t>(blockIdx.x) * a.cols : nullptr;
+    // (a wide row's block is that row's alone: the sums past the held columns
+    // are kept where they will leave, each by one thread)
     if constexpr (kWide) {
         if (part)
             for (uint32_t i = (NV * TPR + lid) * VEC; i < a.cols; i += TPR * VEC)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) part[i + e] = 0.0f;
+                for (uint32_t e = 0; e < VEC && i + e < a.cols; ++e) part[i + e] = 0.0f;
     }
     uint32_t turn = 0;
-    for (uint32_t row = group; row < a.rows; row += groups, turn ^= 1u) {
+    for (uint32_t row = blockIdx.x * kRows + threadIdx.x / TPR; row < a.rows; row += gridDim.x * kRows, turn ^= 1u) {
         const T *s = static_cast<const T *>(a.s) + row * a.s_stride;
         const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
         const T *ds = a.dsum ? static_cast<const T *>(a.dsum) + row * a.dsum_stride : nullptr;
         T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
         const float r = a.rstd[row];
-        // (held packed, as loaded: the floats of a row of four vectors a
-        // thread would not fit the registers of 1024 threads)
-        Packed<T, VEC> sv[NV], dv[NV];
+        // (held packed, as loaded: the floats of four vectors a thread would
+        // not fit the registers of 1024 threads)
+        Vec sv[NV], dv[NV], gv[NV];
         float total = 0.0f;
         // h = s * rstd, d = dy * weight, raw = dy of one vector
-        auto expand = [&](uint32_t i, const Packed<T, VEC> &ps, const Packed<T, VEC> &pd, float (&h)[VEC],
-                          float (&d)[VEC], float (&raw)[VEC]) {
+        auto expand = [&](uint32_t i, const Vec &ps, const Vec &pd, float (&h)[VEC], float (&d)[VEC],
+                          float (&raw)[VEC]) {
             float w[VEC];
-            unpack<T, VEC>(ps, h);
-            unpack<T, VEC>(pd, raw);
-            load_weight<T, VEC>(a.weight, a.weight_f32, i, w);
+            load_weight<T>(a.weight, a.weight_f32, i, a.cols - i, w);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                h[e] *= r;
+                h[e] = static_cast<float>(ps[e]) * r;
+                raw[e] = static_cast<float>(pd[e]);
                 d[e] = raw[e] * w[e];
             }
         };
+        // the incoming gradients of the sum; zeros without them
+        auto through = [&](uint32_t i) { return ds ? load_row(ds + i, a.cols - i) : Vec{}; };
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t i = (j * TPR + lid) * VEC;
             if (i < a.cols) {
-                sv[j] = load_packed<T, VEC>(s + i);
-                dv[j] = load_packed<T, VEC>(dy + i);
+                sv[j] = load_row(s + i, a.cols - i);
+                dv[j] = load_row(dy + i, a.cols - i);
+                if constexpr (NV == 1) gv[j] = through(i);
             }
         }
 #pragma unroll
@@ -240,48 +304,58 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void df11_rms_norm_grad_kern
         if constexpr (kWide) {
             for (uint32_t i = (NV * TPR + lid) * VEC; i < a.cols; i += TPR * VEC) {
                 float h[VEC], d[VEC], raw[VEC];
-                expand(i, load_packed<T, VEC>(s + i), load_packed<T, VEC>(dy + i), h, d, raw);
+                expand(i, load_row(s + i, a.cols - i), load_row(dy + i, a.cols - i), h, d, raw);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     total += d[e] * h[e];
-                    if (part) part[i + e] += raw[e] * h[e];
+                    if (part && i + e < a.cols) part[i + e] += raw[e] * h[e];
                 }
             }
         }
         // (two sets of wave sums, in turn: a wave may enter the next row's
         // sum while another still reads this one's)
         const float mean = row_total<TPR>(total, s_part[turn]) * inv;
-        auto put = [&](uint32_t i, const Packed<T, VEC> &ps, const Packed<T, VEC> &pd) {
+        auto put = [&](uint32_t i, const Vec &ps, const Vec &pd, const Vec &pg) {
             float g[VEC], h[VEC], d[VEC], raw[VEC];
-            if (ds) {
-                load_vec<T, VEC>(ds + i, g);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) g[e] = 0.0f;
-            }
             expand(i, ps, pd, h, d, raw);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) g[e] += r * (d[e] - h[e] * mean);
-            store_vec<T, VEC>(dx + i, g);
+            for (int e = 0; e < VEC; ++e) g[e] = static_cast<float>(pg[e]) + r * (d[e] - h[e] * mean);
+            store_row(dx + i, a.cols - i, g);
         };
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint32_t i = (j * TPR + lid) * VEC;
-            if (i < a.cols) put(i, sv[j], dv[j]);
+            if (i < a.cols) {
+                if constexpr (NV > 1) gv[j] = through(i);
+                put(i, sv[j], dv[j], gv[j]);
+            }
         }
         if constexpr (kWide) {
             for (uint32_t i = (NV * TPR + lid) * VEC; i < a.cols; i += TPR * VEC)
-                put(i, load_packed<T, VEC>(s + i), load_packed<T, VEC>(dy + i));
+                put(i, load_row(s + i, a.cols - i), load_row(dy + i, a.cols - i), through(i));
         }
     }
-    if (part) {
+    if (!part) return;
+    if constexpr (kRows > 1) {
+        static_assert(NV == 1);
+        __shared__ float s_acc[VEC][kRows][TPR];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const uint32_t i = (j * TPR + lid) * VEC;
-            if (i < a.cols)
+        for (int e = 0; e < VEC; ++e) s_acc[e][threadIdx.x / TPR][lid] = acc[0][e];
+        __syncthreads();
+        if (threadIdx.x >= TPR) return;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) part[i + e] = acc[j][e];
-        }
+        for (int e = 0; e < VEC; ++e)
+            for (int g = 1; g < kRows; ++g) acc[0][e] += s_acc[e][g][lid];
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t i = (j * TPR + lid) * VEC;
+#pragma unroll
+        for (int q = 0; q < VEC; q += 4)
+            if (i + q < a.cols) {
+                const float f[4] = {acc[j][q], acc[j][q + 1], acc[j][q + 2], acc[j][q + 3]};
+                store_row(part + i + q, a.cols - i - q, f);
+            }
     }
 }
 
@@ -305,63 +379,55 @@ __global__ __launch_bounds__(1024) void df11_column_sum_kernel(const float *p, u
 }
 
 // Threads per row and vectors per thread for a row of n vectors: the fewest
-// threads that hold the row in at most four vectors each, so that rows of up
-// to 256 vectors need no barrier.  1024 threads hold two vectors each (or
-// eight single elements, where rows are not aligned to vectors): what their
-// registers allow in the backward pass.  Past that the remainder is read twice.
+// threads that hold it at a vector each, up to the 1024 of a block.  Several
+// vectors a thread leave the loads of a row to fewer waves: bf16 rows of 2048,
+// 64 threads of four vectors against 256 of one, 64 rows forward 4.4 against
+// 3.0 us and backward 11.6 against 5.4, 16384 rows 55 against 49 and 156
+// against 65.  More threads than vectors idle: 262144 rows of 128, 64 threads
+// against 16, forward 88 against 50 us; 8192 rows of 4096, 1024 against 512,
+// 72 against 50.  Past 4096 vectors the remainder of a row is read twice: four
+// vectors held against two, 1024 rows of 32768, forward 54 against 58 us and
+// backward 71 against 119; two held where they suffice, 2048 rows of 16384,
+// 54.5 against 57.5 and 58.8 against 62.1.
 struct RowShape {
     uint32_t threads, vectors;
     bool wide;
 };
 
-constexpr int kMostHeld(int vec) { return vec == 1 ? 8 : 2; }
-
-RowShape row_shape(uint64_t n, uint32_t vec) {
-    if (n <= 64) return {64, 1, false};
-    if (n <= 128) return {64, 2, false};
-    if (n <= 256) return {64, 4, false};
-    if (n <= 512) return {256, 2, false};
-    if (n <= 1024) return {256, 4, false};
-    const uint32_t most = static_cast<uint32_t>(kMostHeld(static_cast<int>(vec)));
-    return {1024, most, n > 1024ull * most};
+RowShape row_shape(uint64_t n) {
+    for (uint32_t threads : {16u, 32u, 64u, 128u, 256u, 512u, 1024u})
+        if (n <= threads) return {threads, 1, false};
+    return {1024, n <= 2048 ? 2u : 4u, n > 4096};
 }
 
-// Elements per vector: 16 bytes where the rows of every tensor are aligned
-// to that and the width is a whole number of vectors, else one element.
-uint32_t row_vector(uint32_t bytes, uint32_t cols, const void *const *ptrs, const uint64_t *strides, int n) {
-    const uint32_t per = 16u / bytes;
-    bool whole = cols % per == 0;
-    for (int i = 0; i < n; ++i)
-        if (ptrs[i]) whole = whole && aligned(ptrs[i], 16) && strides[i] % per == 0;
-    return whole ? per : 1u;
-}
-
-template <template <typename, int, int, int, bool> class Pick, typename T, int VEC>
+template <template <typename, int, int, bool> class Pick, typename T>
 const void *pick_shape(const RowShape &s) {
-    if (s.wide) return Pick<T, VEC, kMostHeld(VEC), 1024, true>::get();
-    if (s.threads == 1024) return Pick<T, VEC, kMostHeld(VEC), 1024, false>::get();
-    if (s.threads == 256) return s.vectors == 2 ? Pick<T, VEC, 2, 256, false>::get() : Pick<T, VEC, 4, 256, false>::get();
-    return s.vectors == 1   ? Pick<T, VEC, 1, 64, false>::get()
-           : s.vectors == 2 ? Pick<T, VEC, 2, 64, false>::get()
-                            : Pick<T, VEC, 4, 64, false>::get();
-}
-
-template <template <typename, int, int, int, bool> class Pick>
-const void *pick_kernel(uint32_t dtype, uint32_t vec, const RowShape &s) {
-    if (dtype == DF11_FP32) return vec > 1 ? pick_shape<Pick, float, 4>(s) : pick_shape<Pick, float, 1>(s);
-    if (dtype == DF11_BF16) return vec > 1 ? pick_shape<Pick, bf16_t, 8>(s) : pick_shape<Pick, bf16_t, 1>(s);
-    return vec > 1 ? pick_shape<Pick, fp16_t, 8>(s) : pick_shape<Pick, fp16_t, 1>(s);
-}
-
-template <typename T, int VEC, int NV, int TPR, bool kWide>
-struct NormKernel {
-    static const void *get() { return reinterpret_cast<const void *>(&df11_rms_norm_kernel<T, VEC, NV, TPR, kWide>); }
-};
-template <typename T, int VEC, int NV, int TPR, bool kWide>
-struct NormGradKernel {
-    static const void *get() {
-        return reinterpret_cast<const void *>(&df11_rms_norm_grad_kernel<T, VEC, NV, TPR, kWide>);
+    if (s.wide) return Pick<T, 4, 1024, true>::get();
+    if (s.vectors > 1) return s.vectors == 2 ? Pick<T, 2, 1024, false>::get() : Pick<T, 4, 1024, false>::get();
+    switch (s.threads) {
+    case 16: return Pick<T, 1, 16, false>::get();
+    case 32: return Pick<T, 1, 32, false>::get();
+    case 64: return Pick<T, 1, 64, false>::get();
+    case 128: return Pick<T, 1, 128, false>::get();
+    case 256: return Pick<T, 1, 256, false>::get();
+    case 512: return Pick<T, 1, 512, false>::get();
+    default: return Pick<T, 1, 1024, false>::get();
     }
+}
+
+template <template <typename, int, int, bool> class Pick>
+const void *pick_kernel(uint32_t dtype, const RowShape &s) {
+    if (dtype == DF11_FP32) return pick_shape<Pick, float>(s);
+    return dtype == DF11_BF16 ? pick_shape<Pick, bf16_t>(s) : pick_shape<Pick, fp16_t>(s);
+}
+
+template <typename T, int NV, int TPR, bool kWide>
+struct NormKernel {
+    static const void *get() { return reinterpret_cast<const void *>(&df11_rms_norm_kernel<T, NV, TPR, kWide>); }
+};
+template <typename T, int NV, int TPR, bool kWide>
+struct NormGradKernel {
+    static const void *get() { return reinterpret_cast<const void *>(&df11_rms_norm_grad_kernel<T, NV, TPR, kWide>); }
 };
 
 // Bytes from a row tensor's first to its last element.
@@ -377,19 +443,18 @@ bool apart_or_same(const void *out, uint64_t out_stride, const void *in, uint64_
     return !overlaps(out, span_bytes(rows, cols, out_stride, bytes), in, span_bytes(rows, cols, in_stride, bytes));
 }
 
-// Row groups of the backward pass when it sums the weight's gradient: a
-// group's partial sums cost four bytes a column written and read again, so a
-// group takes at least eight rows, and there are at most two blocks a CU.
-constexpr uint32_t kGradRowsPerGroup = 4;
-constexpr uint32_t kGradMaxGroups = 512;
+// Blocks of the backward pass when it sums the weight's gradient: a block's
+// sums cost four bytes a column written and read again, so each row group of
+// a block takes at least kGradRows rows, and the launch has at most
+// kGradThreads threads.  Bf16 rows of 4096, with the column sums after it: 64
+// rows at one, two and four rows a group 6.3, 6.4 and 7.9 us, 512 rows 12.1,
+// 10.1 and 10.3; 8192 rows in 2^18 threads 53.5 us, in 2^17 57.2.
+constexpr uint32_t kGradRows = 2, kGradThreads = 1u << 18;
 
-uint32_t grad_groups(uint32_t rows, uint32_t per_block) {
-    const uint32_t want = std::min(kGradMaxGroups, (rows + kGradRowsPerGroup - 1) / kGradRowsPerGroup);
-    return std::max(1u, (want + per_block - 1) / per_block) * per_block;
+uint32_t grad_blocks(uint32_t rows, uint32_t per_block, uint32_t block) {
+    const uint32_t each = kGradRows * per_block;
+    return std::max(1u, std::min(kGradThreads / block, (rows + each - 1) / each));
 }
-
-// (for the largest number of row groups a block can hold)
-uint32_t grad_groups_bound(uint32_t rows) { return grad_groups(rows, 256u / kWaveSize); }
 
 // Most blocks of a launch (a grid's threads are counted in 32 bits); the rows
 // past them are taken in further turns.
@@ -450,18 +515,23 @@ int df11_rms_norm(const void *x, uint64_t x_stride, const void *residual, uint64
         return DF11_E_INVALID_ARG;
     NormArgs a{x, residual, weight, sum, y, rstd, x_stride, residual_stride, sum_stride, y_stride, rows, cols,
                weight && weight_dtype == DF11_FP32, eps};
-    uint32_t vec = row_vector(bytes, cols, ptrs, strides, 4);
-    if (weight && !aligned(weight, 16)) vec = 1;
-    const RowShape shape = row_shape((cols + vec - 1) / vec, vec);
-    const uint32_t block = std::max(256u, shape.threads), per_block = block / shape.threads;
+    const RowShape shape = row_shape((static_cast<uint64_t>(cols) * bytes + 15) / 16);
+    const uint32_t block = block_threads(static_cast<int>(shape.threads)), per_block = block / shape.threads;
     (void)hipGetLastError();
     void *params[] = {&a};
-    return launch_kernel(pick_kernel<NormKernel>(dtype, vec, shape), dim3(std::min(kMaxBlocks, (rows + per_block - 1) / per_block)),
+    return launch_kernel(pick_kernel<NormKernel>(dtype, shape), dim3(std::min(kMaxBlocks, (rows + per_block - 1) / per_block)),
                          dim3(block), params, 0, static_cast<hipStream_t>(hip_stream), nullptr, nullptr);
 }
 
 uint64_t df11_rms_norm_grad_workspace(uint32_t rows, uint32_t cols) {
-    return rows ? 4ull * grad_groups_bound(rows) * cols : 0;
+    // (for the most blocks of any type's row shape)
+    uint64_t blocks = 0;
+    for (const uint32_t bytes : {2u, 4u}) {
+        const RowShape shape = row_shape((static_cast<uint64_t>(cols) * bytes + 15) / 16);
+        const uint32_t block = block_threads(static_cast<int>(shape.threads));
+        blocks = std::max<uint64_t>(blocks, grad_blocks(rows, block / shape.threads, block));
+    }
+    return rows ? 4ull * blocks * cols : 0;
 }
 
 int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uint32_t weight_dtype, const float *rstd,
@@ -502,24 +572,22 @@ int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uin
                 return DF11_E_INVALID_ARG;
     }
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-    uint32_t groups = 0;
+    uint32_t blocks = 0;
     float *partial = dweight ? static_cast<float *>(workspace) : nullptr;
     (void)hipGetLastError();
     if (rows) {
-        uint32_t vec = row_vector(bytes, cols, ptrs, strides, 4);
-        if (weight && !aligned(weight, 16)) vec = 1;
-        const RowShape shape = row_shape((cols + vec - 1) / vec, vec);
-        const uint32_t block = std::max(256u, shape.threads), per_block = block / shape.threads;
-        groups = dweight ? grad_groups(rows, per_block)
-                         : std::min(kMaxBlocks, (rows + per_block - 1) / per_block) * per_block;
+        const RowShape shape = row_shape((static_cast<uint64_t>(cols) * bytes + 15) / 16);
+        const uint32_t block = block_threads(static_cast<int>(shape.threads)), per_block = block / shape.threads;
+        blocks = dweight ? grad_blocks(rows, per_block, block)
+                         : std::min(kMaxBlocks, (rows + per_block - 1) / per_block);
         NormGradArgs a{s, weight, rstd, dy, dsum, dx, partial, s_stride, dy_stride, dsum_stride, dx_stride, rows, cols,
                        weight && weight_dtype == DF11_FP32};
         void *params[] = {&a};
-        const int rc = launch_kernel(pick_kernel<NormGradKernel>(dtype, vec, shape), dim3(groups / per_block),
+        const int rc = launch_kernel(pick_kernel<NormGradKernel>(dtype, shape), dim3(blocks),
                                      dim3(block), params, 0, stream, nullptr, nullptr);
         if (rc) return rc;
     }
-    return dweight ? df11::column_sums(partial, groups, cols, dweight, weight_dtype, stream) : DF11_OK;
+    return dweight ? df11::column_sums(partial, blocks, cols, dweight, weight_dtype, stream) : DF11_OK;
 }
 
 }  // extern "C"

@@ -416,7 +416,8 @@ int forward(Call &c, const df11_epilogue *e, void *workspace, uint64_t workspace
 // Tokens of one block of the slopes' kernel: as many as leave about
 // kSlopeBlocks blocks, between one and eight a wave, but at most
 // kSlopeMaxChunks partial rows of a bias gradient.  (777 tokens of 1024
-// features in blocks of 32 tokens: 100 blocks, 16.6 us.)
+// features: 780 blocks of 4 tokens 5.7 us, 100 of 32 tokens 16.6.  1024
+// tokens of 14336 gated, 294 MB: 44 us, 6.7 TB/s with part of it cached.)
 constexpr uint32_t kSlopeBlocks = 1024, kSlopeMaxChunks = 256;
 
 uint32_t slope_chunk(uint32_t tokens, uint32_t rows) {

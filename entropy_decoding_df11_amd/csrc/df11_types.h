@@ -46,32 +46,6 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[N]) {
     }
 }
 
-// N consecutive elements as they lie in memory (held packed, two-byte types
-// take half the registers of their floats), and their conversion.
-template <typename T, int N>
-struct Packed {
-    vec_t<T, N> v;
-};
-template <typename T>
-struct Packed<T, 1> {
-    T v;
-};
-
-template <typename T, int N>
-__device__ __forceinline__ Packed<T, N> load_packed(const T *p) {
-    return *reinterpret_cast<const Packed<T, N> *>(p);
-}
-
-template <typename T, int N>
-__device__ __forceinline__ void unpack(const Packed<T, N> &p, float (&f)[N]) {
-    if constexpr (N == 1) {
-        f[0] = static_cast<float>(p.v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = static_cast<float>(p.v[i]);
-    }
-}
-
 // One element of a buffer whose type is known at run time (wave-uniform).
 __device__ __forceinline__ float load_as(const void *p, uint64_t i, uint32_t dtype) {
     if (dtype == DF11_FP32) return static_cast<const float *>(p)[i];

@@ -491,7 +491,7 @@ int df11_matmul_batch(const df11_device_stream *ws, uint32_t n_streams, const ui
  * model: what a forward through compressed weights computes between one
  * product and the next.  Strides are in elements.  A buffer of elements is
  * aligned to one element unless stated otherwise; 16-byte aligned rows are
- * read and written in 16-byte vectors.  Every sum is taken in float in an
+ * read and written fastest.  Every sum is taken in float in an
  * order that the shapes alone fix, so that a call's results do not change
  * from run to run, and every result is rounded once.  None of these calls
  * uses memory of the library's own: calls that share no output and no

@@ -229,3 +229,51 @@ def test_norm_repeats_and_replays(torch_cuda):
         torch.cuda.synchronize()
         got = [t.clone() for t in held]
         assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@pytest.mark.parametrize("kind", ["bfloat16", "float32"])
+def test_norm_unaligned_rows_leave_their_surroundings(torch_cuda, kind):
+    """Widths around every number of threads a row takes, whole vectors and
+    one element off, at bases and strides aligned to one element only: the
+    values, and the elements between the rows, which stay as they were."""
+    torch = torch_cuda
+    from entropy_decoding_df11_amd import df11
+    dt = getattr(torch, kind)
+    vec = 16 // dt.itemsize
+    for threads in (1, 16, 32, 64, 128, 256, 512, 1024, 2048, 4096):
+        for cols in (threads * vec - 1, threads * vec, threads * vec + 1):
+            _note(f"norm unaligned {kind} {cols}")
+            base = torch.randn(3, cols + 5, device="cuda").to(dt)
+            x, r = base[:, 1:cols + 1], base.roll(7, 1)[:, 3:cols + 3]
+            w = (1 + 0.3 * torch.randn(cols + 1, device="cuda")).to(dt)[1:]
+            y64 = _forward64(torch, x, w, r, 1e-5)[3]
+            s64 = (x.float() + r.float()).to(dt)
+            out, sums = (torch.full((3, cols + 3), v, device="cuda", dtype=dt) for v in (7.0, 9.0))
+            y, s = df11.rms_norm(x, weight=w, residual=r, out=out[:, 1:cols + 1], sum_out=sums[:, 2:cols + 2])
+            _check_y(torch, y, y64, cols)
+            assert torch.equal(s, s64)
+            assert bool((out[:, :1] == 7).all()) and bool((out[:, cols + 1:] == 7).all())
+            assert bool((sums[:, :2] == 9).all()) and bool((sums[:, cols + 2:] == 9).all())
+            # the same in place, in rows that touch
+            xi, ri = x.contiguous(), r.contiguous()
+            df11.rms_norm(xi, weight=w, residual=ri, out=ri, sum_out=xi)
+            assert torch.equal(ri, y) and torch.equal(xi, s)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 100), (37, 128), (700, 200), (3000, 520), (700, 1030), (1100, 4096),
+                                       (600, 8200), (300, 33000)])
+def test_norm_weight_gradient_over_many_rows(torch_cuda, rows, cols):
+    """The weight's gradient where row groups of one block, blocks and rows
+    beyond them each add up."""
+    torch = torch_cuda
+    from entropy_decoding_df11_amd import df11
+    _note(f"norm weight gradient {rows}x{cols}")
+    for dt in (torch.bfloat16, torch.float32):
+        x, _, w, dy, _ = _inputs(torch, rows, cols, dt, seed=rows)
+        leaves = x.clone().requires_grad_(), w.clone().requires_grad_()
+        dw = torch.autograd.grad(df11.rms_norm(leaves[0], weight=leaves[1]), leaves, dy)[1]
+        h = _forward64(torch, x, w, None, 1e-5)[1]
+        t = dy.double() * h
+        # each product rounded and added at most once per row, rstd's own error
+        bound = _half_step(torch, torch.float32, t.sum(0)) + 1.01 * U * t.abs().sum(0) * (rows + _depth(cols) / 2 + 8)
+        assert bool(((dw.double() - t.sum(0)).abs() <= bound).all())
