@@ -88,12 +88,14 @@ __device__ __forceinline__ void find_ranges(const PartialStream &s, uint32_t p, 
 
 // One workgroup adds the slots of one panel for up to TOKENS tokens: a lane
 // per output feature, the slots split between the four waves, whose sums
-// meet in LDS in wave order.  Few tokens leave the loads of few slots in
-// flight at a time, so a wave then takes several slots at once.
+// meet in LDS in wave order.  A wave takes several slots at once, so that
+// more loads than one slot's are in flight.  What bounds it is the chain of a
+// launch, the ranges' search and two rounds of loads: 4.5 us of a product's
+// 45 for 4096 x 14336 at one token, whose slots are half a megabyte.
 template <bool kGated, int TOKENS>
 __global__ __launch_bounds__(256) void df11_sum_slots_kernel(SumArgs a) {
     constexpr int kStreams = kGated ? 2 : 1;
-    constexpr int kAtOnce = TOKENS >= 16 ? 2 : TOKENS >= 4 ? 4 : 8;  // slots
+    constexpr int kAtOnce = TOKENS >= 4 ? 4 : 8;  // slots
     __shared__ Found s_found[kStreams];
     __shared__ float s_sum[kStreams][4][TOKENS][kWaveSize];
     const uint32_t p = blockIdx.x, t0 = blockIdx.y * TOKENS;
@@ -332,15 +334,22 @@ int slots_impl(const Call &c, void *workspace, uint64_t workspace_bytes, hipStre
     a.n_tokens = c.n_tokens;
     a.features = c.out_features;
     void *params[] = {&a};
-    const uint32_t each = c.n_tokens <= 1 ? 1 : c.n_tokens <= 4 ? 4 : 16;  // tokens of a workgroup
-    const auto pick = [each](auto gated) {
+    // Tokens of a workgroup: one while two workgroups a CU have not come
+    // together, then four, so that a panel's ranges are searched for less
+    // often.  Whole products, one and four tokens a workgroup: 1024 x 4096 at
+    // 16 tokens 14.1 and 14.9 us, 4096 x 4096 at 8 tokens 21.0 and 21.6, at 32
+    // 30.3 and 28.7, 14336 x 4096 at 16 tokens 54.2 and 49.0.  (Sixteen tokens
+    // a workgroup: 19.4, 24.3, 31.3 and 50.4.)
+    const uint32_t panels = c.out_features / kPanelRows;
+    const bool one = c.n_tokens == 1 || static_cast<uint64_t>(panels) * c.n_tokens <= 512;
+    const uint32_t each = one ? 1 : 4;
+    const auto pick = [one](auto gated) {
         constexpr bool kGated = decltype(gated)::value;
-        return each == 1   ? reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 1>)
-               : each == 4 ? reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 4>)
-                           : reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 16>);
+        return one ? reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 1>)
+                   : reinterpret_cast<const void *>(&df11_sum_slots_kernel<kGated, 4>);
     };
     return launch_kernel(c.n == 2 ? pick(std::true_type{}) : pick(std::false_type{}),
-                         dim3(c.out_features / kPanelRows, (c.n_tokens + each - 1) / each), dim3(256), params, 0,
+                         dim3(panels, (c.n_tokens + each - 1) / each), dim3(256), params, 0,
                          stream, nullptr, nullptr);
 }
 
