@@ -426,7 +426,7 @@ int forward(Call &c, const df11_epilogue *e, void *workspace, uint64_t workspace
 // kSlopeBlocks blocks, between one and eight a wave, but at most
 // kSlopeMaxChunks partial rows of a bias gradient.  (777 tokens of 1024
 // features: 780 blocks of 4 tokens 5.7 us, 100 of 32 tokens 16.6.  1024
-// tokens of 14336 gated, 294 MB: 44 us, 6.7 TB/s with part of it cached.)
+// tokens of 14336 gated move 206 MB: 44 us, 4.7 TB/s.)
 constexpr uint32_t kSlopeBlocks = 1024, kSlopeMaxChunks = 256;
 
 uint32_t slope_chunk(uint32_t tokens, uint32_t rows) {
