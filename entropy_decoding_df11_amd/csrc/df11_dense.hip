@@ -488,19 +488,20 @@ struct DensePlan {
     uint32_t splits;
 };
 
-// Picks the plan with the least time, by times in microseconds measured on
-// 256 CUs (products of 128 to 4096 tokens, 1024 to 14336 features): a round
-// of large tiles takes 12 and, a step, 1.75 with every CU busy, 1.25 with
-// half of them (backward 2.15 and 1.65); a round of small tiles 9 and, a
-// step, 1.15 with two workgroups a CU, 0.6 with one (backward 1.2 and
-// 0.93); a split writes and reads its partial sums at 4 TB/s and takes 4 for
-// the second kernel.
+// Picks the plan with the least time, by times in microseconds on 256 CUs
+// fitted to 2400 products (33 to 2048 tokens, 640 to 14336 features, both
+// kinds of tile in 1 to 32 splits): a round of small tiles takes 2.7 and, a
+// step, 0.94 with two workgroups a CU and 0.72 with one (backward 4.4, 1.12
+// and 0.97), a round of large tiles 4.5 and, a step, 1.25 (backward 6, and 1.9
+// or, half of the CUs busy, 1.7); a split writes and reads its partial sums at
+// 6 TB/s, much of it cached, and takes 1.5 for the second kernel.  The plan
+// taken so is on average 2% slower than the best one tried (backward 1%).
 DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols, int cus) {
     const bool back = mode == kDenseBack;
     const uint64_t n_out = back ? cols : rows, mats = mode == kDenseGated ? 2 : 1, room = static_cast<uint64_t>(cus);
     const uint32_t k_steps = back ? n * (rows / kStep) : (cols + kStep - 1) / kStep;
-    const double large_full = back ? 2.15 : 1.75, large_half = back ? 1.65 : 1.25;
-    const double small_full = back ? 1.2 : 1.15, small_half = back ? 0.93 : 0.6;
+    const double large = back ? 6.0 : 4.5, large_full = back ? 1.9 : 1.25, large_half = back ? 1.7 : 1.25;
+    const double small = back ? 4.4 : 2.7, small_full = back ? 1.12 : 0.94, small_half = back ? 0.97 : 0.72;
     const auto tiles = [&](uint64_t edge, uint64_t outs) {
         return (tokens + edge - 1) / edge * ((outs * mats + edge - 1) / edge);
     };
@@ -520,17 +521,17 @@ DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows,
     };
     for (uint32_t splits = 1; splits <= 32 && splits <= k_steps; splits *= 2) {
         const double steps = (k_steps + splits - 1) / splits;
-        const double sum = splits > 1 ? 4.0 + 8.0 * splits * mats * tokens * n_out / 4e6 : 0.0;
-        consider(sum + time(tiles(128, n_out) * splits, 2 * room, 9.0, small_full, small_half, steps), {0, splits});
-        consider(sum + time(tiles(256, n_out) * splits, room, 12.0, large_full, large_half, steps),
+        const double sum = splits > 1 ? 1.5 + 8.0 * splits * mats * tokens * n_out / 6e6 : 0.0;
+        consider(sum + time(tiles(128, n_out) * splits, 2 * room, small, small_full, small_half, steps), {0, splits});
+        consider(sum + time(tiles(256, n_out) * splits, room, large, large_full, large_half, steps),
                  {static_cast<uint32_t>(n_out), splits});
     }
     // Whole rounds of large tiles, the rest small.
     const uint64_t m_tiles = (tokens + 255ull) / 256, outs = 256 / mats, n_tiles = (n_out + outs - 1) / outs;
     const uint64_t whole = m_tiles * n_tiles / room * room / m_tiles;
     if (whole && whole < n_tiles)
-        consider(time(whole * m_tiles, room, 12.0, large_full, large_half, k_steps) +
-                     time(tiles(128, n_out - whole * outs), 2 * room, 9.0, small_full, small_half, k_steps),
+        consider(time(whole * m_tiles, room, large, large_full, large_half, k_steps) +
+                     time(tiles(128, n_out - whole * outs), 2 * room, small, small_full, small_half, k_steps),
                  {static_cast<uint32_t>(whole * outs), 1});
     return best;
 }
