@@ -461,12 +461,18 @@ struct SplitRows {
             float z[2][8], b0[8], b1[8];
             for (uint32_t m = 0; m < kMats; ++m) {
                 const float *p = a.partial + m * plane + static_cast<uint64_t>(token) * a.n_out + col;
-                load8(p, z[m]);
-                for (uint32_t s = 1; s < a.splits; ++s) {
-                    float more[8];
-                    load8(p + s * kMats * plane, more);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[m][e] += more[e];
+                for (int e = 0; e < 8; ++e) z[m][e] = 0.0f;
+                // (four splits' loads in flight; past the last one again, not added)
+                for (uint32_t s = 0; s < a.splits; s += 4u) {
+                    float more[4][8];
+#pragma unroll
+                    for (uint32_t k = 0; k < 4u; ++k) load8(p + min(s + k, a.splits - 1u) * kMats * plane, more[k]);
+#pragma unroll
+                    for (uint32_t k = 0; k < 4u; ++k)
+                        if (s + k < a.splits)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) z[m][e] += more[k][e];
                 }
             }
             load_biases<MODE>(a, col, b0, b1);
@@ -493,9 +499,10 @@ struct DensePlan {
 // kinds of tile in 1 to 32 splits): a round of small tiles takes 2.7 and, a
 // step, 0.94 with two workgroups a CU and 0.72 with one (backward 4.4, 1.12
 // and 0.97), a round of large tiles 4.5 and, a step, 1.25 (backward 6, and 1.9
-// or, half of the CUs busy, 1.7); a split writes and reads its partial sums at
-// 6 TB/s, much of it cached, and takes 1.5 for the second kernel.  The plan
-// taken so is on average 2% slower than the best one tried (backward 1%).
+// or, half of the CUs busy, 1.7); a split product writes and reads its partial
+// sums at 6 TB/s, much of it cached, and takes 1.5 and 0.2 a split for the
+// second kernel.  The plan taken so is on average 0.4% slower than the best
+// one tried (backward 0.2%), 5% at most.
 DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols, int cus) {
     const bool back = mode == kDenseBack;
     const uint64_t n_out = back ? cols : rows, mats = mode == kDenseGated ? 2 : 1, room = static_cast<uint64_t>(cus);
@@ -521,7 +528,7 @@ DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows,
     };
     for (uint32_t splits = 1; splits <= 32 && splits <= k_steps; splits *= 2) {
         const double steps = (k_steps + splits - 1) / splits;
-        const double sum = splits > 1 ? 1.5 + 8.0 * splits * mats * tokens * n_out / 6e6 : 0.0;
+        const double sum = splits > 1 ? 1.5 + 0.2 * splits + 8.0 * splits * mats * tokens * n_out / 6e6 : 0.0;
         consider(sum + time(tiles(128, n_out) * splits, 2 * room, small, small_full, small_half, steps), {0, splits});
         consider(sum + time(tiles(256, n_out) * splits, room, large, large_full, large_half, steps),
                  {static_cast<uint32_t>(n_out), splits});
