@@ -286,7 +286,7 @@ def _launch_product(dev, ws, x, biases, act, residual, out, out_dtype, keep):
     first, second = ws[0]._stream_struct, ws[1]._stream_struct if len(ws) == 2 else None
     nbytes = lib.df11_epilogue_workspace(first, second, tokens)
     work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    # (only a decode uses the weights' work counters)
+    # (only a decode uses the weights' work counters, and none that is captured)
     handle = _stream(dev) if tokens <= _lib.EPILOGUE_FUSED_TOKENS else _claim(ws, dev)
     if second is None:
         status = lib.df11_matmul_epilogue(first, x_ptr, xs, tokens, in_f, out_f, e, work.data_ptr(), nbytes, handle)

@@ -554,7 +554,7 @@ int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uin
  *                    exactly on residual (same address, stride and type)
  *   pre              device, n_tokens x out_features floats each, row-major,
  *                    16-byte aligned: receive z + bias (both or neither for a gated product),
- *                    for df11_matmul_grad; or NULL
+ *                    for df11_matmul_epilogue_grad; or NULL
  *   activation       one of DF11_ACT_*
  * Types are DF11_BF16 or DF11_FP32.  Everything up to out is float; out is
  * rounded once. */
@@ -592,8 +592,10 @@ uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_
  * zero does not hide it).  Up to DF11_EPILOGUE_FUSED_TOKENS tokens the decode
  * is fused into the product; beyond, the stream is decoded into the workspace,
  * which uses its schedule counters like df11_decompress: such calls that share
- * a stream's counters must not overlap in time.  With no tokens or
- * no outputs nothing is launched.  Errors: DF11_E_INVALID_ARG,
+ * a stream's counters must not overlap in time.  Calls captured into a graph
+ * use no counters, so that replays may overlap any other call (but not another
+ * replay of the same graph, which has the same outputs).  With no tokens or no
+ * outputs nothing is launched.  Errors: DF11_E_INVALID_ARG,
  * DF11_E_BAD_STREAM, DF11_E_TOO_LARGE (n_tokens * features >= 2^32),
  * DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
 int df11_matmul_epilogue(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t n_tokens,

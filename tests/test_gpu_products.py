@@ -513,3 +513,39 @@ def test_gradients_of_shared_and_broadcast_inputs(torch_cuda, tokens):
     p, = torch.autograd.grad(df11.matmul_epilogue(w, x), x, dy.bfloat16())
     off = float((s.double() - p.double() - dy.bfloat16().double()).norm() / s.double().norm())
     assert off <= 2.0 ** -7
+
+
+def test_replays_on_two_streams_at_once(torch_cuda):
+    """Two graphs of the same weights, forward and backward, and eager calls,
+    on three streams without a wait between."""
+    torch = torch_cuda
+    _note("graphs on two streams")
+    w, _ = _weight(4096, 4096)
+    u, _ = _weight(4096, 4096, "normal", 1)
+    dy = _x(torch, 100, 4096, seed=9)
+
+    def step(x):
+        a = x.detach().requires_grad_()
+        y = df11.matmul_epilogue(u, df11.gated_matmul(w, u, a), residual=a)
+        return y.detach(), torch.autograd.grad(y, a, dy)[0]
+
+    xs = [_x(torch, 100, 4096, seed=s) for s in range(3)]
+    want = [step(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    graphs = []
+    for x in xs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = step(x)
+        graphs.append((g, held))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            last = step(xs[2])
+    torch.cuda.synchronize()
+    for got, expected in zip([held for _, held in graphs] + [last], want):
+        assert all(torch.equal(a, b) for a, b in zip(got, expected))
