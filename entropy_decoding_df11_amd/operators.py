@@ -107,6 +107,8 @@ def _ptr(t) -> Optional[int]:
 
 def _rowwise(t):
     """A gradient that autograd hands over, with rows at one stride."""
+    if t.numel() == 0:
+        return t
     try:
         _rows(t, t.shape[-1], "gradient")
         return t
@@ -302,6 +304,9 @@ def _launch_product_grad(dev, ws, pre, dy, act, x_shape, want_x, biases):
     """(dx or None, the biases' gradients): biases[i] is the type of a bias
     whose gradient is wanted, or None."""
     out_f, in_f = ws[0].shape
+    if out_f == 0:
+        return (torch.zeros(x_shape, dtype=torch.bfloat16, device=dev) if want_x else None,
+                [None if b is None else torch.empty(0, dtype=b, device=dev) for b in biases])
     dy2, dys = _rows(dy, out_f, "dy")
     tokens = dy2.shape[0]
     dx = torch.empty(x_shape, dtype=torch.bfloat16, device=dev) if want_x else None

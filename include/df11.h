@@ -648,7 +648,8 @@ uint64_t df11_epilogue_grad_workspace(const df11_device_stream *w, const df11_de
  * through the frozen compressed weights: the streams are decoded into the
  * workspace.  Sizes, streams, workspace, sums and errors as for the forward
  * calls, and out_features at most 2^22; no output may overlap anything else.
- * With no tokens dbias is zero. */
+ * With no tokens dbias is zero; with no out_features nothing is launched, dx
+ * stays as it is. */
 int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_stream *up, uint32_t n_tokens,
                               uint32_t in_features, uint32_t out_features, const df11_product_grad *g,
                               void *workspace, uint64_t workspace_bytes, void *hip_stream);

@@ -549,3 +549,21 @@ def test_replays_on_two_streams_at_once(torch_cuda):
     torch.cuda.synchronize()
     for got, expected in zip([held for _, held in graphs] + [last], want):
         assert all(torch.equal(a, b) for a, b in zip(got, expected))
+
+
+@pytest.mark.parametrize("shape", [(5, 1024), (2, 40, 1024), (0, 1024)])
+def test_weights_without_outputs(torch_cuda, shape):
+    """A weight of no rows gives no outputs, and a gradient of zero."""
+    torch = torch_cuda
+    _note(f"no outputs {shape}")
+    w = df11.compress(np.zeros(0, np.uint16), shape=(0, 1024), layout="mfma_tiles")
+    b = torch.zeros(0, device="cuda", requires_grad=True)
+    held = torch.full((4, 2, 40, 1024), float("nan"), device="cuda")  # (freed memory is not zero)
+    del held
+    for op in (lambda x: df11.matmul_epilogue(w, x, bias=b, activation="gelu"),
+               lambda x: df11.gated_matmul(w, w, x, gate_bias=b)):
+        x = torch.randn(shape, device="cuda").bfloat16().requires_grad_()
+        y = op(x)
+        assert y.shape == shape[:-1] + (0,)
+        dx, db = torch.autograd.grad(y, (x, b), torch.empty_like(y))
+        assert dx.shape == x.shape and bool((dx == 0).all()) and db.shape == (0,)
