@@ -157,9 +157,11 @@ struct SlopeArgs {
     const void *dy;
     const float *pre[2];
     uint16_t *dz[2];     // BF16, tokens x features; or null
-    float *partial[2];   // [chunk][features]: sums of dz over the chunk's tokens; or null
+    // Sums of dz over a chunk's tokens, or null: [chunk][features] of float,
+    // or with one chunk the bias gradient itself, of sum_dtype.
+    void *sums[2];
     uint64_t dy_stride;
-    uint32_t dy_dtype, dy_vec, act, tokens, features, chunk;
+    uint32_t dy_dtype, sum_dtype, dy_vec, act, tokens, features, chunk;
 };
 
 // A wave takes four columns per lane of every fourth token of the block's
@@ -201,17 +203,17 @@ __global__ __launch_bounds__(256) void df11_slope_kernel(SlopeArgs a) {
             for (int e = 0; e < 4; ++e) sum[m][e] += d[m][e];
         }
     }
-    if (!a.partial[0] && !a.partial[1]) return;
+    if (!a.sums[0] && !a.sums[1]) return;
     for (int m = 0; m < kMats; ++m)
         for (int e = 0; e < 4 && wave; ++e) s_sum[m][wave - 1u][4u * lane + e] = sum[m][e];
     __syncthreads();
     if (wave || col >= a.features) return;
     for (int m = 0; m < kMats; ++m) {
-        if (!a.partial[m]) continue;
+        if (!a.sums[m]) continue;
         for (uint32_t e = 0; e < 4; ++e) {
             float v = sum[m][e];
             for (int w = 0; w < 3; ++w) v += s_sum[m][w][4u * lane + e];
-            a.partial[m][static_cast<uint64_t>(blockIdx.y) * a.features + col + e] = v;
+            store_as(a.sums[m], static_cast<uint64_t>(blockIdx.y) * a.features + col + e, a.sum_dtype, v);
         }
     }
 }
@@ -436,9 +438,13 @@ int forward(Call &c, const df11_epilogue *e, void *workspace, uint64_t workspace
 // kSlopeMaxChunks partial rows of a bias gradient.  (777 tokens of 1024
 // features: 780 blocks of 4 tokens 5.7 us, 100 of 32 tokens 16.6.  1024
 // tokens of 14336 gated move 206 MB: 44 us, 4.7 TB/s.)
-constexpr uint32_t kSlopeBlocks = 1024, kSlopeMaxChunks = 256;
+// Up to kSlopeOneChunk tokens are one chunk, which needs no kernel to add the
+// chunks, at 1.1 us for every four tokens of it (the bias gradient of 4096
+// features: 8 tokens 4.5 us, 9 tokens in three chunks 5.4, 16 in one 6.8).
+constexpr uint32_t kSlopeBlocks = 1024, kSlopeMaxChunks = 256, kSlopeOneChunk = 8;
 
 uint32_t slope_chunk(uint32_t tokens, uint32_t rows) {
+    if (tokens <= kSlopeOneChunk) return tokens;
     const uint64_t strips = (rows + 255) / 256;
     const uint32_t want = static_cast<uint32_t>(std::min<uint64_t>(32, tokens * strips / kSlopeBlocks));
     return std::max((std::max(want, 1u) + 3) / 4 * 4, (tokens + kSlopeMaxChunks - 1) / kSlopeMaxChunks);
@@ -462,7 +468,7 @@ bool grad_plan(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens,
         p.dz[i] = at;
         if (i < n && g.dx && p.own_dz) at += round_up(2ull * tokens * rows, 256);
         p.partial[i] = at;
-        if (i < n && g.dbias[i]) at += round_up(4ull * p.chunks * rows, 256);
+        if (i < n && g.dbias[i] && p.chunks > 1) at += round_up(4ull * p.chunks * rows, 256);
     }
     p.weights = at;
     if (g.dx) at += decoded_bytes(ws, n);
@@ -553,10 +559,11 @@ int backward(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens, u
     for (uint32_t i = 0; i < n; ++i) {
         a.pre[i] = needs_pre ? g->pre[i] : nullptr;
         if (g->dx && p.own_dz) a.dz[i] = reinterpret_cast<uint16_t *>(base + p.dz[i]);
-        if (g->dbias[i]) a.partial[i] = reinterpret_cast<float *>(base + p.partial[i]);
+        if (g->dbias[i]) a.sums[i] = p.chunks > 1 ? base + p.partial[i] : g->dbias[i];
     }
+    a.sum_dtype = p.chunks > 1 ? static_cast<uint32_t>(DF11_FP32) : g->bias_dtype;
     (void)hipGetLastError();
-    if (a.dz[0] || a.partial[0] || a.partial[1]) {
+    if (a.dz[0] || a.sums[0] || a.sums[1]) {
         void *params[] = {&a};
         rc = launch_kernel(n == 2 ? reinterpret_cast<const void *>(&df11_slope_kernel<true>)
                                   : reinterpret_cast<const void *>(&df11_slope_kernel<false>),
@@ -564,8 +571,8 @@ int backward(const df11_device_stream *const *ws, uint32_t n, uint32_t tokens, u
         if (rc) return rc;
     }
     for (uint32_t i = 0; i < n; ++i) {
-        if (!g->dbias[i]) continue;
-        rc = df11::column_sums(a.partial[i], p.chunks, rows, g->dbias[i], g->bias_dtype, stream);
+        if (!g->dbias[i] || p.chunks == 1) continue;
+        rc = df11::column_sums(static_cast<const float *>(a.sums[i]), p.chunks, rows, g->dbias[i], g->bias_dtype, stream);
         if (rc) return rc;
     }
     if (!g->dx) return DF11_OK;
