@@ -32,7 +32,9 @@
 // fifth of the CUs busy a step of 256 x 256 takes 1.2 us against 0.85 of
 // MFMAs.  128 x 128 tiles (two workgroups a CU, a quarter more LDS traffic a
 // MFMA) take 505 us on that product and win where 256 x 256 leave CUs idle
-// (2048 tokens, 4096 -> 4096: 64 against 92 us).
+// (2048 tokens, 4096 -> 4096: 64 against 92 us).  Tiles between the two, 128 x
+// 256 or 256 x 128 in four waves, win nowhere (the same product 10 and 14 us
+// more than 128 x 128): one wave a SIMD waits for its LDS reads.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
