@@ -19,7 +19,8 @@
 // ds_read_b64_tr_b16 gathers from 4 rows x 16 columns at a time.
 //
 // Rows past the last token and outputs past the last row of W lie past the
-// end of their buffer resource, whose loads give zero.
+// end of their buffer resource by the lane's own offset, and are not read
+// (df11_dense_tiles.h); what their places in LDS hold reaches no output.
 //
 // What bounds it: on a full chip, power.  4096 tokens, 14336 -> 4096 take
 // 415 us (1.16 PFLOP/s) on random operands and 295 us (1.63 PFLOP/s) on
@@ -43,6 +44,7 @@
 
 #include "df11.h"
 #include "df11_dense.h"
+#include "df11_dense_tiles.h"
 #include "df11_device.h"
 
 namespace {
@@ -58,7 +60,7 @@ typedef short shortx4 __attribute__((ext_vector_type(4)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 using Resource = __amdgpu_buffer_rsrc_t;
 
-constexpr uint32_t kStep = 64;  // K elements of one step
+constexpr uint32_t kStep = df11::kDenseStep;
 // Token tiles that follow each other before the next output tile: an XCD's 32
 // (or 64) tiles at a time then read fewest distinct rows and columns.  8192
 // tokens, 4096 -> 4096: 227 us against 241 without bands (128 x 128 tiles 263
@@ -82,15 +84,16 @@ struct DenseArgs {
     Epilogue e;
 };
 
-// A buffer resource over `bytes` bytes from p (loads past them give zero).
-__device__ __forceinline__ Resource resource(const void *p, uint64_t bytes) {
-    const uint32_t n = bytes > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, n, 0x00020000);
+// A buffer resource over a window of the operand at p (nothing past it is read).
+__device__ __forceinline__ Resource resource(const uint16_t *p, df11::DenseWindow w) {
+    const uint32_t n = w.bytes > 0xFFFFFFFFull ? 0xFFFFFFFFu : static_cast<uint32_t>(w.bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + w.at / 2u), 0, n, 0x00020000);
 }
 
-// 16 bytes a lane from r, lane_at + at, to the wave-uniform LDS address dst + 16 lane.
-__device__ __forceinline__ void load_to_lds(Resource r, uint8_t *dst, uint32_t lane_at, uint32_t at) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, lane_at, at, 0, 0);
+// 16 bytes a lane from r, lane_at bytes on, to the wave-uniform LDS address
+// dst + 16 lane.  (No scalar offset: df11_dense_tiles.h.)
+__device__ __forceinline__ void load_to_lds(Resource r, uint8_t *dst, uint32_t lane_at) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, lane_at, 0, 0, 0);
 }
 
 // Four rows x 16 columns of 2-byte elements, transposed across a quarter
@@ -320,33 +323,28 @@ void df11_dense_kernel(DenseArgs a) {
 
     const uint32_t rows_here = min(static_cast<uint32_t>(BM), a.tokens - m0);
     const uint32_t k_len = MODE == kDenseBack ? a.panels * 64u : a.tile_ks * 32u;
-    const uint64_t left_span = ((rows_here - 1u) * a.left_stride + k_len) * 2u;
-    // A load takes eight rows of 128 bytes: this lane's row and chunk.
-    const uint32_t left_at = (lane >> 3) * static_cast<uint32_t>(a.left_stride) * 2u +
-                             16u * ((lane & 7u) ^ (lane >> 3));
-    const uint32_t eight_rows = 16u * static_cast<uint32_t>(a.left_stride);
+    const uint32_t stride = static_cast<uint32_t>(a.left_stride);
+    const uint32_t left_at = df11::dense_left_lane(lane, stride);
 
     // Sends for one step.  (Forward, an odd last k-step: the upper half of
     // the step holds whatever follows, and its products are left out.)
     auto issue = [&](uint32_t step, uint8_t *stage) {
         const uint32_t one = MODE == kDenseBack && step >= a.k_steps_one ? 1u : 0u;
         const uint32_t ks = step - one * a.k_steps_one;  // step of this matrix
-        const Resource left = resource(a.left[one] + m0 * a.left_stride, left_span);
+        const Resource left = resource(a.left[one], df11::dense_left_window(m0, rows_here, a.left_stride, k_len, ks));
 #pragma unroll
         for (int i = 0; i < kLeftLoads; ++i)
-            load_to_lds(left, stage + 1024u * (wave + W * i), left_at, 128u * ks + (wave + W * i) * eight_rows);
+            load_to_lds(left, stage + 1024u * (wave + W * i), left_at + df11::dense_left_group(wave + W * i, stride));
         stage += kLeftBytes;
         if constexpr (MODE == kDenseBack) {
-            // panel ks, its k-steps from output n0 on: four blocks each
-            const uint64_t at = (n0 / 32u) * 4096ull;
-            const Resource w = resource(a.w[one] + (ks * panel_bytes + at) / 2u, panel_bytes - at);
+            const Resource w = resource(a.w[one], df11::dense_back_window(n0, ks, panel_bytes));
 #pragma unroll
             for (int i = 0; i < kRightLoads; ++i)
-                load_to_lds(w, stage + 1024u * (wave + W * i), 16u * lane, 1024u * (wave + W * i));
+                load_to_lds(w, stage + 1024u * (wave + W * i), 16u * lane + df11::dense_back_block(wave + W * i));
         } else {
-            const uint64_t at = (n0 / 64u) * panel_bytes + 8192ull * ks, n = a.panels * panel_bytes - at;
-            const Resource w0 = resource(a.w[0] + at / 2u, n);
-            const Resource w1 = MODE == kDenseGated ? resource(a.w[1] + at / 2u, n) : w0;
+            const df11::DenseWindow window = df11::dense_right_window(n0, ks, a.panels, panel_bytes);
+            const Resource w0 = resource(a.w[0], window);
+            const Resource w1 = MODE == kDenseGated ? resource(a.w[1], window) : w0;
 #pragma unroll
             for (int i = 0; i < kRightLoads; ++i) {
                 const uint32_t b = wave + W * i, half = b / (BN / 16u), nb = b % (BN / 16u);
@@ -356,8 +354,8 @@ void df11_dense_kernel(DenseArgs a) {
                 const uint32_t r16 = MODE == kDenseGated
                                          ? (n0 & 63u) / 16u + (nb / TN) * (TN / 2) + nb % (TN / 2)
                                          : nb;
-                load_to_lds(second ? w1 : w0, stage + 1024u * b, 16u * lane,
-                            (r16 / 4u) * static_cast<uint32_t>(panel_bytes) + half * 4096u + (r16 & 3u) * 1024u);
+                load_to_lds(second ? w1 : w0, stage + 1024u * b,
+                            16u * lane + df11::dense_right_block(r16, half, static_cast<uint32_t>(panel_bytes)));
             }
         }
     };
