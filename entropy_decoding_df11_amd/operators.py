@@ -15,7 +15,8 @@ As in df11.py every step runs in libdf11.so on torch's current stream, or on
 the stream given; this module checks and passes arguments.  A call at one
 token is a few microseconds on the GPU, so what runs on every call is kept
 short here: the stream's handle is asked for without making a Stream object,
-and shapes are checked once, in the forward call.
+and shapes are checked once, in the forward call.  Calls of one weight may
+overlap, on any streams and from any threads.
 """
 
 from __future__ import annotations
@@ -88,17 +89,6 @@ def _run(dev, stream, launch, *args):
 def _stream(dev) -> int:
     """Handle of torch's current stream on dev."""
     return torch._C._cuda_getCurrentRawStream(dev.index)
-
-
-def _claim(ws, dev) -> int:
-    """The current stream's handle, ordered after the weights' launches on
-    other streams (DF11Tensor._claim)."""
-    handle = _stream(dev)
-    for w in ws:
-        last = w._last_stream
-        if last is None or last.cuda_stream != handle:
-            w._claim(None)
-    return handle
 
 
 def _ptr(t) -> Optional[int]:
@@ -288,13 +278,13 @@ def _launch_product(dev, ws, x, biases, act, residual, out, out_dtype, keep):
     first, second = ws[0]._stream_struct, ws[1]._stream_struct if len(ws) == 2 else None
     nbytes = lib.df11_epilogue_workspace(first, second, tokens)
     work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    # (only a decode uses the weights' work counters, and none that is captured)
-    handle = _stream(dev) if tokens <= _lib.EPILOGUE_FUSED_TOKENS else _claim(ws, dev)
+    # (no product uses the weights' work counters: nothing to order it after)
     if second is None:
-        status = lib.df11_matmul_epilogue(first, x_ptr, xs, tokens, in_f, out_f, e, work.data_ptr(), nbytes, handle)
+        status = lib.df11_matmul_epilogue(first, x_ptr, xs, tokens, in_f, out_f, e, work.data_ptr(), nbytes,
+                                          _stream(dev))
     else:
         status = lib.df11_gated_matmul(first, second, x_ptr, xs, tokens, in_f, out_f, e, work.data_ptr(), nbytes,
-                                       handle)
+                                       _stream(dev))
     if status:
         _lib.check(status, "df11_matmul_epilogue" if second is None else "df11_gated_matmul")
     return out, pre
@@ -324,7 +314,7 @@ def _launch_product_grad(dev, ws, pre, dy, act, x_shape, want_x, biases):
     nbytes = lib.df11_epilogue_grad_workspace(first, second, tokens, g) if tokens else 0
     work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     status = lib.df11_matmul_epilogue_grad(first, second, tokens, in_f, out_f, g, work.data_ptr(), nbytes,
-                                           _claim(ws, dev))
+                                           _stream(dev))
     if status:
         _lib.check(status, "df11_matmul_epilogue_grad")
     return dx, db

@@ -590,12 +590,11 @@ uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_
  * device, not by timing.  A token whose x holds an infinity or a NaN gives
  * infinities or NaN in its own outputs alone (0 * inf included: a weight of
  * zero does not hide it).  Up to DF11_EPILOGUE_FUSED_TOKENS tokens the decode
- * is fused into the product; beyond, the stream is decoded into the workspace,
- * which uses its schedule counters like df11_decompress: such calls that share
- * a stream's counters must not overlap in time.  Calls captured into a graph
- * use no counters, so that replays may overlap any other call (but not another
- * replay of the same graph, which has the same outputs).  With no tokens or no
- * outputs nothing is launched.  Errors: DF11_E_INVALID_ARG,
+ * is fused into the product; beyond, the stream is decoded into the workspace.
+ * A stream's schedule counters are not used: calls of one stream may overlap in
+ * time, on any streams and from any threads, and so may a captured call's
+ * replays (but not two replays of one graph, which have the same outputs).
+ * With no tokens or no outputs nothing is launched.  Errors: DF11_E_INVALID_ARG,
  * DF11_E_BAD_STREAM, DF11_E_TOO_LARGE (n_tokens * features >= 2^32),
  * DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
 int df11_matmul_epilogue(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t n_tokens,

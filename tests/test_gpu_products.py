@@ -567,3 +567,73 @@ def test_weights_without_outputs(torch_cuda, shape):
         assert y.shape == shape[:-1] + (0,)
         dx, db = torch.autograd.grad(y, (x, b), torch.empty_like(y))
         assert dx.shape == x.shape and bool((dx == 0).all()) and db.shape == (0,)
+
+
+@pytest.mark.parametrize("rows", [4096, 12544])
+@pytest.mark.parametrize("tokens", [4, 40, 300])
+def test_products_leave_the_work_counters_alone(torch_cuda, tokens, rows):
+    """The weights' work counters (those of their dynamic schedule) may be in
+    use by another thread's launch while a product or its backward pass runs:
+    whatever they hold, the result is the same, and they hold it afterwards."""
+    torch = torch_cuda
+    _note(f"work counters {tokens} {rows}")
+    w, _ = _weight(rows, 4096)
+    u, _ = _weight(rows, 4096, "normal", 1)
+    x, dy = _x(torch, tokens, 4096, seed=2), _x(torch, tokens, rows, seed=3)
+
+    def step():
+        a = x.detach().requires_grad_()
+        y = df11.matmul_epilogue(u, a, residual=df11.gated_matmul(w, u, a))
+        return y.detach(), torch.autograd.grad(y, a, dy)[0]
+
+    want = step()
+    counters = [t._schedule for t in (w, u)]
+    assert all(t._stream_struct.schedule == c.data_ptr() and not bool(c.any()) for t, c in zip((w, u), counters))
+    for c in counters:
+        c.fill_(3)
+    got = step()
+    left = [bool((c == 3).all()) for c in counters]
+    for c in counters:
+        c.zero_()
+    assert all(left) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_products_from_threads_at_once(torch_cuda):
+    """The same weights in two threads with a stream each, forward and
+    backward, beside decompressions of them in a third."""
+    torch = torch_cuda
+    import threading
+    _note("threads")
+    w, _ = _weight(12544, 4096)
+    u, _ = _weight(12544, 4096, "normal", 1)
+    xs, dy = [_x(torch, 100, 4096, seed=s) for s in range(2)], _x(torch, 100, 12544, seed=9)
+
+    def step(x):
+        a = x.detach().requires_grad_()
+        y = df11.matmul_epilogue(u, a, residual=df11.gated_matmul(w, u, a))
+        return y.detach(), torch.autograd.grad(y, a, dy)[0]
+
+    want = [step(x) for x in xs]
+    flat = w.decompress()
+    torch.cuda.synchronize()
+    same = [[], [], []]
+
+    def products(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [step(xs[i]) for _ in range(20)]
+            torch.cuda.current_stream().synchronize()
+            same[i] = [torch.equal(a, b) for g in got for a, b in zip(g, want[i])]
+
+    def decodes():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [w.decompress() for _ in range(20)]
+            torch.cuda.current_stream().synchronize()
+            same[2] = [torch.equal(g.view(torch.int16), flat.view(torch.int16)) for g in got]
+
+    threads = [threading.Thread(target=products, args=(i,)) for i in range(2)] + [threading.Thread(target=decodes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [len(s) for s in same] == [40, 40, 20] and all(all(s) for s in same)
