@@ -375,11 +375,17 @@ __global__ void df11_zero_counters_kernel(uint32_t *p) {
     for (uint32_t i = threadIdx.x; i < kCounterWords; i += blockDim.x) p[i] = 0;
 }
 
+// Whether there are two different streams.  (Streams may share a buffer: those
+// of a matrix and of its negative have the same exponents.)
+bool two_streams(const df11_device_stream *const *ws, uint32_t n) {
+    return n == 2 && (ws[1]->enc != ws[0]->enc || ws[1]->sm != ws[0]->sm);
+}
+
 // Bytes of the decoded weights (one copy of a stream given twice) and of the
 // counters of their decode.
 uint64_t decoded_bytes(const df11_device_stream *const *ws, uint32_t n) {
     const uint64_t one = round_up(2 * ws[0]->h.n_elements, 256);
-    if (n == 1 || ws[1]->enc == ws[0]->enc) return one;
+    if (!two_streams(ws, n)) return one;
     return 2 * one + (ws[0]->h.n_elements >= kCounted ? round_up(4 * kCounterWords, 256) : 0);
 }
 
@@ -390,7 +396,7 @@ int decode_weights(const df11_device_stream *const *ws, uint32_t n, void *worksp
     const uint64_t one = round_up(2 * ws[0]->h.n_elements, 256);
     df11_device_stream flat[2];
     uint16_t *to[2];
-    const bool both = n == 2 && ws[1]->enc != ws[0]->enc;
+    const bool both = two_streams(ws, n);
     // (streams without counters of their own ask for the static schedule)
     const bool counted = both && ws[0]->h.n_elements >= kCounted && ws[0]->schedule && ws[1]->schedule;
     uint32_t *counters = counted ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + 2 * one) : nullptr;

@@ -637,3 +637,27 @@ def test_products_from_threads_at_once(torch_cuda):
         t.join()
     torch.cuda.synchronize()
     assert [len(s) for s in same] == [40, 40, 20] and all(all(s) for s in same)
+
+
+@pytest.mark.parametrize("tokens", [3, 40])
+def test_gate_and_up_that_share_a_buffer(torch_cuda, tokens):
+    """up = -gate: the same exponents, so the same encoded stream, beside signs
+    of its own."""
+    torch = torch_cuda
+    _note(f"shared buffer {tokens}")
+    w, w64 = _weight(640, 1056)
+    u = w.clone()
+    u._bufs["sm"] ^= 0x80
+    u._bufs["enc"] = w._bufs["enc"]
+    u._stream_struct.enc = w._bufs["enc"].data_ptr()
+    assert torch.equal(u.decompress().double(), -w64)
+    x = _x(torch, tokens, 1056, seed=4)
+    a = x.clone().requires_grad_()
+    h = df11.gated_matmul(w, u, a, activation="none", out_dtype=torch.float32)
+    _assert_close(h.detach(), *_expected(torch, x, (w64, -w64), (None, None), "none", None, torch.float32))
+    dy = _side(torch, (tokens, 640), torch.float32, 6)
+    dx, = torch.autograd.grad(h, a, dy)
+    z = x.double() @ w64.t()
+    want = -2 * (dy.double() * z) @ w64
+    # (norm-wise: dz rounded to BF16, 2^-8, and dx rounded once more)
+    assert float((dx.double() - want).norm()) <= 2.0 ** -7 * float(want.norm())
