@@ -359,22 +359,29 @@ __global__ __launch_bounds__(block_threads(TPR)) void df11_rms_norm_grad_kernel(
     }
 }
 
+// Most blocks of a launch (a grid's threads are counted in 32 bits); the rows
+// or columns past them are taken in further turns.
+constexpr uint32_t kMaxBlocks = 1u << 20;
+
 // out[c] = sum over the rows of p[row][c], in row order within each of the
 // block's 16 slices of rows, then over the slices.
 __global__ __launch_bounds__(1024) void df11_column_sum_kernel(const float *p, uint32_t rows, uint32_t cols,
                                                                void *out, uint32_t dtype) {
     __shared__ float s_sum[16][kWaveSize];
     const uint32_t lane = threadIdx.x & (kWaveSize - 1), slice = threadIdx.x / kWaveSize;
-    const uint32_t c = blockIdx.x * kWaveSize + lane;
-    float v = 0.0f;
-    if (c < cols)
+    for (uint32_t c0 = blockIdx.x * kWaveSize; c0 < cols; c0 += gridDim.x * kWaveSize) {
+        const uint32_t c = c0 + lane;
+        float v = 0.0f;
+        if (c < cols)
 #pragma unroll 8
-        for (uint32_t r = slice; r < rows; r += 16u) v += p[static_cast<uint64_t>(r) * cols + c];
-    s_sum[slice][lane] = v;
-    __syncthreads();
-    if (slice == 0 && c < cols) {
-        for (uint32_t k = 1; k < 16u; ++k) v += s_sum[k][lane];
-        store_as(out, c, dtype, v);
+            for (uint32_t r = slice; r < rows; r += 16u) v += p[static_cast<uint64_t>(r) * cols + c];
+        s_sum[slice][lane] = v;
+        __syncthreads();
+        if (slice == 0 && c < cols) {
+            for (uint32_t k = 1; k < 16u; ++k) v += s_sum[k][lane];
+            store_as(out, c, dtype, v);
+        }
+        __syncthreads();
     }
 }
 
@@ -456,10 +463,6 @@ uint32_t grad_blocks(uint32_t rows, uint32_t per_block, uint32_t block) {
     return std::max(1u, std::min(kGradThreads / block, (rows + each - 1) / each));
 }
 
-// Most blocks of a launch (a grid's threads are counted in 32 bits); the rows
-// past them are taken in further turns.
-constexpr uint32_t kMaxBlocks = 1u << 20;
-
 constexpr uint64_t kMaxRowElements = 1ull << 40;  // keeps row * stride * bytes within 64 bits
 
 }  // namespace
@@ -469,7 +472,8 @@ namespace df11 {
 int column_sums(const float *p, uint32_t rows, uint32_t cols, void *out, uint32_t dtype, hipStream_t stream) {
     void *params[] = {&p, &rows, &cols, &out, &dtype};
     return launch_kernel(reinterpret_cast<const void *>(&df11_column_sum_kernel),
-                         dim3((cols + kWaveSize - 1) / kWaveSize), dim3(1024), params, 0, stream, nullptr, nullptr);
+                         dim3(std::min(kMaxBlocks, (cols + kWaveSize - 1) / kWaveSize)), dim3(1024), params, 0, stream,
+                         nullptr, nullptr);
 }
 
 }  // namespace df11

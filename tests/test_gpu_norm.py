@@ -277,3 +277,25 @@ def test_norm_weight_gradient_over_many_rows(torch_cuda, rows, cols):
         # each product rounded and added at most once per row, rstd's own error
         bound = _half_step(torch, torch.float32, t.sum(0)) + 1.01 * U * t.abs().sum(0) * (rows + _depth(cols) / 2 + 8)
         assert bool(((dw.double() - t.sum(0)).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("cols", [(1 << 26) + 70, 1 << 28])
+def test_norm_weight_gradient_of_the_widest_rows(torch_cuda, cols):
+    """More columns than one launch has threads for.  x is 1 or -1: a wave's
+    sum of squares is a whole number up to 2^24 and exact, the 16 waves' sum is
+    rounded at most 16 times, so rstd is within 2^-20 of 1, and dweight = dy x
+    rstd rounds to dy x, which is a BF16 number itself."""
+    torch = torch_cuda
+    from entropy_decoding_df11_amd import df11
+    _note(f"norm gradient of {cols} columns")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = (torch.randint(0, 2, (1, cols), device="cuda", generator=g, dtype=torch.int8) * 2 - 1).bfloat16()
+    dy = torch.randn(1, cols, device="cuda", generator=g, dtype=torch.bfloat16)
+    w = torch.ones(cols, device="cuda", dtype=torch.bfloat16).requires_grad_()
+    dw, = torch.autograd.grad(df11.rms_norm(x, weight=w, eps=0.0), w, dy)
+    same = torch.equal(dw, (dy * x)[0])
+    assert same
+    dw0, = torch.autograd.grad(df11.rms_norm(x[:0], weight=w), w, dy[:0])
+    zero = not bool(dw0.any())
+    assert zero
