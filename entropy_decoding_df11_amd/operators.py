@@ -33,6 +33,8 @@ _DTYPES = {}
 _FLOATS = ()
 _Norm = _Product = None
 
+_MAX_ROWS = 1 << 30
+
 
 def _import_torch() -> None:
     global torch, _FLOATS
@@ -114,6 +116,9 @@ def _check_norm(x, weight, residual, out, sum_out):
     if x.dim() == 0 or x.shape[-1] == 0:
         raise ValueError("x must have at least one column")
     code = wcode = _dtype(x, "x")
+    # (the C ABI counts rows and columns in 32 bits)
+    if x.shape[-1] > _MAX_ROWS or x.numel() > _MAX_ROWS * x.shape[-1]:
+        raise ValueError("x must have at most 2^30 rows and 2^30 columns")
     dev = x.device
     for name, t in (("residual", residual), ("out", out), ("sum_out", sum_out)):
         if t is not None:
@@ -186,8 +191,8 @@ def rms_norm(x: "torch.Tensor", weight: Optional["torch.Tensor"] = None,  # noqa
     weight.  With one: (y, s), s = x + residual rounded to x's dtype and y the
     norm of s.
 
-    x: bfloat16, float16 or float32, at least one column, rows at one stride
-    (any stride).  weight: one element per column, of x's dtype or float32
+    x: bfloat16, float16 or float32, 1 to 2^30 columns and up to 2^30 rows at
+    one stride (any stride).  weight: one element per column, of x's dtype or float32
     (None: ones).  residual, out, sum_out: x's shape and dtype; out and
     sum_out may each be x or residual themselves.  The sums are float32; y and
     s are rounded once.  Where an input requires a gradient the outputs carry
@@ -221,6 +226,8 @@ def _check_product(ws, x, biases, activation, residual, out, out_dtype):
         _same_device(dev, "up", ws[1]._bufs["enc"])
     if x.dtype != torch.bfloat16 or x.dim() == 0 or x.shape[-1] != in_f:
         raise ValueError("x must be a bfloat16 (..., in_features) tensor")
+    if x.numel() // in_f * max(in_f, out_f) >= 1 << 32:
+        raise ValueError("tokens times features must be below 2^32")
     _same_device(dev, "x", x)
     act = _lib.ACTIVATIONS.get(activation)
     if act is None:
@@ -339,7 +346,8 @@ def matmul_epilogue(w, x: "torch.Tensor", bias: Optional["torch.Tensor"] = None,
     (df11_matmul_epilogue), for any number of tokens.
 
     w: a DF11Tensor compressed with layout="mfma_tiles"; x: bfloat16 (...,
-    in_features), rows at one stride and 16-byte aligned; bias: bfloat16 or
+    in_features), rows at one stride and 16-byte aligned, tokens times features
+    (in or out) below 2^32; bias: bfloat16 or
     float32, one element per output feature; activation: None, "relu", "silu",
     "gelu" or "gelu_tanh"; residual: bfloat16 or float32 (..., out_features).
     Returns out, bfloat16 unless out or out_dtype says float32; out may be the

@@ -224,3 +224,20 @@ def test_product_grad_refuses_second_parts():
     assert _product_grad(t=1 << 26) == TOO_LARGE
     assert _product_grad(dx=None) == 0  # nothing asked for, nothing launched
     assert _product_grad(t=0, dy=None, dx=None, pre=(None, None)) == 0
+
+
+def test_bindings_refuse_sizes_beyond_32_bits():
+    """Counts that the C ABI takes in 32 bits are refused, not taken modulo 2^32
+    (expanded tensors: their one row is all the memory there is)."""
+    import torch
+    from entropy_decoding_df11_amd import df11
+    for shape in (((1 << 32) + 4, 1), ((1 << 32), 1), (1, (1 << 32) + 4), ((1 << 30) + 1, 1), (1, (1 << 30) + 1)):
+        x = torch.zeros(1, 1, dtype=torch.bfloat16).expand(shape)
+        with pytest.raises(ValueError, match="2\\^30"):
+            df11.rms_norm(x)
+    for tokens in ((1 << 32) + 4, 1 << 26):
+        x = torch.zeros(1, 64, dtype=torch.bfloat16).expand(tokens, 64)
+        with pytest.raises(ValueError, match="2\\^32"):
+            df11.matmul_epilogue(_FakeWeight(), x)
+        with pytest.raises(ValueError, match="2\\^32"):
+            df11.gated_matmul(_FakeWeight(), _FakeWeight(), x)
