@@ -41,8 +41,8 @@ def _import_torch() -> None:
     import torch as module
     _DTYPES.update({module.bfloat16: _lib.BF16, module.float16: _lib.FP16, module.float32: _lib.FP32})
     _FLOATS = (module.bfloat16, module.float32)
-    torch = module
-    _make_functions()
+    _make_functions(module)
+    torch = module  # last: a call of another thread that sees it needs the rest
 
 
 def _dtype(t: "torch.Tensor", what: str) -> int:  # noqa: F821
@@ -373,7 +373,7 @@ def gated_matmul(gate, up, x: "torch.Tensor", gate_bias: Optional["torch.Tensor"
 # Gradients.
 # ---------------------------------------------------------------------------
 
-def _make_functions() -> None:
+def _make_functions(torch) -> None:
     global _Norm, _Product
     from torch.autograd.function import once_differentiable
 

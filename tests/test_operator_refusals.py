@@ -241,3 +241,23 @@ def test_bindings_refuse_sizes_beyond_32_bits():
             df11.matmul_epilogue(_FakeWeight(), x)
         with pytest.raises(ValueError, match="2\\^32"):
             df11.gated_matmul(_FakeWeight(), _FakeWeight(), x)
+
+
+def test_first_call_publishes_torch_last(monkeypatch):
+    """A call that finds the module's torch set relies on everything else the
+    first call fills in, which another thread may still be doing."""
+    from entropy_decoding_df11_amd import operators
+    seen = []
+    make = operators._make_functions
+
+    def watched(*a):
+        make(*a)
+        seen.append(operators.torch)
+
+    monkeypatch.setattr(operators, "torch", None)
+    monkeypatch.setattr(operators, "_make_functions", watched)
+    monkeypatch.setattr(operators, "_Norm", None)
+    monkeypatch.setattr(operators, "_Product", None)
+    operators._import_torch()
+    import torch
+    assert seen == [None] and operators.torch is torch and operators._Norm and operators._Product
