@@ -72,6 +72,16 @@ def _same_device(dev, what: str, t) -> None:
         raise ValueError(f"{what} must be on {dev}, not on {t.device}")
 
 
+def _check_outputs(*outs):
+    """The outputs that the caller gave.  They are written behind autograd's
+    back: none may be part of a graph itself, and each one's version has to be
+    raised afterwards, for the graphs that have kept it."""
+    given = [t for t in outs if t is not None]
+    if given and torch.is_grad_enabled() and any(t.requires_grad for t in given):
+        raise ValueError("an output that is given must not require a gradient")
+    return given
+
+
 def _run(dev, stream, launch, *args):
     """launch(*args) with dev current and, if given, stream: allocations made
     there belong to the stream of the launch."""
@@ -205,7 +215,10 @@ def rms_norm(x: "torch.Tensor", weight: Optional["torch.Tensor"] = None,  # noqa
         if out is not None or sum_out is not None or stream is not None:
             raise ValueError("out, sum_out and stream are for calls without gradients")
         return _Norm.apply(x, weight, residual, eps, code, wcode)
+    given = _check_outputs(out, sum_out)
     y, s, _ = _run(x.device, stream, _launch_norm, x, weight, residual, eps, out, sum_out, False, code, wcode)
+    if given:
+        torch.autograd.graph.increment_version(given)
     return y if residual is None else (y, s)
 
 
@@ -336,7 +349,11 @@ def _product(ws, x, biases, activation, residual, out, out_dtype, stream):
         if out is not None or stream is not None:
             raise ValueError("out and stream are for calls without gradients")
         return _Product.apply(x, residual, biases[0], biases[-1] if len(ws) == 2 else None, ws, act, out_dtype)
-    return _run(dev, stream, _launch_product, ws, x, biases, act, residual, out, out_dtype, False)[0]
+    given = _check_outputs(out)
+    y = _run(dev, stream, _launch_product, ws, x, biases, act, residual, out, out_dtype, False)[0]
+    if given:
+        torch.autograd.graph.increment_version(given)
+    return y
 
 
 def matmul_epilogue(w, x: "torch.Tensor", bias: Optional["torch.Tensor"] = None,  # noqa: F821

@@ -661,3 +661,21 @@ def test_gate_and_up_that_share_a_buffer(torch_cuda, tokens):
     want = -2 * (dy.double() * z) @ w64
     # (norm-wise: dz rounded to BF16, 2^-8, and dx rounded once more)
     assert float((dx.double() - want).norm()) <= 2.0 ** -7 * float(want.norm())
+
+
+def test_outputs_given_are_known_to_autograd(torch_cuda):
+    """A tensor that a graph has kept and an operator then overwrites fails the
+    backward pass, as it does under torch's own operators."""
+    torch = torch_cuda
+    _note("versions")
+    w, _ = _weight(640, 1056)
+    x = torch.randn(3, 1056, device="cuda").bfloat16()
+    r = torch.randn(3, 640, device="cuda").bfloat16()
+    for write in (lambda t: df11.rms_norm(t, out=t), lambda t: df11.rms_norm(t, residual=t.clone(), sum_out=t),
+                  lambda t: df11.matmul_epilogue(w, x, residual=t, out=t),
+                  lambda t: df11.gated_matmul(w, w, x, out=t)):
+        kept = r.clone()
+        y = torch.ones_like(kept).requires_grad_() * kept
+        write(kept)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()

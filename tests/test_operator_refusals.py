@@ -261,3 +261,17 @@ def test_first_call_publishes_torch_last(monkeypatch):
     operators._import_torch()
     import torch
     assert seen == [None] and operators.torch is torch and operators._Norm and operators._Product
+
+
+def test_bindings_refuse_outputs_that_require_a_gradient():
+    import torch
+    from entropy_decoding_df11_amd import df11
+    x, y = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16)
+    for call in (lambda: df11.rms_norm(x, out=x.clone().requires_grad_()),
+                 lambda: df11.rms_norm(x, residual=x, sum_out=x.clone().requires_grad_() * 1),
+                 lambda: df11.matmul_epilogue(_FakeWeight(), x, out=y.clone().requires_grad_()),
+                 lambda: df11.gated_matmul(_FakeWeight(), _FakeWeight(), x, out=y.clone().requires_grad_() * 1)):
+        with pytest.raises(ValueError, match="must not require a gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="on a GPU"):
+            call()
