@@ -12,7 +12,10 @@ and the norm's weight.  (The compressed weights are frozen: they have none.)
     h = gated_matmul(gate, up, x)                 # silu(x Wg^T) * (x Wu^T)
 
 As in df11.py every step runs in libdf11.so on torch's current stream, or on
-the stream given; this module checks and passes arguments.  A call at one
+the stream given; this module checks and passes arguments.  The caller orders
+a stream that it gives after whatever makes the inputs and before whatever
+reads the outputs; the tensors may be freed at once, the weights must stay
+until the stream has run.  A call at one
 token is a few microseconds on the GPU, so what runs on every call is kept
 short here: the stream's handle is asked for without making a Stream object,
 and shapes are checked once, in the forward call.  Calls of one weight may
@@ -84,14 +87,27 @@ def _check_outputs(*outs):
 
 def _run(dev, stream, launch, *args):
     """launch(*args) with dev current and, if given, stream: allocations made
-    there belong to the stream of the launch."""
+    there belong to the stream of the launch.  The caching allocator is told
+    which tensors a given stream uses beside their own, so that one that is
+    freed early is not handed out again while the stream has yet to get to it;
+    and that the caller's stream will read the outputs."""
     if dev.type != "cuda":
         raise ValueError("tensors must be on a GPU")
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream must be on {dev}, not on {stream.device}")
+        caller = torch.cuda.current_stream(dev)
         with torch.cuda.stream(stream):
-            return launch(dev, *args)
+            outs = launch(dev, *args)
+        if stream != caller:
+            for group in (args, *(a for a in args if isinstance(a, tuple))):
+                for t in group:
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(stream)
+            for t in outs:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(caller)
+        return outs
     if dev.index == torch._C._cuda_getDevice():
         return launch(dev, *args)
     with torch.cuda.device(dev):

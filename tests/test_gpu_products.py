@@ -679,3 +679,53 @@ def test_outputs_given_are_known_to_autograd(torch_cuda):
         write(kept)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.sum().backward()
+
+
+def test_inputs_freed_before_their_stream_runs(torch_cuda):
+    """Inputs of a call on a busy stream, freed at once: their memory is not
+    handed out again before the stream has read them, nor an output's while
+    the caller's stream may still read it."""
+    torch = torch_cuda
+    _note("freed inputs")
+    w, _ = _weight(4096, 4096)
+    u, _ = _weight(4096, 4096, "normal", 1)
+    side = torch.cuda.Stream()
+
+    def inputs():
+        return _x(torch, 5000, 4096, seed=1), _x(torch, 5000, 4096, seed=2)
+
+    def once(op):
+        x, r = inputs()
+        want = op(x, r, None)
+        del x, r
+        torch.cuda.synchronize()
+        x, r = inputs()
+        at = {x.data_ptr(), r.data_ptr()}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = op(x, r, side)
+        del x, r
+        fresh = [torch.full((5000, 4096), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+        apart = not at & {t.data_ptr() for t in fresh}
+        torch.cuda.synchronize()
+        same = torch.equal(got, want)
+        assert apart and same
+
+    once(lambda x, r, s: df11.rms_norm(x, residual=r, stream=s)[0])
+    once(lambda x, r, s: df11.matmul_epilogue(w, x, residual=r, stream=s))
+    once(lambda x, r, s: df11.gated_matmul(w, u, x, residual=r, stream=s))
+    x, _ = inputs()
+    side.wait_stream(torch.cuda.current_stream())
+    y = df11.rms_norm(x, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    side.synchronize()
+    torch.cuda._sleep(20_000_000)
+    kept, at = y.clone(), y.data_ptr()
+    del y
+    with torch.cuda.stream(side):
+        fresh = torch.full((5000, 4096), float("nan"), device="cuda", dtype=torch.bfloat16)
+    apart = fresh.data_ptr() != at
+    torch.cuda.synchronize()
+    same = torch.equal(kept, df11.rms_norm(x))
+    assert apart and same
