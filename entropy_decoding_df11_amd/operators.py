@@ -15,11 +15,12 @@ As in df11.py every step runs in libdf11.so on torch's current stream, or on
 the stream given; this module checks and passes arguments.  The caller orders
 a stream that it gives after whatever makes the inputs and before whatever
 reads the outputs; the tensors may be freed at once, the weights must stay
-until the stream has run.  A call at one
-token is a few microseconds on the GPU, so what runs on every call is kept
-short here: the stream's handle is asked for without making a Stream object,
-and shapes are checked once, in the forward call.  Calls of one weight may
-overlap, on any streams and from any threads.
+until the stream has run.  Calls of one weight may overlap, on any streams and
+from any threads.
+
+A call at one token is a few microseconds on the GPU, so what runs on every
+call is kept short here: the stream's handle is asked for without making a
+Stream object, and shapes are checked once, in the forward call.
 """
 
 from __future__ import annotations

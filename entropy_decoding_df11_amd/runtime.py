@@ -136,24 +136,29 @@ FUSED_MAX_TOKENS_ROWS = 8
 
 
 def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5):
-    """block_forward through the operators around the products, for any number
-    of tokens: rms_norm, q, k and v (one matmul_batch up to
+    """block_forward through the operators around the products, for x of any
+    leading dimensions: rms_norm, q, k and v (one matmul_batch up to
     FUSED_MAX_TOKENS_TILES tokens, else and under autograd matmul_epilogue),
     o and down with the residual in their epilogue (matmul_epilogue), gate and
     up as one gated product (gated_matmul).  blk holds one DF11 stream per
     weight in MFMA tile order (compress_block(..., codebook="per_weight",
     layout="mfma_tiles")).  Every operator computes in float32 and rounds its
-    output once.  Differentiable with respect to x (the weights are frozen)."""
+    output once.  matmul_batch adds with float atomics and uses the weights'
+    work counters: with it the last bits may differ from call to call, and
+    calls on one block must not overlap; the other operators repeat theirs and
+    may.  Differentiable with respect to x (the weights are frozen)."""
     import torch
     from .df11 import matmul_batch
 
     w = {nm: t for (nm, _, _), t in zip(blk.views, blk.tensors)}
     qkv = [w[nm] for nm in ("q_proj", "k_proj", "v_proj")]
     h = rms_norm(x, eps=eps)
-    if x.shape[0] > FUSED_MAX_TOKENS_TILES or (torch.is_grad_enabled() and x.requires_grad):
+    tokens = x.numel() // x.shape[-1]
+    if not 0 < tokens <= FUSED_MAX_TOKENS_TILES or (torch.is_grad_enabled() and x.requires_grad):
         q, k, v = (matmul_epilogue(t, h) for t in qkv)
     else:
-        q, k, v = (y.to(x.dtype) for y in matmul_batch(qkv, [h] * 3))
+        q, k, v = (y.to(x.dtype).view(*x.shape[:-1], -1)
+                   for y in matmul_batch(qkv, [h.view(tokens, x.shape[-1])] * 3))
     a = q + (k * v).repeat_interleave(q.shape[-1] // k.shape[-1], dim=-1)
     x = matmul_epilogue(w["o_proj"], a, residual=x)
     h = gated_matmul(w["gate_proj"], w["up_proj"], rms_norm(x, eps=eps))

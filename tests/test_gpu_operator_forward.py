@@ -8,6 +8,7 @@ at most as large relative to the output's largest magnitude.  Ten of them
 add to 10 * 2^-8 = 4% of it at most; the test allows 2%, as the fused forward's
 test does against the resident weights (which rounds as often)."""
 
+import math
 import sys
 
 import numpy as np
@@ -119,3 +120,16 @@ def test_operator_forward_replays(torch_cuda, block, tokens):
         if tokens > 64:  # (the q, k, v product of fewer tokens adds with atomics)
             same = torch.equal(got, runtime.operator_model_forward(x, blocks))
             assert same
+
+
+@pytest.mark.parametrize("tokens", [(2, 3), (2, 40), (3, 30), (70, 1), (5, 0), ()])
+def test_operator_forward_of_any_leading_dimensions(torch_cuda, block, tokens):
+    torch = torch_cuda
+    from entropy_decoding_df11_amd import runtime
+    _note(f"operator forward {tokens}")
+    blk, resident = block
+    x = _x(torch, math.prod(tokens), 3).view(*tokens, 1024)
+    got = runtime.operator_block_forward(x, blk)
+    assert got.shape == x.shape and got.dtype == x.dtype
+    if x.numel():
+        _close(got.view(-1, 1024), _forward64(torch, x.view(-1, 1024), resident), 0.02)
