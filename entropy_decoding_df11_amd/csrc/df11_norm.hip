@@ -463,7 +463,9 @@ uint32_t grad_blocks(uint32_t rows, uint32_t per_block, uint32_t block) {
     return std::max(1u, std::min(kGradThreads / block, (rows + each - 1) / each));
 }
 
-constexpr uint64_t kMaxRowElements = 1ull << 40;  // keeps row * stride * bytes within 64 bits
+// Whether the last row begins within 2^58 elements, so that its bytes and the
+// extents that the overlap checks compare stay within 64 bits.
+bool rows_fit(uint32_t rows, uint64_t stride) { return rows <= 1 || stride <= (1ull << 58) / (rows - 1ull); }
 
 }  // namespace
 
@@ -493,7 +495,7 @@ int df11_rms_norm(const void *x, uint64_t x_stride, const void *residual, uint64
     const uint64_t strides[] = {x_stride, residual_stride, sum_stride, y_stride};
     for (int i = 0; i < 4; ++i) {
         if (!ptrs[i]) continue;
-        if (!aligned(ptrs[i], bytes) || strides[i] > kMaxRowElements) return DF11_E_INVALID_ARG;
+        if (!aligned(ptrs[i], bytes) || !rows_fit(rows, strides[i])) return DF11_E_INVALID_ARG;
         // inputs may repeat a row (stride 0) or overlap themselves; outputs may not
         if (i >= 2 && strides[i] < cols && rows > 1) return DF11_E_INVALID_ARG;
     }
@@ -553,7 +555,7 @@ int df11_rms_norm_grad(const void *s, uint64_t s_stride, const void *weight, uin
     const void *ptrs[] = {s, dy, dsum, dx};
     const uint64_t strides[] = {s_stride, dy_stride, dsum_stride, dx_stride};
     for (int i = 0; i < 4 && rows; ++i)
-        if (ptrs[i] && (!aligned(ptrs[i], bytes) || strides[i] > kMaxRowElements)) return DF11_E_INVALID_ARG;
+        if (ptrs[i] && (!aligned(ptrs[i], bytes) || !rows_fit(rows, strides[i]))) return DF11_E_INVALID_ARG;
     if (rows > 1 && dx_stride < cols) return DF11_E_INVALID_ARG;
     const uint64_t need = dweight ? df11_rms_norm_grad_workspace(rows, cols) : 0;
     if (need && (!workspace || !aligned(workspace, 16))) return DF11_E_INVALID_ARG;

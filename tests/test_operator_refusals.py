@@ -275,3 +275,21 @@ def test_bindings_refuse_outputs_that_require_a_gradient():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="on a GPU"):
             call()
+
+
+# (a last row ends 2^65 bytes on: the extent of a tensor in 64 bits, 128 here, hides what it overlaps)
+@pytest.mark.parametrize("bad", [
+    dict(rows=(1 << 24) + 1, xs=1 << 40, y=A + 0x1000, ys=64),
+    dict(rows=(1 << 24) + 1, ys=1 << 40, y=A - 0x1000, x=A),
+    dict(rows=(1 << 24) + 1, r=C, rs=1 << 40, y=C + 0x1000),
+])
+def test_norm_refuses_strides_past_the_address_space(bad):
+    assert _norm(**bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=(1 << 24) + 1, ss=1 << 40, dx=A + 0x1000), dict(rows=(1 << 24) + 1, dys=1 << 40, dx=C + 0x1000),
+    dict(rows=(1 << 24) + 1, dxs=1 << 40, dx=C - 0x1000), dict(rows=(1 << 24) + 1, ds=E, dss=1 << 40, dx=E + 0x1000),
+])
+def test_norm_grad_refuses_strides_past_the_address_space(bad):
+    assert _grad(**bad) == INVALID
