@@ -729,3 +729,56 @@ def test_inputs_freed_before_their_stream_runs(torch_cuda):
     torch.cuda.synchronize()
     same = torch.equal(kept, df11.rms_norm(x))
     assert apart and same
+
+
+# As test_product_gradients, but for the kink: where z lies within its own
+# error dz of 0 the slope may be that of the other side, an error of |dy| (times
+# the other factor of a gated product) in that element's dz; elsewhere the slope
+# is exact.
+@pytest.mark.parametrize("rows,cols,kind", [(64, 32, "normal"), (192, 96, "normal"), (64, 1024, "stress"),
+                                            (640, 1056, "normal")])
+@pytest.mark.parametrize("tokens", [1, 17, 64, 129, 300])
+def test_relu_gradients(torch_cuda, rows, cols, kind, tokens):
+    torch = torch_cuda
+    _note(f"relu gradient {tokens} x {cols} -> {rows} {kind}")
+    w, w64 = _weight(rows, cols, kind)
+    u, u64 = _weight(rows, cols, kind, 1)
+    x = _x(torch, tokens, cols, seed=tokens)
+    for gated in (False, True):
+        for bdt, odt in ((None, torch.bfloat16), (torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16)):
+            ws = (w64, u64) if gated else (w64,)
+            biases = [None if bdt is None else _side(torch, (rows,), bdt, 3 + i) for i in range(len(ws))]
+            dy = _side(torch, (tokens, rows), odt, 6)
+            leaves = [t.clone().requires_grad_() for t in (x, *biases) if t is not None]
+            bl = leaves[1:] if bdt is not None else [None] * len(ws)
+            if gated:
+                y = df11.gated_matmul(w, u, leaves[0], gate_bias=bl[0], up_bias=bl[1], activation="relu", out_dtype=odt)
+            else:
+                y = df11.matmul_epilogue(w, leaves[0], bias=bl[0], activation="relu", out_dtype=odt)
+            _assert_close(y.detach(), *_expected(torch, x, ws, biases, "relu", None, odt))
+            grads = torch.autograd.grad(y, leaves, dy)
+            zs = [_linear64(x, m, b) for m, b in zip(ws, biases)]
+            z, dz = zs[0]
+            d64, on = dy.double(), (z > 0).double()
+            kink = (z.abs() <= dz).double()
+            if gated:
+                z1, dz1 = zs[1]
+                ds = [d64 * z1 * on, d64 * z.relu()]
+                err = [d64.abs() * (kink * (z1.abs() + dz1) + on * dz1), d64.abs() * (on + kink) * dz]
+            else:
+                ds = [d64 * on]
+                err = [d64.abs() * kink]
+            err = [e + 16 * U * d.abs() for e, d in zip(err, ds)]
+            dx64 = sum(d @ m for d, m in zip(ds, ws))
+            size = sum(d.abs() @ m.abs() for d, m in zip(ds, ws))
+            bound = sum((e + 2.0 ** -8 * (d.abs() + e)) @ m.abs() for d, e, m in zip(ds, err, ws))
+            bound = bound + 1.01 * len(ws) * rows * U * (size + bound)
+            _assert_close(grads[0], dx64, bound + _half_step(torch, torch.bfloat16, dx64.abs() + bound))
+            for i, b in enumerate(biases):
+                if b is not None:
+                    b64 = ds[i].sum(0)
+                    eb = err[i].sum(0) + 1.01 * (tokens + 8) * U * (ds[i].abs().sum(0) + err[i].sum(0))
+                    assert grads[1 + i].dtype == b.dtype
+                    _assert_close(grads[1 + i], b64, eb + _half_step(torch, b.dtype, b64.abs() + eb))
+            # (the kink must not swallow the test: hardly any element lies in it)
+            assert float(kink.mean()) <= 0.01
