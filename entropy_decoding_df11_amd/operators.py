@@ -25,7 +25,6 @@ Stream object, and shapes are checked once, in the forward call.
 
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple, Union
 
 from . import _lib
@@ -81,7 +80,7 @@ def _check_outputs(*outs):
     back: none may be part of a graph itself, and each one's version has to be
     raised afterwards, for the graphs that have kept it."""
     given = [t for t in outs if t is not None]
-    if given and torch.is_grad_enabled() and any(t.requires_grad for t in given):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in given):
         raise ValueError("an output that is given must not require a gradient")
     return given
 
@@ -232,7 +231,7 @@ def rms_norm(x: "torch.Tensor", weight: Optional["torch.Tensor"] = None,  # noqa
         if out is not None or sum_out is not None or stream is not None:
             raise ValueError("out, sum_out and stream are for calls without gradients")
         return _Norm.apply(x, weight, residual, eps, code, wcode)
-    given = _check_outputs(out, sum_out)
+    given = None if out is None and sum_out is None else _check_outputs(out, sum_out)
     y, s, _ = _run(x.device, stream, _launch_norm, x, weight, residual, eps, out, sum_out, False, code, wcode)
     if given:
         torch.autograd.graph.increment_version(given)
@@ -366,7 +365,7 @@ def _product(ws, x, biases, activation, residual, out, out_dtype, stream):
         if out is not None or stream is not None:
             raise ValueError("out and stream are for calls without gradients")
         return _Product.apply(x, residual, biases[0], biases[-1] if len(ws) == 2 else None, ws, act, out_dtype)
-    given = _check_outputs(out)
+    given = None if out is None else _check_outputs(out)
     y = _run(dev, stream, _launch_product, ws, x, biases, act, residual, out, out_dtype, False)[0]
     if given:
         torch.autograd.graph.increment_version(given)
