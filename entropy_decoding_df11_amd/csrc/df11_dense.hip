@@ -22,16 +22,20 @@
 // end of their buffer resource by the lane's own offset, and are not read
 // (df11_dense_tiles.h); what their places in LDS hold reaches no output.
 //
-// What bounds it: on a full chip, power.  4096 tokens, 14336 -> 4096 take
+// What the forms tried on a full chip showed: 4096 tokens, 14336 -> 4096 take
 // 415 us (1.16 PFLOP/s) on random operands and 295 us (1.63 PFLOP/s) on
-// zeros, with the same instructions; the MFMAs alone, without loads or LDS
-// reads, take 264.  So every form tried ends within 3% of the same time:
-// four waves of 128 x 128 with the accumulators pinned by hand (which read a
-// third less from LDS) 411 to 418 us, half-steps of 32 in a ring of four or
-// five buffers 417 and 419, v_mfma_f32_32x32x16_bf16 416.  (Operands of W
-// straight from memory to registers double the L1's traffic: 445.)  With a
-// fifth of the CUs busy a step of 256 x 256 takes 1.2 us against 0.85 of
-// MFMAs.  128 x 128 tiles (two workgroups a CU, a quarter more LDS traffic a
+// zeros, with the same instructions, so the operands' values, and with them
+// the clock that the power allows, decide; the MFMAs alone, without loads or
+// LDS reads, take 264.  Every other form ends within 3% of the same time: four
+// waves of 128 x 128 with the accumulators pinned by hand (which read a third
+// less from LDS) 411 to 418 us, half-steps of 32 in a ring of four or five
+// buffers 417 and 419, v_mfma_f32_32x32x16_bf16 416.  (Operands of W straight
+// from memory to registers double the L1's traffic: 445.)  It is no limit of
+// the card: the library's product of 1999 tokens, 4096 -> 28672 takes 339 us
+// where this one takes 393 to 434 at MFMAs 64% busy.  What is left to look
+// into is the work beside the MFMAs (595 MB read for 218 MB of operands; a
+// quarter of the backward product's LDS reads in conflict).  With a fifth of
+// the CUs busy a step of 256 x 256 takes 1.2 us against 0.85 of MFMAs.  128 x 128 tiles (two workgroups a CU, a quarter more LDS traffic a
 // MFMA) take 505 us on that product and win where 256 x 256 leave CUs idle
 // (2048 tokens, 4096 -> 4096: 64 against 92 us).  Tiles between the two, 128 x
 // 256 or 256 x 128 in four waves, win nowhere (the same product 10 and 14 us
@@ -501,8 +505,13 @@ struct DensePlan {
 // and 0.97), a round of large tiles 4.5 and, a step, 1.25 (backward 6, and 1.9
 // or, half of the CUs busy, 1.7); a split product writes and reads its partial
 // sums at 6 TB/s, much of it cached, and takes 1.5 and 0.2 a split for the
-// second kernel.  The plan taken so is on average 0.4% slower than the best
-// one tried (backward 0.2%), 5% at most.
+// second kernel.  On the products of the fit the plan taken so is on average
+// 0.4% slower than the best one tried (backward 0.2%), 5% at most; the plans
+// of large tiles with a rest of small ones were not among them.  The times
+// rank plans and foretell none: fitted to short runs, they fall short of long
+// products on a full chip, whose steps of large tiles take 1.43 to 1.84 us
+// (4096 tokens, 14336 -> 4096: 285 us here, 415 measured; in small tiles 426
+// and 505), so that there the choice leans to large tiles.
 DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols, int cus) {
     const bool back = mode == kDenseBack;
     const uint64_t n_out = back ? cols : rows, mats = mode == kDenseGated ? 2 : 1, room = static_cast<uint64_t>(cus);

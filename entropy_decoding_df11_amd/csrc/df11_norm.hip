@@ -18,10 +18,11 @@
 // change from call to call.  (The rows' sums of the weight's gradient depend
 // on the number of rows too.)
 //
-// What bounds them is memory.  bf16 with a residual, data not cached: forward
-// 8192 x 4096 (268 MB) 49.6 us, 5.4 TB/s; 64 rows of it 3.1 us; backward with
-// the weight's gradient 8192 x 4096 (268 MB) 53.5 us, 5.0 TB/s; 2048 rows of
-// it 18.7 us and 64 rows 6.4.  A large copy reaches 4.75 TB/s.
+// What bounds them is memory.  bf16 with a residual, kernels' own times on
+// buffers taken in turn (none cached): forward 8192 x 4096 (268 MB) 49.8 us,
+// 5.4 TB/s; 2048 rows of it 15.8 us, 64 rows 4.3; backward with the weight's
+// gradient, the column sums after it added, 44.6 + 4.0 (268 MB, 5.5 TB/s),
+// 16.6 + 4.0 and 8.4 + 3.1.  A large copy reaches 4.7 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -51,8 +52,9 @@ struct NormArgs {
 // Rows are read and written in vectors of 16 bytes, at any alignment of their
 // elements (the card loads and stores unaligned vectors); a row's last vector
 // may be a part of one, `left` being the elements from its first to the end.
-// (8192 x 4095 bf16 forward 85 us, where no row is aligned to more than its
-// elements; one element at a time 183 us.)
+// (8192 x 4095 bf16 forward 85 to 94 us, where no row is aligned to more than
+// its elements and nearly every vector lies across two aligned ones; one
+// element at a time 183 us.)
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 

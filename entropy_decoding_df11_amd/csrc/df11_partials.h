@@ -20,8 +20,8 @@ namespace df11 {
 constexpr uint32_t kPartialGroups = 2;
 // Most tokens of a product into slots: one sweep with two token tiles.  Four
 // tiles leave the decoder half its waves, and decoding once and multiplying
-// the tiles (df11_dense.h) is faster: 14336 -> 4096 at 33 tokens 79 against
-// 154 us, 4096 -> 4096 36 against 56; at 32 tokens 76 against 63, 36 against 32.
+// the tiles (df11_dense.h) is faster: 14336 -> 4096 at 33 tokens 69 against
+// 154 us, 4096 -> 4096 36 against 56; at 32 tokens two tiles take 60 and 29.
 constexpr uint32_t kPartialTokens = DF11_EPILOGUE_FUSED_TOKENS;
 
 // g / d for a global k-step g < 2^21 (2^32 elements of 2048 each) and the d =

@@ -387,7 +387,8 @@ def matmul_epilogue(w, x: "torch.Tensor", bias: Optional["torch.Tensor"] = None,
     residual itself.  Everything before out is float32, and the same call gives
     the same bits again.  Where x, bias or residual require a gradient the
     output carries it (then neither out nor stream may be given): the sums
-    before an activation are kept for it in float32, and w itself is frozen."""
+    before an activation are kept for it in float32, dz is rounded to bfloat16
+    for x's gradient (not for the bias's), and w itself is frozen."""
     return _product((w,), x, (bias,), activation, residual, out, out_dtype, stream)
 
 

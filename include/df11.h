@@ -514,7 +514,8 @@ int df11_matmul_batch(const df11_device_stream *ws, uint32_t n_streams, const ui
  *   rstd       device, rows floats, or NULL; kept for df11_rms_norm_grad
  * sum and y may each lie exactly on x or on residual (same address and
  * stride), but not on each other.  A row with a NaN is NaN throughout; one with
- * an infinity is NaN there and zero elsewhere; other rows are not touched by
+ * an infinity is NaN there and zero elsewhere, and one whose squares pass
+ * float's range (magnitudes of 1e19) is zero; other rows are not touched by
  * either.  Errors: DF11_E_INVALID_ARG (types, sizes, alignment,
  * output rows that overlap, other overlaps), DF11_E_HIP. */
 int df11_rms_norm(const void *x, uint64_t x_stride, const void *residual, uint64_t residual_stride,
@@ -588,8 +589,9 @@ uint64_t df11_epilogue_workspace(const df11_device_stream *w, const df11_device_
  *                 one each
  * Sums are taken in float in an order fixed by the stream, the shapes and the
  * device, not by timing.  A token whose x holds an infinity or a NaN gives
- * infinities or NaN in its own outputs alone (0 * inf included: a weight of
- * zero does not hide it).  Up to DF11_EPILOGUE_FUSED_TOKENS tokens the decode
+ * infinities or NaN in its own sums alone (0 * inf included: a weight of zero
+ * does not hide it, and where two ranges of the stream meet, up to
+ * DF11_EPILOGUE_FUSED_TOKENS tokens, a sum may be NaN for an infinity).  Up to DF11_EPILOGUE_FUSED_TOKENS tokens the decode
  * is fused into the product; beyond, the stream is decoded into the workspace.
  * A stream's schedule counters are not used: calls of one stream may overlap in
  * time, on any streams and from any threads, and so may a captured call's
@@ -624,7 +626,7 @@ int df11_gated_matmul(const df11_device_stream *gate, const df11_device_stream *
  *   dx           device, n_tokens x in_features of dx_dtype, or NULL
  *   dbias        device, out_features of bias_dtype each, or NULL
  * Types are DF11_BF16 or DF11_FP32.  dz is rounded to BF16 for dx, the matrix
- * cores' operand type, and stays float for dbias. */
+ * cores' operand type (at most 2^-8 of each dz), and stays float for dbias. */
 typedef struct df11_product_grad {
     const void *dy;
     const float *pre[2];
