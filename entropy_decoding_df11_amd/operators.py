@@ -16,7 +16,8 @@ the stream given; this module checks and passes arguments.  The caller orders
 a stream that it gives after whatever makes the inputs and before whatever
 reads the outputs; the tensors may be freed at once, the weights must stay
 until the stream has run.  Calls of one weight may overlap, on any streams and
-from any threads.
+from any threads, and may be captured into graphs (a backward pass, as with
+torch's own operators, from leaves that no eager graph still holds).
 
 A call at one token is a few microseconds on the GPU, so what runs on every
 call is kept short here: the stream's handle is asked for without making a
@@ -218,8 +219,8 @@ def rms_norm(x: "torch.Tensor", weight: Optional["torch.Tensor"] = None,  # noqa
     norm of s.
 
     x: bfloat16, float16 or float32, 1 to 2^30 columns and up to 2^30 rows at
-    one stride (any stride).  weight: one element per column, of x's dtype or float32
-    (None: ones).  residual, out, sum_out: x's shape and dtype; out and
+    one stride (any stride).  weight: one element per column, of x's dtype or
+    float32 (None: ones).  residual, out, sum_out: x's shape and dtype; out and
     sum_out may each be x or residual themselves.  The sums are float32; y and
     s are rounded once.  Where an input requires a gradient the outputs carry
     it (then neither out, sum_out nor stream may be given)."""
@@ -380,9 +381,9 @@ def matmul_epilogue(w, x: "torch.Tensor", bias: Optional["torch.Tensor"] = None,
 
     w: a DF11Tensor compressed with layout="mfma_tiles"; x: bfloat16 (...,
     in_features), rows at one stride and 16-byte aligned, tokens times features
-    (in or out) below 2^32; bias: bfloat16 or
-    float32, one element per output feature; activation: None, "relu", "silu",
-    "gelu" or "gelu_tanh"; residual: bfloat16 or float32 (..., out_features).
+    (in or out) below 2^32; bias: bfloat16 or float32, one element per output
+    feature; activation: None, "relu", "silu", "gelu" or "gelu_tanh"; residual:
+    bfloat16 or float32 (..., out_features).
     Returns out, bfloat16 unless out or out_dtype says float32; out may be the
     residual itself.  Everything before out is float32, and the same call gives
     the same bits again.  Where x, bias or residual require a gradient the

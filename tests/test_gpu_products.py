@@ -707,7 +707,7 @@ def test_inputs_freed_before_their_stream_runs(torch_cuda):
         got = op(x, r, side)
         del x, r
         fresh = [torch.full((5000, 4096), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(2)]
-        apart = not at & {t.data_ptr() for t in fresh}
+        apart = not at & {t.data_ptr() for t in fresh} or side.query()  # (or the stream is through already)
         torch.cuda.synchronize()
         same = torch.equal(got, want)
         assert apart and same
@@ -725,7 +725,7 @@ def test_inputs_freed_before_their_stream_runs(torch_cuda):
     del y
     with torch.cuda.stream(side):
         fresh = torch.full((5000, 4096), float("nan"), device="cuda", dtype=torch.bfloat16)
-    apart = fresh.data_ptr() != at
+    apart = fresh.data_ptr() != at or torch.cuda.current_stream().query()
     torch.cuda.synchronize()
     same = torch.equal(kept, df11.rms_norm(x))
     assert apart and same
@@ -782,3 +782,40 @@ def test_relu_gradients(torch_cuda, rows, cols, kind, tokens):
                     _assert_close(grads[1 + i], b64, eb + _half_step(torch, b.dtype, b64.abs() + eb))
             # (the kink must not swallow the test: hardly any element lies in it)
             assert float(kink.mean()) <= 0.01
+
+
+def test_long_weights_replay_on_two_streams_at_once(torch_cuda):
+    """Gate and up of 51 M weights each, whose decodes take counters from the
+    call's workspace: two graphs and eager calls on three streams without a
+    wait between, again and again."""
+    torch = torch_cuda
+    _note("graphs of long weights")
+    w, _ = _weight(12544, 4096)
+    u, _ = _weight(12544, 4096, "normal", 1)
+    dy = _x(torch, 50, 12544, seed=9)
+
+    def step(x):
+        a = x.detach().requires_grad_()
+        y = df11.gated_matmul(w, u, a)
+        return y.detach(), torch.autograd.grad(y, a, dy)[0]
+
+    xs = [_x(torch, 50, 4096, seed=s) for s in range(3)]
+    want = [step(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    graphs = []
+    for x in xs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = step(x)
+        graphs.append((g, held))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            last = step(xs[2])
+        torch.cuda.synchronize()
+        for got, expected in zip([held for _, held in graphs] + [last], want):
+            assert all(torch.equal(a, b) for a, b in zip(got, expected))
