@@ -299,3 +299,25 @@ def test_norm_weight_gradient_of_the_widest_rows(torch_cuda, cols):
     dw0, = torch.autograd.grad(df11.rms_norm(x[:0], weight=w), w, dy[:0])
     zero = not bool(dw0.any())
     assert zero
+
+
+def test_norm_of_more_than_32_bits_of_bytes(torch_cuda):
+    """600000 rows of 4096, 4.9 GB, forward and backward: the rows whose
+    elements pass 2^31 and whose bytes pass 2^31 and 2^32, and others, against
+    the same rows by themselves (a row's result depends on the row alone)."""
+    torch = torch_cuda
+    from entropy_decoding_df11_amd import df11
+    _note("norm past 32 bits")
+    rows, cols = 600_000, 4096
+    x, r, dy, ds = (torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16).normal_() for _ in range(4))
+    at = sorted({0, 1, rows - 1} | {limit // cols + k for limit in (1 << 30, 1 << 31) for k in (-1, 0, 1)}
+                | {rows * k // 7 for k in range(1, 7)})
+    at = torch.tensor(at, device="cuda")
+
+    def both(x, r, dy, ds):
+        a = x.detach().requires_grad_()
+        y, s = df11.rms_norm(a, residual=r)
+        return y.detach(), s.detach(), torch.autograd.grad((y, s), a, (dy, ds))[0]
+
+    want = both(x[at], r[at], dy[at], ds[at])
+    assert all(torch.equal(a[at], b) for a, b in zip(both(x, r, dy, ds), want))

@@ -819,3 +819,79 @@ def test_long_weights_replay_on_two_streams_at_once(torch_cuda):
         torch.cuda.synchronize()
         for got, expected in zip([held for _, held in graphs] + [last], want):
             assert all(torch.equal(a, b) for a, b in zip(got, expected))
+
+
+def _some_rows(torch, rows, cols):
+    """A few rows of a long tensor: its ends, where its elements pass 2^31, its
+    BF16 bytes 2^31 and 2^32, and some between."""
+    at = {0, 1, rows - 1, rows - 2}
+    for limit in (1 << 31, 1 << 30, 1 << 32):
+        at |= {t for t in (limit // cols - 1, limit // cols, limit // cols + 1) if t < rows}
+    at |= {rows * k // 7 for k in range(1, 7)}
+    return torch.tensor(sorted(at), device="cuda")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_outputs_past_32_bits(torch_cuda, gated):
+    """Nearly 2^32 outputs, forward and backward: a million tokens of 4096
+    features, 8 GB of them, compared where offsets pass 32 bits."""
+    torch = torch_cuda
+    _note(f"past 32 bits, gated {gated}")
+    tokens, rows, cols, act = 1_048_000, 4096, 32, "none" if gated else "silu"
+    w, w64 = _weight(rows, cols)
+    u, u64 = _weight(rows, cols, "normal", 1)
+    ws = (w64, u64) if gated else (w64,)
+    x, dy = _x(torch, tokens, cols, seed=1), _x(torch, tokens, rows, seed=2)
+    a = x.detach().requires_grad_()
+    y = df11.gated_matmul(w, u, a, activation=act) if gated else df11.matmul_epilogue(w, a, activation=act)
+    at = _some_rows(torch, tokens, rows)
+    few = x[at]
+    _assert_close(y.detach()[at], *_expected(torch, few, ws, (None,) * len(ws), act, None, torch.bfloat16))
+    dx, = torch.autograd.grad(y, a, dy)
+    del y
+    # (bounds as in test_product_gradients)
+    zs = [_linear64(few, m, None) for m in ws]
+    d64, (z, dz) = dy[at].double(), zs[0]
+    if gated:
+        z1, dz1 = zs[1]
+        ds, err = [d64 * z1, d64 * z], [d64.abs() * dz1, d64.abs() * dz]
+    else:
+        s64 = _slope64(torch, act, z)
+        ds, err = [d64 * s64], [d64.abs() * dz + 16 * U * d64.abs() * (s64.abs() + z.abs() + 1)]
+    err = [e + 16 * U * d.abs() for e, d in zip(err, ds)]
+    want = sum(d @ m for d, m in zip(ds, ws))
+    size = sum(d.abs() @ m.abs() for d, m in zip(ds, ws))
+    bound = sum((e + 2.0 ** -8 * (d.abs() + e)) @ m.abs() for d, e, m in zip(ds, err, ws))
+    bound = bound + 1.01 * len(ws) * rows * U * (size + bound)
+    _assert_close(dx[at], want, bound + _half_step(torch, torch.bfloat16, want.abs() + bound))
+
+
+@pytest.mark.parametrize("tokens", [20, 300])
+def test_strides_past_32_bits(torch_cuda, tokens):
+    """The longest row strides of x, and outputs and residuals whose last row
+    lies past 2^32 elements."""
+    torch = torch_cuda
+    _note(f"long strides {tokens}")
+    w, w64 = _weight(640, 1056)
+    u, u64 = _weight(640, 1056, "normal", 1)
+    base = _x(torch, tokens, 1056, seed=1)
+    x = torch.empty(tokens << 22, device="cuda", dtype=torch.bfloat16).as_strided((tokens, 1056), (1 << 22, 1))
+    x.copy_(base)
+    stride = (1 << 32) // (tokens - 2)
+    r = torch.empty(stride * tokens, device="cuda", dtype=torch.bfloat16).as_strided((tokens, 640), (stride, 1))
+    y = torch.empty(stride * tokens, device="cuda", dtype=torch.bfloat16).as_strided((tokens, 640), (stride, 1))
+    r.copy_(_side(torch, (tokens, 640), torch.bfloat16, 2))
+    df11.matmul_epilogue(w, x, activation="gelu", residual=r, out=y)
+    _assert_close(y, *_expected(torch, base, (w64,), (None,), "gelu", r, torch.bfloat16))
+    df11.gated_matmul(w, u, x, residual=y, out=r)
+    _assert_close(r, *_expected(torch, base, (w64, u64), (None, None), "silu", y, torch.bfloat16))
+    a = x.detach().requires_grad_()
+    out = df11.matmul_epilogue(w, a)
+    y.copy_(_side(torch, (tokens, 640), torch.bfloat16, 3))
+    g, = torch.autograd.grad(out, a, y, retain_graph=True)
+    g2, = torch.autograd.grad(out, a, y.contiguous())
+    assert torch.equal(g, g2)
+    # the norm's rows, in place
+    n, m = df11.rms_norm(y.contiguous(), residual=r.contiguous())
+    df11.rms_norm(y, residual=r, out=y, sum_out=r)
+    assert torch.equal(y, n) and torch.equal(r, m)
