@@ -7,14 +7,15 @@ include/df11.h); this package is its Python binding, the model-forward helpers
 forwards captured into HIP graphs) and the seeded synthetic workloads.
 """
 
-from .df11 import (DF11Block, DF11BlockBatch, DF11RansTensor, DF11Tensor, HostStream, RansHostStream, build_codebook,
-                   codebook_arrays, compress, compress_block, decode_table, decompress, decompress_batch, encode,
-                   gated_matmul, histogram, linear_batch, matmul_epilogue, rans_compress, rans_encode, rms_norm)
+from .df11 import (DF11Block, DF11BlockBatch, DF11RansTensor, DF11Tensor, HostStream, RansHostStream, append_kv,
+                   build_codebook, codebook_arrays, compress, compress_block, decode_table, decompress, decompress_batch, encode,
+                   gated_matmul, histogram, linear_batch, matmul_epilogue, rans_compress, rans_encode, rms_norm,
+                   rotary_table, tree_attention)
 from ._lib import Df11Error
 
 __all__ = [
     "DF11Block", "DF11BlockBatch", "DF11RansTensor", "DF11Tensor", "Df11Error", "HostStream", "RansHostStream",
-    "build_codebook", "codebook_arrays", "compress", "compress_block", "decode_table", "decompress",
+    "append_kv", "build_codebook", "codebook_arrays", "compress", "compress_block", "decode_table", "decompress",
     "decompress_batch", "encode", "gated_matmul", "histogram", "linear_batch", "matmul_epilogue", "rans_compress",
-    "rans_encode", "rms_norm",
+    "rans_encode", "rms_norm", "rotary_table", "tree_attention",
 ]

@@ -34,6 +34,7 @@ LINEAR_MIN_IN_FEATURES = 512  # DF11_LINEAR_MIN_IN_FEATURES
 EPILOGUE_FUSED_TOKENS = 32  # DF11_EPILOGUE_FUSED_TOKENS
 BF16, FP16, FP32 = 0, 1, 2  # DF11_BF16, DF11_FP16, DF11_FP32
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # DF11_ACT_*
+MAX_HEAD_DIM = 256  # DF11_MAX_HEAD_DIM
 RANS_PROB_BITS = 12  # DF11_RANS_PROB_BITS
 RANS_LANES = 64  # DF11_RANS_LANES
 RANS_STEPS = 512  # DF11_RANS_STEPS
@@ -71,6 +72,9 @@ EXPORTED = [
     "df11_gated_matmul",
     "df11_epilogue_grad_workspace",
     "df11_matmul_epilogue_grad",
+    "df11_append_kv",
+    "df11_tree_attention_workspace",
+    "df11_tree_attention",
     "df11_rans_quantize",
     "df11_rans_encode",
     "df11_rans_build_table",
@@ -166,6 +170,80 @@ class ProductGrad(ctypes.Structure):
         ("dx_dtype", ctypes.c_uint32),
         ("bias_dtype", ctypes.c_uint32),
         ("activation", ctypes.c_uint32),
+    ]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_uint64),
+        ("k_place_stride", ctypes.c_uint64),
+        ("k_head_stride", ctypes.c_uint64),
+        ("v_page_stride", ctypes.c_uint64),
+        ("v_place_stride", ctypes.c_uint64),
+        ("v_head_stride", ctypes.c_uint64),
+        ("n_pages", ctypes.c_uint32),
+        ("page_size", ctypes.c_uint32),
+        ("heads", ctypes.c_uint32),
+        ("head_dim", ctypes.c_uint32),
+        ("dtype", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+    ]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [
+        ("starts", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_uint64),
+        ("n_seqs", ctypes.c_uint32),
+        ("table_pages", ctypes.c_uint32),
+        ("n_tokens", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+    ]
+
+
+class Append(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("rotary", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("k_stride", ctypes.c_uint64),
+        ("k_head_stride", ctypes.c_uint64),
+        ("v_stride", ctypes.c_uint64),
+        ("v_head_stride", ctypes.c_uint64),
+        ("q_stride", ctypes.c_uint64),
+        ("q_head_stride", ctypes.c_uint64),
+        ("q_out_stride", ctypes.c_uint64),
+        ("q_out_head_stride", ctypes.c_uint64),
+        ("rotary_rows", ctypes.c_uint64),
+        ("rotary_dims", ctypes.c_uint32),
+        ("interleaved", ctypes.c_uint32),
+        ("q_heads", ctypes.c_uint32),
+        ("dtype", ctypes.c_uint32),
+    ]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p),
+        ("q_stride", ctypes.c_uint64),
+        ("q_head_stride", ctypes.c_uint64),
+        ("out_stride", ctypes.c_uint64),
+        ("out_head_stride", ctypes.c_uint64),
+        ("mask_stride", ctypes.c_uint64),
+        ("mask_cols", ctypes.c_uint32),
+        ("q_heads", ctypes.c_uint32),
+        ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_uint32),
     ]
 
 
@@ -276,6 +354,11 @@ def load() -> ctypes.CDLL:
                                                ctypes.POINTER(ProductGrad)]),
         "df11_matmul_epilogue_grad": (ctypes.c_int, [ctypes.POINTER(DeviceStream), ctypes.POINTER(DeviceStream), u32,
                                                      u32, u32, ctypes.POINTER(ProductGrad), vp, u64, vp]),
+        "df11_append_kv": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), ctypes.POINTER(Append), vp]),
+        "df11_tree_attention_workspace": (u64, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch),
+                                                ctypes.POINTER(Attention)]),
+        "df11_tree_attention": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch),
+                                               ctypes.POINTER(Attention), vp, u64, vp]),
         "df11_rans_quantize": (ctypes.c_int, [u64p, u32p]),
         "df11_rans_encode": (ctypes.c_int, [u32p, u16p, ctypes.c_uint64, u32p, u32p, u16p, ctypes.c_uint64, u8p,
                                             ctypes.POINTER(RansHeader)]),

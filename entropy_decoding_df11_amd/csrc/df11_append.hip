@@ -1,0 +1,252 @@
+// Keys and values of new tokens into a paged cache, rotated on the way, and
+// their queries rotated (gfx950).
+//
+//   (a, b) -> (a cos - b sin, b cos + a sin)     in float, rounded once
+//
+// Every element is read once and written once.  A thread has one unit of a
+// token: eight rotated pairs (16 elements), or eight elements that are copied,
+// all in 16-byte accesses; a workgroup's units belong to one token, so that
+// what finds its place (sequence, page) is the same for all of its lanes.  The
+// loads of that chain (starts, length, page) and of the elements are
+// independent and go out together.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include <stdint.h>
+
+#include "df11.h"
+#include "df11_device.h"
+#include "df11_kv.h"
+#include "df11_types.h"
+
+namespace {
+
+struct Rows {
+    const void *p;
+    uint64_t stride, head_stride;
+};
+
+struct AppendArgs {
+    df11::KvBatch b;
+    df11::KvPages k_pages, v_pages;
+    Rows k, v, q;
+    void *q_out;
+    uint64_t q_out_stride, q_out_head_stride;
+    const float *rotary;
+    const int32_t *positions;
+    uint64_t rotary_rows;
+    uint32_t n_pages, page_size;
+    uint32_t q_heads, kv_heads, dim, rotary_dims, interleaved;
+    uint32_t units_head;  // units of a rotated head, of a copied one
+    uint32_t units_copy;
+    uint32_t units;       // of a token
+};
+
+// N consecutive elements as floats and back (N * 2 or 16 bytes aligned).
+template <typename T, int N>
+__device__ __forceinline__ void load_unit(const T *p, float (&f)[N]) {
+    if constexpr (sizeof(T) * N > 16) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) load_vec<T, 4>(p + i, *reinterpret_cast<float(*)[4]>(&f[i]));
+    } else {
+        load_vec<T, N>(p, f);
+    }
+}
+
+// N pairs of one head, the unit's first pair being `pair`; from and to point at
+// the head's first element.
+template <typename IN, typename OUT, int N>
+__device__ __forceinline__ void rotate_unit(const IN *from, OUT *to, const float *row, uint32_t half, uint32_t pair,
+                                            bool interleaved, bool known) {
+    float a[N], b[N], c[N], s[N];
+    if (interleaved) {
+        float both[2 * N];
+        if constexpr (N == 1) {
+            both[0] = static_cast<float>(from[2 * pair]);
+            both[1] = static_cast<float>(from[2 * pair + 1]);
+        } else {
+            load_unit(from + 2 * pair, *reinterpret_cast<float(*)[N]>(&both[0]));
+            load_unit(from + 2 * pair + N, *reinterpret_cast<float(*)[N]>(&both[N]));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            a[i] = both[2 * i];
+            b[i] = both[2 * i + 1];
+        }
+    } else {
+        load_unit(from + pair, a);
+        load_unit(from + half + pair, b);
+    }
+    if (known) {
+        load_unit(row + pair, c);
+        load_unit(row + half + pair, s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = s[i] = __builtin_nanf("");
+    }
+    float x[N], y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = a[i] * c[i] - b[i] * s[i];
+        y[i] = b[i] * c[i] + a[i] * s[i];
+    }
+    if (!interleaved) {
+        store_vec<OUT, N>(to + pair, x);
+        store_vec<OUT, N>(to + half + pair, y);
+    } else if constexpr (N == 1) {
+        store_vec<OUT, 1>(to + 2 * pair, x);
+        store_vec<OUT, 1>(to + 2 * pair + 1, y);
+    } else {
+        float lo[N], hi[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            lo[2 * i] = x[i];
+            lo[2 * i + 1] = y[i];
+            hi[2 * i] = x[N / 2 + i];
+            hi[2 * i + 1] = y[N / 2 + i];
+        }
+        store_vec<OUT, N>(to + 2 * pair, lo);
+        store_vec<OUT, N>(to + 2 * pair + N, hi);
+    }
+}
+
+// N: pairs of a rotated unit and elements of a copied one.
+template <typename IN, typename OUT, int N>
+__global__ __launch_bounds__(256) void df11_append_kernel(AppendArgs a) {
+    const uint32_t token = blockIdx.x, unit = blockIdx.y * blockDim.x + threadIdx.x;
+    const int32_t seq = __builtin_amdgcn_readfirstlane(sequence_of(a.b, static_cast<int32_t>(token)));
+    if (seq < 0) return;
+    const int64_t length = a.b.lengths[seq];
+    const int64_t place = length + (static_cast<int64_t>(token) - a.b.starts[seq]);
+    const int64_t position = a.positions ? a.positions[token] : place;
+    const uint32_t q_units = a.q_heads * a.units_head, k_units = a.kv_heads * a.units_head;
+    if (unit >= a.units) return;
+    // What the unit reads and where it goes: q, k or v.
+    const uint32_t kind = unit < q_units ? 0u : unit < q_units + k_units ? 1u : 2u;
+    const uint32_t u = unit - (kind == 0u ? 0u : kind == 1u ? q_units : q_units + k_units);
+    const uint32_t each = kind == 2u ? a.units_copy : a.units_head, head = u / each, part = u % each;
+    const Rows &r = kind == 0u ? a.q : kind == 1u ? a.k : a.v;
+    const IN *from = static_cast<const IN *>(r.p) + token * r.stride + head * r.head_stride;
+    OUT *to;
+    if (kind == 0u) {
+        to = static_cast<OUT *>(a.q_out) + token * a.q_out_stride + head * a.q_out_head_stride;
+    } else {
+        if (length < 0 || place < 0 || place >= static_cast<int64_t>(a.b.table_pages) * a.page_size) return;
+        const uint32_t at = static_cast<uint32_t>(place), page = at / a.page_size;
+        const uint32_t id = static_cast<uint32_t>(a.b.page_table[seq * a.b.table_stride + page]);
+        if (id >= a.n_pages) return;
+        const df11::KvPages &c = kind == 1u ? a.k_pages : a.v_pages;
+        to = static_cast<OUT *>(c.p) + id * c.page_stride + (at - page * a.page_size) * c.place_stride +
+             head * c.head_stride;
+    }
+    const uint32_t half = a.rotary_dims / 2u, turned = half / N;
+    if (kind != 2u && part < turned) {
+        const bool known = position >= 0 && static_cast<uint64_t>(position) < a.rotary_rows;
+        rotate_unit<IN, OUT, N>(from, to, a.rotary + (known ? position : 0) * a.rotary_dims, half, part * N,
+                                a.interleaved, known);
+    } else {
+        const uint32_t d = kind == 2u ? part * N : a.rotary_dims + (part - turned) * N;
+        float f[N];
+        load_unit(from + d, f);
+        store_vec<OUT, N>(to + d, f);
+    }
+}
+
+template <typename IN, typename OUT>
+const void *pick_width(bool wide) {
+    return wide ? reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 8>)
+                : reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 1>);
+}
+
+template <typename OUT>
+const void *pick_in(uint32_t dtype, bool wide) {
+    return dtype == DF11_FP32   ? pick_width<float, OUT>(wide)
+           : dtype == DF11_BF16 ? pick_width<bf16_t, OUT>(wide)
+                                : pick_width<fp16_t, OUT>(wide);
+}
+
+}  // namespace
+
+extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, const df11_append *a, void *hip_stream) {
+    uint64_t k_span = 0, v_span = 0;
+    const int rc = check_kv(c, b, k_span, v_span);
+    if (rc) return rc;
+    const uint32_t bytes = a ? dtype_bytes(a->dtype) : 0, dim = c->head_dim, tokens = b->n_tokens;
+    if (!bytes || !a->q != !a->q_out || (a->q ? !a->q_heads || a->q_heads > kMaxKvHeads : a->q_heads != 0))
+        return DF11_E_INVALID_ARG;
+    if (a->rotary && (a->rotary_dims < 2 || a->rotary_dims % 2 || a->rotary_dims > dim || !aligned(a->rotary, 4) ||
+                      a->rotary_rows > (1ull << 40) || a->interleaved > 1))
+        return DF11_E_INVALID_ARG;
+    if (a->positions && !aligned(a->positions, 4)) return DF11_E_INVALID_ARG;
+    if (tokens == 0 || b->n_seqs == 0) return DF11_OK;
+    if (!a->k || !a->v) return DF11_E_INVALID_ARG;
+    if (a->rotary && !a->rotary_rows) return DF11_E_INVALID_ARG;
+    const uint32_t rotary_dims = a->rotary ? a->rotary_dims : 0;
+    struct In {
+        const void *p;
+        uint64_t stride, head_stride, heads;
+    } ins[] = {{a->q, a->q_stride, a->q_head_stride, a->q_heads},
+               {a->k, a->k_stride, a->k_head_stride, c->heads},
+               {a->v, a->v_stride, a->v_head_stride, c->heads}};
+    bool wide = rotary_dims % 16 == 0 && aligned(a->rotary, 16) && aligned(a->q_out, 16) && a->q_out_stride % 8 == 0 && a->q_out_head_stride % 8 == 0;
+    uint64_t in_spans[3];
+    for (int i = 0; i < 3; ++i) {
+        if (ins[i].stride >= kMaxKvStride || ins[i].head_stride >= (1ull << 32) || !aligned(ins[i].p, bytes))
+            return DF11_E_INVALID_ARG;
+        in_spans[i] = ins[i].p ? kv_span(tokens, ins[i].stride, ins[i].heads, ins[i].head_stride, dim) * bytes : 0;
+        wide = wide && aligned(ins[i].p, 16) && ins[i].stride % 8 == 0 && ins[i].head_stride % 8 == 0;
+    }
+    // The cache's halves, q_out and everything that is read lie apart; q_out
+    // may lie exactly on q.
+    const uint64_t q_out_span = a->q ? 2 * kv_span(tokens, a->q_out_stride, a->q_heads, a->q_out_head_stride, dim) : 0;
+    if (a->q && (!aligned(a->q_out, 2) || a->q_out_stride >= kMaxKvStride || a->q_out_head_stride >= (1ull << 32) ||
+                 !kv_apart(tokens, a->q_out_stride, a->q_heads, a->q_out_head_stride, dim)))
+        return DF11_E_INVALID_ARG;
+    const bool on_q = a->q && a->q == a->q_out && a->q_stride == a->q_out_stride &&
+                      a->q_head_stride == a->q_out_head_stride && a->dtype == c->dtype;
+    const void *outs[] = {c->k, c->v, a->q_out};
+    const uint64_t out_spans[] = {k_span, v_span, q_out_span};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 3; ++j) {
+            if (overlaps(outs[i], out_spans[i], ins[j].p, in_spans[j]) && !(i == 2 && j == 0 && on_q))
+                return DF11_E_INVALID_ARG;
+            if (i == 2 && j < 2 && overlaps(outs[i], out_spans[i], outs[j], out_spans[j])) return DF11_E_INVALID_ARG;
+        }
+        if (!clear_of_batch(*b, outs[i], out_spans[i]) ||
+            overlaps(outs[i], out_spans[i], a->rotary, 4 * a->rotary_rows * rotary_dims) ||
+            overlaps(outs[i], out_spans[i], a->positions, a->positions ? 4ull * tokens : 0))
+            return DF11_E_INVALID_ARG;
+    }
+    AppendArgs k{};
+    k.b = kernel_batch(*b);
+    k.k_pages = df11::KvPages{c->k, c->k_page_stride, c->k_place_stride, c->k_head_stride};
+    k.v_pages = df11::KvPages{c->v, c->v_page_stride, c->v_place_stride, c->v_head_stride};
+    k.q = Rows{a->q, a->q_stride, a->q_head_stride};
+    k.k = Rows{a->k, a->k_stride, a->k_head_stride};
+    k.v = Rows{a->v, a->v_stride, a->v_head_stride};
+    k.q_out = a->q_out;
+    k.q_out_stride = a->q_out_stride;
+    k.q_out_head_stride = a->q_out_head_stride;
+    k.rotary = a->rotary;
+    k.positions = a->positions;
+    k.rotary_rows = a->rotary_rows;
+    k.n_pages = c->n_pages;
+    k.page_size = c->page_size;
+    k.q_heads = a->q_heads;
+    k.kv_heads = c->heads;
+    k.dim = dim;
+    k.rotary_dims = rotary_dims;
+    k.interleaved = a->interleaved;
+    const uint32_t each = wide ? 8 : 1;
+    k.units_head = rotary_dims / 2 / each + (dim - rotary_dims) / each;
+    k.units_copy = dim / each;
+    // (at most 4096 heads of 256 elements, three times)
+    k.units = (a->q_heads + c->heads) * k.units_head + c->heads * k.units_copy;
+    (void)hipGetLastError();
+    void *params[] = {&k};
+    const uint32_t threads = k.units >= 256 ? 256 : 64;
+    return launch_kernel(c->dtype == DF11_BF16 ? pick_in<bf16_t>(a->dtype, wide) : pick_in<fp16_t>(a->dtype, wide),
+                         dim3(tokens, (k.units + threads - 1) / threads), dim3(threads), params, 0,
+                         static_cast<hipStream_t>(hip_stream), nullptr, nullptr);
+}

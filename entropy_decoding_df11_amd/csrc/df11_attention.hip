@@ -1,0 +1,774 @@
+// Attention of a batch's new tokens over a paged cache (gfx950).
+//
+//   out = sum over the visible places j of p_j v_j,  p = softmax(scale q . k_j)
+//
+// in one pass over the places, with the softmax's running maximum and sum: for
+// a row's reference m, w_j = 2^(c (s_j - m)) with c = scale log2(e), and what
+// has been summed is multiplied by 2^(c (m - m')) when the reference moves to
+// m'.  It moves only where a score passes it by 2^8, so that blocks without a
+// new maximum need nothing across lanes; w is at most 2^8, and its relative
+// precision does not depend on the reference.
+//
+// A query head's rows of one key head are the columns of the products, so that
+// all heads of a group read a place once:
+//   S^T = K Q^T    v_mfma_f32_16x16x32: lane l holds places 4 (l / 16) .. + 3 of
+//                  a 16-place tile for row l mod 16
+//   O^T = V^T W^T  of two place tiles at once, with the places in the order in
+//                  which S^T left them (4 (l / 16) .. + 3 of either tile are a
+//                  lane's eight), so that w goes from the softmax to the product
+//                  without leaving its lane; V^T comes from LDS by
+//                  ds_read_b64_tr_b16 in the same order
+// K's operands come straight from memory to registers, V's rows by
+// global_load_lds to LDS that each wave has to itself: waves take the places
+// of a step in turn and meet only at the end of a tile's run.  Sixteen-byte
+// chunks of a V row are permuted by the row in pairs, which spreads the
+// transposed reads over all banks.
+//
+// Work is cut by df11_attention_plan.h; a tile that one workgroup does alone is
+// written at once, the parts of the others go to the workspace and a second
+// kernel joins them in order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include <stdint.h>
+
+#include "df11.h"
+#include "df11_attention_plan.h"
+#include "df11_device.h"
+#include "df11_kv.h"
+#include "df11_types.h"
+
+namespace {
+
+using df11::kStepPlaces;
+using df11::SeqShape;
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kWaves = 4;
+constexpr uint32_t kBlock = 32;  // places of one wave's turn
+static_assert(kStepPlaces == kWaves * kBlock, "a step is one block for each wave");
+
+struct AttentionArgs {
+    df11::KvBatch b;
+    df11::KvPages k, v;
+    const void *q;
+    void *out;
+    float *lse;
+    const uint8_t *mask;
+    uint64_t q_stride, q_head_stride, out_stride, out_head_stride, mask_stride;
+    uint64_t capacity;    // places of a sequence's pages
+    float *parts;         // [workgroup][2][row][dim]
+    float *stats;         // [workgroup][2][row][2]: reference times c, sum
+    uint32_t page_magic, page_shift;  // df11::page_of
+    float c, headroom;    // scale log2(e), 8 / c
+    uint32_t mask_cols, n_pages, page_size, kv_heads, group, dim, workgroups, tile_rows;
+};
+
+__device__ __forceinline__ floatx4 mfma(vec_t<bf16_t, 8> a, vec_t<bf16_t, 8> b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ floatx4 mfma(vec_t<fp16_t, 8> a, vec_t<fp16_t, 8> b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ shortx4 read_transposed(const uint8_t *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4 *)p);
+}
+
+// 16 bytes a lane from memory to the wave-uniform LDS address dst + 16 lane.
+__device__ __forceinline__ void load_to_lds(const void *from, uint8_t *dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 2^(m - to), 0 for a reference of nothing.
+__device__ __forceinline__ float weight_of(float m, float to) { return m == -INFINITY ? 0.0f : exp2_fast(m - to); }
+
+__device__ __forceinline__ SeqShape shape_of(const AttentionArgs &a, uint32_t s) {
+    return df11::seq_shape(a.b.starts[s], a.b.starts[s + 1], a.b.lengths[s], a.b.n_tokens, a.capacity, a.group,
+                           a.tile_rows);
+}
+
+// Units of all sequences, and of those before sequence `until`, by a whole
+// workgroup of 256 threads.
+__device__ __forceinline__ void count_units(const AttentionArgs &a, uint32_t until, uint64_t &all, uint64_t &before,
+                                            uint64_t (*s_part)[2]) {
+    uint64_t sum[2] = {0, 0};
+    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += 256u) {
+        const uint64_t n = df11::seq_units(shape_of(a, s), a.kv_heads);
+        sum[0] += n;
+        if (s < until) sum[1] += n;
+    }
+#pragma unroll
+    for (int m = 32; m; m >>= 1) {
+        sum[0] += __shfl_xor(sum[0], m);
+        sum[1] += __shfl_xor(sum[1], m);
+    }
+    if ((threadIdx.x & 63u) == 0) {
+        s_part[threadIdx.x / 64u][0] = sum[0];
+        s_part[threadIdx.x / 64u][1] = sum[1];
+    }
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        all += s_part[w][0];
+        before += s_part[w][1];
+    }
+    __syncthreads();
+}
+
+// The sequence that holds unit u and its first unit, by a whole workgroup.
+struct Found {
+    uint64_t first;
+    uint32_t seq;
+};
+
+__device__ __forceinline__ Found find_unit(const AttentionArgs &a, uint64_t u, uint64_t (*s_part)[2], Found *s_found) {
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x / 64u;
+    uint64_t base = 0;
+    for (uint32_t at = 0; at < a.b.n_seqs; at += 256u) {
+        const uint32_t s = at + threadIdx.x;
+        const uint64_t n = s < a.b.n_seqs ? df11::seq_units(shape_of(a, s), a.kv_heads) : 0;
+        uint64_t to = n;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const uint64_t other = __shfl_up(to, m);
+            if (lane >= static_cast<uint32_t>(m)) to += other;
+        }
+        if (lane == 63u) s_part[wave][0] = to;
+        __syncthreads();
+        uint64_t first = base + to - n;
+        for (uint32_t w = 0; w < wave; ++w) first += s_part[w][0];
+        if (u >= first && u < first + n) *s_found = Found{first, s};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) base += s_part[w][0];
+        __syncthreads();
+        if (u < base) break;
+    }
+    return *s_found;
+}
+
+// One tile's part of a run.
+struct Part {
+    SeqShape s;
+    uint32_t seq, head, tile;
+    uint32_t step0, step1;  // steps of this run
+    uint32_t limit;         // places that the tile may see
+    bool whole;             // no other run has steps of this tile
+};
+
+// A row of a part's tile: its token among the sequence's and its query head.
+__device__ __forceinline__ void row_of(const AttentionArgs &a, const Part &p, uint32_t row, uint32_t &token,
+                                       uint32_t &head) {
+    const uint32_t at = p.tile * a.tile_rows + row;
+    token = at / a.group;
+    head = p.head * a.group + at % a.group;
+}
+
+template <typename T, int KK, int M, bool kWhole16>
+struct Wave {
+    static constexpr int DP = 32 * KK;         // head_dim padded
+    static constexpr int kChunks = DP / 8;     // 16-byte chunks of a row
+    static constexpr int kTilesD = DP / 16;
+    static constexpr int kVBytes = kBlock * DP * 2;
+    static constexpr int kVLoads = kVBytes / 1024;
+    static constexpr int kVRows = 64 / kChunks;  // rows of one load
+    using Vec = vec_t<T, 8>;
+
+    const AttentionArgs &a;
+    const Part &p;
+    uint8_t *lds;  // two buffers of kVBytes
+    uint32_t lane, wave, quarter, l16;
+    const int32_t *table;
+
+    Vec q[M][KK];
+    floatx4 o[M][kTilesD];
+    float m[M], l[M];  // a lane's row: its reference (raw score) and this lane's part of the sum
+    Vec k[2][KK];
+    uint32_t valid;    // of the block in k: places whose page exists
+
+    // Pair of chunks of a row of V is kept at its number XOR this.
+    static __device__ __forceinline__ uint32_t turn(uint32_t row) {
+        return DP >= 128 ? row & 7u : (row >> 1) & 3u;
+    }
+
+    __device__ __forceinline__ uint32_t page_of(uint32_t place) const {
+        return df11::page_of(place, a.page_magic, a.page_shift);
+    }
+
+    // Page of the place that lane l mod 32 has of the block at key0; an id that
+    // no page has where there is none.
+    __device__ __forceinline__ uint32_t load_id(uint32_t key0) const {
+        const uint32_t place = key0 + (lane & 31u);
+        return place < p.limit ? static_cast<uint32_t>(table[page_of(place)]) : ~0u;
+    }
+
+    // Sends for the block at key0: K to `to`, V to the LDS buffer dst.
+    __device__ __forceinline__ void issue(uint32_t key0, uint32_t id, Vec (&to)[2][KK], uint8_t *dst,
+                                          uint32_t &valid_to) const {
+        valid_to = static_cast<uint32_t>(__ballot(id < a.n_pages));
+        id = id < a.n_pages ? id : 0u;
+        const uint32_t last_chunk = a.dim / 8u - 1u;
+        const T *kp = static_cast<const T *>(a.k.p) + p.head * a.k.head_stride;
+        const T *vp = static_cast<const T *>(a.v.p) + p.head * a.v.head_stride;
+        const uint32_t v_row = lane / kChunks, slot = lane % kChunks;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const T *row;
+            if constexpr (kWhole16) {
+                const uint32_t key = key0 + 16u * t, page = __builtin_amdgcn_readlane(id, 16 * t);
+                const uint32_t off = key - page_of(key) * a.page_size;
+                row = kp + page * a.k.page_stride + off * a.k.place_stride + l16 * a.k.place_stride;
+            } else {
+                const uint32_t key = key0 + 16u * t + l16, page = __shfl(id, 16 * t + l16);
+                const uint32_t off = key - page_of(key) * a.page_size;
+                row = kp + page * a.k.page_stride + off * a.k.place_stride;
+            }
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                const uint32_t chunk = 4u * kk + quarter;
+                to[t][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(chunk, last_chunk));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i) {
+            const uint32_t r = i * kVRows + v_row;  // row of the block
+            const uint32_t chunk = min(slot ^ (2u * turn(r)), last_chunk);
+            const T *row;
+            if constexpr (kWhole16) {
+                const uint32_t t = i * kVRows / 16, key = key0 + 16u * t, page = __builtin_amdgcn_readlane(id, 16 * t);
+                const uint32_t off = key - page_of(key) * a.page_size;
+                row = vp + page * a.v.page_stride + off * a.v.place_stride + (r - 16u * t) * a.v.place_stride;
+            } else {
+                const uint32_t key = key0 + r, page = __shfl(id, r);
+                row = vp + page * a.v.page_stride + (key - page_of(key) * a.page_size) * a.v.place_stride;
+            }
+            load_to_lds(row + 8u * chunk, dst + 1024 * i);
+        }
+    }
+
+    __device__ __forceinline__ void begin() {
+        const uint32_t last_chunk = a.dim / 8u - 1u;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < kTilesD; ++d) o[i][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t token, head;
+            row_of(a, p, 16u * i + l16, token, head);
+            const bool there = token < p.s.rows;
+            const T *row = static_cast<const T *>(a.q) +
+                           (static_cast<uint64_t>(p.s.begin) + (there ? token : 0u)) * a.q_stride +
+                           (there ? head : p.head * a.group) * a.q_head_stride;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                const uint32_t chunk = 4u * kk + quarter;
+                q[i][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(chunk, last_chunk));
+                if (!there || chunk > last_chunk) q[i][kk] = Vec{};
+            }
+        }
+    }
+
+    // The places of the block at key0 that a row sees, as far as this lane has
+    // them: bit 4 t + e is place 16 t + 4 quarter + e.  (Bits and selects only:
+    // out of nested branches around single elements of the scores the compiler
+    // has made code that keeps the masked ones.)
+    __device__ __forceinline__ uint32_t seen(uint32_t token, const uint8_t *mask_row, uint32_t key0) const {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t key = key0 + 16u * t + 4u * quarter;
+            if (a.mask) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t j = key + e - p.s.length;  // (wraps where the place is cached)
+                    uint32_t bit = key + e < p.s.length ? 1u : 0u;
+                    if (j < a.mask_cols) bit |= mask_row[j] != 0 ? 1u : 0u;
+                    bits |= bit << (4 * t + e);
+                }
+            } else {
+                const uint32_t end = p.s.length + token + 1u;  // places that the row sees
+                const uint32_t n = key < end ? min(end - key, 4u) : 0u;
+                bits |= ((1u << n) - 1u) << (4 * t);
+            }
+        }
+        return bits & (((valid >> (4u * quarter)) & 15u) | (((valid >> (16u + 4u * quarter)) & 15u) << 4));
+    }
+
+    __device__ __forceinline__ void compute(uint32_t key0, const uint8_t *v) {
+        floatx4 s[M][2];
+        const uint32_t last_chunk = a.dim / 8u - 1u;
+        if (a.dim != DP) {
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                if (4u * kk + quarter > last_chunk) k[0][kk] = k[1][kk] = Vec{};
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                s[i][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) s[i][t] = mfma(k[t][kk], q[i][kk], s[i][t]);
+            }
+        const bool masked = key0 + kBlock > p.s.length || valid != ~0u;
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                uint32_t token, head;
+                row_of(a, p, 16u * i + l16, token, head);
+                const uint8_t *mask_row =
+                    a.mask ? a.mask + (p.s.begin + static_cast<uint64_t>(min(token, p.s.rows - 1u))) * a.mask_stride
+                           : nullptr;
+                const uint32_t bits = seen(token, mask_row, key0);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[i][t][e] = (bits >> (4 * t + e)) & 1u ? s[i][t][e] : -INFINITY;
+            }
+        }
+        // New references where a score passes the old one by the headroom.
+        float top[M];
+        bool moves = false;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            top[i] = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
+                           fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
+            moves = moves || top[i] > m[i] + a.headroom;
+        }
+        if (__ballot(moves)) {
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                float to = fmaxf(top[i], __shfl_xor(top[i], 16));
+                to = fmaxf(m[i], fmaxf(to, __shfl_xor(to, 32)));
+                const float f = weight_of(m[i] * a.c, to * a.c);
+                m[i] = to;
+                l[i] *= f;
+#pragma unroll
+                for (int d = 0; d < kTilesD; ++d) o[i][d] *= f;
+            }
+        }
+        Vec w[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float mc = m[i] == -INFINITY ? 0.0f : m[i] * a.c;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -mc));
+                    l[i] += x;
+                    s[i][t][e] = x;
+                    w[i][4 * t + e] = static_cast<T>(x);
+                }
+        }
+        if (masked && bad_values(v)) {
+            add_one_by_one(s, v);
+            return;
+        }
+#pragma unroll
+        for (int d = 0; d < kTilesD; ++d) {
+            union {
+                shortx4 s[2];
+                Vec v;
+            } u;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t row = 16u * t + 4u * quarter + (l16 >> 2);
+                u.s[t] = read_transposed(v + row * (2 * DP) + 32u * (d ^ turn(row)) + 8u * (l16 & 3u));
+            }
+#pragma unroll
+            for (int i = 0; i < M; ++i) o[i][d] = mfma(u.v, w[i], o[i][d]);
+        }
+    }
+
+    // Whether the block's rows of V hold an infinity or a NaN: a product would
+    // carry it to rows that do not see its place (0 * inf).
+    __device__ __forceinline__ bool bad_values(const uint8_t *v) const {
+        constexpr uint32_t kExponent = std::is_same_v<T, bf16_t> ? 0x7F80u : 0x7C00u;
+        bool bad = false;
+        for (int i = 0; i < kVLoads; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(v + 1024 * i + 16 * lane);
+            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                bad = bad || (words[e] & kExponent) == kExponent || ((words[e] >> 16) & kExponent) == kExponent;
+        }
+        return __ballot(bad) != 0;
+    }
+
+    // The block's part of o without the matrix cores: places that a row does not
+    // see are left out.
+    __device__ __forceinline__ void add_one_by_one(const floatx4 (&s)[M][2], const uint8_t *v) {
+        for (uint32_t from = 0; from < 4; ++from) {
+#pragma unroll
+            for (int at = 0; at < 8; ++at) {
+                const uint32_t row = 16u * (at / 4) + 4u * from + at % 4;
+#pragma unroll
+                for (int i = 0; i < M; ++i) {
+                    const float x = static_cast<float>(static_cast<T>(__shfl(s[i][at / 4][at % 4], l16 + 16u * from)));
+                    if (x == 0.0f) continue;
+#pragma unroll
+                    for (int d = 0; d < kTilesD; ++d) {
+                        const T *at_v = reinterpret_cast<const T *>(v + row * (2 * DP) + 32u * (d ^ turn(row))) + 4u * quarter;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][d][e] += x * static_cast<float>(at_v[e]);
+                    }
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void run() {
+        const uint32_t first = p.step0 * kStepPlaces + wave * kBlock;
+        const uint32_t end = min(p.limit, p.step1 * kStepPlaces);
+        const uint32_t blocks = first < end ? (end - first + kStepPlaces - 1u) / kStepPlaces : 0u;
+        begin();
+        if (!blocks) return;
+        Vec next[2][KK];
+        uint32_t next_valid;
+        uint8_t *cur = lds, *other = lds + kVBytes;
+        // (this wave's reads of the buffers, for the tile before, are back)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        issue(first, load_id(first), k, cur, valid);
+        uint32_t id = load_id(first + kStepPlaces);
+        for (uint32_t b = 0; b < blocks; ++b) {
+            const uint32_t key0 = first + b * kStepPlaces;
+            // This block has landed, and the other buffer's last reads are back.
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            const bool more = b + 1u < blocks;
+            if (more) {
+                issue(key0 + kStepPlaces, id, next, other, next_valid);
+                id = load_id(key0 + 2u * kStepPlaces);
+            }
+            compute(key0, cur);
+            if (more) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) k[t][kk] = next[t][kk];
+                valid = next_valid;
+            }
+            uint8_t *x = cur;
+            cur = other;
+            other = x;
+        }
+    }
+};
+
+// Joins the waves' sums of a part, row tile by row tile, and writes them: to out
+// and lse if the part is whole, else to the workgroup's slot.
+template <typename T, int KK, int M, bool kWhole16>
+__device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &p, Wave<T, KK, M, kWhole16> &w,
+                                            uint8_t *lds, uint32_t wave_bytes, float (*s_stats)[16][2], uint64_t slot) {
+    constexpr int DP = 32 * KK, kStride = DP + 4;
+    const uint32_t tid = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        float l = w.l[i] + __shfl_xor(w.l[i], 16);
+        l += __shfl_xor(l, 32);
+        // (every wave's reads of its buffers, and of the row tile before, are back)
+        __syncthreads();
+        if (w.quarter == 0) {
+            s_stats[w.wave][w.l16][0] = w.m[i] == -INFINITY ? -INFINITY : w.m[i] * a.c;
+            s_stats[w.wave][w.l16][1] = l;
+        }
+        float *mine = reinterpret_cast<float *>(lds + w.wave * wave_bytes);
+#pragma unroll
+        for (int d = 0; d < Wave<T, KK, M, kWhole16>::kTilesD; ++d)
+            *reinterpret_cast<floatx4 *>(mine + w.l16 * kStride + 16 * d + 4 * w.quarter) = w.o[i][d];
+        __syncthreads();
+        for (uint32_t at = tid; at < 16u * (DP / 8); at += 256u) {
+            const uint32_t r = at / (DP / 8), d = 8u * (at % (DP / 8)), row = 16u * i + r;
+            uint32_t token, head;
+            row_of(a, p, row, token, head);
+            if (token >= p.s.rows || d >= a.dim) continue;
+            float top = -INFINITY, total = 0.0f, sum[8] = {};
+#pragma unroll
+            for (uint32_t x = 0; x < kWaves; ++x) top = fmaxf(top, s_stats[x][r][0]);
+#pragma unroll
+            for (uint32_t x = 0; x < kWaves; ++x) {
+                const float f = weight_of(s_stats[x][r][0], top);
+                if (f == 0.0f) continue;
+                total += f * s_stats[x][r][1];
+                const float *from = reinterpret_cast<const float *>(lds + x * wave_bytes) + r * kStride + d;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += f * from[e];
+            }
+            if (p.whole) {
+                const uint64_t t = static_cast<uint64_t>(p.s.begin) + token;
+                const float f = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] *= f;
+                store_vec<T, 8>(static_cast<T *>(a.out) + t * a.out_stride + head * a.out_head_stride + d, sum);
+                if (a.lse && d == 0)
+                    a.lse[t * (a.kv_heads * a.group) + head] =
+                        total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
+            } else {
+                float *to = a.parts + (slot * a.tile_rows + row) * a.dim + d;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) to[e] = sum[e];
+                if (d == 0) {
+                    float *st = a.stats + (slot * a.tile_rows + row) * 2u;
+                    st[0] = top;
+                    st[1] = total;
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <typename T, int KK, int M, bool kWhole16>
+__global__ __launch_bounds__(256) void df11_attention_kernel(AttentionArgs a) {
+    using W = Wave<T, KK, M, kWhole16>;
+    constexpr uint32_t kWaveBytes = 2u * W::kVBytes;
+    static_assert(kWaveBytes >= 16 * (W::DP + 4) * 4, "a row tile's sums fit a wave's buffers");
+    __shared__ __align__(1024) uint8_t s_mem[kWaves * kWaveBytes];
+    __shared__ float s_stats[kWaves][16][2];
+    __shared__ uint64_t s_part[4][2];
+    __shared__ Found s_found;
+    uint64_t units, unused;
+    count_units(a, 0, units, unused, s_part);
+    if (units == 0) return;
+    const uint32_t runs = df11::runs_of(units, a.workgroups);
+    if (blockIdx.x >= runs) return;
+    const uint32_t run = df11::run_of_workgroup(blockIdx.x, runs);
+    uint64_t u = df11::run_begin(run, units, runs);
+    const uint64_t end = df11::run_begin(run + 1ull, units, runs);
+    Found f = find_unit(a, u, s_part, &s_found);
+    uint32_t seq = __builtin_amdgcn_readfirstlane(f.seq);
+    uint64_t first = f.first;
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+    bool begun = true;  // the run's first tile may have begun in the run before
+    while (u < end && seq < a.b.n_seqs) {
+        Part p;
+        p.s = shape_of(a, seq);
+        const uint64_t here = df11::seq_units(p.s, a.kv_heads);
+        if (u >= first + here) {
+            first += here;
+            ++seq;
+            continue;
+        }
+        const uint64_t tile_no = (u - first) / p.s.steps, tile_first = first + tile_no * p.s.steps;
+        p.seq = seq;
+        p.head = static_cast<uint32_t>(tile_no / p.s.tiles);
+        p.tile = df11::tile_in_turn(static_cast<uint32_t>(tile_no % p.s.tiles), p.s.tiles, a.mask != nullptr);
+        p.step0 = static_cast<uint32_t>(u - tile_first);
+        p.step1 = end - tile_first < p.s.steps ? static_cast<uint32_t>(end - tile_first) : p.s.steps;
+        p.limit = df11::tile_places(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
+        p.whole = p.step0 == 0 && p.step1 == p.s.steps;
+        W w{a, p, s_mem + wave * kWaveBytes, lane, wave, lane >> 4, lane & 15u,
+            a.b.page_table + seq * a.b.table_stride};
+        w.run();
+        finish_part<T, KK, M, kWhole16>(a, p, w, s_mem, kWaveBytes, s_stats, 2ull * run + (begun ? 0u : 1u));
+        begun = false;
+        u = tile_first + p.step1;
+    }
+}
+
+// The parts of one token's rows of one key head, joined in the order of the
+// places: a thread has eight elements of a row.
+template <typename T>
+__global__ __launch_bounds__(256) void df11_attention_join_kernel(AttentionArgs a) {
+    __shared__ uint64_t s_part[4][2];
+    const uint32_t token = blockIdx.x, head = blockIdx.y;
+    const int32_t seq = __builtin_amdgcn_readfirstlane(sequence_of(a.b, static_cast<int32_t>(token)));
+    if (seq < 0) return;
+    uint64_t units, first;
+    count_units(a, static_cast<uint32_t>(seq), units, first, s_part);
+    const SeqShape s = shape_of(a, seq);
+    if (units == 0 || !s.tiles) return;
+    const uint32_t runs = df11::runs_of(units, a.workgroups);
+    const uint32_t i = token - static_cast<uint32_t>(s.begin), chunks = a.dim / 8u;
+    for (uint32_t at = threadIdx.x; at < a.group * chunks; at += 256u) {
+        const uint32_t g = at / chunks, d = 8u * (at % chunks);
+        const uint32_t row = i * a.group + g, tile = row / a.tile_rows, in_tile = row % a.tile_rows;
+        const uint32_t turn = df11::turn_of_tile(tile, s.tiles, a.mask != nullptr);
+        const uint64_t from = first + (static_cast<uint64_t>(head) * s.tiles + turn) * s.steps;
+        const uint32_t lo = df11::run_of(from, units, runs), hi = df11::run_of(from + s.steps - 1u, units, runs);
+        if (lo == hi) continue;
+        float top = -INFINITY, total = 0.0f, sum[8] = {};
+        // A run's first slot holds the tile that it begins with.
+        const uint32_t late = df11::run_begin(lo, units, runs) == from ? 0u : 1u;
+        const auto slot_of = [&](uint32_t r) { return 2ull * r + (r == lo ? late : 0u); };
+        for (uint32_t r = lo; r <= hi; ++r) top = fmaxf(top, a.stats[(slot_of(r) * a.tile_rows + in_tile) * 2u]);
+        for (uint32_t r = lo; r <= hi; ++r) {
+            const uint64_t slot = slot_of(r) * a.tile_rows + in_tile;
+            const float f = weight_of(a.stats[slot * 2u], top);
+            if (f == 0.0f) continue;
+            total += f * a.stats[slot * 2u + 1u];
+            float v[8];
+            load_vec<float, 4>(a.parts + slot * a.dim + d, *reinterpret_cast<float(*)[4]>(&v[0]));
+            load_vec<float, 4>(a.parts + slot * a.dim + d + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += f * v[e];
+        }
+        const float f = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] *= f;
+        const uint32_t q_head = head * a.group + g;
+        store_vec<T, 8>(static_cast<T *>(a.out) + token * a.out_stride + q_head * a.out_head_stride + d, sum);
+        if (a.lse && d == 0)
+            a.lse[static_cast<uint64_t>(token) * (a.kv_heads * a.group) + q_head] =
+                total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
+    }
+}
+
+template <typename T, int KK>
+const void *pick_rows(uint32_t m, bool whole16) {
+    const auto pick = [&](auto rows) {
+        constexpr int M = decltype(rows)::value;
+        return whole16 ? reinterpret_cast<const void *>(&df11_attention_kernel<T, KK, M, true>)
+                       : reinterpret_cast<const void *>(&df11_attention_kernel<T, KK, M, false>);
+    };
+    if constexpr (KK < 8) {
+        if (m == 2) return pick(std::integral_constant<int, 2>{});
+    }
+    return pick(std::integral_constant<int, 1>{});
+}
+
+template <typename T>
+const void *pick_kernel(uint32_t dim, uint32_t m, bool whole16) {
+    return dim <= 64 ? pick_rows<T, 2>(m, whole16) : dim <= 128 ? pick_rows<T, 4>(m, whole16) : pick_rows<T, 8>(m, whole16);
+}
+
+// How a call is launched.
+struct Plan {
+    const void *fn;
+    uint32_t tile_rows, workgroups;
+    uint64_t parts, stats;  // bytes; 0 where no tile is ever cut
+};
+
+int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, Plan &p) {
+    int dev = 0, cus = 0;
+    if (device_cus(dev, cus)) return DF11_E_HIP;
+    const uint32_t group = q_heads / c.heads;
+    // Row tiles of 16, as many as a sequence's rows fill on average (the host
+    // knows no more than that).
+    const uint64_t rows = static_cast<uint64_t>((b.n_tokens + b.n_seqs - 1) / b.n_seqs) * group;
+    const uint32_t m = rows <= 16 || c.head_dim > 128 ? 1 : 2;
+    const bool whole16 = c.page_size % 16 == 0;
+    p.fn = c.dtype == DF11_BF16 ? pick_kernel<bf16_t>(c.head_dim, m, whole16) : pick_kernel<fp16_t>(c.head_dim, m, whole16);
+    p.tile_rows = 16 * m;
+    const int per_cu = resident_per_cu(p.fn, 256, dev, 0);
+    if (per_cu < 1) return DF11_E_HIP;
+    const uint64_t capacity = static_cast<uint64_t>(b.table_pages) * c.page_size;
+    const uint64_t tiles = (static_cast<uint64_t>(b.n_tokens) * group + p.tile_rows - 1) / p.tile_rows + b.n_seqs;
+    const uint64_t units = tiles * c.heads * std::max<uint64_t>(1, (capacity + kStepPlaces - 1) / kStepPlaces);
+    if (static_cast<uint64_t>(b.n_tokens) * group >= (1ull << 31) || units >= (1ull << 31)) return DF11_E_TOO_LARGE;
+    p.workgroups = static_cast<uint32_t>(std::min<uint64_t>(static_cast<uint64_t>(cus) * per_cu, units));
+    const uint64_t slots = capacity > kStepPlaces ? 2ull * p.workgroups * p.tile_rows : 0;
+    p.parts = round_up(slots * c.head_dim * 4, 256);
+    p.stats = round_up(slots * 8, 256);
+    return DF11_OK;
+}
+
+// Checks of what comes beside the cache and the batch (already checked); the
+// spans of q and out in bytes.
+int check_attention(const df11_kv_cache &c, const df11_kv_batch &b, const df11_attention *a, uint64_t &q_span,
+                    uint64_t &out_span) {
+    if (!a || !a->q_heads || a->q_heads > kMaxKvHeads || a->q_heads % c.heads || !(a->scale > 0.0f) ||
+        !std::isfinite(a->scale))
+        return DF11_E_INVALID_ARG;
+    if (b.n_tokens == 0 || b.n_seqs == 0) return DF11_OK;
+    if (!a->q || !a->out || !aligned(a->q, 16) || !aligned(a->out, 16)) return DF11_E_INVALID_ARG;
+    const uint64_t strides[] = {a->q_stride, a->q_head_stride, a->out_stride, a->out_head_stride};
+    for (const uint64_t s : strides)
+        if (s % 8 || s >= kMaxKvStride) return DF11_E_INVALID_ARG;
+    if (!kv_apart(b.n_tokens, a->out_stride, a->q_heads, a->out_head_stride, c.head_dim)) return DF11_E_INVALID_ARG;
+    if (a->lse && !aligned(a->lse, 4)) return DF11_E_INVALID_ARG;
+    if (a->mask && a->mask_stride >= kMaxKvStride) return DF11_E_INVALID_ARG;
+    q_span = 2 * kv_span(b.n_tokens, a->q_stride, a->q_heads, a->q_head_stride, c.head_dim);
+    out_span = 2 * kv_span(b.n_tokens, a->out_stride, a->q_heads, a->out_head_stride, c.head_dim);
+    return DF11_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t df11_tree_attention_workspace(const df11_kv_cache *c, const df11_kv_batch *b, const df11_attention *a) {
+    uint64_t k_span = 0, v_span = 0, q_span = 0, out_span = 0;
+    Plan p{};
+    if (check_kv(c, b, k_span, v_span) || check_attention(*c, *b, a, q_span, out_span)) return 0;
+    if (b->n_tokens == 0 || b->n_seqs == 0 || make_plan(*c, *b, a->q_heads, p)) return 0;
+    return p.parts + p.stats;
+}
+
+int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df11_attention *a, void *workspace,
+                        uint64_t workspace_bytes, void *hip_stream) {
+    uint64_t k_span = 0, v_span = 0, q_span = 0, out_span = 0;
+    int rc = check_kv(c, b, k_span, v_span);
+    if (!rc) rc = check_attention(*c, *b, a, q_span, out_span);
+    if (rc || b->n_tokens == 0 || b->n_seqs == 0) return rc;
+    // Outputs stay clear of everything that is read, but out may lie exactly on q.
+    const uint64_t lse_span = a->lse ? 4ull * b->n_tokens * a->q_heads : 0;
+    const uint64_t mask_span = a->mask ? (b->n_tokens - 1ull) * a->mask_stride + a->mask_cols : 0;
+    const bool on_q = a->q == a->out && a->q_stride == a->out_stride && a->q_head_stride == a->out_head_stride;
+    const void *outs[] = {a->out, a->lse, workspace};
+    uint64_t spans[] = {out_span, lse_span, 0};
+    const auto clear = [&](int i) {
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i], spans[i], outs[j], spans[j])) return false;
+        return !overlaps(outs[i], spans[i], c->k, k_span) && !overlaps(outs[i], spans[i], c->v, v_span) &&
+               ((i == 0 && on_q) || !overlaps(outs[i], spans[i], a->q, q_span)) &&
+               !overlaps(outs[i], spans[i], a->mask, mask_span) && clear_of_batch(*b, outs[i], spans[i]);
+    };
+    if (!clear(0) || !clear(1)) return DF11_E_INVALID_ARG;
+    Plan p{};
+    rc = make_plan(*c, *b, a->q_heads, p);
+    if (rc) return rc;
+    spans[2] = p.parts + p.stats;
+    if (spans[2] && (!workspace || !aligned(workspace, 256))) return DF11_E_INVALID_ARG;
+    if (workspace_bytes < spans[2]) return DF11_E_BUFFER_TOO_SMALL;
+    if (!clear(2)) return DF11_E_INVALID_ARG;
+    AttentionArgs k{};
+    k.b = kernel_batch(*b);
+    k.k = df11::KvPages{c->k, c->k_page_stride, c->k_place_stride, c->k_head_stride};
+    k.v = df11::KvPages{c->v, c->v_page_stride, c->v_place_stride, c->v_head_stride};
+    k.q = a->q;
+    k.out = a->out;
+    k.lse = a->lse;
+    k.mask = a->mask;
+    k.q_stride = a->q_stride;
+    k.q_head_stride = a->q_head_stride;
+    k.out_stride = a->out_stride;
+    k.out_head_stride = a->out_head_stride;
+    k.mask_stride = a->mask_stride;
+    k.capacity = static_cast<uint64_t>(b->table_pages) * c->page_size;
+    k.parts = static_cast<float *>(workspace);
+    k.stats = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + p.parts);
+    k.page_shift = df11::page_shift(c->page_size);
+    k.page_magic = df11::page_magic(c->page_size, k.page_shift);
+    k.c = a->scale * 1.44269504088896341f;
+    k.headroom = std::min(8.0f / k.c, 1e30f);
+    k.mask_cols = a->mask_cols;
+    k.n_pages = c->n_pages;
+    k.page_size = c->page_size;
+    k.kv_heads = c->heads;
+    k.group = a->q_heads / c->heads;
+    k.dim = c->head_dim;
+    k.workgroups = p.workgroups;
+    k.tile_rows = p.tile_rows;
+    (void)hipGetLastError();
+    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    void *params[] = {&k};
+    rc = launch_kernel(p.fn, dim3(p.workgroups), dim3(256), params, 0, stream, nullptr, nullptr);
+    if (rc || !spans[2]) return rc;
+    const void *join = c->dtype == DF11_BF16 ? reinterpret_cast<const void *>(&df11_attention_join_kernel<bf16_t>)
+                                             : reinterpret_cast<const void *>(&df11_attention_join_kernel<fp16_t>);
+    return launch_kernel(join, dim3(b->n_tokens, c->heads), dim3(256), params, 0, stream, nullptr, nullptr);
+}
+
+}  // extern "C"

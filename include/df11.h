@@ -656,6 +656,156 @@ int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_str
                               void *workspace, uint64_t workspace_bytes, void *hip_stream);
 
 /* ---------------------------------------------------------------------------
+ * A paged cache of keys and values, and attention over it.  Not on the page.
+ * Sequence s of a batch holds lengths[s] tokens in the cache and brings the
+ * new tokens starts[s] .. starts[s + 1] - 1 of the batch: its i-th new token
+ * belongs at place lengths[s] + i, which lies in page
+ * page_table[s][place / page_size] at place % page_size.  What the arrays on
+ * the device hold is not known to the host; the kernels check it: a token
+ * before starts[0] or behind starts[n_seqs] belongs to no sequence, and a place
+ * beyond table_pages pages, or in a page outside 0 .. n_pages - 1, is neither
+ * read nor written.  (Starts that decrease give unspecified results, in
+ * bounds.)  All types are DF11_BF16, DF11_FP16 or, where stated, DF11_FP32.
+ * ------------------------------------------------------------------------- */
+
+/* Largest head_dim. */
+#define DF11_MAX_HEAD_DIM 256
+
+/* The cache (host struct of device pointers).  Element (page, place, head, d) of
+ * k is at page * k_page_stride + place * k_place_stride + head * k_head_stride +
+ * d, so that (pages, page_size, heads, head_dim) and (pages, heads, page_size,
+ * head_dim) both fit; likewise v.
+ *   k, v       16-byte aligned, strides multiples of 8, below 2^40
+ *   n_pages    1 .. 2^31 - 1;  page_size 1 .. 2^20;  heads 1 .. 4096
+ *   head_dim   a multiple of 8, 8 .. DF11_MAX_HEAD_DIM
+ *   dtype      DF11_BF16 or DF11_FP16 */
+typedef struct df11_kv_cache {
+    void *k;
+    void *v;
+    uint64_t k_page_stride, k_place_stride, k_head_stride;
+    uint64_t v_page_stride, v_place_stride, v_head_stride;
+    uint32_t n_pages;
+    uint32_t page_size;
+    uint32_t heads;
+    uint32_t head_dim;
+    uint32_t dtype;
+    uint32_t reserved;
+} df11_kv_cache;
+
+/* The batch (host struct of device pointers).
+ *   starts       n_seqs + 1, not decreasing
+ *   lengths      n_seqs
+ *   page_table   n_seqs x table_pages, table_stride from sequence to sequence;
+ *                table_pages * page_size at most 2^30
+ *   n_tokens     rows of the call's per-token arrays, 0 .. 2^24 */
+typedef struct df11_kv_batch {
+    const int32_t *starts;
+    const int32_t *lengths;
+    const int32_t *page_table;
+    uint64_t table_stride;
+    uint32_t n_seqs;
+    uint32_t table_pages;
+    uint32_t n_tokens;
+    uint32_t reserved;
+} df11_kv_batch;
+
+/* What df11_append_kv takes beside them (host struct of device pointers).
+ *   k, v          n_tokens x heads x head_dim of dtype: element (token, head, d)
+ *                 at token * stride + head * head_stride + d
+ *   q             n_tokens x q_heads x head_dim of dtype, q_heads 1 .. 4096; or
+ *                 NULL, with q_heads 0
+ *   q_out         n_tokens x q_heads x head_dim of the cache's dtype; with q only.
+ *                 May lie exactly on q (same address, strides and type)
+ *   rotary        rotary_rows x rotary_dims floats: row p holds the cosines of
+ *                 position p's angles, then their sines; or NULL (no rotation)
+ *   rotary_dims   even, 2 .. head_dim: the dimensions of a head that are rotated,
+ *                 in pairs (d, d + rotary_dims / 2), or (2 d, 2 d + 1) if
+ *                 interleaved; the others are copied
+ *   positions     n_tokens, or NULL (every token's place)
+ *   dtype         DF11_BF16, DF11_FP16 or DF11_FP32
+ * Strides below 2^40, of heads below 2^32. */
+typedef struct df11_append {
+    const void *k;
+    const void *v;
+    const void *q;
+    void *q_out;
+    const float *rotary;
+    const int32_t *positions;
+    uint64_t k_stride, k_head_stride;
+    uint64_t v_stride, v_head_stride;
+    uint64_t q_stride, q_head_stride;
+    uint64_t q_out_stride, q_out_head_stride;
+    uint64_t rotary_rows;
+    uint32_t rotary_dims;
+    uint32_t interleaved;
+    uint32_t q_heads;
+    uint32_t dtype;
+} df11_append;
+
+/* Appends the new tokens' keys and values to the cache, rotated on the way, and
+ * rotates their queries: a pair (a, b) becomes (a cos - b sin, b cos + a sin),
+ * in float and rounded once to the cache's type; v is copied.  A position
+ * outside the table gives NaN.  Rows of q_out that belong to no sequence are
+ * left as they were, and so is the rest of the cache.  Places that two tokens
+ * share receive either one's elements.  One launch; with no tokens none.
+ * Errors: DF11_E_INVALID_ARG (types, sizes, alignment, overlaps), DF11_E_HIP. */
+int df11_append_kv(const df11_kv_cache *cache, const df11_kv_batch *batch, const df11_append *a, void *hip_stream);
+
+/* What df11_tree_attention takes beside the cache and the batch (host struct of
+ * device pointers).
+ *   q, out       n_tokens x q_heads x head_dim of the cache's dtype: element
+ *                (token, head, d) at token * stride + head * head_stride + d;
+ *                16-byte aligned, strides multiples of 8.  Query head h reads
+ *                key head h / (q_heads / heads).  out may lie exactly on q
+ *   lse          n_tokens x q_heads floats, or NULL: the natural logarithm of the
+ *                sum of exp(scale q . k) over what the query sees
+ *   mask         n_tokens x mask_cols bytes, mask_stride from token to token, or
+ *                NULL.  Every query sees the lengths[s] cached places of its
+ *                sequence; of the sequence's new tokens it sees the j-th if byte
+ *                j of its row is not zero (none from mask_cols on), or without a
+ *                mask those up to itself
+ *   scale        positive, finite
+ *   q_heads      a multiple of the cache's heads, at most 4096 */
+typedef struct df11_attention {
+    const void *q;
+    void *out;
+    float *lse;
+    const uint8_t *mask;
+    uint64_t q_stride, q_head_stride;
+    uint64_t out_stride, out_head_stride;
+    uint64_t mask_stride;
+    uint32_t mask_cols;
+    uint32_t q_heads;
+    float scale;
+    uint32_t reserved;
+} df11_attention;
+
+/* Bytes of df11_tree_attention's workspace on the current device, the same for
+ * every content of the batch's arrays; 0 for arguments that the call refuses, or
+ * where nothing needs computing. */
+uint64_t df11_tree_attention_workspace(const df11_kv_cache *cache, const df11_kv_batch *batch,
+                                       const df11_attention *a);
+
+/* Attention of a batch's new tokens (one each when decoding, a tree of drafted
+ * ones, a piece of a prompt) over a paged cache that already holds their keys
+ * and values:
+ *   out = sum over the visible places j of p_j v_j,  p = softmax(scale q . k_j)
+ * Scores, the softmax's maximum and sum, and out's sums are float; p is rounded
+ * to the cache's type for its product with v (the matrix cores' operand type),
+ * not for the softmax's sum; out is rounded once.  A query that sees nothing
+ * gets zeros and an lse of minus infinity.  What a place holds reaches only the
+ * queries that see it: an infinity or a NaN elsewhere in the cache does not.
+ * Rows that belong to no sequence are left as they were.
+ *   workspace    device, 256-byte aligned, df11_tree_attention_workspace bytes;
+ *                holds nothing between calls, but calls that overlap in time need
+ *                one each
+ * Results do not change from run to run.  Errors: DF11_E_INVALID_ARG,
+ * DF11_E_TOO_LARGE (more tiles of queries and places than 2^31),
+ * DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
+int df11_tree_attention(const df11_kv_cache *cache, const df11_kv_batch *batch, const df11_attention *a,
+                        void *workspace, uint64_t workspace_bytes, void *hip_stream);
+
+/* ---------------------------------------------------------------------------
  * rANS exponent coder.  The discussion on the page ("Opini Hacker News")
  * names rANS as an entropy coder that suits SIMD-style instruction sets better
  * than Huffman; the page gives no format, so this one is this library's own:
