@@ -8,14 +8,14 @@ forwards captured into HIP graphs) and the seeded synthetic workloads.
 """
 
 from .df11 import (DF11Block, DF11BlockBatch, DF11RansTensor, DF11Tensor, HostStream, RansHostStream, append_kv,
-                   build_codebook, codebook_arrays, compress, compress_block, decode_table, decompress, decompress_batch, encode,
-                   gated_matmul, histogram, linear_batch, matmul_epilogue, rans_compress, rans_encode, rms_norm,
+                   build_codebook, codebook_arrays, compress, compress_block, decode_table, decompress,
+                   decompress_batch, encode, gated_matmul, histogram, linear_batch, linear_cross_entropy, matmul_epilogue, rans_compress, rans_encode, rms_norm,
                    rotary_table, tree_attention)
 from ._lib import Df11Error
 
 __all__ = [
     "DF11Block", "DF11BlockBatch", "DF11RansTensor", "DF11Tensor", "Df11Error", "HostStream", "RansHostStream",
     "append_kv", "build_codebook", "codebook_arrays", "compress", "compress_block", "decode_table", "decompress",
-    "decompress_batch", "encode", "gated_matmul", "histogram", "linear_batch", "matmul_epilogue", "rans_compress",
+    "decompress_batch", "encode", "gated_matmul", "histogram", "linear_batch", "linear_cross_entropy", "matmul_epilogue", "rans_compress",
     "rans_encode", "rms_norm", "rotary_table", "tree_attention",
 ]

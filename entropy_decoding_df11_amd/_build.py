@@ -41,7 +41,7 @@ HIP_FLAGS = [
 
 HOST_SOURCES = ("df11_host.cpp", "df11_rans_host.cpp")
 DEVICE_SOURCES = ("df11_decode.hip", "df11_rans_decode.hip", "df11_norm.hip", "df11_product.hip",
-                  "df11_dense.hip", "df11_append.hip", "df11_attention.hip")
+                  "df11_dense.hip", "df11_loss.hip", "df11_append.hip", "df11_attention.hip")
 
 
 def _torch_lib_dir() -> str:

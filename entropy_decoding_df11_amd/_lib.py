@@ -72,6 +72,9 @@ EXPORTED = [
     "df11_gated_matmul",
     "df11_epilogue_grad_workspace",
     "df11_matmul_epilogue_grad",
+    "df11_cross_entropy_workspace",
+    "df11_cross_entropy",
+    "df11_cross_entropy_grad",
     "df11_append_kv",
     "df11_tree_attention_workspace",
     "df11_tree_attention",
@@ -170,6 +173,19 @@ class ProductGrad(ctypes.Structure):
         ("dx_dtype", ctypes.c_uint32),
         ("bias_dtype", ctypes.c_uint32),
         ("activation", ctypes.c_uint32),
+    ]
+
+
+class Loss(ctypes.Structure):
+    _fields_ = [
+        ("targets", ctypes.c_void_p),
+        ("loss", ctypes.c_void_p),
+        ("total", ctypes.c_void_p),
+        ("count", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("ignore_index", ctypes.c_int64),
+        ("vocab", ctypes.c_uint32),
+        ("mean", ctypes.c_uint32),
     ]
 
 
@@ -354,6 +370,10 @@ def load() -> ctypes.CDLL:
                                                ctypes.POINTER(ProductGrad)]),
         "df11_matmul_epilogue_grad": (ctypes.c_int, [ctypes.POINTER(DeviceStream), ctypes.POINTER(DeviceStream), u32,
                                                      u32, u32, ctypes.POINTER(ProductGrad), vp, u64, vp]),
+        "df11_cross_entropy_workspace": (u64, [ctypes.POINTER(DeviceStream), u32, ctypes.c_int]),
+        "df11_cross_entropy": (ctypes.c_int, [ctypes.POINTER(DeviceStream), vp, u64, u32, u32, u32,
+                                              ctypes.POINTER(Loss), vp, u64, vp]),
+        "df11_cross_entropy_grad": (ctypes.c_int, [vp, vp, u64, vp, u32, u32, vp, u64, u32, vp]),
         "df11_append_kv": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), ctypes.POINTER(Append), vp]),
         "df11_tree_attention_workspace": (u64, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch),
                                                 ctypes.POINTER(Attention)]),

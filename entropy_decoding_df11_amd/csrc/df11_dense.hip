@@ -56,13 +56,19 @@ namespace {
 using df11::DenseCall;
 using df11::DenseMode;
 using df11::kDenseBack;
+using df11::kDenseBackAdd;
+using df11::kDenseExp;
 using df11::kDenseGated;
 using df11::kDensePlain;
+using df11::kDenseStats;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 using Resource = __amdgpu_buffer_rsrc_t;
+
+constexpr bool is_back(int mode) { return mode == kDenseBack || mode == kDenseBackAdd; }
+constexpr bool is_loss(int mode) { return mode == kDenseStats || mode == kDenseExp; }
 
 constexpr uint32_t kStep = df11::kDenseStep;
 // Token tiles that follow each other before the next output tile: an XCD's 32
@@ -86,6 +92,7 @@ struct DenseArgs {
     uint32_t m_tiles, splits;
     uint32_t vec;          // the epilogue's out and residual allow 16-byte vectors
     Epilogue e;
+    df11::DenseLoss loss;
 };
 
 // A buffer resource over a window of the operand at p (nothing past it is read).
@@ -180,6 +187,16 @@ __device__ __forceinline__ void finish8(const DenseArgs &a, uint32_t token, uint
         y[i] = activate(ACT, z0[i]);
         if constexpr (kGated) y[i] *= z1[i];
     }
+    if constexpr (MODE == kDenseBackAdd) {
+        // (a scale of zero: what is there has not been written yet)
+        const float f = a.loss.scale[token];
+        if (f != 0.0f) {
+            float r[8];
+            load8_as(e.out, token * e.out_stride + col, DF11_FP32, a.vec, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += f * r[i];
+        }
+    }
     if (e.residual) {
         float r[8];
         load8_as(e.residual, token * e.residual_stride + col, e.residual_dtype, a.vec, r);
@@ -194,7 +211,7 @@ __device__ __forceinline__ void finish8(const DenseArgs &a, uint32_t token, uint
 // than the product's last steps).
 template <int MODE, typename F>
 __device__ __forceinline__ void with_activation(uint32_t act, F f) {
-    switch (MODE == kDenseBack ? DF11_ACT_NONE : act) {
+    switch (is_back(MODE) ? DF11_ACT_NONE : act) {
     case DF11_ACT_RELU: f.template run<DF11_ACT_RELU>(); break;
     case DF11_ACT_SILU: f.template run<DF11_ACT_SILU>(); break;
     case DF11_ACT_GELU: f.template run<DF11_ACT_GELU>(); break;
@@ -229,6 +246,64 @@ struct StagedRows {
     }
 };
 
+// The rows of a wave's staged logits, one panel of 64 classes, as statistics and
+// exponentials: eight lanes a token, eight classes a lane.
+template <int MODE, int kStride>
+struct LossRows {
+    const DenseArgs &a;
+    const float *staged;
+    uint32_t rows, token0, col0, lane;
+
+    __device__ __forceinline__ void run() const {
+        // log2(e) in two floats: a logit of 100 keeps its exponential to 2^-24.
+        constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596303350001107901e-8f;
+        const df11::DenseLoss &l = a.loss;
+        if (col0 >= a.n_out) return;
+        const uint32_t c = 8u * (lane % 8u), first = l.first_class + col0 + c;
+#pragma unroll 2
+        for (uint32_t r = lane / 8u; r < rows; r += 8u) {
+            const uint32_t token = token0 + r;
+            if (token >= a.tokens) break;
+            float z[8];
+            load8(staged + r * kStride + c, z);
+            const int64_t at = l.targets[token] - static_cast<int64_t>(first);
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (at == i) {
+                    if (first + i < l.classes) l.target_logit[token] = z[i];
+                    z[i] = -INFINITY;
+                }
+                if (first + i >= l.classes) z[i] = -INFINITY;
+                top = fmaxf(top, z[i]);
+            }
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+            float ref = ceilf(top * kHi);
+            if constexpr (MODE == kDenseExp) {
+                const float known = l.ref ? l.ref[token] : -INFINITY;
+                if (ref <= known + df11::kRefRoom) ref = known;
+            }
+            const float base = ref == -INFINITY ? 0.0f : ref;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                z[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], kLo, __builtin_fmaf(z[i], kHi, -base)));
+                sum += z[i];
+            }
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) sum += __shfl_xor(sum, m);
+            if (c == 0) {
+                float *st = l.stats + 2u * (static_cast<uint64_t>(col0 / 64u) * a.tokens + token);
+                st[0] = ref;
+                st[1] = sum;
+            }
+            if constexpr (MODE == kDenseExp)
+                store8(reinterpret_cast<bf16_t *>(l.exps) + token * l.exps_stride + col0 + c, z);
+        }
+    }
+};
+
 // Passes in which the waves' sums go through LDS (at most 140 KB at a time).
 template <int W, int TM, int TN>
 constexpr int kStagePasses = (W * TM * 16 * (TN * 16 + 4) * 4 + 139999) / 140000;
@@ -253,7 +328,10 @@ __device__ __forceinline__ void write_tile(const DenseArgs &a, const floatx4 (&a
             *reinterpret_cast<floatx4 *>(staged + (16 * i + l16) * kStride + 16 * j + 4 * quarter) =
                 acc[P * TP + i][j];
     const uint32_t t0 = token0 + P * TP * 16;
-    if (a.splits > 1u) {
+    if constexpr (is_loss(MODE)) {
+        static_assert(kOut == 64, "a wave has one panel");
+        LossRows<MODE, kStride>{a, staged, TP * 16u, t0, col0, lane}.run();
+    } else if (a.splits > 1u) {
         constexpr uint32_t kMats = MODE == kDenseGated ? 2u : 1u, kLanes = kOut / 4;
         const uint32_t c = 4u * (lane % kLanes);
         for (uint32_t r = lane / kLanes; r < TP * 16u; r += kWaveSize / kLanes) {
@@ -302,7 +380,7 @@ void df11_dense_kernel(DenseArgs a) {
     constexpr int kLeftLoads = BM / 8 / W, kRightLoads = BN / 8 / W;
     constexpr int kLeftBytes = BM * 128, kStageBytes = (BM + BN) * 128;
     constexpr int kStaged = W * (TM / kStagePasses<W, TM, TN>) * 16 * (TN * 16 + 4) * 4;
-    constexpr int kReads = MODE == kDenseBack ? TM + 2 * TN : TM + TN;
+    constexpr int kReads = is_back(MODE) ? TM + 2 * TN : TM + TN;
     __shared__ __align__(1024) uint8_t s_mem[2 * kStageBytes > kStaged ? 2 * kStageBytes : kStaged];
 
     const uint32_t lane = threadIdx.x & (kWaveSize - 1);
@@ -326,21 +404,21 @@ void df11_dense_kernel(DenseArgs a) {
     const uint64_t panel_bytes = static_cast<uint64_t>(a.tile_ks) * 4096u;
 
     const uint32_t rows_here = min(static_cast<uint32_t>(BM), a.tokens - m0);
-    const uint32_t k_len = MODE == kDenseBack ? a.panels * 64u : a.tile_ks * 32u;
+    const uint32_t k_len = is_back(MODE) ? a.panels * 64u : a.tile_ks * 32u;
     const uint32_t stride = static_cast<uint32_t>(a.left_stride);
     const uint32_t left_at = df11::dense_left_lane(lane, stride);
 
     // Sends for one step.  (Forward, an odd last k-step: the upper half of
     // the step holds whatever follows, and its products are left out.)
     auto issue = [&](uint32_t step, uint8_t *stage) {
-        const uint32_t one = MODE == kDenseBack && step >= a.k_steps_one ? 1u : 0u;
+        const uint32_t one = is_back(MODE) && step >= a.k_steps_one ? 1u : 0u;
         const uint32_t ks = step - one * a.k_steps_one;  // step of this matrix
         const Resource left = resource(a.left[one], df11::dense_left_window(m0, rows_here, a.left_stride, k_len, ks));
 #pragma unroll
         for (int i = 0; i < kLeftLoads; ++i)
             load_to_lds(left, stage + 1024u * (wave + W * i), left_at + df11::dense_left_group(wave + W * i, stride));
         stage += kLeftBytes;
-        if constexpr (MODE == kDenseBack) {
+        if constexpr (is_back(MODE)) {
             const Resource w = resource(a.w[one], df11::dense_back_window(n0, ks, panel_bytes));
 #pragma unroll
             for (int i = 0; i < kRightLoads; ++i)
@@ -375,13 +453,13 @@ void df11_dense_kernel(DenseArgs a) {
     const uint32_t quarter = lane >> 4, l16 = lane & 15u;
     const uint32_t x_at = 128u * (wm * TM * 16u + l16) + 16u * (quarter ^ (l16 & 7u));
     const uint32_t w_at =
-        kLeftBytes + (MODE == kDenseBack ? 1024u * (2u * TN * wn + (quarter >> 1)) + 8u * (l16 & 1u) +
+        kLeftBytes + (is_back(MODE) ? 1024u * (2u * TN * wn + (quarter >> 1)) + 8u * (l16 & 1u) +
                                                16u * (16u * ((l16 >> 1) & 1u) + 8u * (quarter & 1u) + (l16 >> 2))
                                          : 1024u * TN * wn + 16u * lane);
     auto read = [&](const uint8_t *stage, int half, bf16x8 (&fx)[TM], bf16x8 (&fw)[TN]) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            if constexpr (MODE == kDenseBack) {
+            if constexpr (is_back(MODE)) {
                 // outputs 16 (j mod 2) .. of k-step TN / 2 wn + j / 2; rows 32 half + 8 quarter ..
                 const uint8_t *p = stage + w_at + 1024u * (4u * (j / 2) + 2u * half) + 512u * (j & 1);
                 union {
@@ -423,7 +501,7 @@ void df11_dense_kernel(DenseArgs a) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     read(cur, 0, fx0, fw0);
-    const bool odd = MODE != kDenseBack && (a.tile_ks & 1u) && k_end == a.k_steps;
+    const bool odd = !is_back(MODE) && (a.tile_ks & 1u) && k_end == a.k_steps;
     const uint32_t k_full = odd ? k_end - 1u : k_end;
     for (uint32_t step = k_begin; step < k_full; ++step) {
         first_half();
@@ -513,7 +591,7 @@ struct DensePlan {
 // (4096 tokens, 14336 -> 4096: 285 us here, 415 measured; in small tiles 426
 // and 505), so that there the choice leans to large tiles.
 DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols, int cus) {
-    const bool back = mode == kDenseBack;
+    const bool back = is_back(mode);
     const uint64_t n_out = back ? cols : rows, mats = mode == kDenseGated ? 2 : 1, room = static_cast<uint64_t>(cus);
     const uint32_t k_steps = back ? n * (rows / kStep) : (cols + kStep - 1) / kStep;
     const double large = back ? 6.0 : 4.5, large_full = back ? 1.9 : 1.25, large_half = back ? 1.7 : 1.25;
@@ -535,7 +613,8 @@ DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows,
             best = p;
         }
     };
-    for (uint32_t splits = 1; splits <= 32 && splits <= k_steps; splits *= 2) {
+    // (statistics are of whole sums)
+    for (uint32_t splits = 1; splits <= (is_loss(mode) ? 1u : 32u) && splits <= k_steps; splits *= 2) {
         const double steps = (k_steps + splits - 1) / splits;
         const double sum = splits > 1 ? 1.5 + 0.2 * splits + 8.0 * splits * mats * tokens * n_out / 6e6 : 0.0;
         consider(sum + time(tiles(128, n_out) * splits, 2 * room, small, small_full, small_half, steps), {0, splits});
@@ -557,6 +636,9 @@ const void *dense_kernel(DenseMode mode) {
     switch (mode) {
     case kDenseGated: return reinterpret_cast<const void *>(&df11_dense_kernel<WM, WN, TM, TN, kDenseGated>);
     case kDenseBack: return reinterpret_cast<const void *>(&df11_dense_kernel<WM, WN, TM, TN, kDenseBack>);
+    case kDenseStats: return reinterpret_cast<const void *>(&df11_dense_kernel<WM, WN, TM, TN, kDenseStats>);
+    case kDenseExp: return reinterpret_cast<const void *>(&df11_dense_kernel<WM, WN, TM, TN, kDenseExp>);
+    case kDenseBackAdd: return reinterpret_cast<const void *>(&df11_dense_kernel<WM, WN, TM, TN, kDenseBackAdd>);
     default: return reinterpret_cast<const void *>(&df11_dense_kernel<WM, WN, TM, TN, kDensePlain>);
     }
 }
@@ -569,16 +651,16 @@ uint64_t dense_workspace(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t r
     int dev = 0, cus = 0;
     if (device_cus(dev, cus)) return ~0ull;
     const DensePlan p = dense_plan(mode, n, tokens, rows, cols, cus);
-    const uint64_t mats = mode == kDenseGated ? 2 : 1, n_out = mode == kDenseBack ? cols : rows;
+    const uint64_t mats = mode == kDenseGated ? 2 : 1, n_out = is_back(mode) ? cols : rows;
     return p.splits > 1 ? 4ull * p.splits * mats * tokens * n_out : 0;
 }
 
 int dense_product(const DenseCall &c, const Epilogue &e, float *workspace, hipStream_t stream) {
     int dev = 0, cus = 0;
     if (device_cus(dev, cus)) return DF11_E_HIP;
-    const uint32_t n = c.mode == kDensePlain || (c.mode == kDenseBack && !c.w[1]) ? 1 : 2;
+    const uint32_t n = c.mode == kDenseGated || (c.mode == kDenseBack && c.w[1]) ? 2 : 1;
     const DensePlan p = dense_plan(c.mode, n, c.tokens, c.rows, c.cols, cus);
-    const uint32_t one = c.mode == kDenseBack ? c.rows / kStep : (c.cols + kStep - 1) / kStep;
+    const uint32_t one = is_back(c.mode) ? c.rows / kStep : (c.cols + kStep - 1) / kStep;
     DenseArgs a{};
     for (int i = 0; i < 2; ++i) {
         a.left[i] = c.left[i];
@@ -587,12 +669,13 @@ int dense_product(const DenseCall &c, const Epilogue &e, float *workspace, hipSt
     a.left_stride = c.left_stride;
     a.partial = workspace;
     a.tokens = c.tokens;
-    a.n_out = c.mode == kDenseBack ? c.cols : c.rows;
+    a.n_out = is_back(c.mode) ? c.cols : c.rows;
     a.tile_ks = c.cols / 32;
     a.panels = c.rows / 64;
-    a.k_steps = c.mode == kDenseBack ? n * one : one;
+    a.k_steps = is_back(c.mode) ? n * one : one;
     a.k_steps_one = one;
     a.e = e;
+    a.loss = c.loss;
     const uint32_t out_bytes = dtype_bytes(e.out_dtype), res_bytes = dtype_bytes(e.residual_dtype);
     a.vec = aligned(e.out, 16) && e.out_stride * out_bytes % 16 == 0 &&
             (!e.residual || (aligned(e.residual, 16) && e.residual_stride * res_bytes % 16 == 0));
@@ -615,6 +698,7 @@ int dense_product(const DenseCall &c, const Epilogue &e, float *workspace, hipSt
     const uint64_t items = static_cast<uint64_t>(a.tokens) * (a.n_out / 8u);
     const void *sum = c.mode == kDenseGated ? reinterpret_cast<const void *>(&df11_dense_sum_kernel<kDenseGated>)
                       : c.mode == kDenseBack ? reinterpret_cast<const void *>(&df11_dense_sum_kernel<kDenseBack>)
+                      : c.mode == kDenseBackAdd ? reinterpret_cast<const void *>(&df11_dense_sum_kernel<kDenseBackAdd>)
                                              : reinterpret_cast<const void *>(&df11_dense_sum_kernel<kDensePlain>);
     return launch_kernel(sum, dim3(static_cast<uint32_t>(std::min<uint64_t>((items + 255) / 256, 8ull * cus))), dim3(256),
                          params, 0, stream, nullptr, nullptr);

@@ -1,0 +1,571 @@
+// Softmax cross entropy through a compressed output head (gfx950), without
+// keeping the logits:
+//
+//   loss = log(sum_v exp(z_v)) - z_y,  z = x W^T
+//   grad = sum_v p_v W_v - W_y
+//
+// A panel of 64 classes gives each token a pair (r, s): the sum s of
+// 2^(z log2(e) - r) over the panel's classes but the target y, r the largest
+// exponent rounded up.  With S and R the pairs' sum, and u = R ln 2 + ln S - z_y
+// the others against the target,
+//
+//   loss = ln(1 + exp(u)),  sum_{v /= y} p_v = sigma(u),  p_y - 1 = -sigma(u)
+//
+// which lose nothing where the target is all but certain.
+//
+// The gradient comes in the same pass, piece by piece of the vocabulary: a
+// piece's exponentials are the left operand of a second product with the same
+// rows of W, whose sums A stay relative to the token's R:
+//
+//   grad = sigma(u) (A / S - W_y)
+//
+// so that the logits are computed once and W is decoded once (recomputing them
+// in a backward pass of its own would take a third product and a second
+// decode).  R is a whole number: where a later piece moves it, the exponentials
+// in BF16 and A are rescaled exactly.  It moves only where a logit passes it by
+// 2^64; the first piece, which has none yet, is short, since its exponentials
+// are rescaled by a pass of their own.
+//
+// Up to kPartialTokens tokens without a gradient the decode is fused into the
+// product, and its slots' sums end in the pairs; otherwise the head is decoded
+// into the workspace, and the dense product's epilogue makes them.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include <stdint.h>
+
+#include "df11.h"
+#include "df11_decoded.h"
+#include "df11_dense.h"
+#include "df11_device.h"
+#include "df11_epilogue.h"
+#include "df11_partials.h"
+#include "df11_slots.h"
+#include "df11_types.h"
+
+namespace {
+
+using df11::kPartialTokens;
+using df11::Partials;
+using df11::PartialStream;
+
+constexpr uint32_t kFirstPiece = 4096;     // classes
+constexpr uint64_t kPieceExps = 64u << 20;  // exponentials of a later piece, tokens times classes
+constexpr uint64_t kMaxRow = 1ull << 22;
+
+// log2(e) in two floats, and ln 2.
+constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596303350001107901e-8f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct SlotLossArgs {
+    PartialStream s;
+    const float *slots;
+    const int64_t *targets;
+    float *stats, *target_logit;
+    uint32_t n_tokens, classes;
+};
+
+// A panel's pairs from the slots of up to TOKENS tokens.
+template <int TOKENS>
+__global__ __launch_bounds__(256) void df11_loss_slots_kernel(SlotLossArgs a) {
+    __shared__ Found s_found[1];
+    __shared__ float s_sum[1][4][TOKENS][kWaveSize];
+    const uint32_t p = blockIdx.x, t0 = blockIdx.y * TOKENS;
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const uint32_t tokens = min(static_cast<uint32_t>(TOKENS), a.n_tokens - t0);
+    panel_sums<1, TOKENS>(&a.s, a.slots, a.n_tokens, p, t0, tokens, s_found, s_sum);
+    const uint32_t v = kPanelRows * p + lane;
+    for (uint32_t t = wave; t < tokens; t += 4u) {
+        const uint32_t token = t0 + t;
+        float z = (s_sum[0][0][t][lane] + s_sum[0][1][t][lane]) + (s_sum[0][2][t][lane] + s_sum[0][3][t][lane]);
+        if (v >= a.classes) {
+            z = -INFINITY;
+        } else if (a.targets[token] == static_cast<int64_t>(v)) {
+            a.target_logit[token] = z;
+            z = -INFINITY;
+        }
+        float top = z;
+#pragma unroll
+        for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+        const float ref = ceilf(top * kLog2eHi), base = ref == -INFINITY ? 0.0f : ref;
+        float sum = __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2eLo, __builtin_fmaf(z, kLog2eHi, -base)));
+#pragma unroll
+        for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+        if (lane == 0) {
+            float *st = a.stats + 2u * (static_cast<uint64_t>(p) * a.n_tokens + token);
+            st[0] = ref;
+            st[1] = sum;
+        }
+    }
+}
+
+// What a token's end needs.
+struct TokenArgs {
+    const int64_t *targets;
+    int64_t ignore_index;
+    const float *stats, *target_logit;
+    float *ref, *sum, *scale;  // running, [token]
+    uint16_t *exps;
+    uint64_t exps_stride;
+    float *loss;
+    uint32_t n_tokens, classes, panels;
+};
+
+// 2^(r - to), 0 for no class.
+__device__ __forceinline__ float ref_scale(float r, float to) {
+    return r == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r - to);
+}
+
+// A piece's pairs joined to what the token has: one wave a token.  Where the
+// reference moves, or a panel has another, exponentials are brought to it.
+__global__ __launch_bounds__(256) void df11_loss_piece_kernel(TokenArgs a, uint32_t first_piece) {
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1);
+    const uint32_t token = blockIdx.x * 4u + threadIdx.x / kWaveSize;
+    if (token >= a.n_tokens) return;
+    const float *st = a.stats + 2u * token;
+    const uint64_t step = 2ull * a.n_tokens;
+    const float was = first_piece ? -INFINITY : a.ref[token];
+    float top = was;
+    for (uint32_t p = lane; p < a.panels; p += kWaveSize) top = fmaxf(top, st[p * step]);
+#pragma unroll
+    for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+    float sum = 0.0f;
+    for (uint32_t p = lane; p < a.panels; p += kWaveSize) sum += st[p * step + 1u] * ref_scale(st[p * step], top);
+#pragma unroll
+    for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+    const float scale = ref_scale(was, top);
+    if (lane == 0) {
+        a.ref[token] = top;
+        a.sum[token] = first_piece ? sum : a.sum[token] * scale + sum;
+        a.scale[token] = scale;
+    }
+    // Eight lanes a panel.
+    for (uint32_t p = lane / 8u; p < a.panels; p += 8u) {
+        const float r = st[p * step];
+        if (r == top || r == -INFINITY) continue;
+        const float f = ref_scale(r, top);
+        bf16_t *e = reinterpret_cast<bf16_t *>(a.exps) + token * a.exps_stride + 64u * p + 8u * (lane % 8u);
+        float v[8];
+        load_vec<bf16_t, 8>(e, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= f;
+        store_vec<bf16_t, 8>(e, v);
+    }
+}
+
+enum TokenKind { kScored = 0, kIgnored = 1, kNoClass = 2 };
+
+__device__ __forceinline__ TokenKind kind_of(int64_t target, int64_t ignore_index, uint32_t classes) {
+    if (target == ignore_index) return kIgnored;
+    return target >= 0 && target < static_cast<int64_t>(classes) ? kScored : kNoClass;
+}
+
+// The others against the target (u above); nothing else in the vocabulary: -inf.
+__device__ __forceinline__ float others(float ref, float sum, float target_logit) {
+    return sum == 0.0f ? -INFINITY : ref * kLn2 + logf(sum) - target_logit;
+}
+
+__device__ __forceinline__ float loss_of(float u) { return u > 0.0f ? u + log1pf(expf(-u)) : log1pf(expf(u)); }
+
+// Sixteen tokens a workgroup, whose pairs lie next to each other, by 64 threads
+// each.
+__global__ __launch_bounds__(1024) void df11_loss_tokens_kernel(TokenArgs a) {
+    __shared__ float s_pair[64][16][2];
+    const uint32_t t = threadIdx.x % 16u, part = threadIdx.x / 16u, token = blockIdx.x * 16u + t;
+    const bool in = token < a.n_tokens;
+    const float *st = a.stats + 2u * (in ? token : 0u);
+    const uint64_t step = 2ull * a.n_tokens;
+    float top = -INFINITY, sum = 0.0f;
+    for (uint32_t p = part; p < a.panels; p += 64u) {
+        const float r = st[p * step], s = st[p * step + 1u], to = fmaxf(top, r);
+        sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
+        top = to;
+    }
+    s_pair[part][t][0] = top;
+    s_pair[part][t][1] = sum;
+    __syncthreads();
+    for (uint32_t half = 32u; half; half >>= 1) {
+        if (part < half) {
+            const float r = s_pair[part + half][t][0], s = s_pair[part + half][t][1], to = fmaxf(top, r);
+            sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
+            top = to;
+            s_pair[part][t][0] = top;
+            s_pair[part][t][1] = sum;
+        }
+        __syncthreads();
+    }
+    if (part || !in) return;
+    const TokenKind kind = kind_of(a.targets[token], a.ignore_index, a.classes);
+    a.loss[token] = kind == kIgnored   ? 0.0f
+                    : kind == kNoClass ? __builtin_nanf("")
+                                       : loss_of(others(top, sum, a.target_logit[token]));
+}
+
+struct GradRowsArgs {
+    TokenArgs t;
+    const uint16_t *w;  // decoded, in tile order
+    float *grad;        // A on entry
+    uint32_t cols;
+};
+
+// The loss and grad = sigma(u) (A / S - W_y): a workgroup a token.
+__global__ __launch_bounds__(256) void df11_loss_rows_kernel(GradRowsArgs a) {
+    const uint32_t token = blockIdx.x;
+    const int64_t target = a.t.targets[token];
+    const TokenKind kind = kind_of(target, a.t.ignore_index, a.t.classes);
+    float u = 0.0f, inverse = 0.0f;
+    if (kind == kScored) {
+        const float sum = a.t.sum[token];
+        u = others(a.t.ref[token], sum, a.t.target_logit[token]);
+        inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0)
+        a.t.loss[token] = kind == kIgnored ? 0.0f : kind == kNoClass ? __builtin_nanf("") : loss_of(u);
+    const float sigma = 1.0f / (1.0f + expf(-u));
+    const uint32_t row = kind == kScored ? static_cast<uint32_t>(target) : 0u, tile_ks = a.cols / 32u;
+    for (uint32_t c = 8u * (blockIdx.y * 256u + threadIdx.x); c < a.cols; c += 8u * 256u * gridDim.y) {
+        float *g = a.grad + static_cast<uint64_t>(token) * a.cols + c;
+        float v[8], wy[8];
+        if (kind == kScored) {
+            load_vec<float, 4>(g, *reinterpret_cast<float(*)[4]>(&v[0]));
+            load_vec<float, 4>(g + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
+            const uint64_t block = (static_cast<uint64_t>(row / 64u) * tile_ks + c / 32u) * 4u + row % 64u / 16u;
+            load_vec<bf16_t, 8>(reinterpret_cast<const bf16_t *>(a.w) + block * 512u + (row % 16u + 2u * (c % 32u)) * 8u, wy);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = sigma * (v[i] * inverse - wy[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = kind == kIgnored ? 0.0f : __builtin_nanf("");
+        }
+        store_vec<float, 4>(g, *reinterpret_cast<float(*)[4]>(&v[0]));
+        store_vec<float, 4>(g + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
+    }
+}
+
+// The losses' sum or mean, in 64 bits and in an order that their number fixes.
+__global__ __launch_bounds__(1024) void df11_loss_total_kernel(const float *loss, const int64_t *targets,
+                                                              int64_t ignore_index, uint32_t n, uint32_t mean,
+                                                              float *total, float *number) {
+    __shared__ double s_sum[16];
+    __shared__ uint32_t s_count[16];
+    double sum = 0.0;
+    uint32_t count = 0;
+    for (uint32_t t = threadIdx.x; t < n; t += 1024u) {
+        sum += loss[t];
+        count += targets[t] != ignore_index ? 1u : 0u;
+    }
+#pragma unroll
+    for (int m = 32; m; m >>= 1) {
+        sum += __shfl_xor(sum, m);
+        count += __shfl_xor(count, m);
+    }
+    if ((threadIdx.x & 63u) == 0) {
+        s_sum[threadIdx.x / 64u] = sum;
+        s_count[threadIdx.x / 64u] = count;
+    }
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int w = 1; w < 16; ++w) {
+        sum += s_sum[w];
+        count += s_count[w];
+    }
+    if (total) *total = static_cast<float>(mean ? sum / count : sum);
+    if (number) *number = static_cast<float>(count);
+}
+
+struct LossGradArgs {
+    const float *grad, *dy, *count;
+    void *dx;
+    uint64_t dy_stride, dx_stride;
+    uint32_t cols, dx_dtype, vec;
+};
+
+__global__ __launch_bounds__(256) void df11_loss_grad_kernel(LossGradArgs a) {
+    const uint32_t token = blockIdx.x;
+    float g = a.dy[token * a.dy_stride];
+    if (a.count) g = *a.count > 0.0f ? g / *a.count : 0.0f;
+    for (uint32_t c = 8u * (blockIdx.y * 256u + threadIdx.x); c < a.cols; c += 8u * 256u * gridDim.y) {
+        const float *from = a.grad + static_cast<uint64_t>(token) * a.cols + c;
+        float v[8];
+        load_vec<float, 4>(from, *reinterpret_cast<float(*)[4]>(&v[0]));
+        load_vec<float, 4>(from + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= g;
+        const uint64_t at = token * a.dx_stride + c;
+        if (a.vec && a.dx_dtype == DF11_BF16) {
+            store_vec<bf16_t, 8>(static_cast<bf16_t *>(a.dx) + at, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) store_as(a.dx, at + i, a.dx_dtype, v[i]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host.
+
+// Where a call's parts of the workspace begin.
+struct LossPlan {
+    bool slots;         // the fused product
+    uint32_t piece;     // classes of a later piece
+    uint64_t weights, stats, logit, ref, sum, scale, exps, split, end;
+};
+
+// Classes of the piece that begins at class `from`.
+uint32_t piece_at(uint32_t rows, uint32_t piece, uint32_t from) {
+    return std::min(from ? piece : kFirstPiece, rows - from);
+}
+
+bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan &p) {
+    const uint32_t cols = w->tile_cols, rows = static_cast<uint32_t>(w->h.n_elements / cols);
+    p = LossPlan{};
+    uint64_t at = 0;
+    const auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    p.slots = !grad && tokens <= kPartialTokens;
+    if (p.slots) {
+        Partials parts{};
+        if (df11::partial_products(&w, 1, nullptr, 0, tokens, nullptr, 0, nullptr, parts)) return false;
+        p.weights = take(parts.slot_bytes);
+    } else {
+        p.weights = take(decoded_bytes(&w, 1));
+    }
+    p.logit = take(4ull * tokens);
+    uint32_t most = rows;  // classes whose pairs are held at once
+    if (grad) {
+        // Later pieces of about the same size, at least the first one's (a smaller
+        // product does not fill the chip).
+        const uint32_t rest = rows - piece_at(rows, 0, 0);
+        const uint64_t most_classes = std::max<uint64_t>(kFirstPiece, kPieceExps / tokens);
+        const uint64_t pieces = std::max<uint64_t>(1, (rest + most_classes - 1) / most_classes);
+        p.piece = static_cast<uint32_t>(round_up((rest + pieces - 1) / pieces, 256));
+        most = 0;
+        uint64_t split = 0;
+        for (uint32_t from = 0, n; from < rows; from += n) {
+            n = piece_at(rows, p.piece, from);
+            most = std::max(most, n);
+            const uint64_t more = df11::dense_workspace(df11::kDenseBackAdd, 1, tokens, n, cols);
+            if (more == ~0ull) return false;
+            split = std::max(split, more);
+        }
+        p.ref = take(4ull * tokens);
+        p.sum = take(4ull * tokens);
+        p.scale = take(4ull * tokens);
+        p.exps = take(2ull * tokens * most);
+        p.split = take(split);
+    }
+    p.stats = take(8ull * (most / 64) * tokens);
+    p.end = at;
+    return true;
+}
+
+template <typename T>
+T *at(void *workspace, uint64_t offset) {
+    return reinterpret_cast<T *>(static_cast<uint8_t *>(workspace) + offset);
+}
+
+// The pairs of every panel, and the losses from them.
+int loss_only(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t tokens, uint32_t cols,
+              const LossPlan &p, TokenArgs t, void *ws, hipStream_t stream) {
+    const uint32_t rows = static_cast<uint32_t>(w->h.n_elements / cols);
+    int rc;
+    if (p.slots) {
+        Partials parts{};
+        rc = df11::partial_products(&w, 1, x, x_stride, tokens, at<float>(ws, p.weights), p.logit - p.weights, stream, parts);
+        if (rc) return rc;
+        SlotLossArgs a{parts.s[0], at<float>(ws, p.weights), t.targets, at<float>(ws, p.stats), at<float>(ws, p.logit),
+                       tokens, t.classes};
+        void *params[] = {&a};
+        // (tokens of a workgroup as for the products' sums, df11_product.hip)
+        const bool one = tokens == 1 || static_cast<uint64_t>(rows / 64) * tokens <= 512;
+        rc = launch_kernel(one ? reinterpret_cast<const void *>(&df11_loss_slots_kernel<1>)
+                               : reinterpret_cast<const void *>(&df11_loss_slots_kernel<4>),
+                           dim3(rows / 64, one ? tokens : (tokens + 3) / 4), dim3(256), params, 0, stream, nullptr, nullptr);
+    } else {
+        df11::DenseCall d{};
+        rc = decode_weights(&w, 1, at<void>(ws, p.weights), d.w, stream);
+        if (rc) return rc;
+        d.mode = df11::kDenseStats;
+        d.left[0] = x;
+        d.left_stride = x_stride;
+        d.tokens = tokens;
+        d.rows = rows;
+        d.cols = cols;
+        d.loss.targets = t.targets;
+        d.loss.stats = at<float>(ws, p.stats);
+        d.loss.target_logit = at<float>(ws, p.logit);
+        d.loss.classes = t.classes;
+        rc = df11::dense_product(d, Epilogue{}, nullptr, stream);
+    }
+    if (rc) return rc;
+    t.panels = rows / 64;
+    void *params[] = {&t};
+    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_tokens_kernel), dim3((tokens + 15) / 16), dim3(1024),
+                         params, 0, stream, nullptr, nullptr);
+}
+
+// Blocks of a token's columns, eight a thread.
+uint32_t column_blocks(uint32_t cols) { return std::min(64u, (cols / 8 + 255) / 256); }
+
+int loss_and_grad(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t tokens, uint32_t cols,
+                  const LossPlan &p, TokenArgs t, float *grad, void *ws, hipStream_t stream) {
+    const uint32_t rows = static_cast<uint32_t>(w->h.n_elements / cols);
+    const uint16_t *decoded[2] = {};
+    int rc = decode_weights(&w, 1, at<void>(ws, p.weights), decoded, stream);
+    t.ref = at<float>(ws, p.ref);
+    t.sum = at<float>(ws, p.sum);
+    t.scale = at<float>(ws, p.scale);
+    t.exps = at<uint16_t>(ws, p.exps);
+    for (uint32_t from = 0, n; !rc && from < rows; from += n) {
+        n = piece_at(rows, p.piece, from);
+        df11::DenseCall d{};
+        d.mode = df11::kDenseExp;
+        d.left[0] = x;
+        d.left_stride = x_stride;
+        d.w[0] = decoded[0] + static_cast<uint64_t>(from) * cols;  // (whole panels)
+        d.tokens = tokens;
+        d.rows = n;
+        d.cols = cols;
+        d.loss.targets = t.targets;
+        d.loss.stats = at<float>(ws, p.stats);
+        d.loss.target_logit = at<float>(ws, p.logit);
+        d.loss.ref = from ? t.ref : nullptr;
+        d.loss.exps = t.exps;
+        d.loss.exps_stride = n;
+        d.loss.first_class = from;
+        d.loss.classes = t.classes;
+        rc = df11::dense_product(d, Epilogue{}, nullptr, stream);
+        if (rc) break;
+        t.panels = n / 64;
+        t.exps_stride = n;
+        uint32_t first = from == 0;
+        void *params[] = {&t, &first};
+        rc = launch_kernel(reinterpret_cast<const void *>(&df11_loss_piece_kernel), dim3((tokens + 3) / 4), dim3(256),
+                           params, 0, stream, nullptr, nullptr);
+        if (rc) break;
+        d.mode = df11::kDenseBackAdd;
+        d.left[0] = t.exps;
+        d.left_stride = n;
+        d.loss.scale = t.scale;
+        Epilogue e{};
+        e.out = grad;
+        e.out_stride = cols;
+        e.out_dtype = DF11_FP32;
+        rc = df11::dense_product(d, e, at<float>(ws, p.split), stream);
+    }
+    if (rc) return rc;
+    GradRowsArgs a{t, decoded[0], grad, cols};
+    void *params[] = {&a};
+    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_rows_kernel), dim3(tokens, column_blocks(cols)), dim3(256),
+                         params, 0, stream, nullptr, nullptr);
+}
+
+int check_head(const df11_device_stream *w, uint32_t n_tokens, uint32_t in_features, uint32_t out_features) {
+    if (!w) return DF11_E_INVALID_ARG;
+    const int rc = df11::check_stream(w);
+    if (rc) return rc;
+    if (in_features < 32 || in_features % 32 || !out_features || out_features % kPanelRows ||
+        static_cast<uint64_t>(in_features) * out_features != w->h.n_elements || w->tile_cols != in_features)
+        return DF11_E_INVALID_ARG;
+    if (in_features > kMaxRow || out_features > kMaxRow || static_cast<uint64_t>(n_tokens) * in_features >= (1ull << 32))
+        return DF11_E_TOO_LARGE;
+    return DF11_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t df11_cross_entropy_workspace(const df11_device_stream *w, uint32_t n_tokens, int with_grad) {
+    LossPlan p{};
+    if (!w || !n_tokens || df11::check_stream(w) || !w->h.n_elements || !w->tile_cols) return 0;
+    const uint64_t rows = w->h.n_elements / w->tile_cols;
+    if (rows > kMaxRow || check_head(w, n_tokens, w->tile_cols, static_cast<uint32_t>(rows))) return 0;
+    return loss_plan(w, n_tokens, with_grad != 0, p) ? p.end : 0;
+}
+
+int df11_cross_entropy(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t n_tokens,
+                       uint32_t in_features, uint32_t out_features, const df11_loss *l, void *workspace,
+                       uint64_t workspace_bytes, void *hip_stream) {
+    int rc = check_head(w, n_tokens, in_features, out_features);
+    if (rc) return rc;
+    if (!l || !l->vocab || l->vocab > out_features || l->mean > 1 || (l->total && !aligned(l->total, 4)) ||
+        (l->count && !aligned(l->count, 4)))
+        return DF11_E_INVALID_ARG;
+    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    const uint64_t grad_span = l->grad ? 4ull * n_tokens * in_features : 0;
+    if (n_tokens) {
+        if (!x || !aligned(x, 16) || x_stride % 8 || x_stride > kMaxRow || !l->targets || !aligned(l->targets, 8) ||
+            !l->loss || !aligned(l->loss, 4) || (l->grad && !aligned(l->grad, 16)))
+            return DF11_E_INVALID_ARG;
+    }
+    // Everything that is written lies apart from the rest.
+    const uint64_t x_span = n_tokens ? 2 * ((n_tokens - 1ull) * x_stride + in_features) : 0;
+    const void *outs[] = {l->loss, l->total, l->count, l->grad, workspace};
+    uint64_t spans[] = {4ull * n_tokens, l->total ? 4ull : 0ull, l->count ? 4ull : 0ull, grad_span, 0};
+    const auto clear = [&](int i) {
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i], spans[i], outs[j], spans[j])) return false;
+        return !overlaps(outs[i], spans[i], x, x_span) && !overlaps(outs[i], spans[i], l->targets, 8ull * n_tokens) &&
+               !df11::stream_overlaps(w, outs[i], spans[i]);
+    };
+    for (int i = 0; i < 4; ++i)
+        if (!clear(i)) return DF11_E_INVALID_ARG;
+    (void)hipGetLastError();
+    if (n_tokens) {
+        LossPlan p{};
+        if (!loss_plan(w, n_tokens, l->grad != nullptr, p)) return DF11_E_HIP;
+        if (!workspace || !aligned(workspace, 256)) return DF11_E_INVALID_ARG;
+        if (workspace_bytes < p.end) return DF11_E_BUFFER_TOO_SMALL;
+        spans[4] = p.end;
+        if (!clear(4)) return DF11_E_INVALID_ARG;
+        TokenArgs t{};
+        t.targets = l->targets;
+        t.ignore_index = l->ignore_index;
+        t.stats = at<float>(workspace, p.stats);
+        t.target_logit = at<float>(workspace, p.logit);
+        t.loss = l->loss;
+        t.n_tokens = n_tokens;
+        t.classes = l->vocab;
+        rc = l->grad ? loss_and_grad(w, x, x_stride, n_tokens, in_features, p, t, l->grad, workspace, stream)
+                     : loss_only(w, x, x_stride, n_tokens, in_features, p, t, workspace, stream);
+        if (rc) return rc;
+    }
+    if (!l->total && !l->count) return DF11_OK;
+    const float *loss = l->loss;
+    const int64_t *targets = l->targets;
+    int64_t ignore_index = l->ignore_index;
+    uint32_t n = n_tokens, mean = l->mean;
+    float *total = l->total, *count = l->count;
+    void *params[] = {&loss, &targets, &ignore_index, &n, &mean, &total, &count};
+    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_total_kernel), dim3(1), dim3(1024), params, 0, stream,
+                         nullptr, nullptr);
+}
+
+int df11_cross_entropy_grad(const float *grad, const float *dy, uint64_t dy_stride, const float *count,
+                            uint32_t n_tokens, uint32_t in_features, void *dx, uint64_t dx_stride, uint32_t dx_dtype,
+                            void *hip_stream) {
+    const uint32_t bytes = dx_dtype == DF11_FP16 ? 0 : dtype_bytes(dx_dtype);
+    if (!bytes || in_features < 32 || in_features % 32) return DF11_E_INVALID_ARG;
+    if (in_features > kMaxRow || static_cast<uint64_t>(n_tokens) * in_features >= (1ull << 32)) return DF11_E_TOO_LARGE;
+    if (!n_tokens) return DF11_OK;
+    if (!grad || !aligned(grad, 16) || !dy || !aligned(dy, 4) || dy_stride > (1ull << 31) || !dx || !aligned(dx, bytes) ||
+        dx_stride > (1ull << 31) || (n_tokens > 1 && dx_stride < in_features) || (count && !aligned(count, 4)))
+        return DF11_E_INVALID_ARG;
+    const uint64_t span = ((n_tokens - 1ull) * dx_stride + in_features) * bytes;
+    if (overlaps(dx, span, grad, 4ull * n_tokens * in_features) ||
+        overlaps(dx, span, dy, 4 * ((n_tokens - 1ull) * dy_stride + 1)) || overlaps(dx, span, count, count ? 4 : 0))
+        return DF11_E_INVALID_ARG;
+    LossGradArgs a{grad, dy, count, dx, dy_stride, dx_stride, in_features, dx_dtype,
+                   aligned(dx, 16) && dx_stride % 8 == 0 ? 1u : 0u};
+    (void)hipGetLastError();
+    void *params[] = {&a};
+    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_grad_kernel), dim3(n_tokens, column_blocks(in_features)),
+                         dim3(256), params, 0, static_cast<hipStream_t>(hip_stream), nullptr, nullptr);
+}
+
+}  // extern "C"

@@ -32,17 +32,16 @@
 #include "df11_columns.h"
 #include "df11_dense.h"
 #include "df11_device.h"
+#include "df11_decoded.h"
 #include "df11_epilogue.h"
 #include "df11_partials.h"
+#include "df11_slots.h"
 
 namespace {
 
-using df11::kPartialGroups;
 using df11::kPartialTokens;
 using df11::Partials;
 using df11::PartialStream;
-
-constexpr uint32_t kPanelRows = 64;  // output features of one panel
 
 struct SumArgs {
     PartialStream s[2];
@@ -51,100 +50,19 @@ struct SumArgs {
     uint32_t n_tokens, features;
 };
 
-// Panel of element e of a tile-ordered stream.
-__device__ __forceinline__ uint32_t panel_of(const PartialStream &s, uint32_t e) {
-    return df11::panel_of_step(min(e, s.n_elements - 1u) >> 11, s.tile_magic);
-}
-
-__device__ __forceinline__ uint32_t out_pos_of(const PartialStream &s, uint32_t g) {
-    return s.out_pos[min(g, s.n_groups)];
-}
-
-// First super-group of workgroup w's range: floor(w n_super / n_wg), as
-// w * (n_super / n_wg) + floor(w * (n_super % n_wg) / n_wg) in 32 bits
-// (n_wg is a grid size, far below 2^16).
-__device__ __forceinline__ uint32_t range_begin(const PartialStream &s, uint32_t w) {
-    return w * (s.n_super / s.n_wg) + w * (s.n_super % s.n_wg) / s.n_wg;
-}
-
-// The workgroups [lo, hi) whose ranges touch a panel, and the panels that
-// the first of them holds before it.  Ranges follow the stream, so those of
-// a panel are consecutive, and every one but the first begins with it.
-struct Found {
-    uint32_t lo, hi, skip;
-};
-
-// Finds them with all threads at once: a search would wait for one load
-// after the other.
-__device__ __forceinline__ void find_ranges(const PartialStream &s, uint32_t p, Found *f) {
-    for (uint32_t w = threadIdx.x; w < s.n_wg; w += blockDim.x) {
-        const uint32_t a = panel_of(s, out_pos_of(s, range_begin(s, w) * kPartialGroups));
-        const uint32_t b = panel_of(s, max(out_pos_of(s, range_begin(s, w + 1u) * kPartialGroups), 1u) - 1u);
-        if (a <= p && p <= b) {
-            atomicMin(&f->lo, w);
-            atomicMax(&f->hi, w + 1u);
-            atomicMax(&f->skip, p - a);
-        }
-    }
-}
-
-// One workgroup adds the slots of one panel for up to TOKENS tokens: a lane
-// per output feature, the slots split between the four waves, whose sums
-// meet in LDS in wave order.  A wave takes several slots at once, so that
-// more loads than one slot's are in flight.  What bounds it is the chain of a
+// One workgroup adds the slots of one panel for up to TOKENS tokens
+// (panel_sums) and applies the epilogue.  What bounds it is the chain of a
 // launch, the ranges' search and two rounds of loads: 4.5 us of a product's
 // 45 for 4096 x 14336 at one token, whose slots are half a megabyte.
 template <bool kGated, int TOKENS>
 __global__ __launch_bounds__(256) void df11_sum_slots_kernel(SumArgs a) {
     constexpr int kStreams = kGated ? 2 : 1;
-    constexpr int kAtOnce = TOKENS >= 4 ? 4 : 8;  // slots
     __shared__ Found s_found[kStreams];
     __shared__ float s_sum[kStreams][4][TOKENS][kWaveSize];
     const uint32_t p = blockIdx.x, t0 = blockIdx.y * TOKENS;
     const uint32_t lane = threadIdx.x & (kWaveSize - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
     const uint32_t tokens = min(static_cast<uint32_t>(TOKENS), a.n_tokens - t0);
-    const uint64_t slot = static_cast<uint64_t>(kPanelRows) * a.n_tokens;
-    if (threadIdx.x < kStreams) s_found[threadIdx.x] = Found{~0u, 0u, 0u};
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kStreams; ++i) find_ranges(a.s[i], p, &s_found[i]);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kStreams; ++i) {
-        const PartialStream &s = a.s[i];
-        const Found f = s_found[i];
-        const uint32_t n = f.lo < f.hi ? (f.hi - f.lo) * kPartialGroups : 0u, each = (n + 3u) / 4u;
-        const uint32_t begin = wave * each, end = min(n, begin + each);
-        const uint32_t skip = min(f.skip, s.wg_panels - 1u);
-        // Float offset of the c-th group slot's slot.
-        auto at = [&](uint32_t c) {
-            return s.base + (static_cast<uint64_t>(f.lo * kPartialGroups + c) * s.wg_panels +
-                             (c < kPartialGroups ? skip : 0u)) * slot;
-        };
-        float sum[TOKENS];
-#pragma unroll
-        for (int t = 0; t < TOKENS; ++t) sum[t] = 0.0f;
-        const float *slots = a.slots + static_cast<uint64_t>(t0) * kPanelRows + lane;
-        for (uint32_t c = begin; c < end; c += kAtOnce) {
-            // (past the end the last slot again, not added; past the last
-            // token the first one, not written)
-            float v[kAtOnce][TOKENS];
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                const float *q = slots + at(min(c + k, end - 1u));
-#pragma unroll
-                for (int t = 0; t < TOKENS; ++t) v[k][t] = q[t < static_cast<int>(tokens) ? t * kPanelRows : 0u];
-            }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-                if (c + k < end)
-#pragma unroll
-                    for (int t = 0; t < TOKENS; ++t) sum[t] += v[k][t];
-        }
-#pragma unroll
-        for (int t = 0; t < TOKENS; ++t) s_sum[i][wave][t][lane] = sum[t];
-    }
-    __syncthreads();
+    panel_sums<kStreams, TOKENS>(a.s, a.slots, a.n_tokens, p, t0, tokens, s_found, s_sum);
     for (uint32_t t = wave; t < tokens; t += 4u) {
         float z[2] = {};
 #pragma unroll
@@ -361,65 +279,6 @@ uint64_t slots_bytes(const df11_device_stream *const *ws, uint32_t n, uint32_t n
     Partials p{};
     if (df11::partial_products(ws, n, nullptr, 0, n_tokens, nullptr, 0, nullptr, p)) return 0;
     return p.slot_bytes;
-}
-
-// Work counters of a decode.  Those of a weight are left alone: nothing orders
-// this call after launches of the same weight by other threads, or a graph's
-// replays after anything.  Two streams of kCounted weights or more decode by
-// the dynamic schedule with counters of the workspace, zeroed first; shorter
-// ones, and one alone, by the static schedule.  Gate and up of 64 tokens,
-// counters against static: 14336 x 4096 each 131 against 136 us, 8192 x 4096
-// 85 against 83, 4096 x 4096 56.0 against 54.4.
-constexpr uint64_t kCounted = 3ull << 24;
-constexpr uint32_t kCounterWords = 2 * DF11_SCHEDULE_WORDS;
-
-__global__ void df11_zero_counters_kernel(uint32_t *p) {
-    for (uint32_t i = threadIdx.x; i < kCounterWords; i += blockDim.x) p[i] = 0;
-}
-
-// Whether there are two different streams.  (Streams may share a buffer: those
-// of a matrix and of its negative have the same exponents.)
-bool two_streams(const df11_device_stream *const *ws, uint32_t n) {
-    return n == 2 && (ws[1]->enc != ws[0]->enc || ws[1]->sm != ws[0]->sm);
-}
-
-// Bytes of the decoded weights (one copy of a stream given twice) and of the
-// counters of their decode.
-uint64_t decoded_bytes(const df11_device_stream *const *ws, uint32_t n) {
-    const uint64_t one = round_up(2 * ws[0]->h.n_elements, 256);
-    if (!two_streams(ws, n)) return one;
-    return 2 * one + (ws[0]->h.n_elements >= kCounted ? round_up(4 * kCounterWords, 256) : 0);
-}
-
-// Decodes the streams into the workspace in tile order, as they are stored;
-// out[i] receives where.
-int decode_weights(const df11_device_stream *const *ws, uint32_t n, void *workspace, const uint16_t **out,
-                   hipStream_t stream) {
-    const uint64_t one = round_up(2 * ws[0]->h.n_elements, 256);
-    df11_device_stream flat[2];
-    uint16_t *to[2];
-    const bool both = two_streams(ws, n);
-    // (streams without counters of their own ask for the static schedule)
-    const bool counted = both && ws[0]->h.n_elements >= kCounted && ws[0]->schedule && ws[1]->schedule;
-    uint32_t *counters = counted ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + 2 * one) : nullptr;
-    for (uint32_t i = 0; i < n; ++i) {
-        flat[i] = *ws[i];
-        flat[i].tile_cols = 0;
-        flat[i].schedule = counted ? counters + i * DF11_SCHEDULE_WORDS : nullptr;
-        to[i] = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + (both ? i * one : 0));
-        out[i] = to[i];
-    }
-    if (counted) {
-        void *params[] = {&counters};
-        const int rc = launch_kernel(reinterpret_cast<const void *>(&df11_zero_counters_kernel), dim3(1), dim3(256),
-                                     params, 0, stream, nullptr, nullptr);
-        if (rc) return rc;
-    }
-    if (both && flat[0].groups_per_workgroup == flat[1].groups_per_workgroup)
-        return df11_decompress_batch(flat, 2, to, stream);
-    int rc = df11_decompress(&flat[0], to[0], stream);
-    if (!rc && both) rc = df11_decompress(&flat[1], to[1], stream);
-    return rc;
 }
 
 uint64_t forward_workspace(const df11_device_stream *const *ws, uint32_t n, uint32_t n_tokens, uint32_t cols) {

@@ -881,4 +881,5 @@ def rans_compress(tensor: ArrayLike, shape: Optional[Sequence[int]] = None, devi
 
 # The operators around the products, under the same roof as the products.
 from .attention import append_kv, rotary_table, tree_attention  # noqa: E402,F401
+from .loss import linear_cross_entropy  # noqa: E402,F401
 from .operators import gated_matmul, matmul_epilogue, rms_norm  # noqa: E402,F401

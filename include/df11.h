@@ -655,6 +655,69 @@ int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_str
                               uint32_t in_features, uint32_t out_features, const df11_product_grad *g,
                               void *workspace, uint64_t workspace_bytes, void *hip_stream);
 
+/* The softmax cross entropy through a compressed output head, without keeping
+ * the logits (host struct of device pointers).  With z = x W^T over the classes
+ * 0 .. vocab - 1,
+ *   loss = log(sum over v of exp(z_v)) - z_target
+ *   grad = d loss / dx = sum over v of p_v W_v - W_target,  p = softmax(z)
+ *   targets        n_tokens int64.  A token whose target is ignore_index has a
+ *                  loss and a gradient of zero; one whose target is no class
+ *                  otherwise, NaN
+ *   loss           n_tokens floats
+ *   total          a float, or NULL: the sum of loss over the tokens, divided by
+ *                  their number if mean
+ *   count          a float, or NULL: that number (tokens not ignored)
+ *   grad           n_tokens x in_features floats, 16-byte aligned, or NULL; kept
+ *                  for df11_cross_entropy_grad
+ *   vocab          1 .. out_features; W's rows from there on are padding
+ *   mean           0 or 1 */
+typedef struct df11_loss {
+    const int64_t *targets;
+    float *loss;
+    float *total;
+    float *count;
+    float *grad;
+    int64_t ignore_index;
+    uint32_t vocab;
+    uint32_t mean;
+} df11_loss;
+
+/* Bytes of df11_cross_entropy's workspace on the current device (with_grad: with
+ * l->grad); 0 for streams that the call refuses, or where nothing needs
+ * computing. */
+uint64_t df11_cross_entropy_workspace(const df11_device_stream *w, uint32_t n_tokens, int with_grad);
+
+/* The loss, and with l->grad its gradient with respect to x in the same call, W
+ * frozen.  Logits are float and never stored; a token's sum of exponentials is
+ * taken without the target's own, so that the loss and p_target - 1 keep their
+ * relative accuracy where the target is all but certain.  For grad the other
+ * exponentials are rounded to BF16, the matrix cores' operand type (at most 2^-8
+ * of each), piece by piece of the vocabulary, and its sums are float.
+ *   w, x, in_features, out_features   as for df11_matmul_epilogue, out_features
+ *                and in_features up to 2^22, n_tokens * in_features below 2^32
+ *   workspace    device, 256-byte aligned, df11_cross_entropy_workspace bytes;
+ *                holds nothing between calls, but calls that overlap in time need
+ *                one each
+ * A token whose x holds an infinity or a NaN, or whose logits overflow, gets NaN;
+ * others are not touched by it.  Results do not change from run to run; calls of
+ * one stream may overlap in time.  With no tokens only total and count are
+ * written.
+ * Errors: DF11_E_INVALID_ARG, DF11_E_BAD_STREAM, DF11_E_TOO_LARGE,
+ * DF11_E_BUFFER_TOO_SMALL, DF11_E_HIP. */
+int df11_cross_entropy(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t n_tokens,
+                       uint32_t in_features, uint32_t out_features, const df11_loss *l, void *workspace,
+                       uint64_t workspace_bytes, void *hip_stream);
+
+/* x's gradient from the one that df11_cross_entropy kept: dx = g grad, rounded
+ * once, where a token's g is dy[token * dy_stride], or with count (the call's, of a
+ * mean) that over count (zero if it is zero).  dy_stride 0: one
+ * dy for all tokens.  dx: n_tokens x in_features of dx_dtype (DF11_BF16 or
+ * DF11_FP32), dx_stride elements from row to row, overlapping nothing else.
+ * Errors: DF11_E_INVALID_ARG, DF11_E_TOO_LARGE, DF11_E_HIP. */
+int df11_cross_entropy_grad(const float *grad, const float *dy, uint64_t dy_stride, const float *count,
+                            uint32_t n_tokens, uint32_t in_features, void *dx, uint64_t dx_stride, uint32_t dx_dtype,
+                            void *hip_stream);
+
 /* ---------------------------------------------------------------------------
  * A paged cache of keys and values, and attention over it.  Not on the page.
  * Sequence s of a batch holds lengths[s] tokens in the cache and brings the
