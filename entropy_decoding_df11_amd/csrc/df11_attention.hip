@@ -49,9 +49,9 @@ using df11::SeqShape;
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 
-constexpr uint32_t kWaves = 4;
-constexpr uint32_t kBlock = 32;  // places of one wave's turn
-static_assert(kStepPlaces == kWaves * kBlock, "a step is one block for each wave");
+constexpr uint32_t kBlock = 32;   // places of one block of scores
+constexpr uint32_t kFewWaves = 4;  // waves of the kernel for few rows
+static_assert(kStepPlaces == kFewWaves * kBlock, "a step is one block for each wave");
 
 struct AttentionArgs {
     df11::KvBatch b;
@@ -97,11 +97,12 @@ __device__ __forceinline__ SeqShape shape_of(const AttentionArgs &a, uint32_t s)
 }
 
 // Units of all sequences, and of those before sequence `until`, by a whole
-// workgroup of 256 threads.
+// workgroup of THREADS threads.
+template <uint32_t THREADS>
 __device__ __forceinline__ void count_units(const AttentionArgs &a, uint32_t until, uint64_t &all, uint64_t &before,
                                             uint64_t (*s_part)[2]) {
     uint64_t sum[2] = {0, 0};
-    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += 256u) {
+    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += THREADS) {
         const uint64_t n = df11::seq_units(shape_of(a, s), a.kv_heads);
         sum[0] += n;
         if (s < until) sum[1] += n;
@@ -118,7 +119,7 @@ __device__ __forceinline__ void count_units(const AttentionArgs &a, uint32_t unt
     __syncthreads();
     all = before = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (uint32_t w = 0; w < THREADS / 64u; ++w) {
         all += s_part[w][0];
         before += s_part[w][1];
     }
@@ -131,10 +132,11 @@ struct Found {
     uint32_t seq;
 };
 
+template <uint32_t THREADS>
 __device__ __forceinline__ Found find_unit(const AttentionArgs &a, uint64_t u, uint64_t (*s_part)[2], Found *s_found) {
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x / 64u;
     uint64_t base = 0;
-    for (uint32_t at = 0; at < a.b.n_seqs; at += 256u) {
+    for (uint32_t at = 0; at < a.b.n_seqs; at += THREADS) {
         const uint32_t s = at + threadIdx.x;
         const uint64_t n = s < a.b.n_seqs ? df11::seq_units(shape_of(a, s), a.kv_heads) : 0;
         uint64_t to = n;
@@ -149,7 +151,7 @@ __device__ __forceinline__ Found find_unit(const AttentionArgs &a, uint64_t u, u
         for (uint32_t w = 0; w < wave; ++w) first += s_part[w][0];
         if (u >= first && u < first + n) *s_found = Found{first, s};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) base += s_part[w][0];
+        for (uint32_t w = 0; w < THREADS / 64u; ++w) base += s_part[w][0];
         __syncthreads();
         if (u < base) break;
     }
@@ -173,32 +175,212 @@ __device__ __forceinline__ void row_of(const AttentionArgs &a, const Part &p, ui
     head = p.head * a.group + at % a.group;
 }
 
-template <typename T, int KK, int M, bool kWhole16>
-struct Wave {
-    static constexpr int DP = 32 * KK;         // head_dim padded
-    static constexpr int kChunks = DP / 8;     // 16-byte chunks of a row
+// What a wave keeps of its rows: M tiles of 16 from row0 of the part's tile on,
+// lane l having row l mod 16 of each.
+template <typename T, int KK, int M>
+struct Rows {
+    static constexpr int DP = 32 * KK;      // head_dim padded
+    static constexpr int kChunks = DP / 8;  // 16-byte chunks of a row of K or V
     static constexpr int kTilesD = DP / 16;
-    static constexpr int kVBytes = kBlock * DP * 2;
-    static constexpr int kVLoads = kVBytes / 1024;
-    static constexpr int kVRows = 64 / kChunks;  // rows of one load
     using Vec = vec_t<T, 8>;
 
     const AttentionArgs &a;
     const Part &p;
-    uint8_t *lds;  // two buffers of kVBytes
-    uint32_t lane, wave, quarter, l16;
-    const int32_t *table;
+    uint32_t row0, lane, quarter, l16;
 
     Vec q[M][KK];
     floatx4 o[M][kTilesD];
     float m[M], l[M];  // a lane's row: its reference (raw score) and this lane's part of the sum
-    Vec k[2][KK];
-    uint32_t valid;    // of the block in k: places whose page exists
 
-    // Pair of chunks of a row of V is kept at its number XOR this.
+    __device__ __forceinline__ Rows(const AttentionArgs &args, const Part &part, uint32_t first_row)
+        : a(args), p(part), row0(first_row), lane(threadIdx.x & 63u), quarter(lane >> 4), l16(lane & 15u) {
+        const uint32_t last_chunk = a.dim / 8u - 1u;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < kTilesD; ++d) o[i][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t token, head;
+            row_of(a, p, row0 + 16u * i + l16, token, head);
+            const bool there = token < p.s.rows;
+            const T *row = static_cast<const T *>(a.q) +
+                           (static_cast<uint64_t>(p.s.begin) + (there ? token : 0u)) * a.q_stride +
+                           (there ? head : p.head * a.group) * a.q_head_stride;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                const uint32_t chunk = 4u * kk + quarter;
+                q[i][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(chunk, last_chunk));
+                if (!there || chunk > last_chunk) q[i][kk] = Vec{};
+            }
+        }
+    }
+
+    // A pair of chunks of a row of V in LDS is kept at its number XOR this.
     static __device__ __forceinline__ uint32_t turn(uint32_t row) {
         return DP >= 128 ? row & 7u : (row >> 1) & 3u;
     }
+
+    // The places of the block at key0 that a row sees, as far as this lane has
+    // them: bit 4 t + e is place 16 t + 4 quarter + e.  (Bits and selects only:
+    // out of nested branches around single elements of the scores the compiler
+    // has made code that keeps the masked ones.)
+    __device__ __forceinline__ uint32_t seen(uint32_t token, const uint8_t *mask_row, uint32_t key0, uint32_t valid) const {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t key = key0 + 16u * t + 4u * quarter;
+            if (a.mask) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t j = key + e - p.s.length;  // (wraps where the place is cached)
+                    uint32_t bit = key + e < p.s.length ? 1u : 0u;
+                    if (j < a.mask_cols) bit |= mask_row[j] != 0 ? 1u : 0u;
+                    bits |= bit << (4 * t + e);
+                }
+            } else {
+                const uint32_t end = p.s.length + token + 1u;  // places that the row sees
+                const uint32_t n = key < end ? min(end - key, 4u) : 0u;
+                bits |= ((1u << n) - 1u) << (4 * t);
+            }
+        }
+        return bits & (((valid >> (4u * quarter)) & 15u) | (((valid >> (16u + 4u * quarter)) & 15u) << 4));
+    }
+
+    __device__ __forceinline__ bool masked(uint32_t key0, uint32_t valid) const {
+        return key0 + kBlock > p.s.length || valid != ~0u;
+    }
+
+    __device__ __forceinline__ void mask(floatx4 (&s)[M][2], uint32_t key0, uint32_t valid) const {
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            uint32_t token, head;
+            row_of(a, p, row0 + 16u * i + l16, token, head);
+            const uint8_t *mask_row =
+                a.mask ? a.mask + (p.s.begin + static_cast<uint64_t>(min(token, p.s.rows - 1u))) * a.mask_stride : nullptr;
+            const uint32_t bits = seen(token, mask_row, key0, valid);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[i][t][e] = (bits >> (4 * t + e)) & 1u ? s[i][t][e] : -INFINITY;
+        }
+    }
+
+    // Scores to weights (in s, and rounded in w), the reference moved where a
+    // score passes it by the headroom.
+    __device__ __forceinline__ void weigh(floatx4 (&s)[M][2], Vec (&w)[M]) {
+        float top[M];
+        bool moves = false;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            top[i] = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
+                           fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
+            moves = moves || top[i] > m[i] + a.headroom;
+        }
+        if (__ballot(moves)) {
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                float to = fmaxf(top[i], __shfl_xor(top[i], 16));
+                to = fmaxf(m[i], fmaxf(to, __shfl_xor(to, 32)));
+                const float f = weight_of(m[i] * a.c, to * a.c);
+                m[i] = to;
+                l[i] *= f;
+#pragma unroll
+                for (int d = 0; d < kTilesD; ++d) o[i][d] *= f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float mc = m[i] == -INFINITY ? 0.0f : m[i] * a.c;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -mc));
+                    l[i] += x;
+                    s[i][t][e] = x;
+                    w[i][4 * t + e] = static_cast<T>(x);
+                }
+        }
+    }
+
+    // The block's part of o, its rows of V in LDS at v.
+    __device__ __forceinline__ void add(const Vec (&w)[M], const uint8_t *v) {
+#pragma unroll
+        for (int d = 0; d < kTilesD; ++d) {
+            union {
+                shortx4 s[2];
+                Vec v;
+            } u;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t row = 16u * t + 4u * quarter + (l16 >> 2);
+                u.s[t] = read_transposed(v + row * (2 * DP) + 32u * (d ^ turn(row)) + 8u * (l16 & 3u));
+            }
+#pragma unroll
+            for (int i = 0; i < M; ++i) o[i][d] = mfma(u.v, w[i], o[i][d]);
+        }
+    }
+
+    // Whether the block's rows of V hold an infinity or a NaN: a product would
+    // carry it to rows that do not see its place (0 * inf).
+    __device__ __forceinline__ bool bad_values(const uint8_t *v) const {
+        constexpr uint32_t kExponent = std::is_same_v<T, bf16_t> ? 0x7F80u : 0x7C00u;
+        bool bad = false;
+        for (int i = 0; i < static_cast<int>(kBlock) * DP * 2 / 1024; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(v + 1024 * i + 16 * lane);
+            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                bad = bad || (words[e] & kExponent) == kExponent || ((words[e] >> 16) & kExponent) == kExponent;
+        }
+        return __ballot(bad) != 0;
+    }
+
+    // The same as add() without the matrix cores: places that a row does not see
+    // are left out.
+    __device__ __forceinline__ void add_one_by_one(const floatx4 (&s)[M][2], const uint8_t *v) {
+#pragma unroll 1
+        for (uint32_t row = 0; row < kBlock; ++row) {
+            const uint32_t at = 4u * (row >> 4) + (row & 3u), from = l16 + 16u * ((row >> 2) & 3u);
+            const T *at_v = reinterpret_cast<const T *>(v + row * (2 * DP)) + 4u * quarter;
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                float x = s[i][0][0];
+#pragma unroll
+                for (uint32_t e = 1; e < 8; ++e) x = at == e ? s[i][e / 4][e % 4] : x;
+                x = static_cast<float>(static_cast<T>(__shfl(x, from)));
+#pragma unroll
+                for (int d = 0; d < kTilesD; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = static_cast<float>(at_v[16u * (d ^ turn(row)) + e]);
+                        o[i][d][e] += x == 0.0f ? 0.0f : x * y;
+                    }
+            }
+        }
+    }
+};
+
+// A wave of the kernel for few rows: it has all the tile's rows and every fourth
+// block of places.
+template <typename T, int KK, int M, bool kWhole16>
+struct FewWave : Rows<T, KK, M> {
+    using R = Rows<T, KK, M>;
+    using Vec = typename R::Vec;
+    using R::a, R::p, R::lane, R::quarter, R::l16, R::DP, R::kChunks;
+    static constexpr int kVBytes = kBlock * DP * 2;
+    static constexpr int kVLoads = kVBytes / 1024;
+    static constexpr int kVRows = 64 / kChunks;  // rows of one load
+
+    uint8_t *lds;  // two buffers of kVBytes
+    const int32_t *table;
+    Vec k[2][KK];
+    uint32_t valid;  // of the block in k: places whose page exists
+
+    __device__ __forceinline__ FewWave(const AttentionArgs &args, const Part &part, uint8_t *buffers)
+        : R(args, part, 0u), lds(buffers), table(args.b.page_table + part.seq * args.b.table_stride) {}
 
     __device__ __forceinline__ uint32_t page_of(uint32_t place) const {
         return df11::page_of(place, a.page_magic, a.page_shift);
@@ -241,7 +423,7 @@ struct Wave {
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i) {
             const uint32_t r = i * kVRows + v_row;  // row of the block
-            const uint32_t chunk = min(slot ^ (2u * turn(r)), last_chunk);
+            const uint32_t chunk = min(slot ^ (2u * R::turn(r)), last_chunk);
             const T *row;
             if constexpr (kWhole16) {
                 const uint32_t t = i * kVRows / 16, key = key0 + 16u * t, page = __builtin_amdgcn_readlane(id, 16 * t);
@@ -253,55 +435,6 @@ struct Wave {
             }
             load_to_lds(row + 8u * chunk, dst + 1024 * i);
         }
-    }
-
-    __device__ __forceinline__ void begin() {
-        const uint32_t last_chunk = a.dim / 8u - 1u;
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.0f;
-#pragma unroll
-            for (int d = 0; d < kTilesD; ++d) o[i][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t token, head;
-            row_of(a, p, 16u * i + l16, token, head);
-            const bool there = token < p.s.rows;
-            const T *row = static_cast<const T *>(a.q) +
-                           (static_cast<uint64_t>(p.s.begin) + (there ? token : 0u)) * a.q_stride +
-                           (there ? head : p.head * a.group) * a.q_head_stride;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                const uint32_t chunk = 4u * kk + quarter;
-                q[i][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(chunk, last_chunk));
-                if (!there || chunk > last_chunk) q[i][kk] = Vec{};
-            }
-        }
-    }
-
-    // The places of the block at key0 that a row sees, as far as this lane has
-    // them: bit 4 t + e is place 16 t + 4 quarter + e.  (Bits and selects only:
-    // out of nested branches around single elements of the scores the compiler
-    // has made code that keeps the masked ones.)
-    __device__ __forceinline__ uint32_t seen(uint32_t token, const uint8_t *mask_row, uint32_t key0) const {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t key = key0 + 16u * t + 4u * quarter;
-            if (a.mask) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t j = key + e - p.s.length;  // (wraps where the place is cached)
-                    uint32_t bit = key + e < p.s.length ? 1u : 0u;
-                    if (j < a.mask_cols) bit |= mask_row[j] != 0 ? 1u : 0u;
-                    bits |= bit << (4 * t + e);
-                }
-            } else {
-                const uint32_t end = p.s.length + token + 1u;  // places that the row sees
-                const uint32_t n = key < end ? min(end - key, 4u) : 0u;
-                bits |= ((1u << n) - 1u) << (4 * t);
-            }
-        }
-        return bits & (((valid >> (4u * quarter)) & 15u) | (((valid >> (16u + 4u * quarter)) & 15u) << 4));
     }
 
     __device__ __forceinline__ void compute(uint32_t key0, const uint8_t *v) {
@@ -318,122 +451,23 @@ struct Wave {
             for (int t = 0; t < 2; ++t) {
                 s[i][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) s[i][t] = mfma(k[t][kk], q[i][kk], s[i][t]);
+                for (int kk = 0; kk < KK; ++kk) s[i][t] = mfma(k[t][kk], R::q[i][kk], s[i][t]);
             }
-        const bool masked = key0 + kBlock > p.s.length || valid != ~0u;
-        if (masked) {
-#pragma unroll
-            for (int i = 0; i < M; ++i) {
-                uint32_t token, head;
-                row_of(a, p, 16u * i + l16, token, head);
-                const uint8_t *mask_row =
-                    a.mask ? a.mask + (p.s.begin + static_cast<uint64_t>(min(token, p.s.rows - 1u))) * a.mask_stride
-                           : nullptr;
-                const uint32_t bits = seen(token, mask_row, key0);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[i][t][e] = (bits >> (4 * t + e)) & 1u ? s[i][t][e] : -INFINITY;
-            }
-        }
-        // New references where a score passes the old one by the headroom.
-        float top[M];
-        bool moves = false;
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-            top[i] = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
-                           fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
-            moves = moves || top[i] > m[i] + a.headroom;
-        }
-        if (__ballot(moves)) {
-#pragma unroll
-            for (int i = 0; i < M; ++i) {
-                float to = fmaxf(top[i], __shfl_xor(top[i], 16));
-                to = fmaxf(m[i], fmaxf(to, __shfl_xor(to, 32)));
-                const float f = weight_of(m[i] * a.c, to * a.c);
-                m[i] = to;
-                l[i] *= f;
-#pragma unroll
-                for (int d = 0; d < kTilesD; ++d) o[i][d] *= f;
-            }
-        }
+        const bool masked = R::masked(key0, valid);
+        if (masked) R::mask(s, key0, valid);
         Vec w[M];
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-            const float mc = m[i] == -INFINITY ? 0.0f : m[i] * a.c;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -mc));
-                    l[i] += x;
-                    s[i][t][e] = x;
-                    w[i][4 * t + e] = static_cast<T>(x);
-                }
-        }
-        if (masked && bad_values(v)) {
-            add_one_by_one(s, v);
+        R::weigh(s, w);
+        if (masked && R::bad_values(v)) {
+            R::add_one_by_one(s, v);
             return;
         }
-#pragma unroll
-        for (int d = 0; d < kTilesD; ++d) {
-            union {
-                shortx4 s[2];
-                Vec v;
-            } u;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint32_t row = 16u * t + 4u * quarter + (l16 >> 2);
-                u.s[t] = read_transposed(v + row * (2 * DP) + 32u * (d ^ turn(row)) + 8u * (l16 & 3u));
-            }
-#pragma unroll
-            for (int i = 0; i < M; ++i) o[i][d] = mfma(u.v, w[i], o[i][d]);
-        }
+        R::add(w, v);
     }
 
-    // Whether the block's rows of V hold an infinity or a NaN: a product would
-    // carry it to rows that do not see its place (0 * inf).
-    __device__ __forceinline__ bool bad_values(const uint8_t *v) const {
-        constexpr uint32_t kExponent = std::is_same_v<T, bf16_t> ? 0x7F80u : 0x7C00u;
-        bool bad = false;
-        for (int i = 0; i < kVLoads; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(v + 1024 * i + 16 * lane);
-            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                bad = bad || (words[e] & kExponent) == kExponent || ((words[e] >> 16) & kExponent) == kExponent;
-        }
-        return __ballot(bad) != 0;
-    }
-
-    // The block's part of o without the matrix cores: places that a row does not
-    // see are left out.
-    __device__ __forceinline__ void add_one_by_one(const floatx4 (&s)[M][2], const uint8_t *v) {
-        for (uint32_t from = 0; from < 4; ++from) {
-#pragma unroll
-            for (int at = 0; at < 8; ++at) {
-                const uint32_t row = 16u * (at / 4) + 4u * from + at % 4;
-#pragma unroll
-                for (int i = 0; i < M; ++i) {
-                    const float x = static_cast<float>(static_cast<T>(__shfl(s[i][at / 4][at % 4], l16 + 16u * from)));
-                    if (x == 0.0f) continue;
-#pragma unroll
-                    for (int d = 0; d < kTilesD; ++d) {
-                        const T *at_v = reinterpret_cast<const T *>(v + row * (2 * DP) + 32u * (d ^ turn(row))) + 4u * quarter;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i][d][e] += x * static_cast<float>(at_v[e]);
-                    }
-                }
-            }
-        }
-    }
-
-    __device__ __forceinline__ void run() {
+    __device__ __forceinline__ void run(uint32_t wave) {
         const uint32_t first = p.step0 * kStepPlaces + wave * kBlock;
         const uint32_t end = min(p.limit, p.step1 * kStepPlaces);
         const uint32_t blocks = first < end ? (end - first + kStepPlaces - 1u) / kStepPlaces : 0u;
-        begin();
         if (!blocks) return;
         Vec next[2][KK];
         uint32_t next_valid;
@@ -466,44 +500,184 @@ struct Wave {
     }
 };
 
-// Joins the waves' sums of a part, row tile by row tile, and writes them: to out
-// and lse if the part is whole, else to the workgroup's slot.
-template <typename T, int KK, int M, bool kWhole16>
-__device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &p, Wave<T, KK, M, kWhole16> &w,
-                                            uint8_t *lds, uint32_t wave_bytes, float (*s_stats)[16][2], uint64_t slot) {
+// A wave of the kernel for many rows: WR waves have the tile's rows, M row tiles
+// each, and share the places that WK groups of waves take in turn.  K and V come
+// to LDS in tiles of kTile places, in a ring of three: the tile after the next is
+// sent for once every wave has left the one before this, at the one barrier of
+// a tile.
+template <typename T, int KK, int M, int WR, int WK>
+struct ManyWave : Rows<T, KK, M> {
+    using R = Rows<T, KK, M>;
+    using Vec = typename R::Vec;
+    using R::a, R::p, R::lane, R::quarter, R::l16, R::DP, R::kChunks;
+    static constexpr int kWaves = WR * WK;
+    static constexpr int kTile = DP > 128 ? 32 : 64;
+    static constexpr int kBlocks = kTile / static_cast<int>(kBlock) / WK;  // of a wave, a tile
+    static_assert(kBlocks >= 1, "a group of waves has a block of a tile");
+    static constexpr int kHalf = kTile * DP * 2;  // bytes of K or of V
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kLoads = kHalf / 1024 / kWaves;  // of a wave
+    static_assert(kLoads * 1024 * kWaves == kHalf, "whole loads");
+    static constexpr int kLoadRows = 64 / kChunks;
+
+    uint32_t wave, group;
+    uint8_t *lds;
+    const int32_t *table;
+
+    __device__ __forceinline__ ManyWave(const AttentionArgs &args, const Part &part, uint32_t w, uint8_t *ring)
+        : R(args, part, (w % WR) * 16u * M), wave(w), group(w / WR), lds(ring),
+          table(args.b.page_table + part.seq * args.b.table_stride) {}
+
+    __device__ __forceinline__ uint32_t page_of(uint32_t place) const {
+        return df11::page_of(place, a.page_magic, a.page_shift);
+    }
+
+    // Page of the place that lane l has of the tile at key0.
+    __device__ __forceinline__ uint32_t load_id(uint32_t key0) const {
+        const uint32_t place = key0 + lane % kTile;
+        return place < p.limit ? static_cast<uint32_t>(table[page_of(place)]) : ~0u;
+    }
+
+    __device__ __forceinline__ void issue(uint32_t key0, uint32_t id, uint8_t *stage, uint64_t &valid) const {
+        valid = __ballot(id < a.n_pages);
+        id = id < a.n_pages ? id : 0u;
+        const uint32_t last_chunk = a.dim / 8u - 1u, slot = lane % kChunks;
+        const T *kp = static_cast<const T *>(a.k.p) + p.head * a.k.head_stride;
+        const T *vp = static_cast<const T *>(a.v.p) + p.head * a.v.head_stride;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t load = wave + kWaves * i, r = load * kLoadRows + lane / kChunks;  // row of the tile
+            const uint32_t key = key0 + r, off = key - page_of(key) * a.page_size;
+            const uint64_t page = __shfl(id, r);
+            load_to_lds(kp + page * a.k.page_stride + off * a.k.place_stride + 8u * min(slot ^ (r & 7u), last_chunk),
+                        stage + 1024u * load);
+            load_to_lds(vp + page * a.v.page_stride + off * a.v.place_stride +
+                            8u * min(slot ^ (2u * R::turn(r)), last_chunk),
+                        stage + kHalf + 1024u * load);
+        }
+    }
+
+    __device__ __forceinline__ void scores(floatx4 (&s)[M][2], const uint8_t *k) const {
+        const uint32_t last_chunk = a.dim / 8u - 1u;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t *row = k + (16u * t + l16) * (2 * DP);
+#pragma unroll
+            for (int i = 0; i < M; ++i) s[i][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                const uint32_t chunk = 4u * kk + quarter;
+                Vec f = *reinterpret_cast<const Vec *>(row + 16u * (chunk ^ (l16 & 7u)));
+                if (a.dim != DP && chunk > last_chunk) f = Vec{};
+#pragma unroll
+                for (int i = 0; i < M; ++i) s[i][t] = mfma(f, R::q[i][kk], s[i][t]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void compute(uint32_t key0, uint32_t valid, const uint8_t *k, const uint8_t *v) {
+        // (a wave's rows may end before the tile's places do)
+        uint32_t token, head;
+        row_of(a, p, R::row0 + 16u * M - 1u, token, head);
+        if (key0 >= p.limit || (!a.mask && key0 > p.s.length + token)) return;
+        floatx4 s[M][2];
+        scores(s, k);
+        const bool masked = R::masked(key0, valid);
+        if (masked) R::mask(s, key0, valid);
+        Vec w[M];
+        R::weigh(s, w);
+        if (masked && R::bad_values(v)) {
+            R::add_one_by_one(s, v);
+            return;
+        }
+        R::add(w, v);
+    }
+
+    // (called by all waves of the workgroup, with a barrier since the last use of the ring)
+    __device__ __forceinline__ void run() {
+        const uint32_t first = p.step0 * kStepPlaces, end = min(p.limit, p.step1 * kStepPlaces);
+        const uint32_t tiles = first < end ? (end - first + kTile - 1u) / kTile : 0u;
+        if (!tiles) return;
+        uint64_t valid[2] = {0, 0};
+        uint8_t *cur = lds, *next = lds + kStage, *free = lds + 2 * kStage;
+        const uint32_t id0 = load_id(first), id1 = load_id(first + kTile);
+        uint32_t id = load_id(first + 2u * kTile);
+        issue(first, id0, cur, valid[0]);
+        if (tiles > 1u) issue(first + kTile, id1, next, valid[1]);
+        for (uint32_t t = 0; t < tiles; ++t) {
+            const uint32_t key0 = first + t * kTile;
+            // This tile has landed (the next one's loads, sent for after it, may be on
+            // their way), and no wave reads the one before any more.
+            if (t + 1u < tiles) {
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            uint64_t later = 0;
+            if (t + 2u < tiles) {
+                // (the next id first: a wait for it leaves this tile's loads alone)
+                const uint32_t then = load_id(key0 + 3u * kTile);
+                issue(key0 + 2u * kTile, id, free, later);
+                id = then;
+            }
+#pragma unroll 1
+            for (int b = 0; b < kBlocks; ++b) {
+                const uint32_t at = (group * kBlocks + b) * kBlock;
+                compute(key0 + at, static_cast<uint32_t>(valid[0] >> at), cur + at * (2 * DP), cur + kHalf + at * (2 * DP));
+            }
+            valid[0] = valid[1];
+            valid[1] = later;
+            uint8_t *x = cur;
+            cur = next;
+            next = free;
+            free = x;
+        }
+    }
+};
+
+// Joins the sums that WK groups of WR waves have of a part, row tile by row tile
+// of each wave, and writes them: to out and lse if the part is whole, else to the
+// workgroup's slot.
+template <typename T, int KK, int M, int WR, int WK>
+__device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &p, Rows<T, KK, M> &w, uint32_t wave,
+                                            uint8_t *lds, float (*s_stats)[16][2], uint64_t slot) {
     constexpr int DP = 32 * KK, kStride = DP + 4;
-    const uint32_t tid = threadIdx.x;
+    constexpr uint32_t kWaveFloats = 16 * kStride;
+    float *sums = reinterpret_cast<float *>(lds);
 #pragma unroll
     for (int i = 0; i < M; ++i) {
         float l = w.l[i] + __shfl_xor(w.l[i], 16);
         l += __shfl_xor(l, 32);
-        // (every wave's reads of its buffers, and of the row tile before, are back)
+        // (every wave's reads of the places, and of the row tile before, are back)
         __syncthreads();
         if (w.quarter == 0) {
-            s_stats[w.wave][w.l16][0] = w.m[i] == -INFINITY ? -INFINITY : w.m[i] * a.c;
-            s_stats[w.wave][w.l16][1] = l;
+            s_stats[wave][w.l16][0] = w.m[i] == -INFINITY ? -INFINITY : w.m[i] * a.c;
+            s_stats[wave][w.l16][1] = l;
         }
-        float *mine = reinterpret_cast<float *>(lds + w.wave * wave_bytes);
 #pragma unroll
-        for (int d = 0; d < Wave<T, KK, M, kWhole16>::kTilesD; ++d)
-            *reinterpret_cast<floatx4 *>(mine + w.l16 * kStride + 16 * d + 4 * w.quarter) = w.o[i][d];
+        for (int d = 0; d < Rows<T, KK, M>::kTilesD; ++d)
+            *reinterpret_cast<floatx4 *>(sums + wave * kWaveFloats + w.l16 * kStride + 16 * d + 4 * w.quarter) = w.o[i][d];
         __syncthreads();
-        for (uint32_t at = tid; at < 16u * (DP / 8); at += 256u) {
-            const uint32_t r = at / (DP / 8), d = 8u * (at % (DP / 8)), row = 16u * i + r;
+        for (uint32_t at = threadIdx.x; at < WR * 16u * (DP / 8); at += 64u * WR * WK) {
+            const uint32_t from = at / (DP / 8), d = 8u * (at % (DP / 8)), wr = from / 16u, r = from % 16u;
+            const uint32_t row = (wr * M + i) * 16u + r;
             uint32_t token, head;
             row_of(a, p, row, token, head);
             if (token >= p.s.rows || d >= a.dim) continue;
             float top = -INFINITY, total = 0.0f, sum[8] = {};
 #pragma unroll
-            for (uint32_t x = 0; x < kWaves; ++x) top = fmaxf(top, s_stats[x][r][0]);
+            for (uint32_t x = 0; x < WK; ++x) top = fmaxf(top, s_stats[x * WR + wr][r][0]);
 #pragma unroll
-            for (uint32_t x = 0; x < kWaves; ++x) {
-                const float f = weight_of(s_stats[x][r][0], top);
+            for (uint32_t x = 0; x < WK; ++x) {
+                const uint32_t other = x * WR + wr;
+                const float f = weight_of(s_stats[other][r][0], top);
                 if (f == 0.0f) continue;
-                total += f * s_stats[x][r][1];
-                const float *from = reinterpret_cast<const float *>(lds + x * wave_bytes) + r * kStride + d;
+                total += f * s_stats[other][r][1];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] += f * from[e];
+                for (int e = 0; e < 8; ++e) sum[e] += f * sums[other * kWaveFloats + r * kStride + d + e];
             }
             if (p.whole) {
                 const uint64_t t = static_cast<uint64_t>(p.s.begin) + token;
@@ -516,8 +690,8 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
                         total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
             } else {
                 float *to = a.parts + (slot * a.tile_rows + row) * a.dim + d;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) to[e] = sum[e];
+                store_vec<float, 4>(to, *reinterpret_cast<float(*)[4]>(&sum[0]));
+                store_vec<float, 4>(to + 4, *reinterpret_cast<float(*)[4]>(&sum[4]));
                 if (d == 0) {
                     float *st = a.stats + (slot * a.tile_rows + row) * 2u;
                     st[0] = top;
@@ -529,27 +703,22 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
     __syncthreads();
 }
 
-template <typename T, int KK, int M, bool kWhole16>
-__global__ __launch_bounds__(256) void df11_attention_kernel(AttentionArgs a) {
-    using W = Wave<T, KK, M, kWhole16>;
-    constexpr uint32_t kWaveBytes = 2u * W::kVBytes;
-    static_assert(kWaveBytes >= 16 * (W::DP + 4) * 4, "a row tile's sums fit a wave's buffers");
-    __shared__ __align__(1024) uint8_t s_mem[kWaves * kWaveBytes];
-    __shared__ float s_stats[kWaves][16][2];
-    __shared__ uint64_t s_part[4][2];
+// A workgroup's run of units: f(part, slot) for every tile that it has a part of.
+template <uint32_t THREADS, typename F>
+__device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
+    __shared__ uint64_t s_part[THREADS / 64][2];
     __shared__ Found s_found;
     uint64_t units, unused;
-    count_units(a, 0, units, unused, s_part);
+    count_units<THREADS>(a, 0, units, unused, s_part);
     if (units == 0) return;
     const uint32_t runs = df11::runs_of(units, a.workgroups);
     if (blockIdx.x >= runs) return;
     const uint32_t run = df11::run_of_workgroup(blockIdx.x, runs);
     uint64_t u = df11::run_begin(run, units, runs);
     const uint64_t end = df11::run_begin(run + 1ull, units, runs);
-    Found f = find_unit(a, u, s_part, &s_found);
-    uint32_t seq = __builtin_amdgcn_readfirstlane(f.seq);
-    uint64_t first = f.first;
-    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+    const Found found = find_unit<THREADS>(a, u, s_part, &s_found);
+    uint32_t seq = __builtin_amdgcn_readfirstlane(found.seq);
+    uint64_t first = found.first;
     bool begun = true;  // the run's first tile may have begun in the run before
     while (u < end && seq < a.b.n_seqs) {
         Part p;
@@ -568,13 +737,42 @@ __global__ __launch_bounds__(256) void df11_attention_kernel(AttentionArgs a) {
         p.step1 = end - tile_first < p.s.steps ? static_cast<uint32_t>(end - tile_first) : p.s.steps;
         p.limit = df11::tile_places(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
         p.whole = p.step0 == 0 && p.step1 == p.s.steps;
-        W w{a, p, s_mem + wave * kWaveBytes, lane, wave, lane >> 4, lane & 15u,
-            a.b.page_table + seq * a.b.table_stride};
-        w.run();
-        finish_part<T, KK, M, kWhole16>(a, p, w, s_mem, kWaveBytes, s_stats, 2ull * run + (begun ? 0u : 1u));
+        f(p, 2ull * run + (begun ? 0u : 1u));
         begun = false;
         u = tile_first + p.step1;
     }
+}
+
+// Up to 32 rows: the workgroup's waves have them all, and the places in turn.
+template <typename T, int KK, int M, bool kWhole16>
+__global__ __launch_bounds__(64 * kFewWaves) void df11_attention_few_kernel(AttentionArgs a) {
+    using W = FewWave<T, KK, M, kWhole16>;
+    constexpr uint32_t kWaveBytes = 2u * W::kVBytes;
+    static_assert(kWaveBytes >= 16 * (W::DP + 4) * 4, "a row tile's sums fit a wave's buffers");
+    __shared__ __align__(1024) uint8_t s_mem[kFewWaves * kWaveBytes];
+    __shared__ float s_stats[kFewWaves][16][2];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+    for_each_part<64 * kFewWaves>(a, [&](const Part &p, uint64_t slot) {
+        W w(a, p, s_mem + wave * kWaveBytes);
+        w.run(wave);
+        finish_part<T, KK, M, 1, kFewWaves>(a, p, w, wave, s_mem, s_stats, slot);
+    });
+}
+
+// More rows: eight waves share tiles of places in LDS.
+template <typename T, int KK, int M, int WR, int WK>
+__global__ __launch_bounds__(64 * WR * WK) __attribute__((amdgpu_waves_per_eu(WR * WK / 4)))
+void df11_attention_many_kernel(AttentionArgs a) {
+    using W = ManyWave<T, KK, M, WR, WK>;
+    constexpr uint32_t kSums = WR * WK * 16 * (W::DP + 4) * 4;
+    __shared__ __align__(1024) uint8_t s_mem[3 * W::kStage > kSums ? 3 * W::kStage : kSums];
+    __shared__ float s_stats[WR * WK][16][2];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+    for_each_part<64 * WR * WK>(a, [&](const Part &p, uint64_t slot) {
+        W w(a, p, wave, s_mem);
+        w.run();
+        finish_part<T, KK, M, WR, WK>(a, p, w, wave, s_mem, s_stats, slot);
+    });
 }
 
 // The parts of one token's rows of one key head, joined in the order of the
@@ -586,7 +784,7 @@ __global__ __launch_bounds__(256) void df11_attention_join_kernel(AttentionArgs 
     const int32_t seq = __builtin_amdgcn_readfirstlane(sequence_of(a.b, static_cast<int32_t>(token)));
     if (seq < 0) return;
     uint64_t units, first;
-    count_units(a, static_cast<uint32_t>(seq), units, first, s_part);
+    count_units<256>(a, static_cast<uint32_t>(seq), units, first, s_part);
     const SeqShape s = shape_of(a, seq);
     if (units == 0 || !s.tiles) return;
     const uint32_t runs = df11::runs_of(units, a.workgroups);
@@ -625,28 +823,46 @@ __global__ __launch_bounds__(256) void df11_attention_join_kernel(AttentionArgs 
     }
 }
 
+// The kernels, by the rows of their tiles.
 template <typename T, int KK>
-const void *pick_rows(uint32_t m, bool whole16) {
-    const auto pick = [&](auto rows) {
-        constexpr int M = decltype(rows)::value;
-        return whole16 ? reinterpret_cast<const void *>(&df11_attention_kernel<T, KK, M, true>)
-                       : reinterpret_cast<const void *>(&df11_attention_kernel<T, KK, M, false>);
+const void *pick_rows(uint32_t rows, bool whole16) {
+    const auto few = [&](auto m) {
+        constexpr int M = decltype(m)::value;
+        return whole16 ? reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, M, true>)
+                       : reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, M, false>);
     };
-    if constexpr (KK < 8) {
-        if (m == 2) return pick(std::integral_constant<int, 2>{});
+    if (rows == 16) return few(std::integral_constant<int, 1>{});
+    if constexpr (KK == 8) {
+        return rows == 64 ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 1, 4, 1>)
+                          : reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 1, 8, 1>);
+    } else {
+        if (rows == 32) return few(std::integral_constant<int, 2>{});
+        return rows == 64    ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 1, 4, 2>)
+               : rows == 128 ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 2, 4, 2>)
+                             : reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 2, 8, 1>);
     }
-    return pick(std::integral_constant<int, 1>{});
+}
+
+// Rows of a tile: enough for the rows that a sequence has on average (the host
+// knows no more than that).
+uint32_t pick_tile(uint32_t dim, uint64_t rows) {
+    if (dim > 128) return rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+}
+
+uint32_t tile_threads(uint32_t dim, uint32_t rows) {
+    return 64u * (rows <= 16 || (rows == 32 && dim <= 128) ? kFewWaves : rows == 64 && dim > 128 ? 4u : 8u);
 }
 
 template <typename T>
-const void *pick_kernel(uint32_t dim, uint32_t m, bool whole16) {
-    return dim <= 64 ? pick_rows<T, 2>(m, whole16) : dim <= 128 ? pick_rows<T, 4>(m, whole16) : pick_rows<T, 8>(m, whole16);
+const void *pick_kernel(uint32_t dim, uint32_t rows, bool whole16) {
+    return dim <= 64 ? pick_rows<T, 2>(rows, whole16) : dim <= 128 ? pick_rows<T, 4>(rows, whole16) : pick_rows<T, 8>(rows, whole16);
 }
 
 // How a call is launched.
 struct Plan {
     const void *fn;
-    uint32_t tile_rows, workgroups;
+    uint32_t tile_rows, threads, workgroups;
     uint64_t parts, stats;  // bytes; 0 where no tile is ever cut
 };
 
@@ -654,14 +870,13 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     int dev = 0, cus = 0;
     if (device_cus(dev, cus)) return DF11_E_HIP;
     const uint32_t group = q_heads / c.heads;
-    // Row tiles of 16, as many as a sequence's rows fill on average (the host
-    // knows no more than that).
     const uint64_t rows = static_cast<uint64_t>((b.n_tokens + b.n_seqs - 1) / b.n_seqs) * group;
-    const uint32_t m = rows <= 16 || c.head_dim > 128 ? 1 : 2;
     const bool whole16 = c.page_size % 16 == 0;
-    p.fn = c.dtype == DF11_BF16 ? pick_kernel<bf16_t>(c.head_dim, m, whole16) : pick_kernel<fp16_t>(c.head_dim, m, whole16);
-    p.tile_rows = 16 * m;
-    const int per_cu = resident_per_cu(p.fn, 256, dev, 0);
+    p.tile_rows = pick_tile(c.head_dim, rows);
+    p.threads = tile_threads(c.head_dim, p.tile_rows);
+    p.fn = c.dtype == DF11_BF16 ? pick_kernel<bf16_t>(c.head_dim, p.tile_rows, whole16)
+                                : pick_kernel<fp16_t>(c.head_dim, p.tile_rows, whole16);
+    const int per_cu = resident_per_cu(p.fn, p.threads, dev, 0);
     if (per_cu < 1) return DF11_E_HIP;
     const uint64_t capacity = static_cast<uint64_t>(b.table_pages) * c.page_size;
     const uint64_t tiles = (static_cast<uint64_t>(b.n_tokens) * group + p.tile_rows - 1) / p.tile_rows + b.n_seqs;
@@ -764,7 +979,7 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     (void)hipGetLastError();
     const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     void *params[] = {&k};
-    rc = launch_kernel(p.fn, dim3(p.workgroups), dim3(256), params, 0, stream, nullptr, nullptr);
+    rc = launch_kernel(p.fn, dim3(p.workgroups), dim3(p.threads), params, 0, stream, nullptr, nullptr);
     if (rc || !spans[2]) return rc;
     const void *join = c->dtype == DF11_BF16 ? reinterpret_cast<const void *>(&df11_attention_join_kernel<bf16_t>)
                                              : reinterpret_cast<const void *>(&df11_attention_join_kernel<fp16_t>);
