@@ -65,7 +65,7 @@ struct AttentionArgs {
     float *parts;         // [workgroup][2][row][dim]
     float *stats;         // [workgroup][2][row][2]: reference times c, sum
     uint32_t page_magic, page_shift;  // df11::page_of
-    float c, headroom;    // scale log2(e), 8 / c
+    float c;              // scale log2(e)
     uint32_t mask_cols, n_pages, page_size, kv_heads, group, dim, workgroups, tile_rows;
 };
 
@@ -76,11 +76,57 @@ __device__ __forceinline__ floatx4 mfma(vec_t<fp16_t, 8> a, vec_t<fp16_t, 8> b, 
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ shortx4 read_transposed(const uint8_t *p) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4 *)p);
+// Four operands of V^T: for each of four LDS addresses, 4 rows x 16 columns of
+// 2-byte elements transposed across a quarter wave (lane i of the quarter passes
+// the address of row i / 4, columns 4 (i mod 4) .. + 3, and receives column i of
+// the four rows), and the same `next` bytes on.  (With the builtin for one read the
+// compiler waits for every load to LDS in flight first; the block ends with its
+// own wait, so that its results are there.)
+template <int next>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[4], shortx4 (&x)[4][2]) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8\n\t"
+        "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %2, %9\n\t"
+        "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %4, %10\n\t"
+        "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %6, %11\n\t"
+        "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[1][0]), "=&v"(x[1][1]), "=&v"(x[2][0]), "=&v"(x[2][1]), "=&v"(x[3][0]),
+          "=&v"(x[3][1])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(next));
 }
 
-// 16 bytes a lane from memory to the wave-uniform LDS address dst + 16 lane.
+// LDS address of a pointer into it.
+__device__ __forceinline__ uint32_t lds_address(const uint8_t *p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint8_t *)p));
+}
+
+using Resource = __amdgpu_buffer_rsrc_t;
+
+// Waits until at most VM vector memory loads and no LDS reads are in flight.  (The
+// builtin and not assembly: the compiler then knows what has arrived, and adds no
+// waits of its own that would drain the rest.)
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(VM >= 0 && VM < 64, "six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
+}
+
+// 16 bytes a lane from `at` bytes on behind the wave-uniform address `from` to the
+// wave-uniform LDS address dst + 16 lane.
+__device__ __forceinline__ void load_rows_to_lds(const void *from, uint32_t at, uint8_t *dst) {
+    const Resource r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(from), 0, 0xFFFFFFFFu, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, at, 0, 0, 0);
+}
+
+// The same from addresses of each lane's own.  (Slower than it looks: the
+// compiler waits for every load in flight before it reads LDS after one of these,
+// and not after the other kind.)
 __device__ __forceinline__ void load_to_lds(const void *from, uint8_t *dst) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
                                      (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
@@ -175,6 +221,12 @@ __device__ __forceinline__ void row_of(const AttentionArgs &a, const Part &p, ui
     head = p.head * a.group + at % a.group;
 }
 
+// Weights that a reference allows before it moves.
+constexpr float kRoom = 256.0f;
+
+// What a head's chunks past head_dim read.
+__device__ const uint4 g_zeros = {0, 0, 0, 0};
+
 // What a wave keeps of its rows: M tiles of 16 from row0 of the part's tile on,
 // lane l having row l mod 16 of each.
 template <typename T, int KK, int M>
@@ -190,14 +242,14 @@ struct Rows {
 
     Vec q[M][KK];
     floatx4 o[M][kTilesD];
-    float m[M], l[M];  // a lane's row: its reference (raw score) and this lane's part of the sum
+    float ref[M], l[M];  // a lane's row: its reference times c, and this lane's part of the sum
 
     __device__ __forceinline__ Rows(const AttentionArgs &args, const Part &part, uint32_t first_row)
         : a(args), p(part), row0(first_row), lane(threadIdx.x & 63u), quarter(lane >> 4), l16(lane & 15u) {
         const uint32_t last_chunk = a.dim / 8u - 1u;
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            m[i] = -INFINITY;
+            ref[i] = -INFINITY;
             l[i] = 0.0f;
 #pragma unroll
             for (int d = 0; d < kTilesD; ++d) o[i][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -247,10 +299,6 @@ struct Rows {
         return bits & (((valid >> (4u * quarter)) & 15u) | (((valid >> (16u + 4u * quarter)) & 15u) << 4));
     }
 
-    __device__ __forceinline__ bool masked(uint32_t key0, uint32_t valid) const {
-        return key0 + kBlock > p.s.length || valid != ~0u;
-    }
-
     __device__ __forceinline__ void mask(floatx4 (&s)[M][2], uint32_t key0, uint32_t valid) const {
 #pragma unroll
         for (int i = 0; i < M; ++i) {
@@ -267,59 +315,95 @@ struct Rows {
         }
     }
 
-    // Scores to weights (in s, and rounded in w), the reference moved where a
-    // score passes it by the headroom.
+    // Scores to weights (in s, and rounded in w).  A weight past 2^8 (infinite
+    // while there is no reference) says that the reference has to move: then
+    // they are taken again, from the new one.
     __device__ __forceinline__ void weigh(floatx4 (&s)[M][2], Vec (&w)[M]) {
-        float top[M];
+        floatx4 x[M][2];
         bool moves = false;
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            top[i] = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
-                           fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
-            moves = moves || top[i] > m[i] + a.headroom;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][t][e] = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -ref[i]));
+            // (all NaN: no reference, and nothing seen)
+            moves = moves || !(largest(x[i]) <= kRoom);
         }
         if (__ballot(moves)) {
 #pragma unroll
             for (int i = 0; i < M; ++i) {
-                float to = fmaxf(top[i], __shfl_xor(top[i], 16));
-                to = fmaxf(m[i], fmaxf(to, __shfl_xor(to, 32)));
-                const float f = weight_of(m[i] * a.c, to * a.c);
-                m[i] = to;
+                float top = largest(s[i]);
+                top = fmaxf(top, __shfl_xor(top, 16));
+                const float to = fmaxf(ref[i], fmaxf(top, __shfl_xor(top, 32)) * a.c), f = weight_of(ref[i], to);
+                const float base = to == -INFINITY ? 0.0f : to;
+                ref[i] = to;
                 l[i] *= f;
 #pragma unroll
                 for (int d = 0; d < kTilesD; ++d) o[i][d] *= f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][t][e] = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -base));
             }
         }
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            const float mc = m[i] == -INFINITY ? 0.0f : m[i] * a.c;
+            l[i] += ((x[i][0][0] + x[i][0][1]) + (x[i][0][2] + x[i][0][3])) +
+                    ((x[i][1][0] + x[i][1][1]) + (x[i][1][2] + x[i][1][3]));
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -mc));
-                    l[i] += x;
-                    s[i][t][e] = x;
-                    w[i][4 * t + e] = static_cast<T>(x);
+                    s[i][t][e] = x[i][t][e];
+                    w[i][4 * t + e] = static_cast<T>(x[i][t][e]);
                 }
+        }
+    }
+
+    static __device__ __forceinline__ float largest(const floatx4 (&x)[2]) {
+        return fmaxf(fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(x[1][0], x[1][1])),
+                     fmaxf(x[1][2], x[1][3]));
+    }
+
+    // A block's scores to o, where every row sees all of its places.
+    __device__ __forceinline__ void take(floatx4 (&s)[M][2], const uint8_t *v) {
+        Vec w[M];
+        weigh(s, w);
+        add(w, v);
+    }
+
+    // The same where rows may not.
+    __device__ __forceinline__ void take_masked(floatx4 (&s)[M][2], uint32_t key0, uint32_t valid, const uint8_t *v) {
+        const bool some = key0 + kBlock > p.s.length || valid != ~0u;
+        if (some) mask(s, key0, valid);
+        Vec w[M];
+        weigh(s, w);
+        if (some && bad_values(v)) {
+            add_one_by_one(s, v);
+        } else {
+            add(w, v);
         }
     }
 
     // The block's part of o, its rows of V in LDS at v.
     __device__ __forceinline__ void add(const Vec (&w)[M], const uint8_t *v) {
+        // (v is a multiple of 1 KB and a row of 32 bytes times a power of two, so that
+        // d XOR the row's turn is one XOR of the address)
+        const uint32_t row = 4u * quarter + (l16 >> 2);
+        const uint32_t base = lds_address(v) + row * (2 * DP) + 32u * turn(row) + 8u * (l16 & 3u);
 #pragma unroll
-        for (int d = 0; d < kTilesD; ++d) {
+        for (int d = 0; d < kTilesD; d += 4) {
+            const uint32_t at[4] = {base ^ (32u * d), base ^ (32u * (d + 1)), base ^ (32u * (d + 2)), base ^ (32u * (d + 3))};
             union {
-                shortx4 s[2];
-                Vec v;
+                shortx4 s[4][2];
+                Vec v[4];
             } u;
+            read_transposed<16 * 2 * DP>(at, u.s);  // (16 rows on: the same turn)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint32_t row = 16u * t + 4u * quarter + (l16 >> 2);
-                u.s[t] = read_transposed(v + row * (2 * DP) + 32u * (d ^ turn(row)) + 8u * (l16 & 3u));
-            }
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < M; ++i) o[i][d] = mfma(u.v, w[i], o[i][d]);
+                for (int i = 0; i < M; ++i) o[i][d + e] = mfma(u.v[e], w[i], o[i][d + e]);
         }
     }
 
@@ -365,7 +449,7 @@ struct Rows {
 
 // A wave of the kernel for few rows: it has all the tile's rows and every fourth
 // block of places.
-template <typename T, int KK, int M, bool kWhole16>
+template <typename T, int KK, int M, bool kWhole>
 struct FewWave : Rows<T, KK, M> {
     using R = Rows<T, KK, M>;
     using Vec = typename R::Vec;
@@ -386,18 +470,20 @@ struct FewWave : Rows<T, KK, M> {
         return df11::page_of(place, a.page_magic, a.page_shift);
     }
 
-    // Page of the place that lane l mod 32 has of the block at key0; an id that
-    // no page has where there is none.
+    // Page of the place that lane l mod 32 has of the block at key0, or of the
+    // last one.  (Nothing here uses what is loaded, which would wait for it.)
     __device__ __forceinline__ uint32_t load_id(uint32_t key0) const {
-        const uint32_t place = key0 + (lane & 31u);
-        return place < p.limit ? static_cast<uint32_t>(table[page_of(place)]) : ~0u;
+        return static_cast<uint32_t>(table[page_of(min(key0 + (lane & 31u), p.limit - 1u))]);
     }
 
-    // Sends for the block at key0: K to `to`, V to the LDS buffer dst.
+    // Sends for the block at key0, or past the last one for rows that are not used
+    // (the number of loads in flight is the same on every path): K to `to`, V to
+    // the LDS buffer dst.
     __device__ __forceinline__ void issue(uint32_t key0, uint32_t id, Vec (&to)[2][KK], uint8_t *dst,
                                           uint32_t &valid_to) const {
-        valid_to = static_cast<uint32_t>(__ballot(id < a.n_pages));
-        id = id < a.n_pages ? id : 0u;
+        const bool there = id < a.n_pages && key0 + (lane & 31u) < p.limit;
+        valid_to = static_cast<uint32_t>(__ballot(there));
+        id = there ? id : 0u;
         const uint32_t last_chunk = a.dim / 8u - 1u;
         const T *kp = static_cast<const T *>(a.k.p) + p.head * a.k.head_stride;
         const T *vp = static_cast<const T *>(a.v.p) + p.head * a.v.head_stride;
@@ -405,7 +491,7 @@ struct FewWave : Rows<T, KK, M> {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const T *row;
-            if constexpr (kWhole16) {
+            if constexpr (kWhole) {
                 const uint32_t key = key0 + 16u * t, page = __builtin_amdgcn_readlane(id, 16 * t);
                 const uint32_t off = key - page_of(key) * a.page_size;
                 row = kp + page * a.k.page_stride + off * a.k.place_stride + l16 * a.k.place_stride;
@@ -417,34 +503,28 @@ struct FewWave : Rows<T, KK, M> {
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 const uint32_t chunk = 4u * kk + quarter;
-                to[t][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(chunk, last_chunk));
+                to[t][kk] = *(chunk <= last_chunk ? reinterpret_cast<const Vec *>(row + 8u * chunk)
+                                                  : reinterpret_cast<const Vec *>(&g_zeros));
             }
         }
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i) {
             const uint32_t r = i * kVRows + v_row;  // row of the block
             const uint32_t chunk = min(slot ^ (2u * R::turn(r)), last_chunk);
-            const T *row;
-            if constexpr (kWhole16) {
+            if constexpr (kWhole) {
                 const uint32_t t = i * kVRows / 16, key = key0 + 16u * t, page = __builtin_amdgcn_readlane(id, 16 * t);
                 const uint32_t off = key - page_of(key) * a.page_size;
-                row = vp + page * a.v.page_stride + off * a.v.place_stride + (r - 16u * t) * a.v.place_stride;
+                load_rows_to_lds(vp + page * a.v.page_stride + off * a.v.place_stride,
+                                 2u * ((r - 16u * t) * static_cast<uint32_t>(a.v.place_stride) + 8u * chunk), dst + 1024 * i);
             } else {
                 const uint32_t key = key0 + r, page = __shfl(id, r);
-                row = vp + page * a.v.page_stride + (key - page_of(key) * a.page_size) * a.v.place_stride;
+                load_to_lds(vp + page * a.v.page_stride + (key - page_of(key) * a.page_size) * a.v.place_stride + 8u * chunk,
+                            dst + 1024 * i);
             }
-            load_to_lds(row + 8u * chunk, dst + 1024 * i);
         }
     }
 
-    __device__ __forceinline__ void compute(uint32_t key0, const uint8_t *v) {
-        floatx4 s[M][2];
-        const uint32_t last_chunk = a.dim / 8u - 1u;
-        if (a.dim != DP) {
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                if (4u * kk + quarter > last_chunk) k[0][kk] = k[1][kk] = Vec{};
-        }
+    __device__ __forceinline__ void scores(floatx4 (&s)[M][2]) const {
 #pragma unroll
         for (int i = 0; i < M; ++i)
 #pragma unroll
@@ -453,50 +533,50 @@ struct FewWave : Rows<T, KK, M> {
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) s[i][t] = mfma(k[t][kk], R::q[i][kk], s[i][t]);
             }
-        const bool masked = R::masked(key0, valid);
-        if (masked) R::mask(s, key0, valid);
-        Vec w[M];
-        R::weigh(s, w);
-        if (masked && R::bad_values(v)) {
-            R::add_one_by_one(s, v);
-            return;
-        }
-        R::add(w, v);
     }
 
-    __device__ __forceinline__ void run(uint32_t wave) {
-        const uint32_t first = p.step0 * kStepPlaces + wave * kBlock;
-        const uint32_t end = min(p.limit, p.step1 * kStepPlaces);
-        const uint32_t blocks = first < end ? (end - first + kStepPlaces - 1u) / kStepPlaces : 0u;
-        if (!blocks) return;
-        Vec next[2][KK];
-        uint32_t next_valid;
-        uint8_t *cur = lds, *other = lds + kVBytes;
-        // (this wave's reads of the buffers, for the tile before, are back)
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        issue(first, load_id(first), k, cur, valid);
-        uint32_t id = load_id(first + kStepPlaces);
-        for (uint32_t b = 0; b < blocks; ++b) {
-            const uint32_t key0 = first + b * kStepPlaces;
+    // Blocks from key0 on while they are seen whole, or all (kMasked).
+    template <bool kMasked>
+    __device__ __forceinline__ void blocks(uint32_t &key0, uint32_t end, uint32_t &id, uint8_t *&cur, uint8_t *&other) {
+        while (key0 < end && (kMasked || (key0 + kBlock <= p.s.length && valid == ~0u))) {
             // This block has landed, and the other buffer's last reads are back.
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            const bool more = b + 1u < blocks;
-            if (more) {
-                issue(key0 + kStepPlaces, id, next, other, next_valid);
-                id = load_id(key0 + 2u * kStepPlaces);
+            wait_loads<0>();
+            Vec next[2][KK];
+            uint32_t next_valid = 0;
+            const uint32_t then = load_id(key0 + 2u * kStepPlaces);
+            issue(key0 + kStepPlaces, id, next, other, next_valid);
+            id = then;
+            floatx4 s[M][2];
+            scores(s);
+            if constexpr (kMasked) {
+                R::take_masked(s, key0, valid, cur);
+            } else {
+                R::take(s, cur);
             }
-            compute(key0, cur);
-            if (more) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) k[t][kk] = next[t][kk];
-                valid = next_valid;
-            }
+                for (int kk = 0; kk < KK; ++kk) k[t][kk] = next[t][kk];
+            valid = next_valid;
             uint8_t *x = cur;
             cur = other;
             other = x;
+            key0 += kStepPlaces;
         }
+    }
+
+    __device__ __forceinline__ void run(uint32_t wave) {
+        uint32_t key0 = p.step0 * kStepPlaces + wave * kBlock;
+        const uint32_t end = min(p.limit, p.step1 * kStepPlaces);
+        if (key0 >= end) return;
+        uint8_t *cur = lds, *other = lds + kVBytes;
+        // (this wave's reads of the buffers, for the tile before, are back)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        issue(key0, load_id(key0), k, cur, valid);
+        uint32_t id = load_id(key0 + kStepPlaces);
+        blocks<false>(key0, end, id, cur, other);
+        blocks<true>(key0, end, id, cur, other);
+        wait_loads<0>();  // (the buffers are used otherwise next)
     }
 };
 
@@ -505,7 +585,7 @@ struct FewWave : Rows<T, KK, M> {
 // to LDS in tiles of kTile places, in a ring of three: the tile after the next is
 // sent for once every wave has left the one before this, at the one barrier of
 // a tile.
-template <typename T, int KK, int M, int WR, int WK>
+template <typename T, int KK, int M, int WR, int WK, bool kWhole>
 struct ManyWave : Rows<T, KK, M> {
     using R = Rows<T, KK, M>;
     using Vec = typename R::Vec;
@@ -532,33 +612,49 @@ struct ManyWave : Rows<T, KK, M> {
         return df11::page_of(place, a.page_magic, a.page_shift);
     }
 
-    // Page of the place that lane l has of the tile at key0.
+    // Page of the place that lane l has of the tile at key0, or of the last one.
+    // (Nothing here uses what is loaded, which would wait for it.)
     __device__ __forceinline__ uint32_t load_id(uint32_t key0) const {
-        const uint32_t place = key0 + lane % kTile;
-        return place < p.limit ? static_cast<uint32_t>(table[page_of(place)]) : ~0u;
+        return static_cast<uint32_t>(table[page_of(min(key0 + lane % kTile, p.limit - 1u))]);
     }
 
+    // Sends for the tile at key0, or past the last one for rows that are not used:
+    // the number of loads in flight is the same on every path.
     __device__ __forceinline__ void issue(uint32_t key0, uint32_t id, uint8_t *stage, uint64_t &valid) const {
-        valid = __ballot(id < a.n_pages);
-        id = id < a.n_pages ? id : 0u;
+        const bool there = id < a.n_pages && key0 + lane % kTile < p.limit;
+        valid = __ballot(there);
+        id = there ? id : 0u;
         const uint32_t last_chunk = a.dim / 8u - 1u, slot = lane % kChunks;
         const T *kp = static_cast<const T *>(a.k.p) + p.head * a.k.head_stride;
         const T *vp = static_cast<const T *>(a.v.p) + p.head * a.v.head_stride;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t load = wave + kWaves * i, r = load * kLoadRows + lane / kChunks;  // row of the tile
-            const uint32_t key = key0 + r, off = key - page_of(key) * a.page_size;
-            const uint64_t page = __shfl(id, r);
-            load_to_lds(kp + page * a.k.page_stride + off * a.k.place_stride + 8u * min(slot ^ (r & 7u), last_chunk),
-                        stage + 1024u * load);
-            load_to_lds(vp + page * a.v.page_stride + off * a.v.place_stride +
-                            8u * min(slot ^ (2u * R::turn(r)), last_chunk),
-                        stage + kHalf + 1024u * load);
+            const uint32_t load = wave + kWaves * i, r0 = load * kLoadRows, r = r0 + lane / kChunks;  // row of the tile
+            const uint32_t k_chunk = slot ^ k_turn(r), v_chunk = slot ^ (2u * R::turn(r));
+            uint8_t *k_to = stage + 1024u * load, *v_to = k_to + kHalf;
+            if constexpr (kWhole) {
+                const uint32_t key = key0 + r0, off = key - page_of(key) * a.page_size;
+                const uint64_t page = __builtin_amdgcn_readlane(id, r0);
+                const T *k_row = kp + page * a.k.page_stride + off * a.k.place_stride;
+                const T *v_row = vp + page * a.v.page_stride + off * a.v.place_stride;
+                const uint32_t row = lane / kChunks;
+                load_rows_to_lds(k_row, 2u * (row * static_cast<uint32_t>(a.k.place_stride) + 8u * k_chunk), k_to);
+                load_rows_to_lds(v_row, 2u * (row * static_cast<uint32_t>(a.v.place_stride) + 8u * v_chunk), v_to);
+            } else {
+                const uint32_t key = key0 + r, off = key - page_of(key) * a.page_size;
+                const uint64_t page = __shfl(id, r);
+                if (k_chunk <= last_chunk)
+                    load_to_lds(kp + page * a.k.page_stride + off * a.k.place_stride + 8u * k_chunk, k_to);
+                if (v_chunk <= last_chunk)
+                    load_to_lds(vp + page * a.v.page_stride + off * a.v.place_stride + 8u * v_chunk, v_to);
+            }
         }
     }
 
+    // A chunk of a row of K in LDS is kept at its number XOR this.
+    static __device__ __forceinline__ uint32_t k_turn(uint32_t row) { return row & (kChunks < 16 ? 7u : 15u); }
+
     __device__ __forceinline__ void scores(floatx4 (&s)[M][2], const uint8_t *k) const {
-        const uint32_t last_chunk = a.dim / 8u - 1u;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint8_t *row = k + (16u * t + l16) * (2 * DP);
@@ -566,75 +662,80 @@ struct ManyWave : Rows<T, KK, M> {
             for (int i = 0; i < M; ++i) s[i][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                const uint32_t chunk = 4u * kk + quarter;
-                Vec f = *reinterpret_cast<const Vec *>(row + 16u * (chunk ^ (l16 & 7u)));
-                if (a.dim != DP && chunk > last_chunk) f = Vec{};
+                const Vec f = *reinterpret_cast<const Vec *>(row + 16u * ((4u * kk + quarter) ^ k_turn(l16)));
 #pragma unroll
                 for (int i = 0; i < M; ++i) s[i][t] = mfma(f, R::q[i][kk], s[i][t]);
             }
         }
     }
 
-    __device__ __forceinline__ void compute(uint32_t key0, uint32_t valid, const uint8_t *k, const uint8_t *v) {
-        // (a wave's rows may end before the tile's places do)
-        uint32_t token, head;
-        row_of(a, p, R::row0 + 16u * M - 1u, token, head);
-        if (key0 >= p.limit || (!a.mask && key0 > p.s.length + token)) return;
-        floatx4 s[M][2];
-        scores(s, k);
-        const bool masked = R::masked(key0, valid);
-        if (masked) R::mask(s, key0, valid);
-        Vec w[M];
-        R::weigh(s, w);
-        if (masked && R::bad_values(v)) {
-            R::add_one_by_one(s, v);
-            return;
+    // Where a run stands: the tile at key0 is in cur, the next one in next or on its way.
+    struct Ring {
+        uint32_t key0, end, id;  // id: of the tile after the next
+        uint64_t valid, valid_next;
+        uint8_t *cur, *next, *free;
+    };
+
+    // Tiles from r.key0 on while they are seen whole, or all (kMasked).
+    template <bool kMasked>
+    __device__ __forceinline__ void tiles(Ring &r) {
+        constexpr uint64_t kAll = kTile == 64 ? ~0ull : (1ull << (kTile % 64)) - 1u;
+        while (r.key0 < r.end && (kMasked || (r.key0 + kTile <= p.s.length && (r.valid & kAll) == kAll))) {
+            // This tile has landed (the next one's loads, sent for after it, may be on
+            // their way), and no wave reads the one before any more.
+            wait_loads<2 * kLoads>();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            uint64_t later = 0;
+            // (the next id first: a wait for it leaves the tile's loads alone)
+            const uint32_t then = load_id(r.key0 + 3u * kTile);
+            issue(r.key0 + 2u * kTile, r.id, r.free, later);
+            r.id = then;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const uint32_t at = (group * kBlocks + b) * kBlock, key0 = r.key0 + at;
+                const uint8_t *k = r.cur + at * (2 * DP), *v = k + kHalf;
+                floatx4 s[M][2];
+                if constexpr (kMasked) {
+                    // (a wave's rows may end before the tile's places do)
+                    uint32_t token, head;
+                    row_of(a, p, R::row0 + 16u * M - 1u, token, head);
+                    if (key0 < p.limit && (a.mask || key0 <= p.s.length + token)) {
+                        scores(s, k);
+                        R::take_masked(s, key0, static_cast<uint32_t>(r.valid >> at), v);
+                    }
+                } else {
+                    scores(s, k);
+                    R::take(s, v);
+                }
+            }
+            r.key0 += kTile;
+            r.valid = r.valid_next;
+            r.valid_next = later;
+            uint8_t *x = r.cur;
+            r.cur = r.next;
+            r.next = r.free;
+            r.free = x;
         }
-        R::add(w, v);
     }
 
     // (called by all waves of the workgroup, with a barrier since the last use of the ring)
     __device__ __forceinline__ void run() {
-        const uint32_t first = p.step0 * kStepPlaces, end = min(p.limit, p.step1 * kStepPlaces);
-        const uint32_t tiles = first < end ? (end - first + kTile - 1u) / kTile : 0u;
-        if (!tiles) return;
-        uint64_t valid[2] = {0, 0};
-        uint8_t *cur = lds, *next = lds + kStage, *free = lds + 2 * kStage;
-        const uint32_t id0 = load_id(first), id1 = load_id(first + kTile);
-        uint32_t id = load_id(first + 2u * kTile);
-        issue(first, id0, cur, valid[0]);
-        if (tiles > 1u) issue(first + kTile, id1, next, valid[1]);
-        for (uint32_t t = 0; t < tiles; ++t) {
-            const uint32_t key0 = first + t * kTile;
-            // This tile has landed (the next one's loads, sent for after it, may be on
-            // their way), and no wave reads the one before any more.
-            if (t + 1u < tiles) {
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
-            } else {
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            uint64_t later = 0;
-            if (t + 2u < tiles) {
-                // (the next id first: a wait for it leaves this tile's loads alone)
-                const uint32_t then = load_id(key0 + 3u * kTile);
-                issue(key0 + 2u * kTile, id, free, later);
-                id = then;
-            }
-#pragma unroll 1
-            for (int b = 0; b < kBlocks; ++b) {
-                const uint32_t at = (group * kBlocks + b) * kBlock;
-                compute(key0 + at, static_cast<uint32_t>(valid[0] >> at), cur + at * (2 * DP), cur + kHalf + at * (2 * DP));
-            }
-            valid[0] = valid[1];
-            valid[1] = later;
-            uint8_t *x = cur;
-            cur = next;
-            next = free;
-            free = x;
+        Ring r{p.step0 * kStepPlaces, min(p.limit, p.step1 * kStepPlaces), 0, 0, 0, lds, lds + kStage, lds + 2 * kStage};
+        if (r.key0 >= r.end) return;
+        if (!kWhole && a.dim != DP) {
+            // Chunks past head_dim are never loaded: zeros, as in q.
+            for (uint32_t at = threadIdx.x; at < 3u * kStage / 16u; at += 64u * kWaves)
+                reinterpret_cast<uint4 *>(lds)[at] = uint4{0, 0, 0, 0};
+            __syncthreads();
         }
+        const uint32_t id0 = load_id(r.key0), id1 = load_id(r.key0 + kTile);
+        r.id = load_id(r.key0 + 2u * kTile);
+        issue(r.key0, id0, r.cur, r.valid);
+        issue(r.key0 + kTile, id1, r.next, r.valid_next);
+        tiles<false>(r);
+        tiles<true>(r);
+        wait_loads<0>();  // (the ring is used otherwise next)
     }
 };
 
@@ -654,7 +755,7 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
         // (every wave's reads of the places, and of the row tile before, are back)
         __syncthreads();
         if (w.quarter == 0) {
-            s_stats[wave][w.l16][0] = w.m[i] == -INFINITY ? -INFINITY : w.m[i] * a.c;
+            s_stats[wave][w.l16][0] = w.ref[i];
             s_stats[wave][w.l16][1] = l;
         }
 #pragma unroll
@@ -744,9 +845,9 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
 }
 
 // Up to 32 rows: the workgroup's waves have them all, and the places in turn.
-template <typename T, int KK, int M, bool kWhole16>
+template <typename T, int KK, int M, bool kWhole>
 __global__ __launch_bounds__(64 * kFewWaves) void df11_attention_few_kernel(AttentionArgs a) {
-    using W = FewWave<T, KK, M, kWhole16>;
+    using W = FewWave<T, KK, M, kWhole>;
     constexpr uint32_t kWaveBytes = 2u * W::kVBytes;
     static_assert(kWaveBytes >= 16 * (W::DP + 4) * 4, "a row tile's sums fit a wave's buffers");
     __shared__ __align__(1024) uint8_t s_mem[kFewWaves * kWaveBytes];
@@ -760,10 +861,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void df11_attention_few_kernel(Atte
 }
 
 // More rows: eight waves share tiles of places in LDS.
-template <typename T, int KK, int M, int WR, int WK>
+template <typename T, int KK, int M, int WR, int WK, bool kWhole>
 __global__ __launch_bounds__(64 * WR * WK) __attribute__((amdgpu_waves_per_eu(WR * WK / 4)))
 void df11_attention_many_kernel(AttentionArgs a) {
-    using W = ManyWave<T, KK, M, WR, WK>;
+    using W = ManyWave<T, KK, M, WR, WK, kWhole>;
     constexpr uint32_t kSums = WR * WK * 16 * (W::DP + 4) * 4;
     __shared__ __align__(1024) uint8_t s_mem[3 * W::kStage > kSums ? 3 * W::kStage : kSums];
     __shared__ float s_stats[WR * WK][16][2];
@@ -825,21 +926,27 @@ __global__ __launch_bounds__(256) void df11_attention_join_kernel(AttentionArgs 
 
 // The kernels, by the rows of their tiles.
 template <typename T, int KK>
-const void *pick_rows(uint32_t rows, bool whole16) {
+const void *pick_rows(uint32_t rows, bool whole) {
     const auto few = [&](auto m) {
         constexpr int M = decltype(m)::value;
-        return whole16 ? reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, M, true>)
+        return whole ? reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, M, true>)
                        : reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, M, false>);
     };
     if (rows == 16) return few(std::integral_constant<int, 1>{});
+    const auto many = [&](auto m, auto wr, auto wk) {
+        constexpr int M = decltype(m)::value, WR = decltype(wr)::value, WK = decltype(wk)::value;
+        return whole ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, M, WR, WK, true>)
+                       : reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, M, WR, WK, false>);
+    };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 8> eight;
     if constexpr (KK == 8) {
-        return rows == 64 ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 1, 4, 1>)
-                          : reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 1, 8, 1>);
+        return rows == 64 ? many(one, four, one) : many(one, eight, one);
     } else {
-        if (rows == 32) return few(std::integral_constant<int, 2>{});
-        return rows == 64    ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 1, 4, 2>)
-               : rows == 128 ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 2, 4, 2>)
-                             : reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, 2, 8, 1>);
+        if (rows == 32) return few(two);
+        return rows == 64 ? many(one, four, two) : rows == 128 ? many(two, four, two) : many(two, eight, one);
     }
 }
 
@@ -855,9 +962,12 @@ uint32_t tile_threads(uint32_t dim, uint32_t rows) {
 }
 
 template <typename T>
-const void *pick_kernel(uint32_t dim, uint32_t rows, bool whole16) {
-    return dim <= 64 ? pick_rows<T, 2>(rows, whole16) : dim <= 128 ? pick_rows<T, 4>(rows, whole16) : pick_rows<T, 8>(rows, whole16);
+const void *pick_kernel(uint32_t dim, uint32_t rows, bool whole) {
+    return dim <= 64 ? pick_rows<T, 2>(rows, whole) : dim <= 128 ? pick_rows<T, 4>(rows, whole) : pick_rows<T, 8>(rows, whole);
 }
+
+// Largest stride between places whose 16 fit 32 bits of offset.
+constexpr uint64_t kMaxPlaceStride = 1u << 26;
 
 // How a call is launched.
 struct Plan {
@@ -871,11 +981,16 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     if (device_cus(dev, cus)) return DF11_E_HIP;
     const uint32_t group = q_heads / c.heads;
     const uint64_t rows = static_cast<uint64_t>((b.n_tokens + b.n_seqs - 1) / b.n_seqs) * group;
-    const bool whole16 = c.page_size % 16 == 0;
     p.tile_rows = pick_tile(c.head_dim, rows);
     p.threads = tile_threads(c.head_dim, p.tile_rows);
-    p.fn = c.dtype == DF11_BF16 ? pick_kernel<bf16_t>(c.head_dim, p.tile_rows, whole16)
-                                : pick_kernel<fp16_t>(c.head_dim, p.tile_rows, whole16);
+    // Whether the rows of one load are places of one page, and fill it: then a load
+    // has one address and 32-bit offsets.
+    const uint32_t together = p.tile_rows <= 16 || (p.tile_rows == 32 && c.head_dim <= 128) ? 16 : 8;
+    const bool few = together == 16;
+    const bool whole = c.page_size % together == 0 && (few || c.head_dim == 64 || c.head_dim == 128 || c.head_dim == 256) &&
+                       c.k_place_stride <= kMaxPlaceStride && c.v_place_stride <= kMaxPlaceStride;
+    p.fn = c.dtype == DF11_BF16 ? pick_kernel<bf16_t>(c.head_dim, p.tile_rows, whole)
+                                : pick_kernel<fp16_t>(c.head_dim, p.tile_rows, whole);
     const int per_cu = resident_per_cu(p.fn, p.threads, dev, 0);
     if (per_cu < 1) return DF11_E_HIP;
     const uint64_t capacity = static_cast<uint64_t>(b.table_pages) * c.page_size;
@@ -967,7 +1082,6 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     k.page_shift = df11::page_shift(c->page_size);
     k.page_magic = df11::page_magic(c->page_size, k.page_shift);
     k.c = a->scale * 1.44269504088896341f;
-    k.headroom = std::min(8.0f / k.c, 1e30f);
     k.mask_cols = a->mask_cols;
     k.n_pages = c->n_pages;
     k.page_size = c->page_size;
