@@ -43,15 +43,32 @@
 
 namespace {
 
-using df11::kStepPlaces;
+using df11::kFewStep;
+using df11::kManyStep;
 using df11::SeqShape;
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kBlock = 32;   // places of one block of scores
-constexpr uint32_t kFewWaves = 4;  // waves of the kernel for few rows
-static_assert(kStepPlaces == kFewWaves * kBlock, "a step is one block for each wave");
+// Waves of the kernel for few rows, by the head's padded size: as many as have room
+// for their rows of V.
+template <int KK>
+constexpr uint32_t kFewWaves = KK > 4 ? 4 : 8;
+static_assert(kFewStep == kFewWaves<4> * kBlock, "a step is a block for each wave");
+
+// Parts of a tile whose loads one thread of the second kernel has in flight, and
+// the most tiles that it joins.
+constexpr uint32_t kJoinAtOnce = 8, kMaxCuts = 1024;
+
+// A tile that a run begins and leaves to the runs after it.
+struct Cut {
+    int32_t begin;          // of its sequence: the first token, tokens
+    uint32_t rows, head, tile;
+    uint32_t run, last;     // runs that have parts of it; last 0: there is none
+    uint32_t slot;          // of run's two slots; the others have it in their first
+    uint32_t reserved;
+};
 
 struct AttentionArgs {
     df11::KvBatch b;
@@ -64,9 +81,11 @@ struct AttentionArgs {
     uint64_t capacity;    // places of a sequence's pages
     float *parts;         // [workgroup][2][row][dim]
     float *stats;         // [workgroup][2][row][2]: reference times c, sum
+    Cut *cut;             // [workgroup]; null where no tile is ever cut
     uint32_t page_magic, page_shift;  // df11::page_of
     float c;              // scale log2(e)
     uint32_t mask_cols, n_pages, page_size, kv_heads, group, dim, workgroups, tile_rows;
+    uint32_t step;  // places of a unit
 };
 
 __device__ __forceinline__ floatx4 mfma(vec_t<bf16_t, 8> a, vec_t<bf16_t, 8> b, floatx4 c) {
@@ -139,69 +158,39 @@ __device__ __forceinline__ float weight_of(float m, float to) { return m == -INF
 
 __device__ __forceinline__ SeqShape shape_of(const AttentionArgs &a, uint32_t s) {
     return df11::seq_shape(a.b.starts[s], a.b.starts[s + 1], a.b.lengths[s], a.b.n_tokens, a.capacity, a.group,
-                           a.tile_rows);
+                           a.tile_rows, a.step, a.mask != nullptr);
 }
 
-// Units of all sequences, and of those before sequence `until`, by a whole
-// workgroup of THREADS threads.
-template <uint32_t THREADS>
-__device__ __forceinline__ void count_units(const AttentionArgs &a, uint32_t until, uint64_t &all, uint64_t &before,
-                                            uint64_t (*s_part)[2]) {
-    uint64_t sum[2] = {0, 0};
-    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += THREADS) {
-        const uint64_t n = df11::seq_units(shape_of(a, s), a.kv_heads);
-        sum[0] += n;
-        if (s < until) sum[1] += n;
-    }
-#pragma unroll
-    for (int m = 32; m; m >>= 1) {
-        sum[0] += __shfl_xor(sum[0], m);
-        sum[1] += __shfl_xor(sum[1], m);
-    }
-    if ((threadIdx.x & 63u) == 0) {
-        s_part[threadIdx.x / 64u][0] = sum[0];
-        s_part[threadIdx.x / 64u][1] = sum[1];
-    }
-    __syncthreads();
-    all = before = 0;
-#pragma unroll
-    for (uint32_t w = 0; w < THREADS / 64u; ++w) {
-        all += s_part[w][0];
-        before += s_part[w][1];
-    }
-    __syncthreads();
-}
-
-// The sequence that holds unit u and its first unit, by a whole workgroup.
+// The sequence that holds a unit, and its first unit.
 struct Found {
-    uint64_t first;
-    uint32_t seq;
+    uint32_t first, seq;
 };
 
+// Units of all sequences, by a whole workgroup of THREADS threads; a thread's own
+// sequence of the first THREADS, and the units up to its end, in `mine`.
 template <uint32_t THREADS>
-__device__ __forceinline__ Found find_unit(const AttentionArgs &a, uint64_t u, uint64_t (*s_part)[2], Found *s_found) {
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x / 64u;
-    uint64_t base = 0;
-    for (uint32_t at = 0; at < a.b.n_seqs; at += THREADS) {
-        const uint32_t s = at + threadIdx.x;
-        const uint64_t n = s < a.b.n_seqs ? df11::seq_units(shape_of(a, s), a.kv_heads) : 0;
-        uint64_t to = n;
+__device__ __forceinline__ uint64_t scan_units(const AttentionArgs &a, uint32_t at, uint64_t base, uint64_t &n,
+                                               uint64_t &mine, uint64_t *s_part) {
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x / 64u, s = at + threadIdx.x;
+    n = s < a.b.n_seqs ? df11::seq_units(shape_of(a, s), a.kv_heads) : 0;
+    mine = n;
+    const uint32_t here = min(64u, a.b.n_seqs - at);  // (lanes that have a sequence, in any wave)
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const uint64_t other = __shfl_up(to, m);
-            if (lane >= static_cast<uint32_t>(m)) to += other;
-        }
-        if (lane == 63u) s_part[wave][0] = to;
-        __syncthreads();
-        uint64_t first = base + to - n;
-        for (uint32_t w = 0; w < wave; ++w) first += s_part[w][0];
-        if (u >= first && u < first + n) *s_found = Found{first, s};
-#pragma unroll
-        for (uint32_t w = 0; w < THREADS / 64u; ++w) base += s_part[w][0];
-        __syncthreads();
-        if (u < base) break;
+    for (uint32_t m = 1; m < 64u; m <<= 1) {
+        if (m >= here) break;
+        const uint64_t other = __shfl_up(mine, m);
+        if (lane >= m) mine += other;
     }
-    return *s_found;
+    if (lane == here - 1u) s_part[wave] = mine;
+    __syncthreads();
+    uint64_t all = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < THREADS / 64u; ++w) {
+        if (at + 64u * w >= a.b.n_seqs) break;
+        if (w == wave) mine += base + all;
+        all += s_part[w];
+    }
+    return base + all;
 }
 
 // One tile's part of a run.
@@ -209,7 +198,7 @@ struct Part {
     SeqShape s;
     uint32_t seq, head, tile;
     uint32_t step0, step1;  // steps of this run
-    uint32_t limit;         // places that the tile may see
+    uint32_t plain, limit;  // places that every row of the tile sees, that some row may see
     bool whole;             // no other run has steps of this tile
 };
 
@@ -328,7 +317,7 @@ struct Rows {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][t][e] = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -ref[i]));
             // (all NaN: no reference, and nothing seen)
-            moves = moves || !(largest(x[i]) <= kRoom);
+            moves |= !(largest(x[i]) <= kRoom);
         }
         if (__ballot(moves)) {
 #pragma unroll
@@ -375,7 +364,7 @@ struct Rows {
 
     // The same where rows may not.
     __device__ __forceinline__ void take_masked(floatx4 (&s)[M][2], uint32_t key0, uint32_t valid, const uint8_t *v) {
-        const bool some = key0 + kBlock > p.s.length || valid != ~0u;
+        const bool some = key0 + kBlock > p.plain || valid != ~0u;
         if (some) mask(s, key0, valid);
         Vec w[M];
         weigh(s, w);
@@ -447,10 +436,12 @@ struct Rows {
     }
 };
 
-// A wave of the kernel for few rows: it has all the tile's rows and every fourth
-// block of places.
-template <typename T, int KK, int M, bool kWhole>
-struct FewWave : Rows<T, KK, M> {
+// A wave of the kernel for few rows: it has all the tile's rows, and the waves take
+// the blocks of places in turn.
+template <typename T, int KK, bool kWhole>
+struct FewWave : Rows<T, KK, 1> {
+    static constexpr int M = 1;
+    static constexpr uint32_t kStep = kFewWaves<KK> * kBlock;  // places of all waves' turns
     using R = Rows<T, KK, M>;
     using Vec = typename R::Vec;
     using R::a, R::p, R::lane, R::quarter, R::l16, R::DP, R::kChunks;
@@ -538,13 +529,13 @@ struct FewWave : Rows<T, KK, M> {
     // Blocks from key0 on while they are seen whole, or all (kMasked).
     template <bool kMasked>
     __device__ __forceinline__ void blocks(uint32_t &key0, uint32_t end, uint32_t &id, uint8_t *&cur, uint8_t *&other) {
-        while (key0 < end && (kMasked || (key0 + kBlock <= p.s.length && valid == ~0u))) {
+        while (key0 < end && (kMasked || (key0 + kBlock <= p.plain && valid == ~0u))) {
             // This block has landed, and the other buffer's last reads are back.
             wait_loads<0>();
             Vec next[2][KK];
             uint32_t next_valid = 0;
-            const uint32_t then = load_id(key0 + 2u * kStepPlaces);
-            issue(key0 + kStepPlaces, id, next, other, next_valid);
+            const uint32_t then = load_id(key0 + 2u * kStep);
+            issue(key0 + kStep, id, next, other, next_valid);
             id = then;
             floatx4 s[M][2];
             scores(s);
@@ -561,19 +552,19 @@ struct FewWave : Rows<T, KK, M> {
             uint8_t *x = cur;
             cur = other;
             other = x;
-            key0 += kStepPlaces;
+            key0 += kStep;
         }
     }
 
     __device__ __forceinline__ void run(uint32_t wave) {
-        uint32_t key0 = p.step0 * kStepPlaces + wave * kBlock;
-        const uint32_t end = min(p.limit, p.step1 * kStepPlaces);
+        uint32_t key0 = p.step0 * a.step + wave * kBlock;
+        const uint32_t end = min(p.limit, p.step1 * a.step);
         if (key0 >= end) return;
         uint8_t *cur = lds, *other = lds + kVBytes;
         // (this wave's reads of the buffers, for the tile before, are back)
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         issue(key0, load_id(key0), k, cur, valid);
-        uint32_t id = load_id(key0 + kStepPlaces);
+        uint32_t id = load_id(key0 + kStep);
         blocks<false>(key0, end, id, cur, other);
         blocks<true>(key0, end, id, cur, other);
         wait_loads<0>();  // (the buffers are used otherwise next)
@@ -676,11 +667,13 @@ struct ManyWave : Rows<T, KK, M> {
         uint8_t *cur, *next, *free;
     };
 
-    // Tiles from r.key0 on while they are seen whole, or all (kMasked).
-    template <bool kMasked>
+    // Tiles from r.key0 on: kPlain while they are seen whole, kMasked all, kIdle all
+    // for a wave without rows, which only sends for its part of them.
+    enum Kind { kPlain, kMasked, kIdle };
+    template <Kind kKind>
     __device__ __forceinline__ void tiles(Ring &r) {
         constexpr uint64_t kAll = kTile == 64 ? ~0ull : (1ull << (kTile % 64)) - 1u;
-        while (r.key0 < r.end && (kMasked || (r.key0 + kTile <= p.s.length && (r.valid & kAll) == kAll))) {
+        while (r.key0 < r.end && (kKind != kPlain || (r.key0 + kTile <= p.plain && (r.valid & kAll) == kAll))) {
             // This tile has landed (the next one's loads, sent for after it, may be on
             // their way), and no wave reads the one before any more.
             wait_loads<2 * kLoads>();
@@ -696,7 +689,7 @@ struct ManyWave : Rows<T, KK, M> {
                 const uint32_t at = (group * kBlocks + b) * kBlock, key0 = r.key0 + at;
                 const uint8_t *k = r.cur + at * (2 * DP), *v = k + kHalf;
                 floatx4 s[M][2];
-                if constexpr (kMasked) {
+                if constexpr (kKind == kMasked) {
                     // (a wave's rows may end before the tile's places do)
                     uint32_t token, head;
                     row_of(a, p, R::row0 + 16u * M - 1u, token, head);
@@ -704,7 +697,7 @@ struct ManyWave : Rows<T, KK, M> {
                         scores(s, k);
                         R::take_masked(s, key0, static_cast<uint32_t>(r.valid >> at), v);
                     }
-                } else {
+                } else if constexpr (kKind == kPlain) {
                     scores(s, k);
                     R::take(s, v);
                 }
@@ -721,7 +714,7 @@ struct ManyWave : Rows<T, KK, M> {
 
     // (called by all waves of the workgroup, with a barrier since the last use of the ring)
     __device__ __forceinline__ void run() {
-        Ring r{p.step0 * kStepPlaces, min(p.limit, p.step1 * kStepPlaces), 0, 0, 0, lds, lds + kStage, lds + 2 * kStage};
+        Ring r{p.step0 * a.step, min(p.limit, p.step1 * a.step), 0, 0, 0, lds, lds + kStage, lds + 2 * kStage};
         if (r.key0 >= r.end) return;
         if (!kWhole && a.dim != DP) {
             // Chunks past head_dim are never loaded: zeros, as in q.
@@ -733,8 +726,14 @@ struct ManyWave : Rows<T, KK, M> {
         r.id = load_id(r.key0 + 2u * kTile);
         issue(r.key0, id0, r.cur, r.valid);
         issue(r.key0 + kTile, id1, r.next, r.valid_next);
-        tiles<false>(r);
-        tiles<true>(r);
+        uint32_t token, head;
+        row_of(a, p, R::row0, token, head);
+        if (token < p.s.rows) {
+            tiles<kPlain>(r);
+            tiles<kMasked>(r);
+        } else {
+            tiles<kIdle>(r);
+        }
         wait_loads<0>();  // (the ring is used otherwise next)
     }
 };
@@ -807,56 +806,83 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
 // A workgroup's run of units: f(part, slot) for every tile that it has a part of.
 template <uint32_t THREADS, typename F>
 __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
-    __shared__ uint64_t s_part[THREADS / 64][2];
+    __shared__ uint64_t s_part[THREADS / 64];
     __shared__ Found s_found;
-    uint64_t units, unused;
-    count_units<THREADS>(a, 0, units, unused, s_part);
-    if (units == 0) return;
-    const uint32_t runs = df11::runs_of(units, a.workgroups);
+    // Units of all sequences; then the one that this run begins in.  (Up to THREADS
+    // sequences the first round has both.)
+    uint64_t units = 0, n = 0, mine = 0;
+    for (uint32_t at = 0; at < a.b.n_seqs; at += THREADS) {
+        if (at) __syncthreads();
+        units = scan_units<THREADS>(a, at, units, n, mine, s_part);
+    }
+    const bool none = units == 0 || units >= df11::kMaxUnits;
+    const uint32_t all = static_cast<uint32_t>(units), runs = none ? 0u : df11::runs_of(all, a.workgroups);
+    // What the second kernel finds of a run: the tile that it begins and leaves.
+    if (a.cut && blockIdx.x >= runs && threadIdx.x == 0) a.cut[blockIdx.x].last = 0;
     if (blockIdx.x >= runs) return;
     const uint32_t run = df11::run_of_workgroup(blockIdx.x, runs);
-    uint64_t u = df11::run_begin(run, units, runs);
-    const uint64_t end = df11::run_begin(run + 1ull, units, runs);
-    const Found found = find_unit<THREADS>(a, u, s_part, &s_found);
-    uint32_t seq = __builtin_amdgcn_readfirstlane(found.seq);
-    uint64_t first = found.first;
+    uint32_t u = df11::run_begin(run, all, runs);
+    const uint32_t end = df11::run_begin(run + 1u, all, runs);
+    uint64_t base = 0;
+    for (uint32_t at = 0; at < a.b.n_seqs; at += THREADS) {
+        if (a.b.n_seqs > THREADS) {
+            __syncthreads();
+            base = scan_units<THREADS>(a, at, base, n, mine, s_part);
+        }
+        if (u >= mine - n && u < mine) s_found = Found{static_cast<uint32_t>(mine - n), at + threadIdx.x};
+    }
+    __syncthreads();
+    uint32_t seq = __builtin_amdgcn_readfirstlane(s_found.seq), first = __builtin_amdgcn_readfirstlane(s_found.first);
     bool begun = true;  // the run's first tile may have begun in the run before
+    bool left = false;
     while (u < end && seq < a.b.n_seqs) {
         Part p;
         p.s = shape_of(a, seq);
-        const uint64_t here = df11::seq_units(p.s, a.kv_heads);
+        const uint32_t one = p.s.tiles ? static_cast<uint32_t>(df11::units_before(p.s, p.s.tiles)) : 0u;
+        const uint32_t here = one * a.kv_heads;
         if (u >= first + here) {
             first += here;
             ++seq;
             continue;
         }
-        const uint64_t tile_no = (u - first) / p.s.steps, tile_first = first + tile_no * p.s.steps;
         p.seq = seq;
-        p.head = static_cast<uint32_t>(tile_no / p.s.tiles);
-        p.tile = df11::tile_in_turn(static_cast<uint32_t>(tile_no % p.s.tiles), p.s.tiles, a.mask != nullptr);
-        p.step0 = static_cast<uint32_t>(u - tile_first);
-        p.step1 = end - tile_first < p.s.steps ? static_cast<uint32_t>(end - tile_first) : p.s.steps;
+        p.head = (u - first) / one;
+        const uint32_t head_first = first + p.head * one;
+        p.tile = df11::tile_of(p.s, u - head_first);
+        const uint32_t tile_first = head_first + static_cast<uint32_t>(df11::units_before(p.s, p.tile));
+        const uint32_t steps = df11::tile_units(p.s, p.tile);
+        p.step0 = u - tile_first;
+        p.step1 = min(end - tile_first, steps);
+        p.plain = df11::tile_plain(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
         p.limit = df11::tile_places(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
-        p.whole = p.step0 == 0 && p.step1 == p.s.steps;
+        p.whole = p.step0 == 0 && p.step1 == steps;
+        if (a.cut && p.step0 == 0 && !p.whole) {
+            left = true;
+            if (threadIdx.x == 0)
+                a.cut[run] = Cut{p.s.begin, p.s.rows, p.head, p.tile, run, df11::run_of(tile_first + steps - 1u, all, runs),
+                                 begun ? 0u : 1u, 0u};
+        }
         f(p, 2ull * run + (begun ? 0u : 1u));
         begun = false;
         u = tile_first + p.step1;
     }
+    if (a.cut && !left && threadIdx.x == 0) a.cut[run].last = 0;
 }
 
-// Up to 32 rows: the workgroup's waves have them all, and the places in turn.
-template <typename T, int KK, int M, bool kWhole>
-__global__ __launch_bounds__(64 * kFewWaves) void df11_attention_few_kernel(AttentionArgs a) {
-    using W = FewWave<T, KK, M, kWhole>;
-    constexpr uint32_t kWaveBytes = 2u * W::kVBytes;
+// Up to 16 rows: the workgroup's waves have them all, and the places in turn.
+template <typename T, int KK, bool kWhole>
+__global__ __launch_bounds__(64 * kFewWaves<KK>) __attribute__((amdgpu_waves_per_eu(kFewWaves<KK> / 4)))
+void df11_attention_few_kernel(AttentionArgs a) {
+    using W = FewWave<T, KK, kWhole>;
+    constexpr uint32_t kWaves = kFewWaves<KK>, kWaveBytes = 2u * W::kVBytes;
     static_assert(kWaveBytes >= 16 * (W::DP + 4) * 4, "a row tile's sums fit a wave's buffers");
-    __shared__ __align__(1024) uint8_t s_mem[kFewWaves * kWaveBytes];
-    __shared__ float s_stats[kFewWaves][16][2];
+    __shared__ __align__(1024) uint8_t s_mem[kWaves * kWaveBytes];
+    __shared__ float s_stats[kWaves][16][2];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
-    for_each_part<64 * kFewWaves>(a, [&](const Part &p, uint64_t slot) {
+    for_each_part<64 * kWaves>(a, [&](const Part &p, uint64_t slot) {
         W w(a, p, s_mem + wave * kWaveBytes);
         w.run(wave);
-        finish_part<T, KK, M, 1, kFewWaves>(a, p, w, wave, s_mem, s_stats, slot);
+        finish_part<T, KK, 1, 1, kWaves>(a, p, w, wave, s_mem, s_stats, slot);
     });
 }
 
@@ -876,67 +902,127 @@ void df11_attention_many_kernel(AttentionArgs a) {
     });
 }
 
-// The parts of one token's rows of one key head, joined in the order of the
-// places: a thread has eight elements of a row.
+// Joins `at`-th vector of eight elements of a cut tile, row by row.  kWaves: waves of
+// the workgroup that take the vector's parts together, a stretch each, in the
+// order of the places.
+template <typename T, uint32_t kWaves>
+__device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c, uint32_t at, float (*s_sum)[10][64]) {
+    const uint32_t chunks = a.dim / 8u, row = at / chunks, d = 8u * (at % chunks), lane = threadIdx.x & 63u;
+    const uint32_t wave = kWaves > 1 ? threadIdx.x / 64u : 0u;
+    const uint32_t in_tiles = c.tile * a.tile_rows + row, token = in_tiles / a.group;
+    const bool there = row < a.tile_rows && token < c.rows;
+    const uint32_t in = there ? row : 0u;
+    const auto slot_of = [&](uint32_t r) { return (2ull * r + (r == c.run ? c.slot : 0u)) * a.tile_rows + in; };
+    const uint32_t each = (c.last - c.run + kWaves) / kWaves;
+    const uint32_t begin = c.run + wave * each, end = min(begin + each, c.last + 1u);
+    float top = -INFINITY, total = 0.0f, sum[8] = {};
+    for (uint32_t r = begin; r < end; r += kJoinAtOnce) {
+        float st[kJoinAtOnce][2], v[kJoinAtOnce][8];
+#pragma unroll
+        for (uint32_t k = 0; k < kJoinAtOnce; ++k) {  // (past the last one again, not added)
+            const uint64_t slot = slot_of(min(r + k, end - 1u));
+            load_vec<float, 2>(a.stats + slot * 2u, st[k]);
+            load_vec<float, 4>(a.parts + slot * a.dim + d, *reinterpret_cast<float(*)[4]>(&v[k][0]));
+            load_vec<float, 4>(a.parts + slot * a.dim + d + 4, *reinterpret_cast<float(*)[4]>(&v[k][4]));
+        }
+        float to = top;
+#pragma unroll
+        for (uint32_t k = 0; k < kJoinAtOnce; ++k) to = fmaxf(to, st[k][0]);
+        const float old = weight_of(top, to);
+        total *= old;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] *= old;
+#pragma unroll
+        for (uint32_t k = 0; k < kJoinAtOnce; ++k) {
+            const float f = r + k < end ? weight_of(st[k][0], to) : 0.0f;
+            if (f == 0.0f) continue;
+            total += f * st[k][1];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += f * v[k][e];
+        }
+        top = to;
+    }
+    if constexpr (kWaves > 1) {
+        __syncthreads();  // (the vectors before have been read)
+        s_sum[wave][8][lane] = top;
+        s_sum[wave][9][lane] = total;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_sum[wave][e][lane] = sum[e];
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (uint32_t w = 1; w < kWaves; ++w) {
+            const float to = fmaxf(top, s_sum[w][8][lane]), old = weight_of(top, to), f = weight_of(s_sum[w][8][lane], to);
+            total *= old;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] *= old;
+            if (f != 0.0f) {
+                total += f * s_sum[w][9][lane];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += f * s_sum[w][e][lane];
+            }
+            top = to;
+        }
+    }
+    if (!there) return;
+    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] *= f;
+    const uint64_t t = static_cast<uint64_t>(c.begin) + token;
+    const uint32_t head = c.head * a.group + in_tiles % a.group;
+    store_vec<T, 8>(static_cast<T *>(a.out) + t * a.out_stride + head * a.out_head_stride + d, sum);
+    if (a.lse && d == 0)
+        a.lse[t * (a.kv_heads * a.group) + head] =
+            total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
+}
+
+// Joins the parts of the tiles that runs begin and leave to others.  Every
+// workgroup finds all of them, in the same order, those of many parts first, and
+// takes its share of their vectors: 64 at a time with all four waves, or of a tile
+// of few parts 64 for each wave.
 template <typename T>
 __global__ __launch_bounds__(256) void df11_attention_join_kernel(AttentionArgs a) {
-    __shared__ uint64_t s_part[4][2];
-    const uint32_t token = blockIdx.x, head = blockIdx.y;
-    const int32_t seq = __builtin_amdgcn_readfirstlane(sequence_of(a.b, static_cast<int32_t>(token)));
-    if (seq < 0) return;
-    uint64_t units, first;
-    count_units<256>(a, static_cast<uint32_t>(seq), units, first, s_part);
-    const SeqShape s = shape_of(a, seq);
-    if (units == 0 || !s.tiles) return;
-    const uint32_t runs = df11::runs_of(units, a.workgroups);
-    const uint32_t i = token - static_cast<uint32_t>(s.begin), chunks = a.dim / 8u;
-    for (uint32_t at = threadIdx.x; at < a.group * chunks; at += 256u) {
-        const uint32_t g = at / chunks, d = 8u * (at % chunks);
-        const uint32_t row = i * a.group + g, tile = row / a.tile_rows, in_tile = row % a.tile_rows;
-        const uint32_t turn = df11::turn_of_tile(tile, s.tiles, a.mask != nullptr);
-        const uint64_t from = first + (static_cast<uint64_t>(head) * s.tiles + turn) * s.steps;
-        const uint32_t lo = df11::run_of(from, units, runs), hi = df11::run_of(from + s.steps - 1u, units, runs);
-        if (lo == hi) continue;
-        float top = -INFINITY, total = 0.0f, sum[8] = {};
-        // A run's first slot holds the tile that it begins with.
-        const uint32_t late = df11::run_begin(lo, units, runs) == from ? 0u : 1u;
-        const auto slot_of = [&](uint32_t r) { return 2ull * r + (r == lo ? late : 0u); };
-        for (uint32_t r = lo; r <= hi; ++r) top = fmaxf(top, a.stats[(slot_of(r) * a.tile_rows + in_tile) * 2u]);
-        for (uint32_t r = lo; r <= hi; ++r) {
-            const uint64_t slot = slot_of(r) * a.tile_rows + in_tile;
-            const float f = weight_of(a.stats[slot * 2u], top);
-            if (f == 0.0f) continue;
-            total += f * a.stats[slot * 2u + 1u];
-            float v[8];
-            load_vec<float, 4>(a.parts + slot * a.dim + d, *reinterpret_cast<float(*)[4]>(&v[0]));
-            load_vec<float, 4>(a.parts + slot * a.dim + d + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
+    __shared__ uint32_t s_count[2][4], s_cut[2][kMaxCuts];
+    __shared__ float s_sum[4][10][64];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+    uint32_t found[2] = {0, 0};  // of many parts, of few
+    for (uint32_t at = 0; at < a.workgroups; at += 256u) {
+        const uint32_t w = at + threadIdx.x;
+        uint32_t parts = 0;
+        if (w < a.workgroups && a.cut[w].last) parts = a.cut[w].last - a.cut[w].run + 1u;
+        const uint64_t of[2] = {__ballot(parts > kJoinAtOnce), __ballot(parts && parts <= kJoinAtOnce)};
+        __syncthreads();
+        if (lane < 2u) s_count[lane][wave] = static_cast<uint32_t>(__popcll(of[lane]));
+        __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += f * v[e];
+        for (int k = 0; k < 2; ++k) {
+            uint32_t first = found[k];
+#pragma unroll
+            for (uint32_t x = 0; x < 4u; ++x) {
+                if (x < wave) first += s_count[k][x];
+                found[k] += s_count[k][x];
+            }
+            if ((of[k] >> lane) & 1u) s_cut[k][first + __popcll(of[k] & ((1ull << lane) - 1u))] = w;
         }
-        const float f = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] *= f;
-        const uint32_t q_head = head * a.group + g;
-        store_vec<T, 8>(static_cast<T *>(a.out) + token * a.out_stride + q_head * a.out_head_stride + d, sum);
-        if (a.lse && d == 0)
-            a.lse[static_cast<uint64_t>(token) * (a.kv_heads * a.group) + q_head] =
-                total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
     }
+    __syncthreads();
+    const uint32_t items = (a.tile_rows * (a.dim / 8u) + 63u) / 64u;
+    for (uint32_t i = blockIdx.x; i < found[0] * items; i += gridDim.x)
+        join_vector<T, 4>(a, a.cut[s_cut[0][i / items]], (i % items) * 64u + lane, s_sum);
+    for (uint32_t i = blockIdx.x * 4u + wave; i < found[1] * items; i += gridDim.x * 4u)
+        join_vector<T, 1>(a, a.cut[s_cut[1][i / items]], (i % items) * 64u + lane, s_sum);
 }
 
 // The kernels, by the rows of their tiles.
 template <typename T, int KK>
 const void *pick_rows(uint32_t rows, bool whole) {
-    const auto few = [&](auto m) {
-        constexpr int M = decltype(m)::value;
-        return whole ? reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, M, true>)
-                       : reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, M, false>);
-    };
-    if (rows == 16) return few(std::integral_constant<int, 1>{});
+    if (rows == 16)
+        return whole ? reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, true>)
+                     : reinterpret_cast<const void *>(&df11_attention_few_kernel<T, KK, false>);
     const auto many = [&](auto m, auto wr, auto wk) {
         constexpr int M = decltype(m)::value, WR = decltype(wr)::value, WK = decltype(wk)::value;
         return whole ? reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, M, WR, WK, true>)
-                       : reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, M, WR, WK, false>);
+                     : reinterpret_cast<const void *>(&df11_attention_many_kernel<T, KK, M, WR, WK, false>);
     };
     const std::integral_constant<int, 1> one;
     const std::integral_constant<int, 2> two;
@@ -945,7 +1031,6 @@ const void *pick_rows(uint32_t rows, bool whole) {
     if constexpr (KK == 8) {
         return rows == 64 ? many(one, four, one) : many(one, eight, one);
     } else {
-        if (rows == 32) return few(two);
         return rows == 64 ? many(one, four, two) : rows == 128 ? many(two, four, two) : many(two, eight, one);
     }
 }
@@ -953,13 +1038,10 @@ const void *pick_rows(uint32_t rows, bool whole) {
 // Rows of a tile: enough for the rows that a sequence has on average (the host
 // knows no more than that).
 uint32_t pick_tile(uint32_t dim, uint64_t rows) {
-    if (dim > 128) return rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    return rows <= 16 ? 16 : rows <= 64 ? 64 : rows <= 128 || dim > 128 ? 128 : 256;
 }
 
-uint32_t tile_threads(uint32_t dim, uint32_t rows) {
-    return 64u * (rows <= 16 || (rows == 32 && dim <= 128) ? kFewWaves : rows == 64 && dim > 128 ? 4u : 8u);
-}
+uint32_t tile_threads(uint32_t dim, uint32_t rows) { return dim > 128 && rows <= 64 ? 256 : 512; }
 
 template <typename T>
 const void *pick_kernel(uint32_t dim, uint32_t rows, bool whole) {
@@ -972,8 +1054,8 @@ constexpr uint64_t kMaxPlaceStride = 1u << 26;
 // How a call is launched.
 struct Plan {
     const void *fn;
-    uint32_t tile_rows, threads, workgroups;
-    uint64_t parts, stats;  // bytes; 0 where no tile is ever cut
+    uint32_t tile_rows, threads, workgroups, step;
+    uint64_t parts, stats, cut;  // bytes; 0 where no tile is ever cut
 };
 
 int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, Plan &p) {
@@ -985,8 +1067,8 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     p.threads = tile_threads(c.head_dim, p.tile_rows);
     // Whether the rows of one load are places of one page, and fill it: then a load
     // has one address and 32-bit offsets.
-    const uint32_t together = p.tile_rows <= 16 || (p.tile_rows == 32 && c.head_dim <= 128) ? 16 : 8;
-    const bool few = together == 16;
+    const bool few = p.tile_rows == 16;
+    const uint32_t together = few ? 16 : 8;
     const bool whole = c.page_size % together == 0 && (few || c.head_dim == 64 || c.head_dim == 128 || c.head_dim == 256) &&
                        c.k_place_stride <= kMaxPlaceStride && c.v_place_stride <= kMaxPlaceStride;
     p.fn = c.dtype == DF11_BF16 ? pick_kernel<bf16_t>(c.head_dim, p.tile_rows, whole)
@@ -995,12 +1077,15 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     if (per_cu < 1) return DF11_E_HIP;
     const uint64_t capacity = static_cast<uint64_t>(b.table_pages) * c.page_size;
     const uint64_t tiles = (static_cast<uint64_t>(b.n_tokens) * group + p.tile_rows - 1) / p.tile_rows + b.n_seqs;
-    const uint64_t units = tiles * c.heads * std::max<uint64_t>(1, (capacity + kStepPlaces - 1) / kStepPlaces);
-    if (static_cast<uint64_t>(b.n_tokens) * group >= (1ull << 31) || units >= (1ull << 31)) return DF11_E_TOO_LARGE;
-    p.workgroups = static_cast<uint32_t>(std::min<uint64_t>(static_cast<uint64_t>(cus) * per_cu, units));
-    const uint64_t slots = capacity > kStepPlaces ? 2ull * p.workgroups * p.tile_rows : 0;
+    p.step = df11::unit_places(capacity, few);
+    // (a tile without a mask may count a unit for its own tokens beside the pages')
+    const uint64_t units = tiles * c.heads * ((capacity + p.step - 1) / p.step + 2);
+    if (static_cast<uint64_t>(b.n_tokens) * group >= (1ull << 31) || units >= df11::kMaxUnits) return DF11_E_TOO_LARGE;
+    p.workgroups = static_cast<uint32_t>(std::min<uint64_t>({static_cast<uint64_t>(cus) * per_cu, units, kMaxCuts}));
+    const uint64_t slots = capacity > p.step ? 2ull * p.workgroups * p.tile_rows : 0;
     p.parts = round_up(slots * c.head_dim * 4, 256);
     p.stats = round_up(slots * 8, 256);
+    p.cut = slots ? round_up(p.workgroups * sizeof(Cut), 256) : 0;
     return DF11_OK;
 }
 
@@ -1033,7 +1118,7 @@ uint64_t df11_tree_attention_workspace(const df11_kv_cache *c, const df11_kv_bat
     Plan p{};
     if (check_kv(c, b, k_span, v_span) || check_attention(*c, *b, a, q_span, out_span)) return 0;
     if (b->n_tokens == 0 || b->n_seqs == 0 || make_plan(*c, *b, a->q_heads, p)) return 0;
-    return p.parts + p.stats;
+    return p.parts + p.stats + p.cut;
 }
 
 int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df11_attention *a, void *workspace,
@@ -1059,7 +1144,7 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     Plan p{};
     rc = make_plan(*c, *b, a->q_heads, p);
     if (rc) return rc;
-    spans[2] = p.parts + p.stats;
+    spans[2] = p.parts + p.stats + p.cut;
     if (spans[2] && (!workspace || !aligned(workspace, 256))) return DF11_E_INVALID_ARG;
     if (workspace_bytes < spans[2]) return DF11_E_BUFFER_TOO_SMALL;
     if (!clear(2)) return DF11_E_INVALID_ARG;
@@ -1079,6 +1164,7 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     k.capacity = static_cast<uint64_t>(b->table_pages) * c->page_size;
     k.parts = static_cast<float *>(workspace);
     k.stats = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + p.parts);
+    k.cut = p.cut ? reinterpret_cast<Cut *>(static_cast<uint8_t *>(workspace) + p.parts + p.stats) : nullptr;
     k.page_shift = df11::page_shift(c->page_size);
     k.page_magic = df11::page_magic(c->page_size, k.page_shift);
     k.c = a->scale * 1.44269504088896341f;
@@ -1090,6 +1176,7 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     k.dim = c->head_dim;
     k.workgroups = p.workgroups;
     k.tile_rows = p.tile_rows;
+    k.step = p.step;
     (void)hipGetLastError();
     const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     void *params[] = {&k};
@@ -1097,7 +1184,10 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     if (rc || !spans[2]) return rc;
     const void *join = c->dtype == DF11_BF16 ? reinterpret_cast<const void *>(&df11_attention_join_kernel<bf16_t>)
                                              : reinterpret_cast<const void *>(&df11_attention_join_kernel<fp16_t>);
-    return launch_kernel(join, dim3(b->n_tokens, c->heads), dim3(256), params, 0, stream, nullptr, nullptr);
+    // (every item its own workgroup where that fills the chip no more than twice)
+    const uint64_t items = static_cast<uint64_t>(p.workgroups) * ((p.tile_rows * (c->head_dim / 8) + 63) / 64);
+    return launch_kernel(join, dim3(static_cast<uint32_t>(std::min<uint64_t>(items, 2ull * kMaxCuts))), dim3(256), params, 0,
+                         stream, nullptr, nullptr);
 }
 
 }  // extern "C"

@@ -4,10 +4,12 @@
 //
 // A unit is one tile of a sequence's query rows (row = token * group + head
 // within the group of query heads that share a key head) against one step of
-// kStepPlaces places.  Sequence by sequence, key head by key head, tile by tile,
+// places.  Sequence by sequence, key head by key head, tile by tile,
 // step by step the units are numbered, and the workgroups take equal runs of
 // them, whatever the lengths are: a run may begin and end inside a tile, whose
-// parts the second kernel joins.
+// parts the second kernel joins.  With a mask every tile has all of a sequence's
+// steps; without one the later tiles see more, and a tile's steps are a bound
+// whose sums have a closed form (at most two steps too many).
 #ifndef DF11_ATTENTION_PLAN_H
 #define DF11_ATTENTION_PLAN_H
 
@@ -15,7 +17,18 @@
 
 namespace df11 {
 
-constexpr uint32_t kStepPlaces = 128;
+// (A step is a block of 32 places for each wave of a workgroup that has few rows,
+// and short enough to be cut evenly for many.)
+constexpr uint32_t kFewStep = 256, kManyStep = 128;
+
+// A sequence's pages up to which its tiles are never cut: then a unit is a whole
+// tile, and no second kernel joins parts.
+constexpr uint64_t kWholePlaces = 1024;
+
+// Places of a unit, for pages of `capacity` places.
+constexpr uint32_t unit_places(uint64_t capacity, bool few) {
+    return capacity <= kWholePlaces ? static_cast<uint32_t>(kWholePlaces) : few ? kFewStep : kManyStep;
+}
 
 // A sequence as the kernels see it, after the checks of what the device holds.
 struct SeqShape {
@@ -24,12 +37,15 @@ struct SeqShape {
     uint32_t rows;    // of them, those that the call's arrays have
     uint32_t length;  // places cached before them
     uint32_t places;  // places in its pages, length + tokens at most
-    uint32_t tiles, steps;
+    uint32_t tiles;
+    uint32_t first;   // steps of a tile before what the tiles add
+    uint32_t each;    // tiles that add one step, or
+    uint32_t more;    // steps that each tile adds
 };
 
 constexpr SeqShape seq_shape(int32_t begin, int32_t end, int32_t length, uint32_t n_tokens, uint64_t capacity,
-                             uint32_t group, uint32_t tile_rows) {
-    SeqShape s{begin, 0, 0, 0, 0, 0, 0};
+                             uint32_t group, uint32_t tile_rows, uint32_t step, bool masked) {
+    SeqShape s{begin, 0, 0, 0, 0, 0, 0, 1, 0};
     if (begin < 0 || end <= begin || length < 0 || static_cast<uint32_t>(begin) >= n_tokens) return s;
     const uint32_t last = static_cast<uint32_t>(end) < n_tokens ? static_cast<uint32_t>(end) : n_tokens;
     s.tokens = static_cast<uint32_t>(end - begin);
@@ -38,27 +54,69 @@ constexpr SeqShape seq_shape(int32_t begin, int32_t end, int32_t length, uint32_
     const uint64_t all = static_cast<uint64_t>(s.length) + s.tokens;
     s.places = static_cast<uint32_t>(all < capacity ? all : capacity);
     s.tiles = static_cast<uint32_t>((static_cast<uint64_t>(s.rows) * group + tile_rows - 1) / tile_rows);
-    s.steps = (s.places + kStepPlaces - 1) / kStepPlaces;
-    if (!s.steps) s.steps = 1;  // (no pages: its rows are still written)
+    if (masked || capacity <= step || s.tiles <= 1u) {
+        s.first = (s.places + step - 1) / step;
+        if (!s.first) s.first = 1;  // (no pages: its rows are still written)
+    } else {
+        // Tile t ends with token (t + 1) tile_rows / group, rounded up.
+        const uint32_t held = s.length < s.places ? s.length : s.places;
+        const uint64_t tokens = static_cast<uint64_t>(step) * group;  // rows of a step's tokens
+        s.first = (held + step - 1) / step;
+        if (tokens >= tile_rows) {
+            s.each = static_cast<uint32_t>(tokens / tile_rows);
+            s.more = 1;
+        } else {
+            s.more = static_cast<uint32_t>((tile_rows + tokens - 1) / tokens);
+        }
+    }
     return s;
 }
 
+// Units of the tiles before tile t of one key head, and of tile t.
+constexpr uint64_t units_before(const SeqShape &s, uint32_t t) {
+    const uint64_t all = static_cast<uint64_t>(t) * s.first;
+    if (!s.more) return all;
+    const uint64_t whole = t / s.each, rest = t % s.each;
+    // 1 + 1 + .. (each times) + 2 + 2 + ..
+    return all + s.more * (s.each * (whole * (whole + 1) / 2) + rest * (whole + 1));
+}
+constexpr uint32_t tile_units(const SeqShape &s, uint32_t t) {
+    return s.more ? s.first + s.more * (t / s.each + 1) : s.first;
+}
+
+// The tile of unit u < units_before(tiles) of a key head.
+constexpr uint32_t tile_of(const SeqShape &s, uint32_t u) {
+    if (!s.more) return u / s.first;
+    uint32_t lo = 0, hi = s.tiles;  // the last tile that begins at u or before is in [lo, hi)
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (units_before(s, mid) <= u) {
+            lo = mid;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
+}
+
 constexpr uint64_t seq_units(const SeqShape &s, uint32_t kv_heads) {
-    return static_cast<uint64_t>(kv_heads) * s.tiles * s.steps;
+    return s.tiles ? kv_heads * units_before(s, s.tiles) : 0;
 }
 
-// Workgroups that get a run: as many as there are, but no fewer than kMinUnits
-// units each.
-constexpr uint64_t kMinUnits = 1;
-constexpr uint32_t runs_of(uint64_t units, uint32_t workgroups) {
-    const uint64_t most = units / kMinUnits;
-    return most >= workgroups ? workgroups : most ? static_cast<uint32_t>(most) : 1u;
-}
+// The units of a call; more (of starts that decrease) are none at all.
+constexpr uint64_t kMaxUnits = 1ull << 31;
 
-// First unit of run w, and the run of a unit u < units (units < 2^40).
-constexpr uint64_t run_begin(uint64_t w, uint64_t units, uint32_t runs) { return w * units / runs; }
-constexpr uint32_t run_of(uint64_t u, uint64_t units, uint32_t runs) {
-    return static_cast<uint32_t>(((u + 1) * runs + units - 1) / units - 1);
+// Workgroups that get a run: as many as there are units for.
+constexpr uint32_t runs_of(uint32_t units, uint32_t workgroups) { return units < workgroups ? units : workgroups; }
+
+// First unit of run w: the first units % runs of them have one unit more.  And the
+// run of a unit.
+constexpr uint32_t run_begin(uint32_t w, uint32_t units, uint32_t runs) {
+    return w * (units / runs) + (w < units % runs ? w : units % runs);
+}
+constexpr uint32_t run_of(uint32_t u, uint32_t units, uint32_t runs) {
+    const uint32_t each = units / runs, more = units % runs, longer = more * (each + 1u);
+    return u < longer ? u / (each + 1u) : more + (u - longer) / each;
 }
 
 // The run of workgroup i: neighbouring runs, which share a sequence's places, on
@@ -66,16 +124,6 @@ constexpr uint32_t run_of(uint64_t u, uint64_t units, uint32_t runs) {
 constexpr uint32_t run_of_workgroup(uint32_t i, uint32_t runs) {
     const uint32_t xcd = i % 8u, each = runs / 8u, rest = runs % 8u;
     return xcd * each + (xcd < rest ? xcd : rest) + i / 8u;
-}
-
-// Tile of the t-th place in the order of work: without a mask later tiles see
-// more, so that light and heavy ones take turns.
-constexpr uint32_t tile_in_turn(uint32_t t, uint32_t tiles, bool masked) {
-    return masked ? t : t % 2u ? tiles - 1u - t / 2u : t / 2u;
-}
-
-constexpr uint32_t turn_of_tile(uint32_t tile, uint32_t tiles, bool masked) {
-    return masked ? tile : tile < (tiles + 1u) / 2u ? 2u * tile : 2u * (tiles - 1u - tile) + 1u;
 }
 
 // place / page_size for places below 2^31 and pages up to 2^20: with 2^s the
@@ -91,6 +139,12 @@ constexpr uint32_t page_magic(uint32_t page_size, uint32_t shift) {
 }
 constexpr uint32_t page_of(uint32_t place, uint32_t magic, uint32_t shift) {
     return static_cast<uint32_t>((static_cast<uint64_t>(place) * magic) >> (31u + shift));
+}
+
+// Places that every row of a tile sees, as far as they exist.
+constexpr uint32_t tile_plain(const SeqShape &s, uint32_t tile, uint32_t tile_rows, uint32_t group, bool masked) {
+    const uint64_t sees = masked ? s.length : s.length + static_cast<uint64_t>(tile) * tile_rows / group + 1;
+    return static_cast<uint32_t>(sees < s.places ? sees : s.places);
 }
 
 // Places that some row of a tile may see.

@@ -9,7 +9,6 @@ import pytest
 
 REPO = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(REPO, "entropy_decoding_df11_amd", "csrc")
-STEP = 128
 
 
 @pytest.fixture(scope="module")
@@ -38,7 +37,7 @@ def test_pages(cli):
 
 
 @pytest.mark.parametrize("units,workgroups", [(1, 512), (7, 512), (511, 512), (512, 512), (513, 512), (100003, 512),
-                                              (5, 1), ((1 << 31) - 1, 1024)])
+                                              (5, 1), ((1 << 31) - 1, 1023)])
 def test_runs_cover_the_units(cli, units, workgroups):
     (line,) = cli([f"R {units} {workgroups}"])
     runs, begins = line[0], line[1:]
@@ -60,29 +59,35 @@ def test_every_workgroup_has_its_run(cli, runs):
         assert mine == list(range(mine[0], mine[0] + len(mine))) if mine else True
 
 
-@pytest.mark.parametrize("tiles", [1, 2, 3, 8, 97])
-@pytest.mark.parametrize("masked", [0, 1])
-def test_tiles_take_turns(cli, tiles, masked):
-    (got,) = cli([f"T {tiles} {masked}"])
-    assert sorted(got[0::2]) == list(range(tiles))
-    assert got[1::2] == list(range(tiles))
-
-
 @pytest.mark.parametrize("begin,end,length,n_tokens,capacity", [
     (0, 1, 0, 1, 128), (3, 40, 1000, 64, 4096), (3, 40, 1000, 20, 4096), (0, 5, 100, 5, 96), (0, 5, 100, 5, 0),
     (4, 4, 9, 8, 64), (5, 4, 9, 8, 64), (-1, 4, 9, 8, 64), (0, 4, -1, 8, 64), (8, 12, 1, 8, 64),
-    (0, 7, (1 << 31) - 1, 7, 1 << 30), (-2 ** 31, 2 ** 31 - 1, 0, 8, 64), (0, 2 ** 31 - 1, 5, 8, 64)])
-@pytest.mark.parametrize("group,tile_rows", [(1, 16), (4, 16), (7, 32)])
+    (0, 7, (1 << 31) - 1, 7, 1 << 30), (-2 ** 31, 2 ** 31 - 1, 0, 8, 64), (0, 2 ** 31 - 1, 5, 8, 64),
+    (0, 900, 0, 900, 4096), (0, 900, 2500, 1000, 4096), (0, 900, 2500, 1000, 2000), (7, 900, 130, 700, 1 << 20)])
+@pytest.mark.parametrize("group,tile_rows", [(1, 16), (4, 16), (7, 32), (1, 256), (5, 128), (64, 16)])
+@pytest.mark.parametrize("step", [128, 1024])
 @pytest.mark.parametrize("masked", [0, 1])
-def test_shapes(cli, begin, end, length, n_tokens, capacity, group, tile_rows, masked):
-    (got,) = cli([f"S {begin} {end} {length} {n_tokens} {capacity} {group} {tile_rows} 3 {masked}"])
+def test_shapes(cli, begin, end, length, n_tokens, capacity, group, tile_rows, step, masked):
+    (got,) = cli([f"S {begin} {end} {length} {n_tokens} {capacity} {group} {tile_rows} {step} 3 {masked}"])
     if begin < 0 or end <= begin or length < 0 or begin >= n_tokens:
-        assert got[0] == 0 and got[6] == 0
+        assert got[0] == 0 and got[5] == 0
         return
     tokens, rows = end - begin, min(end, n_tokens) - begin
     places = min(length + tokens, capacity)
-    tiles, steps = -(-rows * group // tile_rows), max(1, -(-places // STEP))
-    assert got[:7] == [tokens, rows, length, places, tiles, steps, 3 * tiles * steps]
-    for tile, seen in enumerate(got[7:]):
-        last = min((tile * tile_rows + tile_rows - 1) // group, rows - 1)
-        assert seen == (places if masked else min(places, length + last + 1))
+    tiles = -(-rows * group // tile_rows)
+    assert got[:5] == [tokens, rows, length, places, tiles]
+    units = 0
+    for tile in range(tiles):
+        plain, seen, own, before, first, last = got[6 + 6 * tile:12 + 6 * tile]
+        assert plain == min(places, length if masked else length + tile * tile_rows // group + 1)
+        row = min((tile * tile_rows + tile_rows - 1) // group, rows - 1)
+        assert seen == (places if masked else min(places, length + row + 1))
+        # enough for what the tile sees, and not many more
+        assert before == units and first == last == tile and own * step >= seen and own >= 1
+        # (a table that ends before the sequence does bounds what is seen, not the steps)
+        most = -(-(length + row + 1) // step) + 2 + -(-(tile_rows // group + 2) // step)
+        assert own <= (max(1, -(-places // step)) if masked else most)
+        if masked or capacity <= step:
+            assert own == max(1, -(-places // step))
+        units += own
+    assert got[5] == 3 * units
