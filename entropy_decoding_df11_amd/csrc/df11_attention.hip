@@ -85,7 +85,7 @@ struct AttentionArgs {
     uint32_t page_magic, page_shift;  // df11::page_of
     float c;              // scale log2(e)
     uint32_t mask_cols, n_pages, page_size, kv_heads, group, dim, workgroups, tile_rows;
-    uint32_t step;  // places of a unit
+    uint32_t step, extra;  // places of a unit, units of a tile beside them
 };
 
 __device__ __forceinline__ floatx4 mfma(vec_t<bf16_t, 8> a, vec_t<bf16_t, 8> b, floatx4 c) {
@@ -158,26 +158,26 @@ __device__ __forceinline__ float weight_of(float m, float to) { return m == -INF
 
 __device__ __forceinline__ SeqShape shape_of(const AttentionArgs &a, uint32_t s) {
     return df11::seq_shape(a.b.starts[s], a.b.starts[s + 1], a.b.lengths[s], a.b.n_tokens, a.capacity, a.group,
-                           a.tile_rows, a.step, a.mask != nullptr);
+                           a.tile_rows, a.step, a.extra, a.mask != nullptr);
 }
 
 // The sequence that holds a unit, and its first unit.
 struct Found {
     uint32_t first, seq;
+    SeqShape shape;
 };
 
 // Units of all sequences, by a whole workgroup of THREADS threads; a thread's own
 // sequence of the first THREADS, and the units up to its end, in `mine`.
 template <uint32_t THREADS>
-__device__ __forceinline__ uint64_t scan_units(const AttentionArgs &a, uint32_t at, uint64_t base, uint64_t &n,
-                                               uint64_t &mine, uint64_t *s_part) {
+__device__ __forceinline__ uint64_t scan_units(const AttentionArgs &a, uint32_t at, uint64_t base, SeqShape &shape,
+                                               uint64_t &n, uint64_t &mine, uint64_t *s_part) {
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x / 64u, s = at + threadIdx.x;
-    n = s < a.b.n_seqs ? df11::seq_units(shape_of(a, s), a.kv_heads) : 0;
+    shape = shape_of(a, min(s, a.b.n_seqs - 1u));
+    n = s < a.b.n_seqs ? df11::seq_units(shape, a.kv_heads) : 0;
     mine = n;
     const uint32_t here = min(64u, a.b.n_seqs - at);  // (lanes that have a sequence, in any wave)
-#pragma unroll
-    for (uint32_t m = 1; m < 64u; m <<= 1) {
-        if (m >= here) break;
+    for (uint32_t m = 1; m < here; m <<= 1) {
         const uint64_t other = __shfl_up(mine, m);
         if (lane >= m) mine += other;
     }
@@ -235,13 +235,21 @@ struct Rows {
 
     __device__ __forceinline__ Rows(const AttentionArgs &args, const Part &part, uint32_t first_row)
         : a(args), p(part), row0(first_row), lane(threadIdx.x & 63u), quarter(lane >> 4), l16(lane & 15u) {
-        const uint32_t last_chunk = a.dim / 8u - 1u;
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             ref[i] = -INFINITY;
             l[i] = 0.0f;
 #pragma unroll
             for (int d = 0; d < kTilesD; ++d) o[i][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    }
+
+    // Sends for the queries.  (Rows past the last one have another's: their sums go
+    // nowhere.)
+    __device__ __forceinline__ void load_queries() {
+        const uint32_t last_chunk = a.dim / 8u - 1u;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
             uint32_t token, head;
             row_of(a, p, row0 + 16u * i + l16, token, head);
             const bool there = token < p.s.rows;
@@ -249,12 +257,19 @@ struct Rows {
                            (static_cast<uint64_t>(p.s.begin) + (there ? token : 0u)) * a.q_stride +
                            (there ? head : p.head * a.group) * a.q_head_stride;
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                const uint32_t chunk = 4u * kk + quarter;
-                q[i][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(chunk, last_chunk));
-                if (!there || chunk > last_chunk) q[i][kk] = Vec{};
-            }
+            for (int kk = 0; kk < KK; ++kk)
+                q[i][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(4u * kk + quarter, last_chunk));
         }
+    }
+
+    // Zeros in their chunks past head_dim, as in K's.
+    __device__ __forceinline__ void pad_queries() {
+        if (a.dim == DP) return;
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                if (4u * kk + quarter >= a.dim / 8u) q[i][kk] = Vec{};
     }
 
     // A pair of chunks of a row of V in LDS is kept at its number XOR this.
@@ -268,39 +283,38 @@ struct Rows {
     // has made code that keeps the masked ones.)
     __device__ __forceinline__ uint32_t seen(uint32_t token, const uint8_t *mask_row, uint32_t key0, uint32_t valid) const {
         uint32_t bits = 0;
+        if (mask_row && a.mask_cols) {
+            // (eight loads at once, of the last column where there is none)
+            uint32_t byte[8];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t key = key0 + 16u * t + 4u * quarter;
-            if (a.mask) {
+            for (int e = 0; e < 8; ++e)
+                byte[e] = mask_row[min(key0 + 16u * (e / 4) + 4u * quarter + e % 4 - p.s.length, a.mask_cols - 1u)];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t j = key + e - p.s.length;  // (wraps where the place is cached)
-                    uint32_t bit = key + e < p.s.length ? 1u : 0u;
-                    if (j < a.mask_cols) bit |= mask_row[j] != 0 ? 1u : 0u;
-                    bits |= bit << (4 * t + e);
-                }
-            } else {
-                const uint32_t end = p.s.length + token + 1u;  // places that the row sees
-                const uint32_t n = key < end ? min(end - key, 4u) : 0u;
+            for (int e = 0; e < 8; ++e) {
+                // (a cached place's j wraps)
+                const uint32_t key = key0 + 16u * (e / 4) + 4u * quarter + e % 4, j = key - p.s.length;
+                bits |= (key < p.s.length ? 1u : j < a.mask_cols && byte[e] ? 1u : 0u) << e;
+            }
+        } else {
+            const uint32_t end = p.s.length + (mask_row ? 0u : token + 1u);  // places that the row sees
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t key = key0 + 16u * t + 4u * quarter, n = key < end ? min(end - key, 4u) : 0u;
                 bits |= ((1u << n) - 1u) << (4 * t);
             }
         }
         return bits & (((valid >> (4u * quarter)) & 15u) | (((valid >> (16u + 4u * quarter)) & 15u) << 4));
     }
 
-    __device__ __forceinline__ void mask(floatx4 (&s)[M][2], uint32_t key0, uint32_t valid) const {
+    // The same of every row tile.
+    __device__ __forceinline__ void look(uint32_t (&bits)[M], uint32_t key0, uint32_t valid) const {
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             uint32_t token, head;
             row_of(a, p, row0 + 16u * i + l16, token, head);
             const uint8_t *mask_row =
                 a.mask ? a.mask + (p.s.begin + static_cast<uint64_t>(min(token, p.s.rows - 1u))) * a.mask_stride : nullptr;
-            const uint32_t bits = seen(token, mask_row, key0, valid);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[i][t][e] = (bits >> (4 * t + e)) & 1u ? s[i][t][e] : -INFINITY;
+            bits[i] = seen(token, mask_row, key0, valid);
         }
     }
 
@@ -363,12 +377,17 @@ struct Rows {
     }
 
     // The same where rows may not.
-    __device__ __forceinline__ void take_masked(floatx4 (&s)[M][2], uint32_t key0, uint32_t valid, const uint8_t *v) {
-        const bool some = key0 + kBlock > p.plain || valid != ~0u;
-        if (some) mask(s, key0, valid);
+    __device__ __forceinline__ void take_masked(floatx4 (&s)[M][2], const uint32_t (&bits)[M], const uint8_t *v) {
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            some |= bits[i] != 255u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[i][e / 4][e % 4] = (bits[i] >> e) & 1u ? s[i][e / 4][e % 4] : -INFINITY;
+        }
         Vec w[M];
         weigh(s, w);
-        if (some && bad_values(v)) {
+        if (__ballot(some) && bad_values(v)) {
             add_one_by_one(s, v);
         } else {
             add(w, v);
@@ -538,9 +557,11 @@ struct FewWave : Rows<T, KK, 1> {
             issue(key0 + kStep, id, next, other, next_valid);
             id = then;
             floatx4 s[M][2];
+            uint32_t bits[M];
+            if constexpr (kMasked) R::look(bits, key0, valid);
             scores(s);
             if constexpr (kMasked) {
-                R::take_masked(s, key0, valid, cur);
+                R::take_masked(s, bits, cur);
             } else {
                 R::take(s, cur);
             }
@@ -563,8 +584,11 @@ struct FewWave : Rows<T, KK, 1> {
         uint8_t *cur = lds, *other = lds + kVBytes;
         // (this wave's reads of the buffers, for the tile before, are back)
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        issue(key0, load_id(key0), k, cur, valid);
+        const uint32_t id0 = load_id(key0);
         uint32_t id = load_id(key0 + kStep);
+        R::load_queries();
+        issue(key0, id0, k, cur, valid);
+        R::pad_queries();
         blocks<false>(key0, end, id, cur, other);
         blocks<true>(key0, end, id, cur, other);
         wait_loads<0>();  // (the buffers are used otherwise next)
@@ -684,18 +708,27 @@ struct ManyWave : Rows<T, KK, M> {
             const uint32_t then = load_id(r.key0 + 3u * kTile);
             issue(r.key0 + 2u * kTile, r.id, r.free, later);
             r.id = then;
+            uint32_t bits[kBlocks][M];
+            if constexpr (kKind == kMasked) {
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    const uint32_t at = (group * kBlocks + b) * kBlock;
+                    R::look(bits[b], r.key0 + at, static_cast<uint32_t>(r.valid >> at));
+                }
+            }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
-                const uint32_t at = (group * kBlocks + b) * kBlock, key0 = r.key0 + at;
+                const uint32_t at = (group * kBlocks + b) * kBlock;
                 const uint8_t *k = r.cur + at * (2 * DP), *v = k + kHalf;
                 floatx4 s[M][2];
                 if constexpr (kKind == kMasked) {
                     // (a wave's rows may end before the tile's places do)
-                    uint32_t token, head;
-                    row_of(a, p, R::row0 + 16u * M - 1u, token, head);
-                    if (key0 < p.limit && (a.mask || key0 <= p.s.length + token)) {
+                    bool some = false;
+#pragma unroll
+                    for (int i = 0; i < M; ++i) some |= bits[b][i] != 0;
+                    if (__ballot(some)) {
                         scores(s, k);
-                        R::take_masked(s, key0, static_cast<uint32_t>(r.valid >> at), v);
+                        R::take_masked(s, bits[b], v);
                     }
                 } else if constexpr (kKind == kPlain) {
                     scores(s, k);
@@ -724,8 +757,10 @@ struct ManyWave : Rows<T, KK, M> {
         }
         const uint32_t id0 = load_id(r.key0), id1 = load_id(r.key0 + kTile);
         r.id = load_id(r.key0 + 2u * kTile);
+        R::load_queries();
         issue(r.key0, id0, r.cur, r.valid);
         issue(r.key0 + kTile, id1, r.next, r.valid_next);
+        R::pad_queries();
         uint32_t token, head;
         row_of(a, p, R::row0, token, head);
         if (token < p.s.rows) {
@@ -811,9 +846,10 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
     // Units of all sequences; then the one that this run begins in.  (Up to THREADS
     // sequences the first round has both.)
     uint64_t units = 0, n = 0, mine = 0;
+    SeqShape shape;
     for (uint32_t at = 0; at < a.b.n_seqs; at += THREADS) {
         if (at) __syncthreads();
-        units = scan_units<THREADS>(a, at, units, n, mine, s_part);
+        units = scan_units<THREADS>(a, at, units, shape, n, mine, s_part);
     }
     const bool none = units == 0 || units >= df11::kMaxUnits;
     const uint32_t all = static_cast<uint32_t>(units), runs = none ? 0u : df11::runs_of(all, a.workgroups);
@@ -827,22 +863,23 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
     for (uint32_t at = 0; at < a.b.n_seqs; at += THREADS) {
         if (a.b.n_seqs > THREADS) {
             __syncthreads();
-            base = scan_units<THREADS>(a, at, base, n, mine, s_part);
+            base = scan_units<THREADS>(a, at, base, shape, n, mine, s_part);
         }
-        if (u >= mine - n && u < mine) s_found = Found{static_cast<uint32_t>(mine - n), at + threadIdx.x};
+        if (u >= mine - n && u < mine) s_found = Found{static_cast<uint32_t>(mine - n), at + threadIdx.x, shape};
     }
     __syncthreads();
     uint32_t seq = __builtin_amdgcn_readfirstlane(s_found.seq), first = __builtin_amdgcn_readfirstlane(s_found.first);
     bool begun = true;  // the run's first tile may have begun in the run before
     bool left = false;
-    while (u < end && seq < a.b.n_seqs) {
-        Part p;
-        p.s = shape_of(a, seq);
+    Part p;
+    p.s = s_found.shape;
+    while (u < end) {
         const uint32_t one = p.s.tiles ? static_cast<uint32_t>(df11::units_before(p.s, p.s.tiles)) : 0u;
         const uint32_t here = one * a.kv_heads;
         if (u >= first + here) {
             first += here;
-            ++seq;
+            if (++seq == a.b.n_seqs) break;
+            p.s = shape_of(a, seq);
             continue;
         }
         p.seq = seq;
@@ -850,21 +887,22 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
         const uint32_t head_first = first + p.head * one;
         p.tile = df11::tile_of(p.s, u - head_first);
         const uint32_t tile_first = head_first + static_cast<uint32_t>(df11::units_before(p.s, p.tile));
-        const uint32_t steps = df11::tile_units(p.s, p.tile);
-        p.step0 = u - tile_first;
-        p.step1 = min(end - tile_first, steps);
+        const uint32_t tile_end = tile_first + df11::tile_units(p.s, p.tile), to = min(end, tile_end);
+        p.step0 = df11::steps_before(p.s, u - tile_first);
+        p.step1 = df11::steps_before(p.s, to - tile_first);
+        u = to;
+        if (p.step0 == p.step1) continue;
         p.plain = df11::tile_plain(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
         p.limit = df11::tile_places(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
-        p.whole = p.step0 == 0 && p.step1 == steps;
+        p.whole = p.step0 == 0 && to == tile_end;
         if (a.cut && p.step0 == 0 && !p.whole) {
             left = true;
             if (threadIdx.x == 0)
-                a.cut[run] = Cut{p.s.begin, p.s.rows, p.head, p.tile, run, df11::run_of(tile_first + steps - 1u, all, runs),
+                a.cut[run] = Cut{p.s.begin, p.s.rows, p.head, p.tile, run, df11::run_of(tile_end - 1u, all, runs),
                                  begun ? 0u : 1u, 0u};
         }
         f(p, 2ull * run + (begun ? 0u : 1u));
         begun = false;
-        u = tile_first + p.step1;
     }
     if (a.cut && !left && threadIdx.x == 0) a.cut[run].last = 0;
 }
@@ -1054,7 +1092,7 @@ constexpr uint64_t kMaxPlaceStride = 1u << 26;
 // How a call is launched.
 struct Plan {
     const void *fn;
-    uint32_t tile_rows, threads, workgroups, step;
+    uint32_t tile_rows, threads, workgroups, step, extra;
     uint64_t parts, stats, cut;  // bytes; 0 where no tile is ever cut
 };
 
@@ -1079,7 +1117,8 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     const uint64_t tiles = (static_cast<uint64_t>(b.n_tokens) * group + p.tile_rows - 1) / p.tile_rows + b.n_seqs;
     p.step = df11::unit_places(capacity, few);
     // (a tile without a mask may count a unit for its own tokens beside the pages')
-    const uint64_t units = tiles * c.heads * ((capacity + p.step - 1) / p.step + 2);
+    p.extra = df11::extra_units(capacity, few, c.head_dim);
+    const uint64_t units = tiles * c.heads * ((capacity + p.step - 1) / p.step + 2 + p.extra);
     if (static_cast<uint64_t>(b.n_tokens) * group >= (1ull << 31) || units >= df11::kMaxUnits) return DF11_E_TOO_LARGE;
     p.workgroups = static_cast<uint32_t>(std::min<uint64_t>({static_cast<uint64_t>(cus) * per_cu, units, kMaxCuts}));
     const uint64_t slots = capacity > p.step ? 2ull * p.workgroups * p.tile_rows : 0;
@@ -1177,6 +1216,7 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     k.workgroups = p.workgroups;
     k.tile_rows = p.tile_rows;
     k.step = p.step;
+    k.extra = p.extra;
     (void)hipGetLastError();
     const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     void *params[] = {&k};

@@ -9,7 +9,10 @@
 // them, whatever the lengths are: a run may begin and end inside a tile, whose
 // parts the second kernel joins.  With a mask every tile has all of a sequence's
 // steps; without one the later tiles see more, and a tile's steps are a bound
-// whose sums have a closed form (at most two steps too many).
+// whose sums have a closed form (at most two steps too many).  A tile counts some
+// units more, before its steps, for what it takes beside them (its queries, the
+// first loads that nothing hides, the end of its sums): a run that has only those
+// leaves the tile to the next one.
 #ifndef DF11_ATTENTION_PLAN_H
 #define DF11_ATTENTION_PLAN_H
 
@@ -41,11 +44,12 @@ struct SeqShape {
     uint32_t first;   // steps of a tile before what the tiles add
     uint32_t each;    // tiles that add one step, or
     uint32_t more;    // steps that each tile adds
+    uint32_t extra;   // units of a tile before its steps
 };
 
 constexpr SeqShape seq_shape(int32_t begin, int32_t end, int32_t length, uint32_t n_tokens, uint64_t capacity,
-                             uint32_t group, uint32_t tile_rows, uint32_t step, bool masked) {
-    SeqShape s{begin, 0, 0, 0, 0, 0, 0, 1, 0};
+                             uint32_t group, uint32_t tile_rows, uint32_t step, uint32_t extra, bool masked) {
+    SeqShape s{begin, 0, 0, 0, 0, 0, 0, 1, 0, extra};
     if (begin < 0 || end <= begin || length < 0 || static_cast<uint32_t>(begin) >= n_tokens) return s;
     const uint32_t last = static_cast<uint32_t>(end) < n_tokens ? static_cast<uint32_t>(end) : n_tokens;
     s.tokens = static_cast<uint32_t>(end - begin);
@@ -74,19 +78,22 @@ constexpr SeqShape seq_shape(int32_t begin, int32_t end, int32_t length, uint32_
 
 // Units of the tiles before tile t of one key head, and of tile t.
 constexpr uint64_t units_before(const SeqShape &s, uint32_t t) {
-    const uint64_t all = static_cast<uint64_t>(t) * s.first;
+    const uint64_t all = static_cast<uint64_t>(t) * (s.first + s.extra);
     if (!s.more) return all;
     const uint64_t whole = t / s.each, rest = t % s.each;
     // 1 + 1 + .. (each times) + 2 + 2 + ..
     return all + s.more * (s.each * (whole * (whole + 1) / 2) + rest * (whole + 1));
 }
 constexpr uint32_t tile_units(const SeqShape &s, uint32_t t) {
-    return s.more ? s.first + s.more * (t / s.each + 1) : s.first;
+    return s.extra + s.first + (s.more ? s.more * (t / s.each + 1) : 0u);
 }
+
+// Steps of a tile before its unit i.
+constexpr uint32_t steps_before(const SeqShape &s, uint32_t i) { return i > s.extra ? i - s.extra : 0u; }
 
 // The tile of unit u < units_before(tiles) of a key head.
 constexpr uint32_t tile_of(const SeqShape &s, uint32_t u) {
-    if (!s.more) return u / s.first;
+    if (!s.more) return u / (s.first + s.extra);
     uint32_t lo = 0, hi = s.tiles;  // the last tile that begins at u or before is in [lo, hi)
     while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
@@ -101,6 +108,14 @@ constexpr uint32_t tile_of(const SeqShape &s, uint32_t u) {
 
 constexpr uint64_t seq_units(const SeqShape &s, uint32_t kv_heads) {
     return s.tiles ? kv_heads * units_before(s, s.tiles) : 0;
+}
+
+// Units that a tile counts beside its steps, measured: a tile of many rows takes 12
+// us and a step of it 5.5 (2.5 for heads up to 64, 10 beyond 128), one of few rows 8
+// and 6.5.  (A batch of 24 trees over up to 4096 places, some over a few dozen: 50
+// us without them, when a workgroup had several short tiles.)
+constexpr uint32_t extra_units(uint64_t capacity, bool few, uint32_t dim) {
+    return capacity <= kWholePlaces ? 0u : few || dim > 128u ? 1u : dim > 64u ? 2u : 4u;
 }
 
 // The units of a call; more (of starts that decrease) are none at all.

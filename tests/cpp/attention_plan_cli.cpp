@@ -4,7 +4,7 @@
 //   "R units workgroups"           -> "runs", then "begin" of every run and of the end
 //   "W unit units workgroups"      -> the run of a unit
 //   "X runs"                       -> the run of every workgroup
-//   "S begin end length n_tokens capacity group tile_rows step kv_heads masked"
+//   "S begin end length n_tokens capacity group tile_rows step kv_heads masked extra"
 //                                  -> "tokens rows length places tiles units", then of every tile the places that all
 //                                     of it sees, that some of it may see, its units, the units before it, and its number by its first and last unit
 #include <stdint.h>
@@ -15,8 +15,8 @@
 int main() {
     char kind;
     while (scanf(" %c", &kind) == 1) {
-        long long v[10];
-        const int n = kind == 'S' ? 10 : kind == 'W' ? 3 : kind == 'X' ? 1 : 2;
+        long long v[11];
+        const int n = kind == 'S' ? 11 : kind == 'W' ? 3 : kind == 'X' ? 1 : 2;
         for (int i = 0; i < n; ++i)
             if (scanf("%lld", &v[i]) != 1) return 1;
         if (kind == 'P') {
@@ -38,7 +38,7 @@ int main() {
             const auto u = [&](int i) { return static_cast<uint32_t>(v[i]); };
             const df11::SeqShape s = df11::seq_shape(static_cast<int32_t>(v[0]), static_cast<int32_t>(v[1]),
                                                      static_cast<int32_t>(v[2]), u(3), static_cast<uint64_t>(v[4]), u(5),
-                                                     u(6), u(7), v[9] != 0);
+                                                     u(6), u(7), u(10), v[9] != 0);
             printf("%u %u %u %u %u %llu", s.tokens, s.rows, s.length, s.places, s.tiles,
                    static_cast<unsigned long long>(df11::seq_units(s, u(8))));
             for (uint32_t t = 0; t < s.tiles; ++t) {

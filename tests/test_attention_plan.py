@@ -65,10 +65,10 @@ def test_every_workgroup_has_its_run(cli, runs):
     (0, 7, (1 << 31) - 1, 7, 1 << 30), (-2 ** 31, 2 ** 31 - 1, 0, 8, 64), (0, 2 ** 31 - 1, 5, 8, 64),
     (0, 900, 0, 900, 4096), (0, 900, 2500, 1000, 4096), (0, 900, 2500, 1000, 2000), (7, 900, 130, 700, 1 << 20)])
 @pytest.mark.parametrize("group,tile_rows", [(1, 16), (4, 16), (7, 32), (1, 256), (5, 128), (64, 16)])
-@pytest.mark.parametrize("step", [128, 1024])
+@pytest.mark.parametrize("step,extra", [(128, 0), (128, 4), (1024, 0)])
 @pytest.mark.parametrize("masked", [0, 1])
-def test_shapes(cli, begin, end, length, n_tokens, capacity, group, tile_rows, step, masked):
-    (got,) = cli([f"S {begin} {end} {length} {n_tokens} {capacity} {group} {tile_rows} {step} 3 {masked}"])
+def test_shapes(cli, begin, end, length, n_tokens, capacity, group, tile_rows, step, extra, masked):
+    (got,) = cli([f"S {begin} {end} {length} {n_tokens} {capacity} {group} {tile_rows} {step} 3 {masked} {extra}"])
     if begin < 0 or end <= begin or length < 0 or begin >= n_tokens:
         assert got[0] == 0 and got[5] == 0
         return
@@ -82,12 +82,14 @@ def test_shapes(cli, begin, end, length, n_tokens, capacity, group, tile_rows, s
         assert plain == min(places, length if masked else length + tile * tile_rows // group + 1)
         row = min((tile * tile_rows + tile_rows - 1) // group, rows - 1)
         assert seen == (places if masked else min(places, length + row + 1))
+        assert before == units and first == last == tile
+        units += own
+        own -= extra
         # enough for what the tile sees, and not many more
-        assert before == units and first == last == tile and own * step >= seen and own >= 1
+        assert own * step >= seen and own >= 1
         # (a table that ends before the sequence does bounds what is seen, not the steps)
         most = -(-(length + row + 1) // step) + 2 + -(-(tile_rows // group + 2) // step)
         assert own <= (max(1, -(-places // step)) if masked else most)
         if masked or capacity <= step:
             assert own == max(1, -(-places // step))
-        units += own
     assert got[5] == 3 * units
