@@ -109,8 +109,11 @@ __device__ __forceinline__ void load_to_lds(Resource r, uint8_t *dst, uint32_t l
 
 // Four rows x 16 columns of 2-byte elements, transposed across a quarter
 // wave: lane i of the quarter passes the address of row i / 4, columns
-// 4 (i mod 4) .. + 3, and receives column i of the four rows.
-__device__ __forceinline__ shortx4 read_transposed(const uint8_t *p) {
+// 4 (i mod 4) .. + 3, and receives column i of the four rows.  (The pointer is
+// marked restrict for what that tells of the read: without it the compiler waits for
+// every load to LDS in flight before it, where the kernel's own waits are enough.
+// 2048 tokens, 28000 classes -> 4096: 478 against 406 us.)
+__device__ __forceinline__ shortx4 read_transposed(const uint8_t *__restrict p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4 *)p);
 }
 
@@ -281,7 +284,7 @@ struct LossRows {
             for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
             float ref = ceilf(top * kHi);
             if constexpr (MODE == kDenseExp) {
-                const float known = l.ref ? l.ref[token] : -INFINITY;
+                const float known = l.ref[token];
                 if (ref <= known + df11::kRefRoom) ref = known;
             }
             const float base = ref == -INFINITY ? 0.0f : ref;

@@ -21,10 +21,9 @@
 //
 // so that the logits are computed once and W is decoded once (recomputing them
 // in a backward pass of its own would take a third product and a second
-// decode).  R is a whole number: where a later piece moves it, the exponentials
-// in BF16 and A are rescaled exactly.  It moves only where a logit passes it by
-// 2^64; the first piece, which has none yet, is short, since its exponentials
-// are rescaled by a pass of their own.
+// decode).  R begins as the target's own exponent, from a dot product of x with
+// its row of W.  It is a whole number: where a logit passes it by 2^64 it moves, and
+// the exponentials in BF16 and A are rescaled exactly.
 //
 // Up to kPartialTokens tokens without a gradient the decode is fused into the
 // product, and its slots' sums end in the pairs; otherwise the head is decoded
@@ -50,8 +49,8 @@ using df11::kPartialTokens;
 using df11::Partials;
 using df11::PartialStream;
 
-constexpr uint32_t kFirstPiece = 4096;     // classes
-constexpr uint64_t kPieceExps = 64u << 20;  // exponentials of a later piece, tokens times classes
+constexpr uint64_t kPieceExps = 128u << 20;  // exponentials of a piece, tokens times classes
+constexpr uint32_t kLeastPiece = 4096;       // classes (a smaller product does not fill the chip)
 constexpr uint64_t kMaxRow = 1ull << 22;
 
 // log2(e) in two floats, and ln 2.
@@ -117,40 +116,111 @@ __device__ __forceinline__ float ref_scale(float r, float to) {
     return r == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r - to);
 }
 
-// A piece's pairs joined to what the token has: one wave a token.  Where the
-// reference moves, or a panel has another, exponentials are brought to it.
-__global__ __launch_bounds__(256) void df11_loss_piece_kernel(TokenArgs a, uint32_t first_piece) {
-    const uint32_t lane = threadIdx.x & (kWaveSize - 1);
-    const uint32_t token = blockIdx.x * 4u + threadIdx.x / kWaveSize;
-    if (token >= a.n_tokens) return;
-    const float *st = a.stats + 2u * token;
-    const uint64_t step = 2ull * a.n_tokens;
-    const float was = first_piece ? -INFINITY : a.ref[token];
-    float top = was;
-    for (uint32_t p = lane; p < a.panels; p += kWaveSize) top = fmaxf(top, st[p * step]);
-#pragma unroll
-    for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-    float sum = 0.0f;
-    for (uint32_t p = lane; p < a.panels; p += kWaveSize) sum += st[p * step + 1u] * ref_scale(st[p * step], top);
-#pragma unroll
-    for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
-    const float scale = ref_scale(was, top);
-    if (lane == 0) {
-        a.ref[token] = top;
-        a.sum[token] = first_piece ? sum : a.sum[token] * scale + sum;
-        a.scale[token] = scale;
+// Eight consecutive elements of row `row` of a decoded matrix in tile order.
+__device__ __forceinline__ void load_row8(const uint16_t *w, uint32_t row, uint32_t c, uint32_t cols, float (&v)[8]) {
+    const uint64_t block = (static_cast<uint64_t>(row / 64u) * (cols / 32u) + c / 32u) * 4u + row % 64u / 16u;
+    load_vec<bf16_t, 8>(reinterpret_cast<const bf16_t *>(w) + block * 512u + (row % 16u + 2u * (c % 32u)) * 8u, v);
+}
+
+// Tokens of a workgroup of 1024 threads whose pairs lie next to each other, and the
+// threads of each.
+constexpr uint32_t kTokens = 8, kParts = 1024 / kTokens;
+
+// The pairs (top, sum) of a token's threads joined in a fixed order, in its first.
+__device__ __forceinline__ void join_pairs(float (*s_pair)[kTokens][2], uint32_t part, uint32_t t, float &top, float &sum) {
+    s_pair[part][t][0] = top;
+    s_pair[part][t][1] = sum;
+    __syncthreads();
+    for (uint32_t half = kParts / 2u; half; half >>= 1) {
+        if (part < half) {
+            const float r = s_pair[part + half][t][0], s = s_pair[part + half][t][1], to = fmaxf(top, r);
+            sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
+            top = to;
+            s_pair[part][t][0] = top;
+            s_pair[part][t][1] = sum;
+        }
+        __syncthreads();
     }
-    // Eight lanes a panel.
-    for (uint32_t p = lane / 8u; p < a.panels; p += 8u) {
-        const float r = st[p * step];
-        if (r == top || r == -INFINITY) continue;
-        const float f = ref_scale(r, top);
-        bf16_t *e = reinterpret_cast<bf16_t *>(a.exps) + token * a.exps_stride + 64u * p + 8u * (lane % 8u);
-        float v[8];
-        load_vec<bf16_t, 8>(e, v);
+}
+
+// The references that the tokens begin with: the exponent, rounded up, of their
+// target's logit, or where the target is no class of another one's, which is as
+// good a guess; none if it is not finite.  The targets' rows are kept for the
+// gradient's end: in tile order a row's vectors lie in a line of memory each, and
+// reading it again would take eight times what it has.  A workgroup a token.
+__global__ __launch_bounds__(256) void df11_loss_first_kernel(TokenArgs a, const uint16_t *x, uint64_t x_stride,
+                                                             const uint16_t *w, uint32_t cols, uint16_t *kept) {
+    __shared__ float s_sum[4];
+    const uint32_t token = blockIdx.x;
+    const int64_t target = a.targets[token];
+    const uint32_t row = target >= 0 && target < static_cast<int64_t>(a.classes) ? static_cast<uint32_t>(target) : 0u;
+    float z = 0.0f;
+#pragma unroll 2
+    for (uint32_t c = 8u * threadIdx.x; c < cols; c += 8u * 256u) {
+        float u[8], v[8];
+        load_vec<bf16_t, 8>(reinterpret_cast<const bf16_t *>(x) + token * x_stride + c, u);
+        load_row8(w, row, c, cols, v);
+        store_vec<bf16_t, 8>(reinterpret_cast<bf16_t *>(kept) + static_cast<uint64_t>(token) * cols + c, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= f;
-        store_vec<bf16_t, 8>(e, v);
+        for (int i = 0; i < 8; ++i) z += u[i] * v[i];
+    }
+#pragma unroll
+    for (int m = 32; m; m >>= 1) z += __shfl_xor(z, m);
+    if (threadIdx.x % kWaveSize == 0) s_sum[threadIdx.x / kWaveSize] = z;
+    __syncthreads();
+    if (threadIdx.x) return;
+    const float ref = ceilf((s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * kLog2eHi);
+    a.ref[token] = fabsf(ref) < INFINITY ? ref : -INFINITY;
+    a.sum[token] = 0.0f;
+}
+
+// A piece's pairs joined to what the tokens have.  Where the reference moves, or a
+// panel has another, exponentials are brought to it.
+__global__ __launch_bounds__(1024) void df11_loss_piece_kernel(TokenArgs a, uint32_t first_piece) {
+    __shared__ float s_pair[kParts][kTokens][2];
+    __shared__ float s_to[kTokens];
+    __shared__ uint32_t s_other[kTokens];
+    const uint32_t t = threadIdx.x % kTokens, part = threadIdx.x / kTokens, token = blockIdx.x * kTokens + t;
+    const bool in = token < a.n_tokens;
+    const float *st = a.stats + 2u * (in ? token : 0u);
+    const uint64_t step = 2ull * a.n_tokens;
+    const float was = in ? a.ref[token] : -INFINITY;
+    if (threadIdx.x < kTokens) s_other[threadIdx.x] = 0;
+    float top = was, sum = 0.0f;
+    bool other = false;  // a reference that is not the token's
+    for (uint32_t p = part; p < a.panels; p += kParts) {
+        const float r = st[p * step], s = st[p * step + 1u], to = fmaxf(top, r);
+        sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
+        top = to;
+        other = other || (r != was && r != -INFINITY);
+    }
+    join_pairs(s_pair, part, t, top, sum);
+    if (part == 0 && in) {
+        // (the pairs of no class leave a token's first reference as it is)
+        const float scale = first_piece ? 0.0f : ref_scale(was, top);
+        a.ref[token] = top;
+        a.sum[token] = a.sum[token] * scale + sum;
+        a.scale[token] = scale;
+        s_to[t] = top;
+    }
+    if (other && in) s_other[t] = 1;
+    __syncthreads();
+    // Eight lanes a panel, all of the workgroup one token after the other.
+    for (uint32_t i = 0; i < kTokens; ++i) {
+        if (!s_other[i]) continue;
+        const uint32_t mine = blockIdx.x * kTokens + i;
+        const float to = s_to[i];
+        for (uint32_t p = threadIdx.x / 8u; p < a.panels; p += 1024u / 8u) {
+            const float r = a.stats[2u * mine + p * step];
+            if (r == to || r == -INFINITY) continue;
+            const float f = ref_scale(r, to);
+            bf16_t *e = reinterpret_cast<bf16_t *>(a.exps) + mine * a.exps_stride + 64u * p + 8u * (threadIdx.x % 8u);
+            float v[8];
+            load_vec<bf16_t, 8>(e, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= f;
+            store_vec<bf16_t, 8>(e, v);
+        }
     }
 }
 
@@ -168,33 +238,20 @@ __device__ __forceinline__ float others(float ref, float sum, float target_logit
 
 __device__ __forceinline__ float loss_of(float u) { return u > 0.0f ? u + log1pf(expf(-u)) : log1pf(expf(u)); }
 
-// Sixteen tokens a workgroup, whose pairs lie next to each other, by 64 threads
-// each.
+// The losses from the pairs of all panels.
 __global__ __launch_bounds__(1024) void df11_loss_tokens_kernel(TokenArgs a) {
-    __shared__ float s_pair[64][16][2];
-    const uint32_t t = threadIdx.x % 16u, part = threadIdx.x / 16u, token = blockIdx.x * 16u + t;
+    __shared__ float s_pair[kParts][kTokens][2];
+    const uint32_t t = threadIdx.x % kTokens, part = threadIdx.x / kTokens, token = blockIdx.x * kTokens + t;
     const bool in = token < a.n_tokens;
     const float *st = a.stats + 2u * (in ? token : 0u);
     const uint64_t step = 2ull * a.n_tokens;
     float top = -INFINITY, sum = 0.0f;
-    for (uint32_t p = part; p < a.panels; p += 64u) {
+    for (uint32_t p = part; p < a.panels; p += kParts) {
         const float r = st[p * step], s = st[p * step + 1u], to = fmaxf(top, r);
         sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
         top = to;
     }
-    s_pair[part][t][0] = top;
-    s_pair[part][t][1] = sum;
-    __syncthreads();
-    for (uint32_t half = 32u; half; half >>= 1) {
-        if (part < half) {
-            const float r = s_pair[part + half][t][0], s = s_pair[part + half][t][1], to = fmaxf(top, r);
-            sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
-            top = to;
-            s_pair[part][t][0] = top;
-            s_pair[part][t][1] = sum;
-        }
-        __syncthreads();
-    }
+    join_pairs(s_pair, part, t, top, sum);
     if (part || !in) return;
     const TokenKind kind = kind_of(a.targets[token], a.ignore_index, a.classes);
     a.loss[token] = kind == kIgnored   ? 0.0f
@@ -204,7 +261,7 @@ __global__ __launch_bounds__(1024) void df11_loss_tokens_kernel(TokenArgs a) {
 
 struct GradRowsArgs {
     TokenArgs t;
-    const uint16_t *w;  // decoded, in tile order
+    const uint16_t *kept;  // the targets' rows, [token][cols]
     float *grad;        // A on entry
     uint32_t cols;
 };
@@ -223,15 +280,13 @@ __global__ __launch_bounds__(256) void df11_loss_rows_kernel(GradRowsArgs a) {
     if (blockIdx.y == 0 && threadIdx.x == 0)
         a.t.loss[token] = kind == kIgnored ? 0.0f : kind == kNoClass ? __builtin_nanf("") : loss_of(u);
     const float sigma = 1.0f / (1.0f + expf(-u));
-    const uint32_t row = kind == kScored ? static_cast<uint32_t>(target) : 0u, tile_ks = a.cols / 32u;
     for (uint32_t c = 8u * (blockIdx.y * 256u + threadIdx.x); c < a.cols; c += 8u * 256u * gridDim.y) {
         float *g = a.grad + static_cast<uint64_t>(token) * a.cols + c;
         float v[8], wy[8];
+        load_vec<float, 4>(g, *reinterpret_cast<float(*)[4]>(&v[0]));
+        load_vec<float, 4>(g + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
         if (kind == kScored) {
-            load_vec<float, 4>(g, *reinterpret_cast<float(*)[4]>(&v[0]));
-            load_vec<float, 4>(g + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
-            const uint64_t block = (static_cast<uint64_t>(row / 64u) * tile_ks + c / 32u) * 4u + row % 64u / 16u;
-            load_vec<bf16_t, 8>(reinterpret_cast<const bf16_t *>(a.w) + block * 512u + (row % 16u + 2u * (c % 32u)) * 8u, wy);
+            load_vec<bf16_t, 8>(reinterpret_cast<const bf16_t *>(a.kept) + static_cast<uint64_t>(token) * a.cols + c, wy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = sigma * (v[i] * inverse - wy[i]);
         } else {
@@ -308,14 +363,12 @@ __global__ __launch_bounds__(256) void df11_loss_grad_kernel(LossGradArgs a) {
 // Where a call's parts of the workspace begin.
 struct LossPlan {
     bool slots;         // the fused product
-    uint32_t piece;     // classes of a later piece
-    uint64_t weights, stats, logit, ref, sum, scale, exps, split, end;
+    uint32_t piece;     // classes of a piece (the last one may have fewer)
+    uint64_t weights, stats, logit, ref, sum, scale, kept, exps, split, end;
 };
 
 // Classes of the piece that begins at class `from`.
-uint32_t piece_at(uint32_t rows, uint32_t piece, uint32_t from) {
-    return std::min(from ? piece : kFirstPiece, rows - from);
-}
+uint32_t piece_at(uint32_t rows, uint32_t piece, uint32_t from) { return std::min(piece, rows - from); }
 
 bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan &p) {
     const uint32_t cols = w->tile_cols, rows = static_cast<uint32_t>(w->h.n_elements / cols);
@@ -337,12 +390,10 @@ bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan
     p.logit = take(4ull * tokens);
     uint32_t most = rows;  // classes whose pairs are held at once
     if (grad) {
-        // Later pieces of about the same size, at least the first one's (a smaller
-        // product does not fill the chip).
-        const uint32_t rest = rows - piece_at(rows, 0, 0);
-        const uint64_t most_classes = std::max<uint64_t>(kFirstPiece, kPieceExps / tokens);
-        const uint64_t pieces = std::max<uint64_t>(1, (rest + most_classes - 1) / most_classes);
-        p.piece = static_cast<uint32_t>(round_up((rest + pieces - 1) / pieces, 256));
+        // Pieces of about the same size.
+        const uint64_t most_classes = std::max<uint64_t>(kLeastPiece, kPieceExps / tokens);
+        const uint64_t pieces = (rows + most_classes - 1) / most_classes;
+        p.piece = static_cast<uint32_t>(round_up((rows + pieces - 1) / pieces, 256));
         most = 0;
         uint64_t split = 0;
         for (uint32_t from = 0, n; from < rows; from += n) {
@@ -355,6 +406,7 @@ bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan
         p.ref = take(4ull * tokens);
         p.sum = take(4ull * tokens);
         p.scale = take(4ull * tokens);
+        p.kept = take(2ull * tokens * cols);
         p.exps = take(2ull * tokens * most);
         p.split = take(split);
     }
@@ -404,8 +456,8 @@ int loss_only(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride,
     if (rc) return rc;
     t.panels = rows / 64;
     void *params[] = {&t};
-    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_tokens_kernel), dim3((tokens + 15) / 16), dim3(1024),
-                         params, 0, stream, nullptr, nullptr);
+    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_tokens_kernel), dim3((tokens + kTokens - 1) / kTokens),
+                         dim3(1024), params, 0, stream, nullptr, nullptr);
 }
 
 // Blocks of a token's columns, eight a thread.
@@ -420,6 +472,13 @@ int loss_and_grad(const df11_device_stream *w, const uint16_t *x, uint64_t x_str
     t.sum = at<float>(ws, p.sum);
     t.scale = at<float>(ws, p.scale);
     t.exps = at<uint16_t>(ws, p.exps);
+    if (!rc) {
+        const uint16_t *head = decoded[0];
+        uint16_t *kept = at<uint16_t>(ws, p.kept);
+        void *params[] = {&t, &x, &x_stride, &head, &cols, &kept};
+        rc = launch_kernel(reinterpret_cast<const void *>(&df11_loss_first_kernel), dim3(tokens), dim3(256), params, 0,
+                           stream, nullptr, nullptr);
+    }
     for (uint32_t from = 0, n; !rc && from < rows; from += n) {
         n = piece_at(rows, p.piece, from);
         df11::DenseCall d{};
@@ -433,7 +492,7 @@ int loss_and_grad(const df11_device_stream *w, const uint16_t *x, uint64_t x_str
         d.loss.targets = t.targets;
         d.loss.stats = at<float>(ws, p.stats);
         d.loss.target_logit = at<float>(ws, p.logit);
-        d.loss.ref = from ? t.ref : nullptr;
+        d.loss.ref = t.ref;
         d.loss.exps = t.exps;
         d.loss.exps_stride = n;
         d.loss.first_class = from;
@@ -444,7 +503,7 @@ int loss_and_grad(const df11_device_stream *w, const uint16_t *x, uint64_t x_str
         t.exps_stride = n;
         uint32_t first = from == 0;
         void *params[] = {&t, &first};
-        rc = launch_kernel(reinterpret_cast<const void *>(&df11_loss_piece_kernel), dim3((tokens + 3) / 4), dim3(256),
+        rc = launch_kernel(reinterpret_cast<const void *>(&df11_loss_piece_kernel), dim3((tokens + kTokens - 1) / kTokens), dim3(1024),
                            params, 0, stream, nullptr, nullptr);
         if (rc) break;
         d.mode = df11::kDenseBackAdd;
@@ -458,7 +517,7 @@ int loss_and_grad(const df11_device_stream *w, const uint16_t *x, uint64_t x_str
         rc = df11::dense_product(d, e, at<float>(ws, p.split), stream);
     }
     if (rc) return rc;
-    GradRowsArgs a{t, decoded[0], grad, cols};
+    GradRowsArgs a{t, at<uint16_t>(ws, p.kept), grad, cols};
     void *params[] = {&a};
     return launch_kernel(reinterpret_cast<const void *>(&df11_loss_rows_kernel), dim3(tokens, column_blocks(cols)), dim3(256),
                          params, 0, stream, nullptr, nullptr);

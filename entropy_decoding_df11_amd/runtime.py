@@ -12,9 +12,12 @@ two scratch buffers while the caller computes with block i.
 
 from __future__ import annotations
 
+import dataclasses
 from typing import Dict, Iterator, List, Optional, Sequence, Tuple, Union
 
+from .attention import append_kv, tree_attention
 from .df11 import DF11Block, DF11BlockBatch
+from .loss import linear_cross_entropy
 from .operators import gated_matmul, matmul_epilogue, rms_norm
 
 Block = Union[DF11Block, DF11BlockBatch]
@@ -135,7 +138,38 @@ FUSED_MAX_TOKENS_TILES = 64
 FUSED_MAX_TOKENS_ROWS = 8
 
 
-def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5):
+@dataclasses.dataclass
+class Step:
+    """What a step of generation brings beside its tokens, the same for every
+    block (attention.py): where the batch's sequences stand in a paged cache
+    (page_table, starts, lengths), the rotation of their positions, and the mask
+    of drafted trees.  The tensors may be changed in place between the replays
+    of a captured step."""
+
+    page_table: "torch.Tensor"  # noqa: F821
+    starts: "torch.Tensor"  # noqa: F821
+    lengths: "torch.Tensor"  # noqa: F821
+    rotary: Optional["torch.Tensor"] = None  # noqa: F821
+    positions: Optional["torch.Tensor"] = None  # noqa: F821
+    mask: Optional["torch.Tensor"] = None  # noqa: F821
+    interleaved: bool = False
+
+
+def cached_attention(q, k, v, cache: Tuple, step: Step):
+    """The attention of a block: k and v (tokens, kv_heads * head_dim) appended
+    to cache, a pair of (pages, page, kv_heads, head_dim) tensors, and q (tokens,
+    heads * head_dim) attending over it; float32 (a product's sums) or the
+    cache's type.  Returns (tokens, heads * head_dim) of the cache's type."""
+    k_cache, v_cache = cache
+    dim = k_cache.shape[-1]
+    where = (k_cache, v_cache, step.page_table, step.starts, step.lengths)
+    q = append_kv(k.unflatten(-1, (-1, dim)), v.unflatten(-1, (-1, dim)), *where, q=q.unflatten(-1, (-1, dim)),
+                  rotary=step.rotary, positions=step.positions, interleaved=step.interleaved)
+    return tree_attention(q, *where, mask=step.mask, out=q).flatten(1)
+
+
+def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5, cache: Optional[Tuple] = None,
+                           step: Optional[Step] = None):
     """block_forward through the operators around the products, for x of any
     leading dimensions: rms_norm, q, k and v (one matmul_batch up to
     FUSED_MAX_TOKENS_TILES tokens, else and under autograd matmul_epilogue),
@@ -146,10 +180,18 @@ def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5):
     output once.  matmul_batch adds with float atomics and uses the weights'
     work counters: with it the last bits may differ from call to call, and
     calls on one block must not overlap; the other operators repeat theirs and
-    may.  Differentiable with respect to x (the weights are frozen)."""
+    may.  Differentiable with respect to x (the weights are frozen).
+
+    With cache, the block's pair of paged keys and values, and step, x is
+    (tokens, features) and the block attends over the cache (cached_attention;
+    no gradients); without them it has no attention mixing, as block_forward."""
     import torch
     from .df11 import matmul_batch
 
+    if (cache is None) != (step is None):
+        raise ValueError("cache and step go together")
+    if cache is not None and x.dim() != 2:
+        raise ValueError("x must be (tokens, features) for a block that attends")
     w = {nm: t for (nm, _, _), t in zip(blk.views, blk.tensors)}
     qkv = [w[nm] for nm in ("q_proj", "k_proj", "v_proj")]
     h = rms_norm(x, eps=eps)
@@ -157,19 +199,36 @@ def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5):
     if not 0 < tokens <= FUSED_MAX_TOKENS_TILES or (torch.is_grad_enabled() and x.requires_grad):
         q, k, v = (matmul_epilogue(t, h) for t in qkv)
     else:
-        q, k, v = (y.to(x.dtype).view(*x.shape[:-1], -1)
-                   for y in matmul_batch(qkv, [h.view(tokens, x.shape[-1])] * 3))
-    a = q + (k * v).repeat_interleave(q.shape[-1] // k.shape[-1], dim=-1)
+        q, k, v = matmul_batch(qkv, [h.view(tokens, x.shape[-1])] * 3)
+        if cache is None:
+            q, k, v = (y.to(x.dtype).view(*x.shape[:-1], -1) for y in (q, k, v))
+    if cache is None:
+        a = q + (k * v).repeat_interleave(q.shape[-1] // k.shape[-1], dim=-1)
+    else:
+        a = cached_attention(q, k, v, cache, step)
     x = matmul_epilogue(w["o_proj"], a, residual=x)
     h = gated_matmul(w["gate_proj"], w["up_proj"], rms_norm(x, eps=eps))
     return matmul_epilogue(w["down_proj"], h, residual=x)
 
 
-def operator_model_forward(x, blocks: Sequence[DF11BlockBatch]):
-    """operator_block_forward over every block in order."""
-    for blk in blocks:
-        x = operator_block_forward(x, blk)
+def operator_model_forward(x, blocks: Sequence[DF11BlockBatch], caches: Optional[Sequence[Tuple]] = None,
+                           step: Optional[Step] = None):
+    """operator_block_forward over every block in order, with caches (one pair
+    for each block) and step attending over them."""
+    for i, blk in enumerate(blocks):
+        x = operator_block_forward(x, blk, cache=None if caches is None else caches[i], step=step)
     return x
+
+
+def score_tokens(x, blocks: Sequence[DF11BlockBatch], head, targets, caches: Optional[Sequence[Tuple]] = None,
+                 step: Optional[Step] = None, norm=None, eps: float = 1e-5, vocab: Optional[int] = None):
+    """The logarithm of the probability that the model gives each token's target,
+    float32 (tokens,): operator_model_forward, the last norm (weight norm) and the
+    compressed output head, whose logits are not kept (linear_cross_entropy).  What
+    drafted tokens are accepted by, and a text's perplexity.  Targets of -100 give
+    zero."""
+    h = rms_norm(operator_model_forward(x, blocks, caches, step), weight=norm, eps=eps)
+    return -linear_cross_entropy(head, h, targets, vocab=vocab, reduction="none")
 
 
 def fused_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5, scratch=None):

@@ -124,8 +124,9 @@ def test_loss_and_gradient(tokens, rows, cols, vocab, reduction):
 
 
 def test_many_pieces():
-    """More exponentials than a piece holds, several times."""
+    """More exponentials than a piece holds, also where the second piece moves the references."""
     Head(4100, 33024, 32, 33000, seed=2).check()
+    Head(4100, 33024, 32, 33000, seed=2, size=8.0, lean=0.0, scale=lambda v: torch.where(v < 16384, 0.05, 1 + v / 4000)).check()
 
 
 @pytest.mark.parametrize("tokens", [9, 50])
