@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 # DF11_LIB_PATH names another build of the same library (the sanitizer build
 # of the CPU tests); by default the in-tree libdf11.so.
@@ -189,78 +190,21 @@ class Loss(ctypes.Structure):
     ]
 
 
-class KvCache(ctypes.Structure):
-    _fields_ = [
-        ("k", ctypes.c_void_p),
-        ("v", ctypes.c_void_p),
-        ("k_page_stride", ctypes.c_uint64),
-        ("k_place_stride", ctypes.c_uint64),
-        ("k_head_stride", ctypes.c_uint64),
-        ("v_page_stride", ctypes.c_uint64),
-        ("v_place_stride", ctypes.c_uint64),
-        ("v_head_stride", ctypes.c_uint64),
-        ("n_pages", ctypes.c_uint32),
-        ("page_size", ctypes.c_uint32),
-        ("heads", ctypes.c_uint32),
-        ("head_dim", ctypes.c_uint32),
-        ("dtype", ctypes.c_uint32),
-        ("reserved", ctypes.c_uint32),
-    ]
-
-
-class KvBatch(ctypes.Structure):
-    _fields_ = [
-        ("starts", ctypes.c_void_p),
-        ("lengths", ctypes.c_void_p),
-        ("page_table", ctypes.c_void_p),
-        ("table_stride", ctypes.c_uint64),
-        ("n_seqs", ctypes.c_uint32),
-        ("table_pages", ctypes.c_uint32),
-        ("n_tokens", ctypes.c_uint32),
-        ("reserved", ctypes.c_uint32),
-    ]
-
-
-class Append(ctypes.Structure):
-    _fields_ = [
-        ("k", ctypes.c_void_p),
-        ("v", ctypes.c_void_p),
-        ("q", ctypes.c_void_p),
-        ("q_out", ctypes.c_void_p),
-        ("rotary", ctypes.c_void_p),
-        ("positions", ctypes.c_void_p),
-        ("k_stride", ctypes.c_uint64),
-        ("k_head_stride", ctypes.c_uint64),
-        ("v_stride", ctypes.c_uint64),
-        ("v_head_stride", ctypes.c_uint64),
-        ("q_stride", ctypes.c_uint64),
-        ("q_head_stride", ctypes.c_uint64),
-        ("q_out_stride", ctypes.c_uint64),
-        ("q_out_head_stride", ctypes.c_uint64),
-        ("rotary_rows", ctypes.c_uint64),
-        ("rotary_dims", ctypes.c_uint32),
-        ("interleaved", ctypes.c_uint32),
-        ("q_heads", ctypes.c_uint32),
-        ("dtype", ctypes.c_uint32),
-    ]
-
-
-class Attention(ctypes.Structure):
-    _fields_ = [
-        ("q", ctypes.c_void_p),
-        ("out", ctypes.c_void_p),
-        ("lse", ctypes.c_void_p),
-        ("mask", ctypes.c_void_p),
-        ("q_stride", ctypes.c_uint64),
-        ("q_head_stride", ctypes.c_uint64),
-        ("out_stride", ctypes.c_uint64),
-        ("out_head_stride", ctypes.c_uint64),
-        ("mask_stride", ctypes.c_uint64),
-        ("mask_cols", ctypes.c_uint32),
-        ("q_heads", ctypes.c_uint32),
-        ("scale", ctypes.c_float),
-        ("reserved", ctypes.c_uint32),
-    ]
+# The host structures of the paged cache's calls, which a step of generation makes
+# in every block: packing a format takes a fifth of what filling a ctypes structure
+# does.  Fields in the header's order, pointers and strides as 64 bits.
+KV_CACHE = struct.Struct("=8Q6I")
+KV_CACHE_FIELDS = ("k", "v", "k_page_stride", "k_place_stride", "k_head_stride", "v_page_stride", "v_place_stride",
+                   "v_head_stride", "n_pages", "page_size", "heads", "head_dim", "dtype", "reserved")
+KV_BATCH = struct.Struct("=4Q4I")
+KV_BATCH_FIELDS = ("starts", "lengths", "page_table", "table_stride", "n_seqs", "table_pages", "n_tokens", "reserved")
+APPEND = struct.Struct("=15Q4I")
+APPEND_FIELDS = ("k", "v", "q", "q_out", "rotary", "positions", "k_stride", "k_head_stride", "v_stride",
+                 "v_head_stride", "q_stride", "q_head_stride", "q_out_stride", "q_out_head_stride", "rotary_rows",
+                 "rotary_dims", "interleaved", "q_heads", "dtype")
+ATTENTION = struct.Struct("=9Q2IfI")
+ATTENTION_FIELDS = ("q", "out", "lse", "mask", "q_stride", "q_head_stride", "out_stride", "out_head_stride",
+                    "mask_stride", "mask_cols", "q_heads", "scale", "reserved")
 
 
 class RansHeader(ctypes.Structure):
@@ -374,11 +318,10 @@ def load() -> ctypes.CDLL:
         "df11_cross_entropy": (ctypes.c_int, [ctypes.POINTER(DeviceStream), vp, u64, u32, u32, u32,
                                               ctypes.POINTER(Loss), vp, u64, vp]),
         "df11_cross_entropy_grad": (ctypes.c_int, [vp, vp, u64, vp, u32, u32, vp, u64, u32, vp]),
-        "df11_append_kv": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), ctypes.POINTER(Append), vp]),
-        "df11_tree_attention_workspace": (u64, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch),
-                                                ctypes.POINTER(Attention)]),
-        "df11_tree_attention": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch),
-                                               ctypes.POINTER(Attention), vp, u64, vp]),
+        # (structures as bytes, packed by their formats)
+        "df11_append_kv": (ctypes.c_int, [vp, vp, vp, vp]),
+        "df11_tree_attention_workspace": (u64, [vp, vp, vp]),
+        "df11_tree_attention": (ctypes.c_int, [vp, vp, vp, vp, u64, vp]),
         "df11_rans_quantize": (ctypes.c_int, [u64p, u32p]),
         "df11_rans_encode": (ctypes.c_int, [u32p, u16p, ctypes.c_uint64, u32p, u32p, u16p, ctypes.c_uint64, u8p,
                                             ctypes.POINTER(RansHeader)]),

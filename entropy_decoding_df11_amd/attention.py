@@ -27,11 +27,10 @@ given.  Serving's operators: they carry no gradients.
 
 from __future__ import annotations
 
-import math
 from typing import Optional, Tuple, Union
 
 from . import _lib, operators
-from .operators import _check_outputs, _dtype, _run, _same_device, _stream
+from .operators import _check_outputs, _dtype, _ptr, _run, _same_device, _stream
 
 
 def rotary_table(positions: int, dims: int, base: float = 10000.0, device="cuda") -> "torch.Tensor":  # noqa: F821
@@ -48,73 +47,70 @@ def rotary_table(positions: int, dims: int, base: float = 10000.0, device="cuda"
 
 def _check_heads(t, what, dim, heads=None):
     """Checks a (tokens, heads, head_dim) tensor."""
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{what} must be (tokens, heads, head_dim), with the cache's heads and head_dim")
-    if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():
+    if t.stride(2) != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"{what} must be contiguous along its last dimension")
-
-
-def _strides(t, n):
-    """The first n strides, 0 along dimensions of one element (theirs say nothing)."""
-    shape, strides = t.shape, t.stride()
-    return [strides[i] if shape[i] > 1 else 0 for i in range(n)]
 
 
 def _check_cache(k_cache, v_cache, page_table, starts, lengths):
     torch = operators.torch
     dev = k_cache.device
     code = _dtype(k_cache, "k_cache")
-    if code == _lib.FP32 or v_cache.dtype != k_cache.dtype or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if code == _lib.FP32 or v_cache.dtype != k_cache.dtype or len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be (pages, page, kv_heads, head_dim), bfloat16 or float16, alike")
-    pages, page, heads, dim = k_cache.shape
+    pages, page, heads, dim = shape
     if dim % 8 or not 8 <= dim <= _lib.MAX_HEAD_DIM or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
         raise ValueError("head_dim must be a multiple of 8, 8 to 256, and contiguous")
     if not pages or not page or not heads:
         raise ValueError("the cache must have a page, a place and a head")
-    for name, t in (("page_table", page_table), ("starts", starts), ("lengths", lengths)):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
-        _same_device(dev, name, t)
-    _same_device(dev, "v_cache", v_cache)
+    int32 = torch.int32
+    if page_table.dtype != int32 or starts.dtype != int32 or lengths.dtype != int32:
+        raise ValueError("page_table, starts and lengths must be int32")
     if lengths.dim() != 1 or starts.dim() != 1 or page_table.dim() != 2 or not lengths.is_contiguous() or \
-            not starts.is_contiguous() or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            not starts.is_contiguous() or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
         raise ValueError("starts and lengths must be contiguous vectors, page_table a matrix of contiguous rows")
     seqs = lengths.shape[0]
     if starts.shape[0] != seqs + 1 or page_table.shape[0] != seqs:
         raise ValueError("starts must have one element more than lengths, page_table one row for each")
-    return dev, code
+    if not dev == v_cache.device == page_table.device == starts.device == lengths.device:
+        raise ValueError(f"v_cache, page_table, starts and lengths must be on {dev}")
+    return dev, code, shape
 
 
 def _structs(k_cache, v_cache, page_table, starts, lengths, code, tokens):
     pages, page, heads, dim = k_cache.shape
-    cache = _lib.KvCache(k_cache.data_ptr(), v_cache.data_ptr(), *_strides(k_cache, 3), *_strides(v_cache, 3), pages,
-                         page, heads, dim, code)
-    batch = _lib.KvBatch(starts.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), page_table.stride(0),
-                         page_table.shape[0], page_table.shape[1], tokens)
-    return cache, batch
+    k0, k1, k2, _ = k_cache.stride()
+    v0, v1, v2, _ = v_cache.stride()
+    seqs, width = page_table.shape
+    return (_lib.KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, pages, page, heads, dim,
+                               code, 0),
+            _lib.KV_BATCH.pack(starts.data_ptr(), lengths.data_ptr(), page_table.data_ptr(), page_table.stride(0), seqs,
+                               width, tokens, 0))
 
 
-def _no_gradients(*tensors):
-    if operators.torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("the cache's operators carry no gradients: call them under torch.no_grad()")
+_GRADIENTS = "the cache's operators carry no gradients: call them under torch.no_grad()"
 
 
 def _launch_append(dev, k, v, q, k_cache, v_cache, page_table, starts, lengths, rotary, positions, interleaved, q_out,
                    code):
     cache, batch = _structs(k_cache, v_cache, page_table, starts, lengths, code, k.shape[0])
-    ks, vs = _strides(k, 2), _strides(v, 2)
-    a = _lib.Append(k=k.data_ptr(), v=v.data_ptr(), k_stride=ks[0], k_head_stride=ks[1], v_stride=vs[0],
-                    v_head_stride=vs[1], dtype=operators._DTYPES[k.dtype])
+    k0, k1, _ = k.stride()
+    v0, v1, _ = v.stride()
+    q_ptr = out_ptr = q0 = q1 = o0 = o1 = heads = rotary_ptr = rows = dims = 0
     if q is not None:
         if q_out is None:
             q_out = operators.torch.empty(q.shape, dtype=k_cache.dtype, device=dev)
-        a.q, (a.q_stride, a.q_head_stride), a.q_heads = q.data_ptr(), _strides(q, 2), q.shape[1]
-        a.q_out, (a.q_out_stride, a.q_out_head_stride) = q_out.data_ptr(), _strides(q_out, 2)
+        q_ptr, out_ptr, heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+        q0, q1, _ = q.stride()
+        o0, o1, _ = q_out.stride()
     if rotary is not None:
-        a.rotary, a.rotary_rows, a.rotary_dims, a.interleaved = rotary.data_ptr(), rotary.shape[0], rotary.shape[1], \
-            interleaved
-    if positions is not None:
-        a.positions = positions.data_ptr()
+        rotary_ptr, (rows, dims) = rotary.data_ptr(), rotary.shape
+    a = _lib.APPEND.pack(k.data_ptr(), v.data_ptr(), q_ptr, out_ptr, rotary_ptr,
+                         0 if positions is None else positions.data_ptr(), k0, k1, v0, v1, q0, q1, o0, o1, rows, dims,
+                         1 if interleaved else 0, heads, operators._DTYPES[k.dtype])
     status = _lib.load().df11_append_kv(cache, batch, a, _stream(dev))
     if status:
         _lib.check(status, "df11_append_kv")
@@ -141,60 +137,66 @@ def append_kv(k: "torch.Tensor", v: "torch.Tensor", k_cache: "torch.Tensor", v_c
     if operators.torch is None:
         operators._import_torch()
     torch = operators.torch
-    dev, code = _check_cache(k_cache, v_cache, page_table, starts, lengths)
-    dim, heads = k_cache.shape[3], k_cache.shape[2]
+    dev, code, (_, _, heads, dim) = _check_cache(k_cache, v_cache, page_table, starts, lengths)
+    dtype = k.dtype
     _dtype(k, "k")
     _check_heads(k, "k", dim, heads)
     _check_heads(v, "v", dim, heads)
-    if v.shape != k.shape or v.dtype != k.dtype:
+    tokens = k.shape[0]
+    if v.shape[0] != tokens or v.dtype != dtype:
         raise ValueError("v must have k's shape and dtype")
-    for name, t in (("k", k), ("v", v), ("q", q), ("rotary", rotary), ("positions", positions), ("q_out", q_out)):
-        _same_device(dev, name, t)
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out needs q")
-    else:
+    if not dev == k.device == v.device:
+        raise ValueError(f"k and v must be on {dev}, the cache's device")
+    needs = k.requires_grad or v.requires_grad or k_cache.requires_grad or v_cache.requires_grad
+    if q is not None:
         _check_heads(q, "q", dim)
-        if q.shape[0] != k.shape[0] or q.dtype != k.dtype or not q.shape[1]:
+        if q.shape[0] != tokens or q.dtype != dtype or not q.shape[1]:
             raise ValueError("q must have k's tokens and dtype, and a head")
-        if q_out is not None:
-            _check_heads(q_out, "q_out", dim, q.shape[1])
-            if q_out.shape != q.shape or q_out.dtype != k_cache.dtype:
-                raise ValueError("q_out must have q's shape and the cache's dtype")
+        _same_device(dev, "q", q)
+        needs = needs or q.requires_grad
+    if q_out is not None:
+        if q is None:
+            raise ValueError("q_out needs q")
+        _check_heads(q_out, "q_out", dim, q.shape[1])
+        if q_out.shape[0] != tokens or q_out.dtype != k_cache.dtype:
+            raise ValueError("q_out must have q's shape and the cache's dtype")
+        _same_device(dev, "q_out", q_out)
+        needs = needs or q_out.requires_grad
     if rotary is not None:
         if rotary.dtype != torch.float32 or rotary.dim() != 2 or not rotary.is_contiguous() or not rotary.shape[0] or \
                 rotary.shape[1] < 2 or rotary.shape[1] % 2 or rotary.shape[1] > dim:
             raise ValueError("rotary must be float32 (positions, dims), contiguous, dims even and at most head_dim")
+        _same_device(dev, "rotary", rotary)
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.dim() != 1 or positions.shape[0] != k.shape[0] or \
+        if positions.dtype != torch.int32 or positions.dim() != 1 or positions.shape[0] != tokens or \
                 not positions.is_contiguous():
             raise ValueError("positions must be int32, one for each token, contiguous")
-    _no_gradients(k, v, q, k_cache, v_cache, q_out)
-    given = [t for t in (k_cache, v_cache, q_out) if t is not None]
+        _same_device(dev, "positions", positions)
+    if needs and torch.is_grad_enabled():
+        raise ValueError(_GRADIENTS)
     out, = _run(dev, stream, _launch_append, k, v, q, k_cache, v_cache, page_table, starts, lengths, rotary, positions,
                 interleaved, q_out, code)
-    torch.autograd.graph.increment_version(given)
+    torch.autograd.graph.increment_version((k_cache, v_cache) if q_out is None else (k_cache, v_cache, q_out))
     return out
 
 
-def _launch_attention(dev, q, k_cache, v_cache, page_table, starts, lengths, mask, scale, out, lse, code):
+def _launch_attention(dev, q, k_cache, v_cache, page_table, starts, lengths, mask, scale, out, return_lse, code):
     torch = operators.torch
     cache, batch = _structs(k_cache, v_cache, page_table, starts, lengths, code, q.shape[0])
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    qs, os = _strides(q, 2), _strides(out, 2)
-    a = _lib.Attention(q=q.data_ptr(), out=out.data_ptr(), q_stride=qs[0], q_head_stride=qs[1], out_stride=os[0],
-                       out_head_stride=os[1], q_heads=q.shape[1], scale=scale)
-    if lse is not None:
-        a.lse = lse.data_ptr()
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
+    q0, q1, _ = q.stride()
+    o0, o1, _ = out.stride()
+    m_ptr = m0 = cols = 0
     if mask is not None:
-        a.mask, a.mask_stride, a.mask_cols = mask.data_ptr(), mask.stride(0), mask.shape[1]
+        m_ptr, m0, cols = mask.data_ptr(), mask.stride(0), mask.shape[1]
+    a = _lib.ATTENTION.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), m_ptr, q0, q1, o0, o1, m0,
+                            cols, q.shape[1], scale, 0)
     lib = _lib.load()
     nbytes = lib.df11_tree_attention_workspace(cache, batch, a)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    status = lib.df11_tree_attention(cache, batch, a, work.data_ptr(), nbytes, _stream(dev))
+    work = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    status = lib.df11_tree_attention(cache, batch, a, _ptr(work), nbytes, _stream(dev))
     if status:
         _lib.check(status, "df11_tree_attention")
     return out, lse
@@ -221,29 +223,31 @@ def tree_attention(q: "torch.Tensor", k_cache: "torch.Tensor", v_cache: "torch.T
     if operators.torch is None:
         operators._import_torch()
     torch = operators.torch
-    dev, code = _check_cache(k_cache, v_cache, page_table, starts, lengths)
-    dim, heads = k_cache.shape[3], k_cache.shape[2]
+    dev, code, (_, _, heads, dim) = _check_cache(k_cache, v_cache, page_table, starts, lengths)
     _check_heads(q, "q", dim)
     if q.dtype != k_cache.dtype or not q.shape[1] or q.shape[1] % heads:
         raise ValueError("q must have the cache's dtype, and heads a multiple of the cache's")
+    _same_device(dev, "q", q)
     if scale is None:
-        scale = 1.0 / math.sqrt(dim)
-    elif not 0.0 < scale < math.inf:
+        scale = dim ** -0.5
+    elif not 0.0 < scale <= 3.4e38:
         raise ValueError("scale must be positive and finite")
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8) or mask.dim() != 2 or mask.shape[0] != q.shape[0] or \
                 (mask.shape[1] > 1 and mask.stride(1) != 1):
             raise ValueError("mask must be bool or uint8 (tokens, columns), contiguous along a row")
+        _same_device(dev, "mask", mask)
+    given = None
     if out is not None:
         _check_heads(out, "out", dim)
         if out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must have q's shape and dtype")
-    for name, t in (("q", q), ("mask", mask), ("out", out)):
-        _same_device(dev, name, t)
-    _no_gradients(q, k_cache, v_cache)
-    given = None if out is None else _check_outputs(out)
+        _same_device(dev, "out", out)
+        given = _check_outputs(out)
+    if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad) and torch.is_grad_enabled():
+        raise ValueError(_GRADIENTS)
     out, lse = _run(dev, stream, _launch_attention, q, k_cache, v_cache, page_table, starts, lengths, mask, scale, out,
-                    True if return_lse else None, code)
+                    return_lse, code)
     if given:
         torch.autograd.graph.increment_version(given)
     return (out, lse) if return_lse else out

@@ -7,8 +7,7 @@
 // token: eight rotated pairs (16 elements), or eight elements that are copied,
 // all in 16-byte accesses; a workgroup's units belong to one token, so that
 // what finds its place (sequence, page) is the same for all of its lanes.  The
-// loads of that chain (starts, length, page) and of the elements are
-// independent and go out together.
+// elements are asked for before that chain (starts, length, page) is followed.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -54,103 +53,83 @@ __device__ __forceinline__ void load_unit(const T *p, float (&f)[N]) {
     }
 }
 
-// N pairs of one head, the unit's first pair being `pair`; from and to point at
-// the head's first element.
-template <typename IN, typename OUT, int N>
-__device__ __forceinline__ void rotate_unit(const IN *from, OUT *to, const float *row, uint32_t half, uint32_t pair,
-                                            bool interleaved, bool known) {
-    float a[N], b[N], c[N], s[N];
-    if (interleaved) {
-        float both[2 * N];
-        if constexpr (N == 1) {
-            both[0] = static_cast<float>(from[2 * pair]);
-            both[1] = static_cast<float>(from[2 * pair + 1]);
-        } else {
-            load_unit(from + 2 * pair, *reinterpret_cast<float(*)[N]>(&both[0]));
-            load_unit(from + 2 * pair + N, *reinterpret_cast<float(*)[N]>(&both[N]));
-        }
+// N pairs rotated in place: x and y their first and second elements, or both the
+// elements of neighbouring pairs one after the other.
+template <int N>
+__device__ __forceinline__ void turn(float (&x)[N], float (&y)[N], const float (&c)[N], const float (&s)[N],
+                                     bool interleaved) {
+    if (!interleaved || N == 1) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            a[i] = both[2 * i];
-            b[i] = both[2 * i + 1];
+            const float a = x[i], b = y[i];
+            x[i] = a * c[i] - b * s[i];
+            y[i] = b * c[i] + a * s[i];
         }
-    } else {
-        load_unit(from + pair, a);
-        load_unit(from + half + pair, b);
+        return;
     }
-    if (known) {
-        load_unit(row + pair, c);
-        load_unit(row + half + pair, s);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = s[i] = __builtin_nanf("");
-    }
-    float x[N], y[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        x[i] = a[i] * c[i] - b[i] * s[i];
-        y[i] = b[i] * c[i] + a[i] * s[i];
-    }
-    if (!interleaved) {
-        store_vec<OUT, N>(to + pair, x);
-        store_vec<OUT, N>(to + half + pair, y);
-    } else if constexpr (N == 1) {
-        store_vec<OUT, 1>(to + 2 * pair, x);
-        store_vec<OUT, 1>(to + 2 * pair + 1, y);
-    } else {
-        float lo[N], hi[N];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            lo[2 * i] = x[i];
-            lo[2 * i + 1] = y[i];
-            hi[2 * i] = x[N / 2 + i];
-            hi[2 * i + 1] = y[N / 2 + i];
-        }
-        store_vec<OUT, N>(to + 2 * pair, lo);
-        store_vec<OUT, N>(to + 2 * pair + N, hi);
+        float *pair = i < N / 2 ? &x[2 * i] : &y[2 * i - N];
+        const float a = pair[0], b = pair[1];
+        pair[0] = a * c[i] - b * s[i];
+        pair[1] = b * c[i] + a * s[i];
     }
 }
 
 // N: pairs of a rotated unit and elements of a copied one.
 template <typename IN, typename OUT, int N>
 __global__ __launch_bounds__(256) void df11_append_kernel(AppendArgs a) {
-    const uint32_t token = blockIdx.x, unit = blockIdx.y * blockDim.x + threadIdx.x;
-    const int32_t seq = __builtin_amdgcn_readfirstlane(sequence_of(a.b, static_cast<int32_t>(token)));
-    if (seq < 0) return;
-    const int64_t length = a.b.lengths[seq];
-    const int64_t place = length + (static_cast<int64_t>(token) - a.b.starts[seq]);
-    const int64_t position = a.positions ? a.positions[token] : place;
+    const uint32_t token = blockIdx.x, unit = min(blockIdx.y * blockDim.x + threadIdx.x, a.units - 1u);
     const uint32_t q_units = a.q_heads * a.units_head, k_units = a.kv_heads * a.units_head;
-    if (unit >= a.units) return;
-    // What the unit reads and where it goes: q, k or v.
+    const bool mine = blockIdx.y * blockDim.x + threadIdx.x < a.units;
+    // What the unit reads, of q, k or v.
     const uint32_t kind = unit < q_units ? 0u : unit < q_units + k_units ? 1u : 2u;
     const uint32_t u = unit - (kind == 0u ? 0u : kind == 1u ? q_units : q_units + k_units);
     const uint32_t each = kind == 2u ? a.units_copy : a.units_head, head = u / each, part = u % each;
     const Rows &r = kind == 0u ? a.q : kind == 1u ? a.k : a.v;
     const IN *from = static_cast<const IN *>(r.p) + token * r.stride + head * r.head_stride;
+    // Its elements d0 .. and, of a rotated one, d1 .. (neighbouring pairs: the 2 N
+    // elements of N of them).
+    const uint32_t half = a.rotary_dims / 2u, turned = half / N;
+    const bool turns = kind != 2u && part < turned;
+    const uint32_t d0 = turns ? (a.interleaved ? 2u : 1u) * part * N
+                              : (kind == 2u ? part : a.rotary_dims / N + part - turned) * N;
+    const uint32_t d1 = a.interleaved ? d0 + N : d0 + half;
+    float x[N], y[N];
+    load_unit(from + d0, x);
+    if (turns) load_unit(from + d1, y);
+    // Where it goes.
+    const int64_t at = a.positions ? a.positions[token] : 0;
+    const int32_t seq = __builtin_amdgcn_readfirstlane(sequence_of(a.b, static_cast<int32_t>(token)));
+    if (seq < 0 || !mine) return;
+    const int64_t length = a.b.lengths[seq];
+    const int64_t place = length + (static_cast<int64_t>(token) - a.b.starts[seq]);
     OUT *to;
     if (kind == 0u) {
         to = static_cast<OUT *>(a.q_out) + token * a.q_out_stride + head * a.q_out_head_stride;
     } else {
         if (length < 0 || place < 0 || place >= static_cast<int64_t>(a.b.table_pages) * a.page_size) return;
-        const uint32_t at = static_cast<uint32_t>(place), page = at / a.page_size;
+        const uint32_t p = static_cast<uint32_t>(place), page = p / a.page_size;
         const uint32_t id = static_cast<uint32_t>(a.b.page_table[seq * a.b.table_stride + page]);
         if (id >= a.n_pages) return;
         const df11::KvPages &c = kind == 1u ? a.k_pages : a.v_pages;
-        to = static_cast<OUT *>(c.p) + id * c.page_stride + (at - page * a.page_size) * c.place_stride +
-             head * c.head_stride;
+        to = static_cast<OUT *>(c.p) + id * c.page_stride + (p - page * a.page_size) * c.place_stride + head * c.head_stride;
     }
-    const uint32_t half = a.rotary_dims / 2u, turned = half / N;
-    if (kind != 2u && part < turned) {
+    if (turns) {
+        const int64_t position = a.positions ? at : place;
         const bool known = position >= 0 && static_cast<uint64_t>(position) < a.rotary_rows;
-        rotate_unit<IN, OUT, N>(from, to, a.rotary + (known ? position : 0) * a.rotary_dims, half, part * N,
-                                a.interleaved, known);
-    } else {
-        const uint32_t d = kind == 2u ? part * N : a.rotary_dims + (part - turned) * N;
-        float f[N];
-        load_unit(from + d, f);
-        store_vec<OUT, N>(to + d, f);
+        const float *row = a.rotary + (known ? position : 0) * a.rotary_dims + part * N;
+        float c[N], s[N];
+        load_unit(row, c);
+        load_unit(row + half, s);
+        if (!known) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) c[i] = s[i] = __builtin_nanf("");
+        }
+        turn(x, y, c, s, a.interleaved != 0u);
+        store_vec<OUT, N>(to + d1, y);
     }
+    store_vec<OUT, N>(to + d0, x);
 }
 
 template <typename IN, typename OUT>
@@ -168,11 +147,17 @@ const void *pick_in(uint32_t dtype, bool wide) {
 
 }  // namespace
 
-extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, const df11_append *a, void *hip_stream) {
+extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, const df11_append *given, void *hip_stream) {
     uint64_t k_span = 0, v_span = 0;
     const int rc = check_kv(c, b, k_span, v_span);
     if (rc) return rc;
-    const uint32_t bytes = a ? dtype_bytes(a->dtype) : 0, dim = c->head_dim, tokens = b->n_tokens;
+    if (!given) return DF11_E_INVALID_ARG;
+    df11_append used = *given;
+    for (uint64_t *s : {&used.k_stride, &used.v_stride, &used.q_stride, &used.q_out_stride}) *s = kv_stride(b->n_tokens, *s);
+    for (uint64_t *s : {&used.k_head_stride, &used.v_head_stride}) *s = kv_stride(c->heads, *s);
+    for (uint64_t *s : {&used.q_head_stride, &used.q_out_head_stride}) *s = kv_stride(used.q_heads, *s);
+    const df11_append *a = &used;
+    const uint32_t bytes = dtype_bytes(a->dtype), dim = c->head_dim, tokens = b->n_tokens;
     if (!bytes || !a->q != !a->q_out || (a->q ? !a->q_heads || a->q_heads > kMaxKvHeads : a->q_heads != 0))
         return DF11_E_INVALID_ARG;
     if (a->rotary && (a->rotary_dims < 2 || a->rotary_dims % 2 || a->rotary_dims > dim || !aligned(a->rotary, 4) ||
@@ -220,8 +205,8 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
     }
     AppendArgs k{};
     k.b = kernel_batch(*b);
-    k.k_pages = df11::KvPages{c->k, c->k_page_stride, c->k_place_stride, c->k_head_stride};
-    k.v_pages = df11::KvPages{c->v, c->v_page_stride, c->v_place_stride, c->v_head_stride};
+    k.k_pages = kernel_pages(c->k, c->k_page_stride, c->k_place_stride, c->k_head_stride, *c);
+    k.v_pages = kernel_pages(c->v, c->v_page_stride, c->v_place_stride, c->v_head_stride, *c);
     k.q = Rows{a->q, a->q_stride, a->q_head_stride};
     k.k = Rows{a->k, a->k_stride, a->k_head_stride};
     k.v = Rows{a->v, a->v_stride, a->v_head_stride};

@@ -1128,11 +1128,17 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     return DF11_OK;
 }
 
+df11_attention used_strides(df11_attention a, uint32_t n_tokens) {
+    for (uint64_t *s : {&a.q_stride, &a.out_stride, &a.mask_stride}) *s = kv_stride(n_tokens, *s);
+    for (uint64_t *s : {&a.q_head_stride, &a.out_head_stride}) *s = kv_stride(a.q_heads, *s);
+    return a;
+}
+
 // Checks of what comes beside the cache and the batch (already checked); the
 // spans of q and out in bytes.
 int check_attention(const df11_kv_cache &c, const df11_kv_batch &b, const df11_attention *a, uint64_t &q_span,
                     uint64_t &out_span) {
-    if (!a || !a->q_heads || a->q_heads > kMaxKvHeads || a->q_heads % c.heads || !(a->scale > 0.0f) ||
+    if (!a->q_heads || a->q_heads > kMaxKvHeads || a->q_heads % c.heads || !(a->scale > 0.0f) ||
         !std::isfinite(a->scale))
         return DF11_E_INVALID_ARG;
     if (b.n_tokens == 0 || b.n_seqs == 0) return DF11_OK;
@@ -1152,19 +1158,24 @@ int check_attention(const df11_kv_cache &c, const df11_kv_batch &b, const df11_a
 
 extern "C" {
 
-uint64_t df11_tree_attention_workspace(const df11_kv_cache *c, const df11_kv_batch *b, const df11_attention *a) {
+uint64_t df11_tree_attention_workspace(const df11_kv_cache *c, const df11_kv_batch *b, const df11_attention *given) {
     uint64_t k_span = 0, v_span = 0, q_span = 0, out_span = 0;
     Plan p{};
-    if (check_kv(c, b, k_span, v_span) || check_attention(*c, *b, a, q_span, out_span)) return 0;
+    if (check_kv(c, b, k_span, v_span) || !given) return 0;
+    const df11_attention used = used_strides(*given, b->n_tokens), *a = &used;
+    if (check_attention(*c, *b, a, q_span, out_span)) return 0;
     if (b->n_tokens == 0 || b->n_seqs == 0 || make_plan(*c, *b, a->q_heads, p)) return 0;
     return p.parts + p.stats + p.cut;
 }
 
-int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df11_attention *a, void *workspace,
+int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df11_attention *given, void *workspace,
                         uint64_t workspace_bytes, void *hip_stream) {
     uint64_t k_span = 0, v_span = 0, q_span = 0, out_span = 0;
     int rc = check_kv(c, b, k_span, v_span);
-    if (!rc) rc = check_attention(*c, *b, a, q_span, out_span);
+    if (!rc && !given) rc = DF11_E_INVALID_ARG;
+    if (rc) return rc;
+    const df11_attention used = used_strides(*given, b->n_tokens), *a = &used;
+    rc = check_attention(*c, *b, a, q_span, out_span);
     if (rc || b->n_tokens == 0 || b->n_seqs == 0) return rc;
     // Outputs stay clear of everything that is read, but out may lie exactly on q.
     const uint64_t lse_span = a->lse ? 4ull * b->n_tokens * a->q_heads : 0;
@@ -1189,8 +1200,8 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     if (!clear(2)) return DF11_E_INVALID_ARG;
     AttentionArgs k{};
     k.b = kernel_batch(*b);
-    k.k = df11::KvPages{c->k, c->k_page_stride, c->k_place_stride, c->k_head_stride};
-    k.v = df11::KvPages{c->v, c->v_page_stride, c->v_place_stride, c->v_head_stride};
+    k.k = kernel_pages(c->k, c->k_page_stride, c->k_place_stride, c->k_head_stride, *c);
+    k.v = kernel_pages(c->v, c->v_page_stride, c->v_place_stride, c->v_head_stride, *c);
     k.q = a->q;
     k.out = a->out;
     k.lse = a->lse;

@@ -52,6 +52,9 @@ __device__ __forceinline__ int32_t sequence_of(const df11::KvBatch &b, int32_t t
     return rows && heads ? (rows - 1) * stride + (heads - 1) * head_stride + dim : 0;
 }
 
+// A stride as it is used: along one element not at all.
+[[maybe_unused]] uint64_t kv_stride(uint64_t count, uint64_t stride) { return count > 1 ? stride : 0; }
+
 // Whether rows and heads of such a tensor lie apart (the larger stride steps
 // over all that the smaller one reaches).
 [[maybe_unused]] bool kv_apart(uint64_t rows, uint64_t stride, uint64_t heads, uint64_t head_stride, uint64_t dim) {
@@ -69,9 +72,10 @@ __device__ __forceinline__ int32_t sequence_of(const df11::KvBatch &b, int32_t t
     const uint64_t strides[] = {page, place, head}, counts[] = {c.n_pages, c.page_size, c.heads};
     span = c.head_dim;
     for (int i = 0; i < 3; ++i) {
+        if (counts[i] == 1) continue;
         if (strides[i] % 8 || strides[i] >= kMaxKvStride) return false;
         // (2^31 pages of strides below 2^40 would pass 64 bits in bytes)
-        if (counts[i] > 1 && strides[i] > (1ull << 60) / counts[i]) return false;
+        if (strides[i] > (1ull << 60) / counts[i]) return false;
         span += (counts[i] - 1) * strides[i];
     }
     span *= 2;
@@ -102,6 +106,10 @@ __device__ __forceinline__ int32_t sequence_of(const df11::KvBatch &b, int32_t t
     const uint64_t table = b.n_seqs && b.table_pages ? 4 * ((b.n_seqs - 1) * b.table_stride + b.table_pages) : 0;
     return !overlaps(p, bytes, b.starts, 4ull * (b.n_seqs + 1)) && !overlaps(p, bytes, b.lengths, 4ull * b.n_seqs) &&
            !overlaps(p, bytes, b.page_table, table);
+}
+
+[[maybe_unused]] df11::KvPages kernel_pages(void *p, uint64_t page, uint64_t place, uint64_t head, const df11_kv_cache &c) {
+    return df11::KvPages{p, kv_stride(c.n_pages, page), kv_stride(c.page_size, place), kv_stride(c.heads, head)};
 }
 
 [[maybe_unused]] df11::KvBatch kernel_batch(const df11_kv_batch &b) {

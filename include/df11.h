@@ -727,7 +727,8 @@ int df11_cross_entropy_grad(const float *grad, const float *dy, uint64_t dy_stri
  * the device hold is not known to the host; the kernels check it: a token
  * before starts[0] or behind starts[n_seqs] belongs to no sequence, and a place
  * beyond table_pages pages, or in a page outside 0 .. n_pages - 1, is neither
- * read nor written.  (Starts that decrease give unspecified results, in
+ * read nor written.  A stride along a dimension of one element is not used.
+ * (Starts that decrease give unspecified results, in
  * bounds.)  All types are DF11_BF16, DF11_FP16 or, where stated, DF11_FP32.
  * ------------------------------------------------------------------------- */
 

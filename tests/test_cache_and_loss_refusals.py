@@ -21,24 +21,30 @@ def _load():
     return _lib.load()
 
 
+def _pack(format, fields, given):
+    assert not set(given) - set(fields)
+    return format.pack(*((given.get(n) or 0) for n in fields))
+
+
 def _cache(**k):
     """Eight pages of 16 places, two heads of 64."""
     a = dict(k=A, v=B, kp=2048, kl=128, kh=64, vp=2048, vl=128, vh=64, n=8, page=16, heads=2, dim=64, t=0)
     a.update(k)
-    return _lib.KvCache(a["k"], a["v"], a["kp"], a["kl"], a["kh"], a["vp"], a["vl"], a["vh"], a["n"], a["page"], a["heads"],
-                        a["dim"], a["t"])
+    return _lib.KV_CACHE.pack(a["k"] or 0, a["v"] or 0, a["kp"], a["kl"], a["kh"], a["vp"], a["vl"], a["vh"], a["n"], a["page"],
+                              a["heads"], a["dim"], a["t"], 0)
 
 
 def _batch(**k):
     a = dict(starts=C, lengths=C + 0x1000, table=C + 0x2000, stride=4, seqs=3, pages=4, tokens=5)
     a.update(k)
-    return _lib.KvBatch(a["starts"], a["lengths"], a["table"], a["stride"], a["seqs"], a["pages"], a["tokens"])
+    return _lib.KV_BATCH.pack(a["starts"] or 0, a["lengths"] or 0, a["table"] or 0, a["stride"], a["seqs"], a["pages"],
+                              a["tokens"], 0)
 
 
 def _append(cache=None, batch=None, **k):
     a = dict(k=D, v=E, k_stride=128, k_head_stride=64, v_stride=128, v_head_stride=64, dtype=0)
     a.update(k)
-    return _load().df11_append_kv(_cache(**(cache or {})), _batch(**(batch or {})), _lib.Append(**a), None)
+    return _load().df11_append_kv(_cache(**(cache or {})), _batch(**(batch or {})), _pack(_lib.APPEND, _lib.APPEND_FIELDS, a), None)
 
 
 Q = dict(q=F, q_stride=256, q_head_stride=64, q_heads=4, q_out=G, q_out_stride=256, q_out_head_stride=64)
@@ -89,15 +95,15 @@ def test_append_takes_nothing():
     assert _append(batch=dict(tokens=0)) == 0
     assert _append(batch=dict(tokens=0), k=None, v=None) == 0
     assert _append(batch=dict(seqs=0, lengths=None, table=None)) == 0
-    assert _load().df11_append_kv(None, _batch(), _lib.Append(), None) == INVALID
-    assert _load().df11_append_kv(_cache(), None, _lib.Append(), None) == INVALID
+    assert _load().df11_append_kv(None, _batch(), _pack(_lib.APPEND, _lib.APPEND_FIELDS, {}), None) == INVALID
+    assert _load().df11_append_kv(_cache(), None, _pack(_lib.APPEND, _lib.APPEND_FIELDS, {}), None) == INVALID
     assert _load().df11_append_kv(_cache(), _batch(), None, None) == INVALID
 
 
 def _attend(cache=None, batch=None, ws=J, nbytes=1 << 30, entry="run", **k):
     a = dict(q=D, out=E, q_stride=256, q_head_stride=64, out_stride=256, out_head_stride=64, q_heads=4, scale=0.125)
     a.update(k)
-    lib, s = _load(), (_cache(**(cache or {})), _batch(**(batch or {})), _lib.Attention(**a))
+    lib, s = _load(), (_cache(**(cache or {})), _batch(**(batch or {})), _pack(_lib.ATTENTION, _lib.ATTENTION_FIELDS, a))
     return lib.df11_tree_attention_workspace(*s) if entry == "size" else lib.df11_tree_attention(*s, ws, nbytes, None)
 
 
@@ -129,8 +135,58 @@ def test_attention_takes_nothing():
         assert _attend(batch=batch, q=None, out=None, ws=None, nbytes=0) == 0
         assert _attend(batch=batch, entry="size") == 0
     lib = _load()
-    assert lib.df11_tree_attention(None, _batch(), _lib.Attention(), None, 0, None) == INVALID
+    assert lib.df11_tree_attention(None, _batch(), _pack(_lib.ATTENTION, _lib.ATTENTION_FIELDS, {}), None, 0, None) == INVALID
     assert lib.df11_tree_attention(_cache(), _batch(), None, None, 0, None) == INVALID
+
+
+def test_strides_of_one_element_are_not_used():
+    """Whatever they are: one page of one place, one token, one head."""
+    one = dict(n=1, page=1, heads=1, kp=3, kl=5, kh=1 << 50, vp=1, vl=7, vh=9)
+    few = dict(tokens=1)
+    assert _append(cache=one, batch=few, k_stride=1 << 45, k_head_stride=1 << 40, v_stride=3, k=1) == INVALID  # (k itself)
+    assert _append(cache=one, batch=dict(tokens=0), k_stride=1 << 45, k_head_stride=1 << 40, v_stride=3) == 0
+    assert _attend(cache=one, batch=dict(few, seqs=0), q_stride=3, out_stride=5, q_heads=1, q_head_stride=1, out_head_stride=3) == 0
+
+
+def _layout(name, fields):
+    """Offsets and size of a struct of the header, by the C compiler."""
+    import subprocess
+    import tempfile
+    repo = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with tempfile.TemporaryDirectory() as d:
+        src = os.path.join(d, "s.c")
+        with open(src, "w") as f:
+            f.write('#include <stddef.h>\n#include <stdio.h>\n#include "df11.h"\nint main(void) {\n')
+            for n in fields:
+                f.write(f'    printf("%zu ", offsetof({name}, {n}));\n')
+            f.write(f'    printf("%zu\\n", sizeof({name}));\n    return 0;\n}}\n')
+        subprocess.run(["gcc", f"-I{os.path.join(repo, 'include')}", src, "-o", os.path.join(d, "s")], check=True)
+        return [int(v) for v in subprocess.run([os.path.join(d, "s")], capture_output=True, text=True,
+                                               check=True).stdout.split()]
+
+
+@pytest.mark.parametrize("name,format,fields", [
+    ("df11_kv_cache", "KV_CACHE", "KV_CACHE_FIELDS"), ("df11_kv_batch", "KV_BATCH", "KV_BATCH_FIELDS"),
+    ("df11_append", "APPEND", "APPEND_FIELDS"), ("df11_attention", "ATTENTION", "ATTENTION_FIELDS")])
+def test_packed_structures(name, format, fields):
+    import struct
+    format, fields = getattr(_lib, format), getattr(_lib, fields)
+    *offsets, size = _layout(name, fields)
+    assert size == format.size
+    kinds = []
+    for n, c in __import__("re").findall(r"(\d*)([QIf])", format.format):
+        kinds += [c] * int(n or 1)
+    at = 0
+    for offset, kind in zip(offsets, kinds):
+        assert offset == at
+        at += struct.calcsize("=" + kind)
+    assert len(kinds) == len(fields) and at == size
+
+
+def test_loss_structure():
+    fields = [n for n, _ in _lib.Loss._fields_]
+    *offsets, size = _layout("df11_loss", fields)
+    assert [getattr(_lib.Loss, n).offset for n in fields] == offsets and ctypes.sizeof(_lib.Loss) == size
 
 
 def test_cache_binding_refuses():
