@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include "df11.h"
+#include "df11_attention_plan.h"
 #include "df11_device.h"
 #include "df11_kv.h"
 #include "df11_types.h"
@@ -36,10 +37,12 @@ struct AppendArgs {
     const int32_t *positions;
     uint64_t rotary_rows;
     uint32_t n_pages, page_size;
-    uint32_t q_heads, kv_heads, dim, rotary_dims, interleaved;
+    uint32_t q_heads, kv_heads, dim, rotary_dims;
     uint32_t units_head;  // units of a rotated head, of a copied one
     uint32_t units_copy;
     uint32_t units;       // of a token
+    uint32_t head_magic, copy_magic;    // floor(2^32 / units_head) + 1, 0 for one unit
+    uint32_t page_magic, page_shift;    // df11::page_of
 };
 
 // N consecutive elements as floats and back (N * 2 or 16 bytes aligned).
@@ -53,31 +56,21 @@ __device__ __forceinline__ void load_unit(const T *p, float (&f)[N]) {
     }
 }
 
-// N pairs rotated in place: x and y their first and second elements, or both the
-// elements of neighbouring pairs one after the other.
+// N pairs rotated in place, x and y their first and second elements.
 template <int N>
-__device__ __forceinline__ void turn(float (&x)[N], float (&y)[N], const float (&c)[N], const float (&s)[N],
-                                     bool interleaved) {
-    if (!interleaved || N == 1) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float a = x[i], b = y[i];
-            x[i] = a * c[i] - b * s[i];
-            y[i] = b * c[i] + a * s[i];
-        }
-        return;
-    }
+__device__ __forceinline__ void turn(float (&x)[N], float (&y)[N], const float (&c)[N], const float (&s)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        float *pair = i < N / 2 ? &x[2 * i] : &y[2 * i - N];
-        const float a = pair[0], b = pair[1];
-        pair[0] = a * c[i] - b * s[i];
-        pair[1] = b * c[i] + a * s[i];
+        const float a = x[i], b = y[i];
+        x[i] = a * c[i] - b * s[i];
+        y[i] = b * c[i] + a * s[i];
     }
 }
 
-// N: pairs of a rotated unit and elements of a copied one.
-template <typename IN, typename OUT, int N>
+// N: pairs of a rotated unit and elements of a copied one.  kNext: neighbouring
+// pairs, of which a rotated unit has N / 2 (or one): then lanes read and write next to
+// each other in every access.
+template <typename IN, typename OUT, int N, bool kNext>
 __global__ __launch_bounds__(256) void df11_append_kernel(AppendArgs a) {
     const uint32_t token = blockIdx.x, unit = min(blockIdx.y * blockDim.x + threadIdx.x, a.units - 1u);
     const uint32_t q_units = a.q_heads * a.units_head, k_units = a.kv_heads * a.units_head;
@@ -85,19 +78,24 @@ __global__ __launch_bounds__(256) void df11_append_kernel(AppendArgs a) {
     // What the unit reads, of q, k or v.
     const uint32_t kind = unit < q_units ? 0u : unit < q_units + k_units ? 1u : 2u;
     const uint32_t u = unit - (kind == 0u ? 0u : kind == 1u ? q_units : q_units + k_units);
-    const uint32_t each = kind == 2u ? a.units_copy : a.units_head, head = u / each, part = u % each;
+    // (a unit's number times the units of a head is far below 2^32: the quotient by
+    // the multiplication is exact)
+    const uint32_t magic = kind == 2u ? a.copy_magic : a.head_magic;
+    const uint32_t head = magic ? __umulhi(u, magic) : u;
+    const uint32_t part = u - head * (kind == 2u ? a.units_copy : a.units_head);
     const Rows &r = kind == 0u ? a.q : kind == 1u ? a.k : a.v;
     const IN *from = static_cast<const IN *>(r.p) + token * r.stride + head * r.head_stride;
-    // Its elements d0 .. and, of a rotated one, d1 .. (neighbouring pairs: the 2 N
-    // elements of N of them).
-    const uint32_t half = a.rotary_dims / 2u, turned = half / N;
+    // Its elements d0 .. and, of a rotated one of pairs that lie apart, d1 ..
+    constexpr uint32_t kPairs = kNext && N > 1 ? N / 2 : N;  // of a rotated unit
+    const uint32_t half = a.rotary_dims / 2u, turned = half / kPairs;
     const bool turns = kind != 2u && part < turned;
-    const uint32_t d0 = turns ? (a.interleaved ? 2u : 1u) * part * N
-                              : (kind == 2u ? part : a.rotary_dims / N + part - turned) * N;
-    const uint32_t d1 = a.interleaved ? d0 + N : d0 + half;
+    const uint32_t d0 = turns ? (kNext ? 2u : 1u) * part * kPairs
+                              : (kind == 2u ? part * N : a.rotary_dims + (part - turned) * N);
+    const uint32_t d1 = kNext ? d0 + 1u : d0 + half;
+    constexpr bool kTwo = !kNext || N == 1;  // a rotated unit has two accesses
     float x[N], y[N];
     load_unit(from + d0, x);
-    if (turns) load_unit(from + d1, y);
+    if (kTwo && turns) load_unit(from + d1, y);
     // Where it goes.
     const int64_t at = a.positions ? a.positions[token] : 0;
     const int32_t seq = __builtin_amdgcn_readfirstlane(sequence_of(a.b, static_cast<int32_t>(token)));
@@ -109,7 +107,7 @@ __global__ __launch_bounds__(256) void df11_append_kernel(AppendArgs a) {
         to = static_cast<OUT *>(a.q_out) + token * a.q_out_stride + head * a.q_out_head_stride;
     } else {
         if (length < 0 || place < 0 || place >= static_cast<int64_t>(a.b.table_pages) * a.page_size) return;
-        const uint32_t p = static_cast<uint32_t>(place), page = p / a.page_size;
+        const uint32_t p = static_cast<uint32_t>(place), page = df11::page_of(p, a.page_magic, a.page_shift);
         const uint32_t id = static_cast<uint32_t>(a.b.page_table[seq * a.b.table_stride + page]);
         if (id >= a.n_pages) return;
         const df11::KvPages &c = kind == 1u ? a.k_pages : a.v_pages;
@@ -118,31 +116,49 @@ __global__ __launch_bounds__(256) void df11_append_kernel(AppendArgs a) {
     if (turns) {
         const int64_t position = a.positions ? at : place;
         const bool known = position >= 0 && static_cast<uint64_t>(position) < a.rotary_rows;
-        const float *row = a.rotary + (known ? position : 0) * a.rotary_dims + part * N;
-        float c[N], s[N];
+        const float *row = a.rotary + (known ? position : 0) * a.rotary_dims + part * kPairs;
+        float c[kPairs], s[kPairs];
         load_unit(row, c);
         load_unit(row + half, s);
         if (!known) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) c[i] = s[i] = __builtin_nanf("");
+            for (uint32_t i = 0; i < kPairs; ++i) c[i] = s[i] = __builtin_nanf("");
         }
-        turn(x, y, c, s, a.interleaved != 0u);
-        store_vec<OUT, N>(to + d1, y);
+        if constexpr (kTwo) {
+            turn(x, y, c, s);
+            store_vec<OUT, N>(to + d1, y);
+        } else {
+            float first[kPairs], second[kPairs];
+#pragma unroll
+            for (uint32_t i = 0; i < kPairs; ++i) {
+                first[i] = x[2 * i];
+                second[i] = x[2 * i + 1];
+            }
+            turn(first, second, c, s);
+#pragma unroll
+            for (uint32_t i = 0; i < kPairs; ++i) {
+                x[2 * i] = first[i];
+                x[2 * i + 1] = second[i];
+            }
+        }
     }
     store_vec<OUT, N>(to + d0, x);
 }
 
 template <typename IN, typename OUT>
-const void *pick_width(bool wide) {
-    return wide ? reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 8>)
-                : reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 1>);
+const void *pick_width(bool wide, bool next) {
+    if (next)
+        return wide ? reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 8, true>)
+                    : reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 1, true>);
+    return wide ? reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 8, false>)
+                : reinterpret_cast<const void *>(&df11_append_kernel<IN, OUT, 1, false>);
 }
 
 template <typename OUT>
-const void *pick_in(uint32_t dtype, bool wide) {
-    return dtype == DF11_FP32   ? pick_width<float, OUT>(wide)
-           : dtype == DF11_BF16 ? pick_width<bf16_t, OUT>(wide)
-                                : pick_width<fp16_t, OUT>(wide);
+const void *pick_in(uint32_t dtype, bool wide, bool next) {
+    return dtype == DF11_FP32   ? pick_width<float, OUT>(wide, next)
+           : dtype == DF11_BF16 ? pick_width<bf16_t, OUT>(wide, next)
+                                : pick_width<fp16_t, OUT>(wide, next);
 }
 
 }  // namespace
@@ -222,16 +238,22 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
     k.kv_heads = c->heads;
     k.dim = dim;
     k.rotary_dims = rotary_dims;
-    k.interleaved = a->interleaved;
-    const uint32_t each = wide ? 8 : 1;
-    k.units_head = rotary_dims / 2 / each + (dim - rotary_dims) / each;
+    const bool next = a->interleaved != 0 && rotary_dims;
+    const uint32_t each = wide ? 8 : 1, pairs = wide && next ? 4 : each;
+    k.units_head = rotary_dims / 2 / pairs + (dim - rotary_dims) / each;
     k.units_copy = dim / each;
     // (at most 4096 heads of 256 elements, three times)
     k.units = (a->q_heads + c->heads) * k.units_head + c->heads * k.units_copy;
+    const auto magic = [](uint32_t n) { return n > 1 ? static_cast<uint32_t>((1ull << 32) / n + 1u) : 0u; };
+    k.head_magic = magic(k.units_head);
+    k.copy_magic = magic(k.units_copy);
+    k.page_shift = df11::page_shift(c->page_size);
+    k.page_magic = df11::page_magic(c->page_size, k.page_shift);
     (void)hipGetLastError();
     void *params[] = {&k};
     const uint32_t threads = k.units >= 256 ? 256 : 64;
-    return launch_kernel(c->dtype == DF11_BF16 ? pick_in<bf16_t>(a->dtype, wide) : pick_in<fp16_t>(a->dtype, wide),
+    return launch_kernel(c->dtype == DF11_BF16 ? pick_in<bf16_t>(a->dtype, wide, next)
+                                              : pick_in<fp16_t>(a->dtype, wide, next),
                          dim3(tokens, (k.units + threads - 1) / threads), dim3(threads), params, 0,
                          static_cast<hipStream_t>(hip_stream), nullptr, nullptr);
 }
