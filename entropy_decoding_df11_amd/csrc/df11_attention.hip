@@ -156,6 +156,10 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // 2^(m - to), 0 for a reference of nothing.
 __device__ __forceinline__ float weight_of(float m, float to) { return m == -INFINITY ? 0.0f : exp2_fast(m - to); }
 
+// Whether a part adds nothing to its row.  (Scores that are all NaN leave no reference,
+// but a sum that is NaN, which the row has to get.)
+__device__ __forceinline__ bool adds_nothing(float weight, float sum) { return weight == 0.0f && sum == sum; }
+
 __device__ __forceinline__ SeqShape shape_of(const AttentionArgs &a, uint32_t s) {
     return df11::seq_shape(a.b.starts[s], a.b.starts[s + 1], a.b.lengths[s], a.b.n_tokens, a.capacity, a.group,
                            a.tile_rows, a.step, a.extra, a.mask != nullptr);
@@ -809,7 +813,7 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
             for (uint32_t x = 0; x < WK; ++x) {
                 const uint32_t other = x * WR + wr;
                 const float f = weight_of(s_stats[other][r][0], top);
-                if (f == 0.0f) continue;
+                if (adds_nothing(f, s_stats[other][r][1])) continue;
                 total += f * s_stats[other][r][1];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += f * sums[other * kWaveFloats + r * kStride + d + e];
@@ -972,8 +976,8 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
         for (int e = 0; e < 8; ++e) sum[e] *= old;
 #pragma unroll
         for (uint32_t k = 0; k < kJoinAtOnce; ++k) {
-            const float f = r + k < end ? weight_of(st[k][0], to) : 0.0f;
-            if (f == 0.0f) continue;
+            const float f = weight_of(st[k][0], to);
+            if (r + k >= end || adds_nothing(f, st[k][1])) continue;
             total += f * st[k][1];
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += f * v[k][e];
@@ -994,7 +998,7 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
             total *= old;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] *= old;
-            if (f != 0.0f) {
+            if (!adds_nothing(f, s_sum[w][9][lane])) {
                 total += f * s_sum[w][9][lane];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += f * s_sum[w][e][lane];

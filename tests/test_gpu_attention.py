@@ -12,6 +12,7 @@ and the sums over n places lose n e.  All of it reaches an output in proportion
 to sum p |v|, and the output is rounded once more."""
 
 import math
+import threading
 
 import pytest
 
@@ -379,6 +380,75 @@ def test_far_pages():
         halves.append(far)
     got = df11.tree_attention(case.q.to(DEV), *halves, *case.batch)
     assert torch.equal(got, case.attend())
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim,page", [(4, 2, 64, 16), (4, 2, 64, 9), (7, 1, 80, 16), (6, 2, 96, 24),
+                                                      (3, 1, 136, 5), (4, 2, 256, 16), (4, 2, 256, 11)])
+def test_cut_tiles(heads, kv_heads, dim, page, masked):
+    """Tiles of many rows that many workgroups share, of every padded width, with pages of whole and of odd loads."""
+    case = Case([7000, 1500, 0], [70, 1, 33], torch.float16, heads, kv_heads, dim, page, seed=31, first=2, spare=3)
+    case.check(mask=tree(case, seed=31) if masked else None)
+
+
+def test_shared_pages():
+    """Two sequences with one prefix: the same pages in both tables."""
+    case = Case([320, 330], [3, 20], torch.bfloat16, 8, 2, 128, seed=32)
+    case.table[1, :20] = case.table[0, :20]
+    case.upload()
+    case.check()
+
+
+@pytest.mark.parametrize("tokens", [[1, 2], [40, 3]])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_queries_that_are_not_finite(tokens, value):
+    """They spoil their own rows only."""
+    case = Case([2000, 90], tokens, torch.bfloat16, 4, 2, 64, seed=33)
+    q = case.q.clone()
+    q[0, 1, 5] = value
+    out, lse = case.attend(q=q.to(DEV), return_lse=True)
+    o, tol, want, lse_tol = case.expect()
+    others = torch.ones(case.total, case.heads, dtype=torch.bool)
+    others[0, 1] = False
+    assert bool(((out.cpu().double() - o).abs() <= tol)[others].all())
+    assert bool(((lse.cpu().double() - want).abs() <= lse_tol)[others].all())
+    assert bool(out[0, 1].isnan().all()) and bool(lse[0, 1].isnan())
+
+
+def test_far_pages_of_many_rows():
+    case = Case([100], [40], torch.bfloat16, 4, 2, 64, seed=34)
+    n, stride = case.k.shape[0], (1 << 32) // (case.k.shape[0] - 1) // 8 * 8 + 4096
+    halves = []
+    for half in (case.k, case.v):
+        big = torch.empty(stride * n, dtype=case.dtype, device=DEV)
+        far = big.as_strided((n, 16, 2, 64), (stride, 128, 64, 1))
+        far.copy_(half)
+        halves.append(far)
+    got = df11.tree_attention(case.q.to(DEV), *halves, *case.batch)
+    assert torch.equal(got, case.attend())
+
+
+def test_threads():
+    """Calls from threads at once, each on a stream of its own."""
+    cases = [Case([4000, 17], [1, 5 + 30 * s], torch.bfloat16, 8, 2, 128, seed=35 + s) for s in range(3)]
+    qs = [c.q.to(DEV) for c in cases]
+    want = [c.attend(q=q) for c, q in zip(cases, qs)]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        for _ in range(5):
+            got[i].append(cases[i].attend(q=qs[i], stream=stream))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for outs, w in zip(got, want):
+        assert len(outs) == 5 and all(torch.equal(o, w) for o in outs)
 
 
 def test_same_bits_again():
