@@ -193,6 +193,28 @@ def test_targets_that_are_no_class(tokens):
     assert bool(other.isnan())  # nothing to take a mean of
 
 
+@pytest.mark.parametrize("tokens", [9, 50])
+def test_states_that_are_not_finite(tokens):
+    """They spoil their own tokens only: the others keep their bits."""
+    head = Head(tokens, 4160, 64, seed=17)
+    x = head.dx_.clone()
+    for row, value in ((1, math.nan), (2, math.inf), (8, -math.inf)):
+        x[row, 3] = value
+    assert all(int(head.targets[row]) != -100 for row in (1, 2, 8))
+    others = torch.ones(tokens, dtype=torch.bool, device=DEV)
+    others[[1, 2, 8]] = False
+    for gradient in (False, True):
+        results = []
+        for states in (x, head.dx_):
+            states = states.clone().requires_grad_(gradient)
+            loss = head.run_on(states)
+            results.append((loss.detach(), torch.autograd.grad(loss.sum(), states)[0] if gradient else loss))
+        for got, want in zip(*results):
+            assert torch.equal(got[others], want[others])
+            assert not bool(got[[1, 2, 8]].isfinite().flatten(1).all(1).any() if got.dim() == 2 else
+                            got[[1, 2, 8]].isfinite().any())
+
+
 def test_nothing_to_score():
     head = Head(40, 64, 32, seed=8)
     head.dt.fill_(-100)
