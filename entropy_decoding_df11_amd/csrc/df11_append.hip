@@ -8,6 +8,12 @@
 // all in 16-byte accesses; a workgroup's units belong to one token, so that
 // what finds its place (sequence, page) is the same for all of its lanes.  The
 // elements are asked for before that chain (starts, length, page) is followed.
+//
+// Few tokens are bound by the chain, four loads that wait for each other: one token
+// of 32 + 8 + 8 heads of 128 takes 3.2 us (the call from Python 15).  Many are bound
+// by memory: 1536 tokens of float sums 11.3 us (4.0 TB/s of 45 MB), 9400 of FP16
+// with neighbouring pairs 56 us (4.1 TB/s of 232 MB; with two accesses of 16 bytes
+// side by side a lane, which leave every other chunk to the next access, 69).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -18,15 +18,30 @@
 //                  lane's eight), so that w goes from the softmax to the product
 //                  without leaving its lane; V^T comes from LDS by
 //                  ds_read_b64_tr_b16 in the same order
-// K's operands come straight from memory to registers, V's rows by
-// global_load_lds to LDS that each wave has to itself: waves take the places
-// of a step in turn and meet only at the end of a tile's run.  Sixteen-byte
-// chunks of a V row are permuted by the row in pairs, which spreads the
-// transposed reads over all banks.
+// Sixteen-byte chunks of a V row are permuted by the row in pairs, which spreads
+// the transposed reads over all banks (17 thousand conflicts in 17 million cycles
+// of LDS).
+//
+// Up to 16 rows (few): memory is the bound.  K's operands come straight from
+// memory to registers, V's rows to LDS that each wave has to itself; waves take the
+// places of a step in turn and meet only at the end of a tile's run.  64 sequences of
+// one token over up to 8192 places each: 198 us, 5.1 TB/s of 1.01 GB.  With four
+// waves and twice the workgroups 224.
+//
+// More rows: a wave with rows of its own needs all of K and V, so eight waves share
+// tiles of them in LDS (reading them from memory for each wave: 567 us for the tree
+// below, now 178).  A tree of 64 tokens over 131072 places, 256 rows to a key head:
+// 178 us, 3.0 TB/s and 0.77 PFLOP/s at once.  Two waves a SIMD, which the registers
+// allow, keep the matrix cores 37% busy: what is not overlapped is the softmax's
+// instructions between the two products.  (Wave priorities around the products, and
+// the scores of two blocks before their softmax: no faster.)
+//
+// One token over few places is a chain of latencies (lengths, pages, K, V, the
+// waves' sums): 17 us over 700 places, 10 over 16.
 //
 // Work is cut by df11_attention_plan.h; a tile that one workgroup does alone is
 // written at once, the parts of the others go to the workspace and a second
-// kernel joins them in order.
+// kernel joins them in order (6 to 11 us, 23 where prompts cut most tiles).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1078,7 +1093,12 @@ const void *pick_rows(uint32_t rows, bool whole) {
 }
 
 // Rows of a tile: enough for the rows that a sequence has on average (the host
-// knows no more than that).
+// knows no more than that).  Measured, eight sequences over 4096 places, heads of
+// 128, tiles of 16 / 64 / 128 / 256 rows: 41.7 / 43.7 / 47.9 / 56.6 us at 16 rows,
+// 47.3 / 44.4 / 48.1 / 57.2 at 20, 66.2 / 47.3 / 50.4 / 59.7 at 64, 118 / 66.2 / 52.1 /
+// 59.4 at 68, 112 / 68.7 / 54.8 / 62.3 at 128, 197 / 92.5 / 72.6 / 67.8 at 132, 201 / 104 /
+// 80.1 / 75.1 at 256, and 1059 / 371 / 260 / 221 at 2048 over 2048.  Heads of 64 and 256
+// have the same order but for 20 rows of 64 (25.7 / 29.4).
 uint32_t pick_tile(uint32_t dim, uint64_t rows) {
     return rows <= 16 ? 16 : rows <= 64 ? 64 : rows <= 128 || dim > 128 ? 128 : 256;
 }
@@ -1119,9 +1139,11 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     if (per_cu < 1) return DF11_E_HIP;
     const uint64_t capacity = static_cast<uint64_t>(b.table_pages) * c.page_size;
     const uint64_t tiles = (static_cast<uint64_t>(b.n_tokens) * group + p.tile_rows - 1) / p.tile_rows + b.n_seqs;
-    p.step = df11::unit_places(capacity, few);
+    // (an upper bound of the tiles, at most twice as many)
+    const uint32_t uncut = df11::whole_places(few, tiles * c.heads, static_cast<uint32_t>(cus));
+    p.step = df11::unit_places(capacity, few, uncut);
     // (a tile without a mask may count a unit for its own tokens beside the pages')
-    p.extra = df11::extra_units(capacity, few, c.head_dim);
+    p.extra = df11::extra_units(capacity, few, uncut, c.head_dim);
     const uint64_t units = tiles * c.heads * ((capacity + p.step - 1) / p.step + 2 + p.extra);
     if (static_cast<uint64_t>(b.n_tokens) * group >= (1ull << 31) || units >= df11::kMaxUnits) return DF11_E_TOO_LARGE;
     p.workgroups = static_cast<uint32_t>(std::min<uint64_t>({static_cast<uint64_t>(cus) * per_cu, units, kMaxCuts}));

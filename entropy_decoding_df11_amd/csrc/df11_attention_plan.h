@@ -24,13 +24,21 @@ namespace df11 {
 // and short enough to be cut evenly for many.)
 constexpr uint32_t kFewStep = 256, kManyStep = 128;
 
-// A sequence's pages up to which its tiles are never cut: then a unit is a whole
-// tile, and no second kernel joins parts.
-constexpr uint64_t kWholePlaces = 1024;
+// Places of a sequence's pages up to which tiles are never cut: then a unit is a
+// whole tile, and no second kernel joins parts.  Measured in a graph, heads of
+// 128, whole against cut: one token of one sequence 15.9 and 17.0 us at 500
+// places, 20.4 and 16.7 at 960 (a call from Python saves 3 us more without the
+// second launch); 64 sequences 61.0 and 64.2 at 960; 16 trees of 16 tokens 27.6 and
+// 31.3 at 960, 45.9 and 41.4 at 1500; a tree of 32 of one sequence 28.5 and 22.3
+// at 500.  So it is the number of tiles, which fill the chip or not, that decides.
+constexpr uint32_t kMostWhole = 1024, kFewWhole = 768, kManyWhole = 128;
+constexpr uint32_t whole_places(bool few, uint64_t tiles, uint32_t workgroups) {
+    return tiles >= workgroups ? kMostWhole : few ? kFewWhole : kManyWhole;
+}
 
-// Places of a unit, for pages of `capacity` places.
-constexpr uint32_t unit_places(uint64_t capacity, bool few) {
-    return capacity <= kWholePlaces ? static_cast<uint32_t>(kWholePlaces) : few ? kFewStep : kManyStep;
+// Places of a unit, for pages of `capacity` places of which `whole` are never cut.
+constexpr uint32_t unit_places(uint64_t capacity, bool few, uint32_t whole) {
+    return capacity <= whole ? whole : few ? kFewStep : kManyStep;
 }
 
 // A sequence as the kernels see it, after the checks of what the device holds.
@@ -114,8 +122,8 @@ constexpr uint64_t seq_units(const SeqShape &s, uint32_t kv_heads) {
 // us and a step of it 5.5 (2.5 for heads up to 64, 10 beyond 128), one of few rows 8
 // and 6.5.  (A batch of 24 trees over up to 4096 places, some over a few dozen: 50
 // us without them, when a workgroup had several short tiles.)
-constexpr uint32_t extra_units(uint64_t capacity, bool few, uint32_t dim) {
-    return capacity <= kWholePlaces ? 0u : few || dim > 128u ? 1u : dim > 64u ? 2u : 4u;
+constexpr uint32_t extra_units(uint64_t capacity, bool few, uint32_t whole, uint32_t dim) {
+    return capacity <= whole ? 0u : few || dim > 128u ? 1u : dim > 64u ? 2u : 4u;
 }
 
 // The units of a call; more (of starts that decrease) are none at all.
