@@ -513,6 +513,9 @@ struct FewWave : Rows<T, KK, 1> {
         const bool there = id < a.n_pages && key0 + (lane & 31u) < p.limit;
         valid_to = static_cast<uint32_t>(__ballot(there));
         id = there ? id : 0u;
+        // (a block of nothing reads one place over and over: 17.5 us against 18.1 for
+        // one token over 700 places)
+        const uint64_t k_stride = valid_to ? a.k.place_stride : 0, v_stride = valid_to ? a.v.place_stride : 0;
         const uint32_t last_chunk = a.dim / 8u - 1u;
         const T *kp = static_cast<const T *>(a.k.p) + p.head * a.k.head_stride;
         const T *vp = static_cast<const T *>(a.v.p) + p.head * a.v.head_stride;
@@ -523,11 +526,11 @@ struct FewWave : Rows<T, KK, 1> {
             if constexpr (kWhole) {
                 const uint32_t key = key0 + 16u * t, page = __builtin_amdgcn_readlane(id, 16 * t);
                 const uint32_t off = key - page_of(key) * a.page_size;
-                row = kp + page * a.k.page_stride + off * a.k.place_stride + l16 * a.k.place_stride;
+                row = kp + page * a.k.page_stride + off * k_stride + l16 * k_stride;
             } else {
                 const uint32_t key = key0 + 16u * t + l16, page = __shfl(id, 16 * t + l16);
                 const uint32_t off = key - page_of(key) * a.page_size;
-                row = kp + page * a.k.page_stride + off * a.k.place_stride;
+                row = kp + page * a.k.page_stride + off * k_stride;
             }
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
@@ -543,11 +546,11 @@ struct FewWave : Rows<T, KK, 1> {
             if constexpr (kWhole) {
                 const uint32_t t = i * kVRows / 16, key = key0 + 16u * t, page = __builtin_amdgcn_readlane(id, 16 * t);
                 const uint32_t off = key - page_of(key) * a.page_size;
-                load_rows_to_lds(vp + page * a.v.page_stride + off * a.v.place_stride,
-                                 2u * ((r - 16u * t) * static_cast<uint32_t>(a.v.place_stride) + 8u * chunk), dst + 1024 * i);
+                load_rows_to_lds(vp + page * a.v.page_stride + off * v_stride,
+                                 2u * ((r - 16u * t) * static_cast<uint32_t>(v_stride) + 8u * chunk), dst + 1024 * i);
             } else {
                 const uint32_t key = key0 + r, page = __shfl(id, r);
-                load_to_lds(vp + page * a.v.page_stride + (key - page_of(key) * a.page_size) * a.v.place_stride + 8u * chunk,
+                load_to_lds(vp + page * a.v.page_stride + (key - page_of(key) * a.page_size) * v_stride + 8u * chunk,
                             dst + 1024 * i);
             }
         }
