@@ -16,6 +16,7 @@
 // side by side a lane, which leave every other chunk to the next access, 69).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include <stdint.h>
@@ -188,6 +189,13 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
     if (a->positions && !aligned(a->positions, 4)) return DF11_E_INVALID_ARG;
     if (tokens == 0 || b->n_seqs == 0) return DF11_OK;
     if (!a->k || !a->v) return DF11_E_INVALID_ARG;
+    // Places that lie on each other would hold what was written last.
+    const uint64_t apart[][2] = {{c->n_pages, std::min(c->k_page_stride, c->v_page_stride)},
+                                 {c->page_size, std::min(c->k_place_stride, c->v_place_stride)},
+                                 {c->heads, std::min(c->k_head_stride, c->v_head_stride)}};
+    for (const auto &d : apart)
+        if (d[0] > 1 && d[1] < dim) return DF11_E_INVALID_ARG;
+    if (c->k == c->v) return DF11_E_INVALID_ARG;
     if (a->rotary && !a->rotary_rows) return DF11_E_INVALID_ARG;
     const uint32_t rotary_dims = a->rotary ? a->rotary_dims : 0;
     struct In {

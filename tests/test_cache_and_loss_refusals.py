@@ -91,6 +91,13 @@ def test_append_refuses_a_cache_on_the_batch(bad):
     assert _append(cache=bad) == INVALID
 
 
+@pytest.mark.parametrize("bad", [dict(kp=0), dict(vp=56), dict(kl=0), dict(vl=8), dict(kh=0), dict(vh=56), dict(v=A)])
+def test_append_refuses_places_on_each_other(bad):
+    """An expanded cache, or one tensor for both halves; attention, which only reads, takes them."""
+    assert _append(cache=bad) == INVALID
+    assert _attend(cache=bad, batch=dict(seqs=0)) == 0
+
+
 def test_append_takes_nothing():
     assert _append(batch=dict(tokens=0)) == 0
     assert _append(batch=dict(tokens=0), k=None, v=None) == 0
