@@ -31,6 +31,7 @@ struct DenseLoss {
     float *stats;          // [panel of 64 classes][token][2]: r (-inf: no class) and the sum
     float *target_logit;   // [token], written where the target is among the rows
     const float *ref;      // kDenseExp: [token] r to use while no logit passes it by 2^kRefRoom
+    float *rounded;        // kDenseExp: [panel][token], the sum of what exps holds
     uint16_t *exps;        // kDenseExp: [token][exps_stride]
     const float *scale;    // kDenseBackAdd: [token], of what is in e.out
     uint64_t exps_stride;  // a multiple of 8

@@ -301,8 +301,15 @@ struct LossRows {
                 st[0] = ref;
                 st[1] = sum;
             }
-            if constexpr (MODE == kDenseExp)
+            if constexpr (MODE == kDenseExp) {
                 store8(reinterpret_cast<bf16_t *>(l.exps) + token * l.exps_stride + col0 + c, z);
+                float rounded = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) rounded += static_cast<float>(static_cast<bf16_t>(z[i]));
+#pragma unroll
+                for (int m = 1; m < 8; m <<= 1) rounded += __shfl_xor(rounded, m);
+                if (c == 0) l.rounded[static_cast<uint64_t>(col0 / 64u) * a.tokens + token] = rounded;
+            }
         }
     }
 };

@@ -118,7 +118,8 @@ struct TokenArgs {
     const int64_t *targets;
     int64_t ignore_index;
     const float *stats, *target_logit;
-    float *ref, *sum, *scale;  // running, [token]
+    const float *rounded;      // [panel][token]
+    float *ref, *sum, *sum_rounded, *scale;  // running, [token]
     uint16_t *exps;
     uint64_t exps_stride;
     float *loss;
@@ -141,17 +142,24 @@ __device__ __forceinline__ void load_row8(const uint16_t *w, uint32_t row, uint3
 constexpr uint32_t kTokens = 8, kParts = 1024 / kTokens;
 
 // The pairs (top, sum) of a token's threads joined in a fixed order, in its first.
-__device__ __forceinline__ void join_pairs(float (*s_pair)[kTokens][2], uint32_t part, uint32_t t, float &top, float &sum) {
+// (N: sums that share the reference.)
+template <int N>
+__device__ __forceinline__ void join_pairs(float (*s_pair)[kTokens][1 + N], uint32_t part, uint32_t t, float &top,
+                                           float (&sum)[N]) {
     s_pair[part][t][0] = top;
-    s_pair[part][t][1] = sum;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s_pair[part][t][1 + i] = sum[i];
     __syncthreads();
     for (uint32_t half = kParts / 2u; half; half >>= 1) {
         if (part < half) {
-            const float r = s_pair[part + half][t][0], s = s_pair[part + half][t][1], to = fmaxf(top, r);
-            sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
+            const float r = s_pair[part + half][t][0], to = fmaxf(top, r);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                sum[i] = sum[i] * ref_scale(top, to) + s_pair[part + half][t][1 + i] * ref_scale(r, to);
+                s_pair[part][t][1 + i] = sum[i];
+            }
             top = to;
             s_pair[part][t][0] = top;
-            s_pair[part][t][1] = sum;
         }
         __syncthreads();
     }
@@ -186,12 +194,13 @@ __global__ __launch_bounds__(256) void df11_loss_first_kernel(TokenArgs a, const
     const float ref = ceilf((s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * kLog2eHi);
     a.ref[token] = fabsf(ref) < INFINITY ? ref : -INFINITY;
     a.sum[token] = 0.0f;
+    a.sum_rounded[token] = 0.0f;
 }
 
 // A piece's pairs joined to what the tokens have.  Where the reference moves, or a
 // panel has another, exponentials are brought to it.
 __global__ __launch_bounds__(1024) void df11_loss_piece_kernel(TokenArgs a, uint32_t first_piece) {
-    __shared__ float s_pair[kParts][kTokens][2];
+    __shared__ float s_pair[kParts][kTokens][3];
     __shared__ float s_to[kTokens];
     __shared__ uint32_t s_other[kTokens];
     const uint32_t t = threadIdx.x % kTokens, part = threadIdx.x / kTokens, token = blockIdx.x * kTokens + t;
@@ -200,11 +209,14 @@ __global__ __launch_bounds__(1024) void df11_loss_piece_kernel(TokenArgs a, uint
     const uint64_t step = 2ull * a.n_tokens;
     const float was = in ? a.ref[token] : -INFINITY;
     if (threadIdx.x < kTokens) s_other[threadIdx.x] = 0;
-    float top = was, sum = 0.0f;
+    const float *rounded = a.rounded + (in ? token : 0u);
+    float top = was, sum[2] = {0.0f, 0.0f};  // of the exponentials, and as they were rounded
     bool other = false;  // a reference that is not the token's
     for (uint32_t p = part; p < a.panels; p += kParts) {
-        const float r = st[p * step], s = st[p * step + 1u], to = fmaxf(top, r);
-        sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
+        const float r = st[p * step], s = st[p * step + 1u], s2 = rounded[p * static_cast<uint64_t>(a.n_tokens)];
+        const float to = fmaxf(top, r), old = ref_scale(top, to), f = ref_scale(r, to);
+        sum[0] = sum[0] * old + s * f;
+        sum[1] = sum[1] * old + s2 * f;
         top = to;
         other = other || (r != was && r != -INFINITY);
     }
@@ -213,7 +225,8 @@ __global__ __launch_bounds__(1024) void df11_loss_piece_kernel(TokenArgs a, uint
         // (the pairs of no class leave a token's first reference as it is)
         const float scale = first_piece ? 0.0f : ref_scale(was, top);
         a.ref[token] = top;
-        a.sum[token] = a.sum[token] * scale + sum;
+        a.sum[token] = a.sum[token] * scale + sum[0];
+        a.sum_rounded[token] = a.sum_rounded[token] * scale + sum[1];
         a.scale[token] = scale;
         s_to[t] = top;
     }
@@ -259,10 +272,10 @@ __global__ __launch_bounds__(1024) void df11_loss_tokens_kernel(TokenArgs a) {
     const bool in = token < a.n_tokens;
     const float *st = a.stats + 2u * (in ? token : 0u);
     const uint64_t step = 2ull * a.n_tokens;
-    float top = -INFINITY, sum = 0.0f;
+    float top = -INFINITY, sum[1] = {0.0f};
     for (uint32_t p = part; p < a.panels; p += kParts) {
         const float r = st[p * step], s = st[p * step + 1u], to = fmaxf(top, r);
-        sum = sum * ref_scale(top, to) + s * ref_scale(r, to);
+        sum[0] = sum[0] * ref_scale(top, to) + s * ref_scale(r, to);
         top = to;
     }
     join_pairs(s_pair, part, t, top, sum);
@@ -270,7 +283,7 @@ __global__ __launch_bounds__(1024) void df11_loss_tokens_kernel(TokenArgs a) {
     const TokenKind kind = kind_of(a.targets[token], a.ignore_index, a.classes);
     a.loss[token] = kind == kIgnored   ? 0.0f
                     : kind == kNoClass ? __builtin_nanf("")
-                                       : loss_of(others(top, sum, a.target_logit[token]));
+                                       : loss_of(others(top, sum[0], a.target_logit[token]));
 }
 
 struct GradRowsArgs {
@@ -280,7 +293,9 @@ struct GradRowsArgs {
     uint32_t cols;
 };
 
-// The loss and grad = sigma(u) (A / S - W_y): a workgroup a token.
+// The loss and grad = sigma(u) (A / S - W_y): a workgroup a token.  S is here the sum of
+// the rounded exponentials, which A adds too: where few classes have most of the
+// probability (and A is as large as W_y), their roundings cancel in the quotient.
 __global__ __launch_bounds__(256) void df11_loss_rows_kernel(GradRowsArgs a) {
     const uint32_t token = blockIdx.x;
     const int64_t target = a.t.targets[token];
@@ -289,7 +304,8 @@ __global__ __launch_bounds__(256) void df11_loss_rows_kernel(GradRowsArgs a) {
     if (kind == kScored) {
         const float sum = a.t.sum[token];
         u = others(a.t.ref[token], sum, a.t.target_logit[token]);
-        inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float rounded = a.t.sum_rounded[token];
+        inverse = rounded == 0.0f ? 0.0f : 1.0f / rounded;
     }
     if (blockIdx.y == 0 && threadIdx.x == 0)
         a.t.loss[token] = kind == kIgnored ? 0.0f : kind == kNoClass ? __builtin_nanf("") : loss_of(u);
@@ -378,7 +394,7 @@ __global__ __launch_bounds__(256) void df11_loss_grad_kernel(LossGradArgs a) {
 struct LossPlan {
     bool slots;         // the fused product
     uint32_t piece;     // classes of a piece (the last one may have fewer)
-    uint64_t weights, stats, logit, ref, sum, scale, kept, exps, split, end;
+    uint64_t weights, stats, rounded, logit, ref, sum, sum_rounded, scale, kept, exps, split, end;
 };
 
 // Classes of the piece that begins at class `from`.
@@ -419,6 +435,8 @@ bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan
         }
         p.ref = take(4ull * tokens);
         p.sum = take(4ull * tokens);
+        p.sum_rounded = take(4ull * tokens);
+        p.rounded = take(4ull * (most / 64) * tokens);
         p.scale = take(4ull * tokens);
         p.kept = take(2ull * tokens * cols);
         p.exps = take(2ull * tokens * most);
@@ -484,6 +502,8 @@ int loss_and_grad(const df11_device_stream *w, const uint16_t *x, uint64_t x_str
     int rc = decode_weights(&w, 1, at<void>(ws, p.weights), decoded, stream);
     t.ref = at<float>(ws, p.ref);
     t.sum = at<float>(ws, p.sum);
+    t.sum_rounded = at<float>(ws, p.sum_rounded);
+    t.rounded = at<float>(ws, p.rounded);
     t.scale = at<float>(ws, p.scale);
     t.exps = at<uint16_t>(ws, p.exps);
     if (!rc) {
@@ -507,6 +527,7 @@ int loss_and_grad(const df11_device_stream *w, const uint16_t *x, uint64_t x_str
         d.loss.stats = at<float>(ws, p.stats);
         d.loss.target_logit = at<float>(ws, p.logit);
         d.loss.ref = t.ref;
+        d.loss.rounded = at<float>(ws, p.rounded);
         d.loss.exps = t.exps;
         d.loss.exps_stride = n;
         d.loss.first_class = from;
