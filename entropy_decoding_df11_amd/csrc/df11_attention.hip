@@ -263,18 +263,25 @@ struct Rows {
         }
     }
 
-    // Sends for the queries.  (Rows past the last one have another's: their sums go
-    // nowhere.)
+    // Token and query head of this lane's row of row tile i.  Rows past the sequence's
+    // last one have that one's: it is of this tile, so that out may lie on q (another
+    // tile's rows may have been written), and what it sees and scores moves no
+    // reference that it does not move itself.  Their sums go nowhere.
+    __device__ __forceinline__ void query_of(int i, uint32_t &token, uint32_t &head) const {
+        const uint32_t at = min(p.tile * a.tile_rows + row0 + 16u * i + l16, p.s.rows * a.group - 1u);
+        token = at / a.group;
+        head = p.head * a.group + at % a.group;
+    }
+
+    // Sends for the queries.
     __device__ __forceinline__ void load_queries() {
         const uint32_t last_chunk = a.dim / 8u - 1u;
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             uint32_t token, head;
-            row_of(a, p, row0 + 16u * i + l16, token, head);
-            const bool there = token < p.s.rows;
-            const T *row = static_cast<const T *>(a.q) +
-                           (static_cast<uint64_t>(p.s.begin) + (there ? token : 0u)) * a.q_stride +
-                           (there ? head : p.head * a.group) * a.q_head_stride;
+            query_of(i, token, head);
+            const T *row = static_cast<const T *>(a.q) + (static_cast<uint64_t>(p.s.begin) + token) * a.q_stride +
+                           head * a.q_head_stride;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
                 q[i][kk] = *reinterpret_cast<const Vec *>(row + 8u * min(4u * kk + quarter, last_chunk));
@@ -330,9 +337,8 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             uint32_t token, head;
-            row_of(a, p, row0 + 16u * i + l16, token, head);
-            const uint8_t *mask_row =
-                a.mask ? a.mask + (p.s.begin + static_cast<uint64_t>(min(token, p.s.rows - 1u))) * a.mask_stride : nullptr;
+            query_of(i, token, head);
+            const uint8_t *mask_row = a.mask ? a.mask + (p.s.begin + static_cast<uint64_t>(token)) * a.mask_stride : nullptr;
             bits[i] = seen(token, mask_row, key0, valid);
         }
     }
