@@ -191,6 +191,10 @@ def _launch_attention(dev, q, k_cache, v_cache, page_table, starts, lengths, mas
     m_ptr = m0 = cols = 0
     if mask is not None:
         m_ptr, m0, cols = mask.data_ptr(), mask.stride(0), mask.shape[1]
+        if not cols:
+            # (a tensor without elements has no address, which would be no mask: any
+            # other does, since none of it is read)
+            m_ptr, m0 = starts.data_ptr(), 0
     a = _lib.ATTENTION.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), m_ptr, q0, q1, o0, o1, m0,
                             cols, q.shape[1], scale, 0)
     lib = _lib.load()
@@ -211,7 +215,7 @@ def tree_attention(q: "torch.Tensor", k_cache: "torch.Tensor", v_cache: "torch.T
     and values (df11_tree_attention): softmax(scale q k^T) v over what each sees,
     which is its sequence's cached places, and of its new tokens those up to
     itself, or with mask, a bool or uint8 (tokens, columns) tensor, those whose
-    column is set (column j: the sequence's j-th new token).
+    column is set (column j: the sequence's j-th new token; none past the last).
 
     q: (tokens, heads, head_dim) of the cache's type, heads a multiple of the
     cache's (query head h reads key head h // (heads / kv_heads)), rows 16-byte

@@ -1214,7 +1214,7 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     if (rc || b->n_tokens == 0 || b->n_seqs == 0) return rc;
     // Outputs stay clear of everything that is read, but out may lie exactly on q.
     const uint64_t lse_span = a->lse ? 4ull * b->n_tokens * a->q_heads : 0;
-    const uint64_t mask_span = a->mask ? (b->n_tokens - 1ull) * a->mask_stride + a->mask_cols : 0;
+    const uint64_t mask_span = a->mask && a->mask_cols ? (b->n_tokens - 1ull) * a->mask_stride + a->mask_cols : 0;
     const bool on_q = a->q == a->out && a->q_stride == a->out_stride && a->q_head_stride == a->out_head_stride;
     const void *outs[] = {a->out, a->lse, workspace};
     uint64_t spans[] = {out_span, lse_span, 0};

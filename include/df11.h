@@ -825,7 +825,8 @@ int df11_append_kv(const df11_kv_cache *cache, const df11_kv_batch *batch, const
  *   lse          n_tokens x q_heads floats, or NULL: the natural logarithm of the
  *                sum of exp(scale q . k) over what the query sees
  *   mask         n_tokens x mask_cols bytes, mask_stride from token to token, or
- *                NULL.  Every query sees the lengths[s] cached places of its
+ *                NULL (with mask_cols 0 any other address, of which nothing is
+ *                read: no new token sees another or itself).  Every query sees the lengths[s] cached places of its
  *                sequence; of the sequence's new tokens it sees the j-th if byte
  *                j of its row is not zero (none from mask_cols on), or without a
  *                mask those up to itself
