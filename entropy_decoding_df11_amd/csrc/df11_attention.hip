@@ -5,9 +5,15 @@
 // in one pass over the places, with the softmax's running maximum and sum: for
 // a row's reference m, w_j = 2^(c (s_j - m)) with c = scale log2(e), and what
 // has been summed is multiplied by 2^(c (m - m')) when the reference moves to
-// m'.  It moves only where a score passes it by 2^8, so that blocks without a
-// new maximum need nothing across lanes; w is at most 2^8, and its relative
-// precision does not depend on the reference.
+// m'.  It moves only where a weight passes what the type has room for, so that
+// blocks without a new maximum need nothing across lanes.  BF16 has float's range:
+// references are the largest score, weights pass them by 2^8 at most, and a weight's
+// relative rounding depends on nothing.  FP16 loses bits of a weight below 2^-14 and
+// the weight below 2^-25: references lie 2^7 below the largest score and weights
+// reach 2^15, so that weights keep their precision down to 2^-21 of the largest
+// score's when the reference was taken, and from there on are off by 2^-32 of it at
+// most.  (Without the 2^7 a place 17 nats ahead left what others alike had added
+// off by 44%.)
 //
 // A query head's rows of one key head are the columns of the products, so that
 // all heads of a group read a place once:
@@ -229,8 +235,12 @@ __device__ __forceinline__ void row_of(const AttentionArgs &a, const Part &p, ui
     head = p.head * a.group + at % a.group;
 }
 
-// Weights that a reference allows before it moves.
-constexpr float kRoom = 256.0f;
+// Weights that a reference allows before it moves, and how far, in powers of two, it
+// lies below the largest score.
+template <typename T>
+constexpr float kRoom = std::is_same_v<T, fp16_t> ? 32768.0f : 256.0f;
+template <typename T>
+constexpr float kLead = std::is_same_v<T, fp16_t> ? 7.0f : 0.0f;
 
 // What a head's chunks past head_dim read.
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
@@ -343,7 +353,7 @@ struct Rows {
         }
     }
 
-    // Scores to weights (in s, and rounded in w).  A weight past 2^8 (infinite
+    // Scores to weights (in s, and rounded in w).  A weight past the room (infinite
     // while there is no reference) says that the reference has to move: then
     // they are taken again, from the new one.
     __device__ __forceinline__ void weigh(floatx4 (&s)[M][2], Vec (&w)[M]) {
@@ -356,14 +366,15 @@ struct Rows {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][t][e] = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -ref[i]));
             // (all NaN: no reference, and nothing seen)
-            moves |= !(largest(x[i]) <= kRoom);
+            moves |= !(largest(x[i]) <= kRoom<T>);
         }
         if (__ballot(moves)) {
 #pragma unroll
             for (int i = 0; i < M; ++i) {
                 float top = largest(s[i]);
                 top = fmaxf(top, __shfl_xor(top, 16));
-                const float to = fmaxf(ref[i], fmaxf(top, __shfl_xor(top, 32)) * a.c), f = weight_of(ref[i], to);
+                const float to = fmaxf(ref[i], fmaxf(top, __shfl_xor(top, 32)) * a.c - kLead<T>);
+                const float f = weight_of(ref[i], to);
                 const float base = to == -INFINITY ? 0.0f : to;
                 ref[i] = to;
                 l[i] *= f;
