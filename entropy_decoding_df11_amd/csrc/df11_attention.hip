@@ -101,7 +101,7 @@ struct AttentionArgs {
     uint64_t q_stride, q_head_stride, out_stride, out_head_stride, mask_stride;
     uint64_t capacity;    // places of a sequence's pages
     float *parts;         // [workgroup][2][row][dim]
-    float *stats;         // [workgroup][2][row][2]: reference times c, sum
+    float *stats;         // [workgroup][2][row][4]: reference times c, sums of the rounded weights and of them unrounded
     Cut *cut;             // [workgroup]; null where no tile is ever cut
     uint32_t page_magic, page_shift;  // df11::page_of
     float c;              // scale log2(e)
@@ -260,7 +260,14 @@ struct Rows {
 
     Vec q[M][KK];
     floatx4 o[M][kTilesD];
-    float ref[M], l[M];  // a lane's row: its reference times c, and this lane's part of the sum
+    // A lane's row: its reference times c; the sum of its weights as they were rounded,
+    // from a product with ones (four times the same); and this lane's part of their sum
+    // unrounded, which only lse needs.  The quotient takes the first: its roundings are
+    // the numerator's, and cancel as far as values are alike.  (The product adds to it
+    // as to the numerator, in 3% of a call's time for many rows and none for few; rounded
+    // weights added one by one take 6 to 7%.)
+    float ref[M], l[M];
+    floatx4 total[M];
 
     __device__ __forceinline__ Rows(const AttentionArgs &args, const Part &part, uint32_t first_row)
         : a(args), p(part), row0(first_row), lane(threadIdx.x & 63u), quarter(lane >> 4), l16(lane & 15u) {
@@ -268,6 +275,7 @@ struct Rows {
         for (int i = 0; i < M; ++i) {
             ref[i] = -INFINITY;
             l[i] = 0.0f;
+            total[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int d = 0; d < kTilesD; ++d) o[i][d] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
         }
@@ -357,6 +365,7 @@ struct Rows {
     // while there is no reference) says that the reference has to move: then
     // they are taken again, from the new one.
     __device__ __forceinline__ void weigh(floatx4 (&s)[M][2], Vec (&w)[M]) {
+        const T one = static_cast<T>(1.0f);
         floatx4 x[M][2];
         bool moves = false;
 #pragma unroll
@@ -378,6 +387,7 @@ struct Rows {
                 const float base = to == -INFINITY ? 0.0f : to;
                 ref[i] = to;
                 l[i] *= f;
+                total[i] *= f;
 #pragma unroll
                 for (int d = 0; d < kTilesD; ++d) o[i][d] *= f;
 #pragma unroll
@@ -388,8 +398,9 @@ struct Rows {
         }
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            l[i] += ((x[i][0][0] + x[i][0][1]) + (x[i][0][2] + x[i][0][3])) +
-                    ((x[i][1][0] + x[i][1][1]) + (x[i][1][2] + x[i][1][3]));
+            if (a.lse)
+                l[i] += ((x[i][0][0] + x[i][0][1]) + (x[i][0][2] + x[i][0][3])) +
+                        ((x[i][1][0] + x[i][1][1]) + (x[i][1][2] + x[i][1][3]));
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -397,6 +408,7 @@ struct Rows {
                     s[i][t][e] = x[i][t][e];
                     w[i][4 * t + e] = static_cast<T>(x[i][t][e]);
                 }
+            total[i] = mfma(Vec{one, one, one, one, one, one, one, one}, w[i], total[i]);
         }
     }
 
@@ -817,19 +829,23 @@ struct ManyWave : Rows<T, KK, M> {
 // workgroup's slot.
 template <typename T, int KK, int M, int WR, int WK>
 __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &p, Rows<T, KK, M> &w, uint32_t wave,
-                                            uint8_t *lds, float (*s_stats)[16][2], uint64_t slot) {
+                                            uint8_t *lds, float (*s_stats)[16][3], uint64_t slot) {
     constexpr int DP = 32 * KK, kStride = DP + 4;
     constexpr uint32_t kWaveFloats = 16 * kStride;
     float *sums = reinterpret_cast<float *>(lds);
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        float l = w.l[i] + __shfl_xor(w.l[i], 16);
-        l += __shfl_xor(l, 32);
+        float total = w.total[i][0], l = 0.0f;
+        if (a.lse) {
+            l = w.l[i] + __shfl_xor(w.l[i], 16);
+            l += __shfl_xor(l, 32);
+        }
         // (every wave's reads of the places, and of the row tile before, are back)
         __syncthreads();
         if (w.quarter == 0) {
             s_stats[wave][w.l16][0] = w.ref[i];
-            s_stats[wave][w.l16][1] = l;
+            s_stats[wave][w.l16][1] = total;
+            s_stats[wave][w.l16][2] = l;
         }
 #pragma unroll
         for (int d = 0; d < Rows<T, KK, M>::kTilesD; ++d)
@@ -841,7 +857,7 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
             uint32_t token, head;
             row_of(a, p, row, token, head);
             if (token >= p.s.rows || d >= a.dim) continue;
-            float top = -INFINITY, total = 0.0f, sum[8] = {};
+            float top = -INFINITY, total = 0.0f, whole = 0.0f, sum[8] = {};
 #pragma unroll
             for (uint32_t x = 0; x < WK; ++x) top = fmaxf(top, s_stats[x * WR + wr][r][0]);
 #pragma unroll
@@ -850,6 +866,7 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
                 const float f = weight_of(s_stats[other][r][0], top);
                 if (adds_nothing(f, s_stats[other][r][1])) continue;
                 total += f * s_stats[other][r][1];
+                whole += f * s_stats[other][r][2];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += f * sums[other * kWaveFloats + r * kStride + d + e];
             }
@@ -861,16 +878,13 @@ __device__ __forceinline__ void finish_part(const AttentionArgs &a, const Part &
                 store_vec<T, 8>(static_cast<T *>(a.out) + t * a.out_stride + head * a.out_head_stride + d, sum);
                 if (a.lse && d == 0)
                     a.lse[t * (a.kv_heads * a.group) + head] =
-                        total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
+                        total == 0.0f ? -INFINITY : (top + log2f(whole)) * 0.69314718055994531f;
             } else {
                 float *to = a.parts + (slot * a.tile_rows + row) * a.dim + d;
                 store_vec<float, 4>(to, *reinterpret_cast<float(*)[4]>(&sum[0]));
                 store_vec<float, 4>(to + 4, *reinterpret_cast<float(*)[4]>(&sum[4]));
-                if (d == 0) {
-                    float *st = a.stats + (slot * a.tile_rows + row) * 2u;
-                    st[0] = top;
-                    st[1] = total;
-                }
+                const float st[4] = {top, total, whole, 0.0f};
+                if (d == 0) store_vec<float, 4>(a.stats + (slot * a.tile_rows + row) * 4u, st);
             }
         }
     }
@@ -954,7 +968,7 @@ void df11_attention_few_kernel(AttentionArgs a) {
     constexpr uint32_t kWaves = kFewWaves<KK>, kWaveBytes = 2u * W::kVBytes;
     static_assert(kWaveBytes >= 16 * (W::DP + 4) * 4, "a row tile's sums fit a wave's buffers");
     __shared__ __align__(1024) uint8_t s_mem[kWaves * kWaveBytes];
-    __shared__ float s_stats[kWaves][16][2];
+    __shared__ float s_stats[kWaves][16][3];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
     for_each_part<64 * kWaves>(a, [&](const Part &p, uint64_t slot) {
         W w(a, p, s_mem + wave * kWaveBytes);
@@ -970,7 +984,7 @@ void df11_attention_many_kernel(AttentionArgs a) {
     using W = ManyWave<T, KK, M, WR, WK, kWhole>;
     constexpr uint32_t kSums = WR * WK * 16 * (W::DP + 4) * 4;
     __shared__ __align__(1024) uint8_t s_mem[3 * W::kStage > kSums ? 3 * W::kStage : kSums];
-    __shared__ float s_stats[WR * WK][16][2];
+    __shared__ float s_stats[WR * WK][16][3];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
     for_each_part<64 * WR * WK>(a, [&](const Part &p, uint64_t slot) {
         W w(a, p, wave, s_mem);
@@ -983,7 +997,7 @@ void df11_attention_many_kernel(AttentionArgs a) {
 // the workgroup that take the vector's parts together, a stretch each, in the
 // order of the places.
 template <typename T, uint32_t kWaves>
-__device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c, uint32_t at, float (*s_sum)[10][64]) {
+__device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c, uint32_t at, float (*s_sum)[11][64]) {
     const uint32_t chunks = a.dim / 8u, row = at / chunks, d = 8u * (at % chunks), lane = threadIdx.x & 63u;
     const uint32_t wave = kWaves > 1 ? threadIdx.x / 64u : 0u;
     const uint32_t in_tiles = c.tile * a.tile_rows + row, token = in_tiles / a.group;
@@ -992,13 +1006,13 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
     const auto slot_of = [&](uint32_t r) { return (2ull * r + (r == c.run ? c.slot : 0u)) * a.tile_rows + in; };
     const uint32_t each = (c.last - c.run + kWaves) / kWaves;
     const uint32_t begin = c.run + wave * each, end = min(begin + each, c.last + 1u);
-    float top = -INFINITY, total = 0.0f, sum[8] = {};
+    float top = -INFINITY, total = 0.0f, whole = 0.0f, sum[8] = {};
     for (uint32_t r = begin; r < end; r += kJoinAtOnce) {
-        float st[kJoinAtOnce][2], v[kJoinAtOnce][8];
+        float st[kJoinAtOnce][4], v[kJoinAtOnce][8];
 #pragma unroll
         for (uint32_t k = 0; k < kJoinAtOnce; ++k) {  // (past the last one again, not added)
             const uint64_t slot = slot_of(min(r + k, end - 1u));
-            load_vec<float, 2>(a.stats + slot * 2u, st[k]);
+            load_vec<float, 4>(a.stats + slot * 4u, st[k]);
             load_vec<float, 4>(a.parts + slot * a.dim + d, *reinterpret_cast<float(*)[4]>(&v[k][0]));
             load_vec<float, 4>(a.parts + slot * a.dim + d + 4, *reinterpret_cast<float(*)[4]>(&v[k][4]));
         }
@@ -1007,6 +1021,7 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
         for (uint32_t k = 0; k < kJoinAtOnce; ++k) to = fmaxf(to, st[k][0]);
         const float old = weight_of(top, to);
         total *= old;
+        whole *= old;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] *= old;
 #pragma unroll
@@ -1014,6 +1029,7 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
             const float f = weight_of(st[k][0], to);
             if (r + k >= end || adds_nothing(f, st[k][1])) continue;
             total += f * st[k][1];
+            whole += f * st[k][2];
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += f * v[k][e];
         }
@@ -1023,6 +1039,7 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
         __syncthreads();  // (the vectors before have been read)
         s_sum[wave][8][lane] = top;
         s_sum[wave][9][lane] = total;
+        s_sum[wave][10][lane] = whole;
 #pragma unroll
         for (int e = 0; e < 8; ++e) s_sum[wave][e][lane] = sum[e];
         __syncthreads();
@@ -1031,10 +1048,12 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
         for (uint32_t w = 1; w < kWaves; ++w) {
             const float to = fmaxf(top, s_sum[w][8][lane]), old = weight_of(top, to), f = weight_of(s_sum[w][8][lane], to);
             total *= old;
+            whole *= old;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] *= old;
             if (!adds_nothing(f, s_sum[w][9][lane])) {
                 total += f * s_sum[w][9][lane];
+                whole += f * s_sum[w][10][lane];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += f * s_sum[w][e][lane];
             }
@@ -1050,7 +1069,7 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
     store_vec<T, 8>(static_cast<T *>(a.out) + t * a.out_stride + head * a.out_head_stride + d, sum);
     if (a.lse && d == 0)
         a.lse[t * (a.kv_heads * a.group) + head] =
-            total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
+            total == 0.0f ? -INFINITY : (top + log2f(whole)) * 0.69314718055994531f;
 }
 
 // Joins the parts of the tiles that runs begin and leave to others.  Every
@@ -1060,7 +1079,7 @@ __device__ __forceinline__ void join_vector(const AttentionArgs &a, const Cut &c
 template <typename T>
 __global__ __launch_bounds__(256) void df11_attention_join_kernel(AttentionArgs a) {
     __shared__ uint32_t s_count[2][4], s_cut[2][kMaxCuts];
-    __shared__ float s_sum[4][10][64];
+    __shared__ float s_sum[4][11][64];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
     uint32_t found[2] = {0, 0};  // of many parts, of few
     for (uint32_t at = 0; at < a.workgroups; at += 256u) {
@@ -1169,7 +1188,7 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     p.workgroups = static_cast<uint32_t>(std::min<uint64_t>({static_cast<uint64_t>(cus) * per_cu, units, kMaxCuts}));
     const uint64_t slots = capacity > p.step ? 2ull * p.workgroups * p.tile_rows : 0;
     p.parts = round_up(slots * c.head_dim * 4, 256);
-    p.stats = round_up(slots * 8, 256);
+    p.stats = round_up(slots * 16, 256);
     p.cut = slots ? round_up(p.workgroups * sizeof(Cut), 256) : 0;
     return DF11_OK;
 }

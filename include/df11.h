@@ -857,8 +857,8 @@ uint64_t df11_tree_attention_workspace(const df11_kv_cache *cache, const df11_kv
  * and values:
  *   out = sum over the visible places j of p_j v_j,  p = softmax(scale q . k_j)
  * Scores, the softmax's maximum and sum, and out's sums are float; p is rounded
- * to the cache's type for its product with v (the matrix cores' operand type),
- * not for the softmax's sum; out is rounded once.  (That rounding is 2^-8 of p at
+ * to the cache's type for its product with v (the matrix cores' operand type), and
+ * out is divided by the sum of p as rounded (lse has it unrounded) and rounded once.  (That rounding is 2^-8 of p at
  * most in DF11_BF16 and 2^-11 in DF11_FP16, there also up to 2^-32 of the largest
  * score's p: over 2^21 places as much as the result's own.)  A query that sees nothing
  * gets zeros and an lse of minus infinity.  What a place holds reaches only the
