@@ -259,7 +259,10 @@ __device__ __forceinline__ TokenKind kind_of(int64_t target, int64_t ignore_inde
 }
 
 // The others against the target (u above); nothing else in the vocabulary: -inf.
+// (The target is in no sum: where its logit is not finite, which an infinity or a NaN
+// in x always makes it, that has to be said here.)
 __device__ __forceinline__ float others(float ref, float sum, float target_logit) {
+    if (!(fabsf(target_logit) < INFINITY)) return __builtin_nanf("");
     return sum == 0.0f ? -INFINITY : ref * kLn2 + logf(sum) - target_logit;
 }
 

@@ -698,8 +698,9 @@ uint64_t df11_cross_entropy_workspace(const df11_device_stream *w, uint32_t n_to
  *   workspace    device, 256-byte aligned, df11_cross_entropy_workspace bytes;
  *                holds nothing between calls, but calls that overlap in time need
  *                one each
- * A token whose x holds an infinity or a NaN, or whose logits overflow, gets NaN;
- * others are not touched by it.  Results do not change from run to run; calls of
+ * A token whose x holds an infinity or a NaN, or whose target's logit overflows, or
+ * another's to plus infinity, gets NaN (one at minus infinity has p = 0); other
+ * tokens are not touched by it.  Results do not change from run to run; calls of
  * one stream may overlap in time.  With no tokens only total and count are
  * written.
  * Errors: DF11_E_INVALID_ARG, DF11_E_BAD_STREAM, DF11_E_TOO_LARGE,
