@@ -289,6 +289,10 @@ __global__ __launch_bounds__(1024) void df11_loss_tokens_kernel(TokenArgs a) {
                                        : loss_of(others(top, sum[0], a.target_logit[token]));
 }
 
+// The gradient of an ignored token in every element, and no other's in any: what the
+// loss's own gradient holds there, which need not be finite, reaches nothing.
+constexpr float kNothing = -0.0f;
+
 struct GradRowsArgs {
     TokenArgs t;
     const uint16_t *kept;  // the targets' rows, [token][cols]
@@ -321,10 +325,13 @@ __global__ __launch_bounds__(256) void df11_loss_rows_kernel(GradRowsArgs a) {
         if (kind == kScored) {
             load_vec<bf16_t, 8>(reinterpret_cast<const bf16_t *>(a.kept) + static_cast<uint64_t>(token) * a.cols + c, wy);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = sigma * (v[i] * inverse - wy[i]);
+            for (int i = 0; i < 8; ++i) {
+                v[i] = sigma * (v[i] * inverse - wy[i]);
+                if (v[i] == 0.0f) v[i] = 0.0f;  // (never kNothing)
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = kind == kIgnored ? 0.0f : __builtin_nanf("");
+            for (int i = 0; i < 8; ++i) v[i] = kind == kIgnored ? kNothing : __builtin_nanf("");
         }
         store_vec<float, 4>(g, *reinterpret_cast<float(*)[4]>(&v[0]));
         store_vec<float, 4>(g + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
@@ -379,7 +386,8 @@ __global__ __launch_bounds__(256) void df11_loss_grad_kernel(LossGradArgs a) {
         load_vec<float, 4>(from, *reinterpret_cast<float(*)[4]>(&v[0]));
         load_vec<float, 4>(from + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= g;
+        for (int i = 0; i < 8; ++i)
+            v[i] = __float_as_uint(v[i]) == __float_as_uint(kNothing) ? 0.0f : v[i] * g;
         const uint64_t at = token * a.dx_stride + c;
         if (a.vec && a.dx_dtype == DF11_BF16) {
             store_vec<bf16_t, 8>(static_cast<bf16_t *>(a.dx) + at, v);

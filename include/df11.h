@@ -661,7 +661,7 @@ int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_str
  *   loss = log(sum over v of exp(z_v)) - z_target
  *   grad = d loss / dx = sum over v of p_v W_v - W_target,  p = softmax(z)
  *   targets        n_tokens int64.  A token whose target is ignore_index has a
- *                  loss and a gradient of zero; one whose target is no class
+ *                  loss of zero and a gradient of minus zero; one whose target is no class
  *                  otherwise, NaN
  *   loss           n_tokens floats
  *   total          a float, or NULL: the sum of loss over the tokens, divided by
@@ -711,7 +711,8 @@ int df11_cross_entropy(const df11_device_stream *w, const uint16_t *x, uint64_t 
 
 /* x's gradient from the one that df11_cross_entropy kept: dx = g grad, rounded
  * once, where a token's g is dy[token * dy_stride], or with count (the call's, of a
- * mean) that over count (zero if it is zero).  dy_stride 0: one
+ * mean) that over count (zero if it is zero).  An element of grad that is minus zero
+ * (ignored tokens' are, no other's) gives zero whatever g is.  dy_stride 0: one
  * dy for all tokens.  dx: n_tokens x in_features of dx_dtype (DF11_BF16 or
  * DF11_FP32), dx_stride elements from row to row, overlapping nothing else.
  * Errors: DF11_E_INVALID_ARG, DF11_E_TOO_LARGE, DF11_E_HIP. */
