@@ -905,7 +905,7 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
         units = scan_units<THREADS>(a, at, units, shape, n, mine, s_part);
     }
     const bool none = units == 0 || units >= df11::kMaxUnits;
-    const uint32_t all = static_cast<uint32_t>(units), runs = none ? 0u : df11::runs_of(all, a.workgroups);
+    const uint32_t all = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(units)), runs = none ? 0u : df11::runs_of(all, a.workgroups);
     // What the second kernel finds of a run: the tile that it begins and leaves.
     if (a.cut && blockIdx.x >= runs && threadIdx.x == 0) a.cut[blockIdx.x].last = 0;
     if (blockIdx.x >= runs) return;
@@ -921,41 +921,45 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
         if (u >= mine - n && u < mine) s_found = Found{static_cast<uint32_t>(mine - n), at + threadIdx.x, shape};
     }
     __syncthreads();
-    uint32_t seq = __builtin_amdgcn_readfirstlane(s_found.seq), first = __builtin_amdgcn_readfirstlane(s_found.first);
+    const uint32_t first = __builtin_amdgcn_readfirstlane(s_found.first);
     bool begun = true;  // the run's first tile may have begun in the run before
     bool left = false;
     Part p;
     p.s = s_found.shape;
+    p.seq = __builtin_amdgcn_readfirstlane(s_found.seq);
+    const uint32_t one = static_cast<uint32_t>(df11::units_before(p.s, p.s.tiles));  // of a key head
+    p.head = (u - first) / one;
+    p.tile = df11::tile_of(p.s, u - first - p.head * one);
+    uint32_t tile_first = first + p.head * one + static_cast<uint32_t>(df11::units_before(p.s, p.tile));
     while (u < end) {
-        const uint32_t one = p.s.tiles ? static_cast<uint32_t>(df11::units_before(p.s, p.s.tiles)) : 0u;
-        const uint32_t here = one * a.kv_heads;
-        if (u >= first + here) {
-            first += here;
-            if (++seq == a.b.n_seqs) break;
-            p.s = shape_of(a, seq);
-            continue;
-        }
-        p.seq = seq;
-        p.head = (u - first) / one;
-        const uint32_t head_first = first + p.head * one;
-        p.tile = df11::tile_of(p.s, u - head_first);
-        const uint32_t tile_first = head_first + static_cast<uint32_t>(df11::units_before(p.s, p.tile));
         const uint32_t tile_end = tile_first + df11::tile_units(p.s, p.tile), to = min(end, tile_end);
         p.step0 = df11::steps_before(p.s, u - tile_first);
         p.step1 = df11::steps_before(p.s, to - tile_first);
         u = to;
-        if (p.step0 == p.step1) continue;
-        p.plain = df11::tile_plain(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
-        p.limit = df11::tile_places(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
-        p.whole = p.step0 == 0 && to == tile_end;
-        if (a.cut && p.step0 == 0 && !p.whole) {
-            left = true;
-            if (threadIdx.x == 0)
-                a.cut[run] = Cut{p.s.begin, p.s.rows, p.head, p.tile, run, df11::run_of(tile_end - 1u, all, runs),
-                                 begun ? 0u : 1u, 0u};
+        if (p.step0 != p.step1) {
+            p.plain = df11::tile_plain(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
+            p.limit = df11::tile_places(p.s, p.tile, a.tile_rows, a.group, a.mask != nullptr);
+            p.whole = p.step0 == 0 && to == tile_end;
+            if (a.cut && p.step0 == 0 && !p.whole) {
+                left = true;
+                if (threadIdx.x == 0)
+                    a.cut[run] = Cut{p.s.begin, p.s.rows, p.head, p.tile, run, df11::run_of(tile_end - 1u, all, runs),
+                                     begun ? 0u : 1u, 0u};
+            }
+            f(p, 2ull * run + (begun ? 0u : 1u));
+            begun = false;
         }
-        f(p, 2ull * run + (begun ? 0u : 1u));
-        begun = false;
+        // The next tile, of the next key head, of the next sequence that has one.
+        tile_first = tile_end;
+        if (++p.tile < p.s.tiles) continue;
+        p.tile = 0;
+        if (++p.head < a.kv_heads) continue;
+        p.head = 0;
+        if (u == end) break;
+        do {
+            if (++p.seq == a.b.n_seqs) return;  // (never: units are left)
+            p.s = shape_of(a, p.seq);
+        } while (!p.s.tiles);
     }
     if (a.cut && !left && threadIdx.x == 0) a.cut[run].last = 0;
 }

@@ -9,7 +9,11 @@
 // them, whatever the lengths are: a run may begin and end inside a tile, whose
 // parts the second kernel joins.  With a mask every tile has all of a sequence's
 // steps; without one the later tiles see more, and a tile's steps are a bound
-// whose sums have a closed form (at most two steps too many).  A tile counts some
+// whose sums have a closed form: at most one step too many, and for a sequence's last
+// tile, which may not be full, as many more as a full one has of its own.  (With the
+// tiles of a step rounded down, as they were for groups that do not divide a tile's
+// rows, 10000 tokens of groups of 3 had 7021 steps for 4720: 4000 after 4000, three to
+// a key head, 402 us and now 353; 8000 after 100, five to a key head, 294 and 249.)  A tile counts some
 // units more, before its steps, for what it takes beside them (its queries, the
 // first loads that nothing hides, the end of its sums): a run that has only those
 // leaves the tile to the next one.
@@ -50,11 +54,12 @@ struct SeqShape {
     uint32_t places;  // places in its pages, length + tokens at most
     uint32_t tiles;
     uint32_t first;   // steps of a tile before what the tiles add
-    uint32_t each;    // tiles that add one step, or
-    uint32_t more;    // steps that each tile adds
+    uint32_t each;    // tiles that add `more` steps together: up to tile t
+    uint32_t more;    // (t + 1) more / each, rounded up; 0: none
     uint32_t extra;   // units of a tile before its steps
 };
 
+// (tile_rows is a power of two.)
 constexpr SeqShape seq_shape(int32_t begin, int32_t end, int32_t length, uint32_t n_tokens, uint64_t capacity,
                              uint32_t group, uint32_t tile_rows, uint32_t step, uint32_t extra, bool masked) {
     SeqShape s{begin, 0, 0, 0, 0, 0, 0, 1, 0, extra};
@@ -66,20 +71,18 @@ constexpr SeqShape seq_shape(int32_t begin, int32_t end, int32_t length, uint32_
     const uint64_t all = static_cast<uint64_t>(s.length) + s.tokens;
     s.places = static_cast<uint32_t>(all < capacity ? all : capacity);
     s.tiles = static_cast<uint32_t>((static_cast<uint64_t>(s.rows) * group + tile_rows - 1) / tile_rows);
-    if (masked || capacity <= step || s.tiles <= 1u) {
+    if (masked || capacity <= step || s.tiles <= 1u || all > capacity) {
+        // (all > capacity: tokens that have no place, which no closed form is worth)
         s.first = (s.places + step - 1) / step;
         if (!s.first) s.first = 1;  // (no pages: its rows are still written)
     } else {
-        // Tile t ends with token (t + 1) tile_rows / group, rounded up.
-        const uint32_t held = s.length < s.places ? s.length : s.places;
-        const uint64_t tokens = static_cast<uint64_t>(step) * group;  // rows of a step's tokens
-        s.first = (held + step - 1) / step;
-        if (tokens >= tile_rows) {
-            s.each = static_cast<uint32_t>(tokens / tile_rows);
-            s.more = 1;
-        } else {
-            s.more = static_cast<uint32_t>((tile_rows + tokens - 1) / tokens);
-        }
+        // Tile t ends with token (t + 1) tile_rows / group, rounded up, and has that
+        // many places more than are held: so many over `step` steps, rounded up.
+        const uint32_t tokens = step * group;  // rows of a step's tokens
+        const uint32_t lowest = tokens & (0u - tokens), common = lowest < tile_rows ? lowest : tile_rows;
+        s.first = (s.length + step - 1) / step;
+        s.each = tokens / common;
+        s.more = tile_rows / common;
     }
     return s;
 }
@@ -87,13 +90,20 @@ constexpr SeqShape seq_shape(int32_t begin, int32_t end, int32_t length, uint32_
 // Units of the tiles before tile t of one key head, and of tile t.
 constexpr uint64_t units_before(const SeqShape &s, uint32_t t) {
     const uint64_t all = static_cast<uint64_t>(t) * (s.first + s.extra);
-    if (!s.more) return all;
-    const uint64_t whole = t / s.each, rest = t % s.each;
-    // 1 + 1 + .. (each times) + 2 + 2 + ..
-    return all + s.more * (s.each * (whole * (whole + 1) / 2) + rest * (whole + 1));
+    // Of each round of tiles' steps the i-th is one that all have from i each / more
+    // on: 1 + 1 + .. (each times) + 2 + 2 + .. from there.
+    uint64_t steps = 0;
+    for (uint32_t i = 0; i < s.more; ++i) {
+        const uint32_t skip = i ? i * s.each / s.more : 0u;
+        if (t <= skip) break;
+        const uint64_t whole = (t - skip) / s.each, rest = (t - skip) % s.each;
+        steps += s.each * (whole * (whole + 1) / 2) + rest * (whole + 1);
+    }
+    return all + steps;
 }
 constexpr uint32_t tile_units(const SeqShape &s, uint32_t t) {
-    return s.extra + s.first + (s.more ? s.more * (t / s.each + 1) : 0u);
+    return s.extra + s.first +
+           (s.more ? static_cast<uint32_t>(((static_cast<uint64_t>(t) + 1) * s.more + s.each - 1) / s.each) : 0u);
 }
 
 // Steps of a tile before its unit i.

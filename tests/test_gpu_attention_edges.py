@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from test_gpu_attention import DEV, Case, tree  # noqa: E402
+from test_gpu_attention import DEV, E, Case, tree  # noqa: E402
 
 
 # tiles of 16, 64, 128 and 256 rows, the last one of a sequence with rows to spare, some cut over workgroups
@@ -38,3 +38,28 @@ def test_outputs_on_their_queries(heads, kv_heads, dim, lengths, tokens, masked,
 def test_tiles_with_rows_to_spare(heads, kv_heads, dim, lengths, tokens, masked):
     case = Case(lengths, tokens, torch.bfloat16, heads, kv_heads, dim, seed=21)
     case.check(mask=tree(case) if masked else None)
+
+
+@pytest.mark.parametrize("group", [3, 5, 7])
+@pytest.mark.parametrize("lengths,tokens", [([100], [1500]), ([0, 300, 40], [700, 333, 1])])
+def test_prompts_of_odd_groups(group, lengths, tokens):
+    Case(lengths, tokens, torch.bfloat16, group, 1, 64, seed=22).check()
+
+
+@pytest.mark.parametrize("group", [3, 4])
+def test_prompts_longer_than_their_pages(group):
+    """New tokens without a place see the places that there are, in every one of a sequence's tiles."""
+    case = Case([700], [900], torch.bfloat16, group, 1, 64, seed=23)
+    width = 1300 // case.page
+    case.batch = (case.table[:, :width].contiguous().to(DEV), *case.batch[1:])
+    got, lse = case.attend(return_lse=True)
+    p = torch.arange(width * case.page)
+    pages = case.table[0].long()[p // case.page]
+    k, v = (half[pages, p % case.page, 0].double() for half in (case.k, case.v))
+    for h in range(group):
+        z = torch.where(case.seen(0, None)[:, :len(p)], 0.125 * case.q[:, h].double() @ k.t(), -torch.inf)
+        far = (got[:, h].cpu().double() - z.softmax(1) @ v).abs()
+        assert bool((far <= 2.1 * 2.0 ** -8 * (z.softmax(1) @ v.abs())).all())
+        d = 0.125 * (64 + 4) * E * (case.q[:, h].double().abs() @ k.abs().t()).amax(1) + 8 * E * z.abs().nan_to_num(0, 0, 0).amax(1)
+        most = 1.01 * (2 * d + (8 + len(p)) * E + 4 * E * z.logsumexp(1).abs())
+        assert bool(((lse[:, h].cpu().double() - z.logsumexp(1)).abs() <= most).all())
