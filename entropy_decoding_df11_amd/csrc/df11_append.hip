@@ -265,7 +265,9 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
     k.page_magic = df11::page_magic(c->page_size, k.page_shift);
     (void)hipGetLastError();
     void *params[] = {&k};
-    const uint32_t threads = k.units >= 256 ? 256 : 64;
+    // (a dimension of a launch has fewer than 2^32 threads)
+    const uint32_t threads = k.units >= 256 && tokens < kMaxKvTokens ? 256 : 64;
+    static_assert(64ull * kMaxKvTokens < (1ull << 32) && 256ull * (kMaxKvTokens - 1) < (1ull << 32), "a launch holds it");
     return launch_kernel(c->dtype == DF11_BF16 ? pick_in<bf16_t>(a->dtype, wide, next)
                                               : pick_in<fp16_t>(a->dtype, wide, next),
                          dim3(tokens, (k.units + threads - 1) / threads), dim3(threads), params, 0,
