@@ -58,6 +58,11 @@ struct DenseCall {
 // split; 0 if it does not split), or ~0 if the device cannot be asked.
 uint64_t dense_workspace(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols);
 
+// Whether a launch holds the product's workgroups: DF11_OK, DF11_E_TOO_LARGE or
+// DF11_E_HIP.  (dense_product asks too; a caller that launches something else first
+// asks before that.)
+int dense_fits(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols);
+
 // Launches the product with its epilogue (e.pre as for the epilogue; the
 // bias, activation and residual fields are unused backward, where kDenseBackAdd
 // adds to the float e.out; all of it is unused by kDenseStats and kDenseExp).

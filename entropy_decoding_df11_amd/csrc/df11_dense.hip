@@ -641,6 +641,18 @@ DensePlan dense_plan(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows,
     return best;
 }
 
+// Workgroups of outputs [from, to) in tiles of `edge` tokens and mats * outputs.
+uint64_t dense_groups(const DensePlan &p, uint32_t edge, uint64_t mats, uint32_t tokens, uint64_t from, uint64_t to) {
+    const uint64_t outs = edge / mats;
+    return (tokens + edge - 1ull) / edge * ((to - from + outs - 1) / outs) * p.splits;
+}
+
+// A dimension of a launch has fewer than 2^32 threads.
+bool plan_fits(const DensePlan &p, uint64_t mats, uint32_t tokens, uint64_t n_out) {
+    return dense_groups(p, 256, mats, tokens, 0, p.large_out) * 512u < (1ull << 32) &&
+           dense_groups(p, 128, mats, tokens, p.large_out, n_out) * 256u < (1ull << 32);
+}
+
 template <int WM, int WN, int TM, int TN>
 const void *dense_kernel(DenseMode mode) {
     switch (mode) {
@@ -665,11 +677,20 @@ uint64_t dense_workspace(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t r
     return p.splits > 1 ? 4ull * p.splits * mats * tokens * n_out : 0;
 }
 
+int dense_fits(DenseMode mode, uint32_t n, uint32_t tokens, uint32_t rows, uint32_t cols) {
+    int dev = 0, cus = 0;
+    if (device_cus(dev, cus)) return DF11_E_HIP;
+    const DensePlan p = dense_plan(mode, n, tokens, rows, cols, cus);
+    return plan_fits(p, mode == kDenseGated ? 2 : 1, tokens, is_back(mode) ? cols : rows) ? DF11_OK : DF11_E_TOO_LARGE;
+}
+
 int dense_product(const DenseCall &c, const Epilogue &e, float *workspace, hipStream_t stream) {
     int dev = 0, cus = 0;
     if (device_cus(dev, cus)) return DF11_E_HIP;
     const uint32_t n = c.mode == kDenseGated || (c.mode == kDenseBack && c.w[1]) ? 2 : 1;
     const DensePlan p = dense_plan(c.mode, n, c.tokens, c.rows, c.cols, cus);
+    const uint64_t mats = c.mode == kDenseGated ? 2 : 1;
+    if (!plan_fits(p, mats, c.tokens, is_back(c.mode) ? c.cols : c.rows)) return DF11_E_TOO_LARGE;
     const uint32_t one = is_back(c.mode) ? c.rows / kStep : (c.cols + kStep - 1) / kStep;
     DenseArgs a{};
     for (int i = 0; i < 2; ++i) {
@@ -694,12 +715,11 @@ int dense_product(const DenseCall &c, const Epilogue &e, float *workspace, hipSt
     a.splits = p.splits;
     // Outputs [from, to) in tiles of `edge` tokens.
     const auto part = [&](uint32_t edge, uint32_t from, uint32_t to) {
-        const uint32_t outs = c.mode == kDenseGated ? edge / 2 : edge;
         a.out0 = from;
         a.m_tiles = (a.tokens + edge - 1) / edge;
         return launch_kernel(edge == 256 ? dense_kernel<2, 4, 8, 4>(c.mode) : dense_kernel<2, 2, 4, 4>(c.mode),
-                             dim3(a.m_tiles * ((to - from + outs - 1) / outs) * p.splits), dim3(2 * edge), params, 0,
-                             stream, nullptr, nullptr);
+                             dim3(static_cast<uint32_t>(dense_groups(p, edge, mats, a.tokens, from, to))), dim3(2 * edge),
+                             params, 0, stream, nullptr, nullptr);
     };
     int rc = DF11_OK;
     if (p.large_out) rc = part(256, 0, p.large_out);

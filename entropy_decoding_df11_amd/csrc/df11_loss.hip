@@ -66,6 +66,9 @@ using df11::PartialStream;
 constexpr uint64_t kPieceExps = 128u << 20;
 constexpr uint32_t kLeastPiece = 4096;
 constexpr uint64_t kMaxRow = 1ull << 22;
+// Tokens with a gradient: a workgroup of 256 threads each, and a dimension of a launch
+// has fewer than 2^32.
+constexpr uint32_t kMaxGradTokens = (1u << 24) - 1u;
 
 // log2(e) in two floats, and ln 2.
 constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596303350001107901e-8f;
@@ -271,7 +274,8 @@ __device__ __forceinline__ float loss_of(float u) { return u > 0.0f ? u + log1pf
 // The losses from the pairs of all panels.
 __global__ __launch_bounds__(1024) void df11_loss_tokens_kernel(TokenArgs a) {
     __shared__ float s_pair[kParts][kTokens][2];
-    const uint32_t t = threadIdx.x % kTokens, part = threadIdx.x / kTokens, token = blockIdx.x * kTokens + t;
+    const uint32_t t = threadIdx.x % kTokens, part = threadIdx.x / kTokens;
+    const uint32_t token = (blockIdx.y * gridDim.x + blockIdx.x) * kTokens + t;
     const bool in = token < a.n_tokens;
     const float *st = a.stats + 2u * (in ? token : 0u);
     const uint64_t step = 2ull * a.n_tokens;
@@ -411,7 +415,7 @@ struct LossPlan {
 // Classes of the piece that begins at class `from`.
 uint32_t piece_at(uint32_t rows, uint32_t piece, uint32_t from) { return std::min(piece, rows - from); }
 
-bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan &p) {
+int loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan &p) {
     const uint32_t cols = w->tile_cols, rows = static_cast<uint32_t>(w->h.n_elements / cols);
     p = LossPlan{};
     uint64_t at = 0;
@@ -423,14 +427,19 @@ bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan
     p.slots = !grad && tokens <= kPartialTokens;
     if (p.slots) {
         Partials parts{};
-        if (df11::partial_products(&w, 1, nullptr, 0, tokens, nullptr, 0, nullptr, parts)) return false;
+        if (df11::partial_products(&w, 1, nullptr, 0, tokens, nullptr, 0, nullptr, parts)) return DF11_E_HIP;
         p.weights = take(parts.slot_bytes);
     } else {
         p.weights = take(decoded_bytes(&w, 1));
     }
     p.logit = take(4ull * tokens);
     uint32_t most = rows;  // classes whose pairs are held at once
+    if (!grad && !p.slots) {
+        const int rc = df11::dense_fits(df11::kDenseStats, 1, tokens, rows, cols);
+        if (rc) return rc;
+    }
     if (grad) {
+        if (tokens > kMaxGradTokens) return DF11_E_TOO_LARGE;
         // Pieces of about the same size.
         const uint64_t most_classes = std::max<uint64_t>(kLeastPiece, kPieceExps / tokens);
         const uint64_t pieces = (rows + most_classes - 1) / most_classes;
@@ -440,8 +449,11 @@ bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan
         for (uint32_t from = 0, n; from < rows; from += n) {
             n = piece_at(rows, p.piece, from);
             most = std::max(most, n);
+            int rc = df11::dense_fits(df11::kDenseExp, 1, tokens, n, cols);
+            if (!rc) rc = df11::dense_fits(df11::kDenseBackAdd, 1, tokens, n, cols);
+            if (rc) return rc;
             const uint64_t more = df11::dense_workspace(df11::kDenseBackAdd, 1, tokens, n, cols);
-            if (more == ~0ull) return false;
+            if (more == ~0ull) return DF11_E_HIP;
             split = std::max(split, more);
         }
         p.ref = take(4ull * tokens);
@@ -455,7 +467,7 @@ bool loss_plan(const df11_device_stream *w, uint32_t tokens, bool grad, LossPlan
     }
     p.stats = take(8ull * (most / 64) * tokens);
     p.end = at;
-    return true;
+    return DF11_OK;
 }
 
 template <typename T>
@@ -499,7 +511,9 @@ int loss_only(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride,
     if (rc) return rc;
     t.panels = rows / 64;
     void *params[] = {&t};
-    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_tokens_kernel), dim3((tokens + kTokens - 1) / kTokens),
+    // (in rows of 2^21 workgroups where one row of them would be too long for a launch)
+    const uint32_t groups = (tokens + kTokens - 1) / kTokens, row = std::min(groups, 1u << 21);
+    return launch_kernel(reinterpret_cast<const void *>(&df11_loss_tokens_kernel), dim3(row, (groups + row - 1) / row),
                          dim3(1024), params, 0, stream, nullptr, nullptr);
 }
 
@@ -590,7 +604,7 @@ uint64_t df11_cross_entropy_workspace(const df11_device_stream *w, uint32_t n_to
     if (!w || !n_tokens || df11::check_stream(w) || !w->h.n_elements || !w->tile_cols) return 0;
     const uint64_t rows = w->h.n_elements / w->tile_cols;
     if (rows > kMaxRow || check_head(w, n_tokens, w->tile_cols, static_cast<uint32_t>(rows))) return 0;
-    return loss_plan(w, n_tokens, with_grad != 0, p) ? p.end : 0;
+    return loss_plan(w, n_tokens, with_grad != 0, p) ? 0 : p.end;
 }
 
 int df11_cross_entropy(const df11_device_stream *w, const uint16_t *x, uint64_t x_stride, uint32_t n_tokens,
@@ -623,7 +637,8 @@ int df11_cross_entropy(const df11_device_stream *w, const uint16_t *x, uint64_t 
     (void)hipGetLastError();
     if (n_tokens) {
         LossPlan p{};
-        if (!loss_plan(w, n_tokens, l->grad != nullptr, p)) return DF11_E_HIP;
+        rc = loss_plan(w, n_tokens, l->grad != nullptr, p);
+        if (rc) return rc;
         if (!workspace || !aligned(workspace, 256)) return DF11_E_INVALID_ARG;
         if (workspace_bytes < p.end) return DF11_E_BUFFER_TOO_SMALL;
         spans[4] = p.end;
@@ -656,7 +671,8 @@ int df11_cross_entropy_grad(const float *grad, const float *dy, uint64_t dy_stri
                             void *hip_stream) {
     const uint32_t bytes = dx_dtype == DF11_FP16 ? 0 : dtype_bytes(dx_dtype);
     if (!bytes || in_features < 32 || in_features % 32) return DF11_E_INVALID_ARG;
-    if (in_features > kMaxRow || static_cast<uint64_t>(n_tokens) * in_features >= (1ull << 32)) return DF11_E_TOO_LARGE;
+    if (in_features > kMaxRow || static_cast<uint64_t>(n_tokens) * in_features >= (1ull << 32) || n_tokens > kMaxGradTokens)
+        return DF11_E_TOO_LARGE;
     if (!n_tokens) return DF11_OK;
     if (!grad || !aligned(grad, 16) || !dy || !aligned(dy, 4) || dy_stride > (1ull << 31) || !dx || !aligned(dx, bytes) ||
         dx_stride > (1ull << 31) || (n_tokens > 1 && dx_stride < in_features) || (count && !aligned(count, 4)))

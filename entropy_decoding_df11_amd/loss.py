@@ -89,7 +89,7 @@ def linear_cross_entropy(w, x: "torch.Tensor", targets: "torch.Tensor", vocab: O
 
     w: a DF11Tensor compressed with layout="mfma_tiles", (classes, in_features);
     x: bfloat16 (..., in_features), rows at one stride and 16-byte aligned, fewer
-    than 2^32 elements; targets: int64, one for each token; vocab: the classes
+    than 2^32 elements and, with a gradient, 2^24 tokens; targets: int64, one for each token; vocab: the classes
     that count, where w's last rows are padding (None: all rows).  A token whose
     target is ignore_index counts nowhere, one whose target is no class otherwise
     gives NaN.  Returns float32: with reduction "none" the losses, of targets'

@@ -695,6 +695,7 @@ uint64_t df11_cross_entropy_workspace(const df11_device_stream *w, uint32_t n_to
  * of each), piece by piece of the vocabulary, and its sums are float.
  *   w, x, in_features, out_features   as for df11_matmul_epilogue, out_features
  *                and in_features up to 2^22, n_tokens * in_features below 2^32
+ *                and with l->grad n_tokens below 2^24
  *   workspace    device, 256-byte aligned, df11_cross_entropy_workspace bytes;
  *                holds nothing between calls, but calls that overlap in time need
  *                one each
@@ -715,6 +716,7 @@ int df11_cross_entropy(const df11_device_stream *w, const uint16_t *x, uint64_t 
  * (ignored tokens' are, no other's) gives zero whatever g is.  dy_stride 0: one
  * dy for all tokens.  dx: n_tokens x in_features of dx_dtype (DF11_BF16 or
  * DF11_FP32), dx_stride elements from row to row, overlapping nothing else.
+ * n_tokens below 2^24.
  * Errors: DF11_E_INVALID_ARG, DF11_E_TOO_LARGE, DF11_E_HIP. */
 int df11_cross_entropy_grad(const float *grad, const float *dy, uint64_t dy_stride, const float *count,
                             uint32_t n_tokens, uint32_t in_features, void *dx, uint64_t dx_stride, uint32_t dx_dtype,
