@@ -190,12 +190,9 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
     if (tokens == 0 || b->n_seqs == 0) return DF11_OK;
     if (!a->k || !a->v) return DF11_E_INVALID_ARG;
     // Places that lie on each other would hold what was written last.
-    const uint64_t apart[][2] = {{c->n_pages, std::min(c->k_page_stride, c->v_page_stride)},
-                                 {c->page_size, std::min(c->k_place_stride, c->v_place_stride)},
-                                 {c->heads, std::min(c->k_head_stride, c->v_head_stride)}};
-    for (const auto &d : apart)
-        if (d[0] > 1 && d[1] < dim) return DF11_E_INVALID_ARG;
-    if (c->k == c->v) return DF11_E_INVALID_ARG;
+    const Runs k_runs = kv_runs(c->k, c->k_page_stride, c->k_place_stride, c->k_head_stride, *c);
+    const Runs v_runs = kv_runs(c->v, c->v_page_stride, c->v_place_stride, c->v_head_stride, *c);
+    if (!k_runs.nested || !v_runs.nested || !lie_apart(k_runs, v_runs)) return DF11_E_INVALID_ARG;
     if (a->rotary && !a->rotary_rows) return DF11_E_INVALID_ARG;
     const uint32_t rotary_dims = a->rotary ? a->rotary_dims : 0;
     struct In {

@@ -4,6 +4,9 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+#include <utility>
+
 #include <stdint.h>
 
 #include "df11.h"
@@ -65,6 +68,69 @@ __device__ __forceinline__ int32_t sequence_of(const df11::KvBatch &b, int32_t t
            (stride >= dim && head_stride >= (rows - 1) * stride + dim);
 }
 
+// A tensor in memory as runs of `run` bytes along up to three dimensions, the largest
+// stride first, in bytes; dimensions of one element or without a stride left out.
+struct Runs {
+    uintptr_t at;
+    uint64_t run, span;  // span: from the first byte to behind the last
+    uint64_t stride[3], count[3];
+    int dims;
+    bool nested;  // every stride steps over all that the smaller ones reach: no run lies on another
+};
+
+[[maybe_unused]] Runs runs_of(const void *p, uint64_t run, std::initializer_list<std::pair<uint64_t, uint64_t>> dims) {
+    Runs r{reinterpret_cast<uintptr_t>(p), run, run, {}, {}, 0, true};
+    for (const auto &[count, stride] : dims) {
+        if (count <= 1) continue;
+        if (stride == 0) {
+            r.nested = false;
+            continue;
+        }
+        int i = r.dims++;
+        for (; i > 0 && r.stride[i - 1] < stride; --i) {
+            r.stride[i] = r.stride[i - 1];
+            r.count[i] = r.count[i - 1];
+        }
+        r.stride[i] = stride;
+        r.count[i] = count;
+    }
+    for (int i = r.dims; i-- > 0;) {
+        r.nested = r.nested && r.stride[i] >= r.span;
+        r.span += (r.count[i] - 1) * r.stride[i];
+    }
+    return r;
+}
+
+// Whether two tensors are seen to share no byte: their spans lie apart, or, stepping
+// alike along their outermost dimensions, no two of their steps do (parts of one
+// tensor's rows, as a fused product leaves them).
+[[maybe_unused]] bool lie_apart(const Runs &a, const Runs &b) {
+    if (!a.at || !b.at || !a.span || !b.span || a.at + a.span <= b.at || b.at + b.span <= a.at) return true;
+    if (!a.nested || !b.nested || !a.dims || !b.dims || a.stride[0] != b.stride[0]) return false;
+    const auto inner = [](const Runs &r) {
+        Runs in = r;
+        in.span -= (r.count[0] - 1) * r.stride[0];
+        --in.dims;
+        for (int i = 0; i < in.dims; ++i) {
+            in.stride[i] = r.stride[i + 1];
+            in.count[i] = r.count[i + 1];
+        }
+        return in;
+    };
+    // A step of either reaches less than the stride: only those matter whose first
+    // bytes are nearer than that.
+    const int64_t stride = static_cast<int64_t>(a.stride[0]), off = static_cast<int64_t>(b.at - a.at);
+    const Runs x = inner(a);
+    Runs y = inner(b);
+    for (int64_t n = -off / stride - 1; n <= -off / stride + 1; ++n) {
+        // (n: b's step over a's)
+        if (n <= -static_cast<int64_t>(a.count[0]) || n >= static_cast<int64_t>(b.count[0])) continue;
+        y.at = b.at + static_cast<uint64_t>(n * stride);
+        if (!lie_apart(x, y)) return false;
+    }
+    return true;
+}
+
 // Pages x places x heads of one half of the cache, `span` receiving its bytes.
 [[maybe_unused]] bool kv_pages_ok(const void *p, uint64_t page, uint64_t place, uint64_t head, const df11_kv_cache &c,
                                   uint64_t &span) {
@@ -106,6 +172,11 @@ __device__ __forceinline__ int32_t sequence_of(const df11::KvBatch &b, int32_t t
     const uint64_t table = b.n_seqs && b.table_pages ? 4 * ((b.n_seqs - 1) * b.table_stride + b.table_pages) : 0;
     return !overlaps(p, bytes, b.starts, 4ull * (b.n_seqs + 1)) && !overlaps(p, bytes, b.lengths, 4ull * b.n_seqs) &&
            !overlaps(p, bytes, b.page_table, table);
+}
+
+// One half of the cache as runs.
+[[maybe_unused]] Runs kv_runs(const void *p, uint64_t page, uint64_t place, uint64_t head, const df11_kv_cache &c) {
+    return runs_of(p, 2ull * c.head_dim, {{c.n_pages, 2 * page}, {c.page_size, 2 * place}, {c.heads, 2 * head}});
 }
 
 [[maybe_unused]] df11::KvPages kernel_pages(void *p, uint64_t page, uint64_t place, uint64_t head, const df11_kv_cache &c) {

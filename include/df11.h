@@ -816,8 +816,10 @@ typedef struct df11_append {
  * outside the table gives NaN.  Rows of q_out that belong to no sequence are
  * left as they were, and so is the rest of the cache.  Places that two tokens
  * share receive either one's elements.  One launch; with no tokens none.
- * Errors: DF11_E_INVALID_ARG (types, sizes, alignment, overlaps, also of the
- * cache's places), DF11_E_HIP. */
+ * Places, heads and pages lie apart: of each half every stride steps over all that
+ * the smaller ones reach, and so do the halves of each other, which may be parts of
+ * one tensor.  Errors: DF11_E_INVALID_ARG (types, sizes, alignment, overlaps, also of
+ * the cache's places), DF11_E_HIP. */
 int df11_append_kv(const df11_kv_cache *cache, const df11_kv_batch *batch, const df11_append *a, void *hip_stream);
 
 /* What df11_tree_attention takes beside the cache and the batch (host struct of
