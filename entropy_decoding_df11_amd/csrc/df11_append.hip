@@ -202,15 +202,18 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
                {a->k, a->k_stride, a->k_head_stride, c->heads},
                {a->v, a->v_stride, a->v_head_stride, c->heads}};
     bool wide = rotary_dims % 16 == 0 && aligned(a->rotary, 16) && aligned(a->q_out, 16) && a->q_out_stride % 8 == 0 && a->q_out_head_stride % 8 == 0;
-    uint64_t in_spans[3];
+    Runs in_runs[3];
+    const auto runs = [&](const void *p, uint64_t stride, uint64_t heads, uint64_t head_stride, uint64_t size) {
+        return runs_of(p, size * dim, {{tokens, size * stride}, {heads, size * head_stride}});
+    };
     for (int i = 0; i < 3; ++i) {
         if (ins[i].stride >= kMaxKvStride || ins[i].head_stride >= (1ull << 32) || !aligned(ins[i].p, bytes))
             return DF11_E_INVALID_ARG;
-        in_spans[i] = ins[i].p ? kv_span(tokens, ins[i].stride, ins[i].heads, ins[i].head_stride, dim) * bytes : 0;
+        in_runs[i] = runs(ins[i].p, ins[i].stride, ins[i].heads, ins[i].head_stride, bytes);
         wide = wide && aligned(ins[i].p, 16) && ins[i].stride % 8 == 0 && ins[i].head_stride % 8 == 0;
     }
     // The cache's halves, q_out and everything that is read lie apart; q_out
-    // may lie exactly on q.
+    // may lie exactly on q, beside k and v in the rows of one tensor.
     const uint64_t q_out_span = a->q ? 2 * kv_span(tokens, a->q_out_stride, a->q_heads, a->q_out_head_stride, dim) : 0;
     if (a->q && (!aligned(a->q_out, 2) || a->q_out_stride >= kMaxKvStride || a->q_out_head_stride >= (1ull << 32) ||
                  !kv_apart(tokens, a->q_out_stride, a->q_heads, a->q_out_head_stride, dim)))
@@ -219,11 +222,11 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
                       a->q_head_stride == a->q_out_head_stride && a->dtype == c->dtype;
     const void *outs[] = {c->k, c->v, a->q_out};
     const uint64_t out_spans[] = {k_span, v_span, q_out_span};
+    const Runs out_runs[] = {k_runs, v_runs, runs(a->q_out, a->q_out_stride, a->q_heads, a->q_out_head_stride, 2)};
     for (int i = 0; i < 3; ++i) {
         for (int j = 0; j < 3; ++j) {
-            if (overlaps(outs[i], out_spans[i], ins[j].p, in_spans[j]) && !(i == 2 && j == 0 && on_q))
-                return DF11_E_INVALID_ARG;
-            if (i == 2 && j < 2 && overlaps(outs[i], out_spans[i], outs[j], out_spans[j])) return DF11_E_INVALID_ARG;
+            if (!lie_apart(out_runs[i], in_runs[j]) && !(i == 2 && j == 0 && on_q)) return DF11_E_INVALID_ARG;
+            if (i == 2 && j < 2 && !lie_apart(out_runs[i], out_runs[j])) return DF11_E_INVALID_ARG;
         }
         if (!clear_of_batch(*b, outs[i], out_spans[i]) ||
             overlaps(outs[i], out_spans[i], a->rotary, 4 * a->rotary_rows * rotary_dims) ||

@@ -1246,17 +1246,22 @@ int df11_tree_attention(const df11_kv_cache *c, const df11_kv_batch *b, const df
     const df11_attention used = used_strides(*given, b->n_tokens), *a = &used;
     rc = check_attention(*c, *b, a, q_span, out_span);
     if (rc || b->n_tokens == 0 || b->n_seqs == 0) return rc;
-    // Outputs stay clear of everything that is read, but out may lie exactly on q.
+    // Outputs stay clear of everything that is read, but out may lie exactly on q, or
+    // beside it in the rows of one tensor.
     const uint64_t lse_span = a->lse ? 4ull * b->n_tokens * a->q_heads : 0;
     const uint64_t mask_span = a->mask && a->mask_cols ? (b->n_tokens - 1ull) * a->mask_stride + a->mask_cols : 0;
     const bool on_q = a->q == a->out && a->q_stride == a->out_stride && a->q_head_stride == a->out_head_stride;
+    const auto runs = [&](const void *p, uint64_t stride, uint64_t head_stride) {
+        return runs_of(p, 2ull * c->head_dim, {{b->n_tokens, 2 * stride}, {a->q_heads, 2 * head_stride}});
+    };
+    const bool off_q = lie_apart(runs(a->out, a->out_stride, a->out_head_stride), runs(a->q, a->q_stride, a->q_head_stride));
     const void *outs[] = {a->out, a->lse, workspace};
     uint64_t spans[] = {out_span, lse_span, 0};
     const auto clear = [&](int i) {
         for (int j = 0; j < i; ++j)
             if (overlaps(outs[i], spans[i], outs[j], spans[j])) return false;
         return !overlaps(outs[i], spans[i], c->k, k_span) && !overlaps(outs[i], spans[i], c->v, v_span) &&
-               ((i == 0 && on_q) || !overlaps(outs[i], spans[i], a->q, q_span)) &&
+               (i == 0 ? on_q || off_q : !overlaps(outs[i], spans[i], a->q, q_span)) &&
                !overlaps(outs[i], spans[i], a->mask, mask_span) && clear_of_batch(*b, outs[i], spans[i]);
     };
     if (!clear(0) || !clear(1)) return DF11_E_INVALID_ARG;

@@ -783,7 +783,8 @@ typedef struct df11_kv_batch {
  *   q             n_tokens x q_heads x head_dim of dtype, q_heads 1 .. 4096; or
  *                 NULL, with q_heads 0
  *   q_out         n_tokens x q_heads x head_dim of the cache's dtype; with q only.
- *                 May lie exactly on q (same address, strides and type)
+ *                 May lie exactly on q (same address, strides and type).  q, k and
+ *                 v may be parts of the rows of one tensor
  *   rotary        rotary_rows x rotary_dims floats: row p holds the cosines of
  *                 position p's angles, then their sines; or NULL (no rotation)
  *   rotary_dims   even, 2 .. head_dim: the dimensions of a head that are rotated,
