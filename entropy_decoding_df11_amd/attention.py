@@ -22,7 +22,7 @@ hold is checked where it is used: places beyond the table and pages that do not
 exist are neither read nor written.
 
 As in operators.py the calls run on torch's current stream, or on the stream
-given.  Serving's operators: they carry no gradients.
+given.  Serving's operators: they carry no gradients, and refuse tensors that do.
 """
 
 from __future__ import annotations
@@ -30,7 +30,7 @@ from __future__ import annotations
 from typing import Optional, Tuple, Union
 
 from . import _lib, operators
-from .operators import _check_outputs, _dtype, _ptr, _run, _same_device, _stream
+from .operators import _check_outputs, _dtype, _no_tangents, _ptr, _run, _same_device, _stream
 
 
 def rotary_table(positions: int, dims: int, base: float = 10000.0, device="cuda") -> "torch.Tensor":  # noqa: F821
@@ -174,6 +174,7 @@ def append_kv(k: "torch.Tensor", v: "torch.Tensor", k_cache: "torch.Tensor", v_c
         _same_device(dev, "positions", positions)
     if needs and torch.is_grad_enabled():
         raise ValueError(_GRADIENTS)
+    _no_tangents(k, v, q, k_cache, v_cache, q_out, rotary)
     out, = _run(dev, stream, _launch_append, k, v, q, k_cache, v_cache, page_table, starts, lengths, rotary, positions,
                 interleaved, q_out, code)
     torch.autograd.graph.increment_version((k_cache, v_cache) if q_out is None else (k_cache, v_cache, q_out))
@@ -250,6 +251,7 @@ def tree_attention(q: "torch.Tensor", k_cache: "torch.Tensor", v_cache: "torch.T
         given = _check_outputs(out)
     if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad) and torch.is_grad_enabled():
         raise ValueError(_GRADIENTS)
+    _no_tangents(q, k_cache, v_cache, out)
     out, lse = _run(dev, stream, _launch_attention, q, k_cache, v_cache, page_table, starts, lengths, mask, scale, out,
                     return_lse, code)
     if given:

@@ -14,7 +14,7 @@ from __future__ import annotations
 from typing import Optional
 
 from . import _lib, operators
-from .operators import _ptr, _rows, _run, _same_device, _stream
+from .operators import _no_tangents, _ptr, _rows, _run, _same_device, _stream
 
 _Loss = None
 
@@ -103,6 +103,7 @@ def linear_cross_entropy(w, x: "torch.Tensor", targets: "torch.Tensor", vocab: O
         operators._import_torch()
     torch = operators.torch
     dev, vocab = _check(w, x, targets, vocab, reduction)
+    _no_tangents(x)
     if x.requires_grad and torch.is_grad_enabled():
         if stream is not None:
             raise ValueError("stream is for calls without gradients")

@@ -4,7 +4,8 @@ The framework keeps a block's weights compressed and multiplies by them; this
 module has what a forward computes between one product and the next (the C
 ABI's operators in include/df11.h), each differentiable: under torch's
 autograd they give the gradients of the activations, the biases, the residual
-and the norm's weight.  (The compressed weights are frozen: they have none.)
+and the norm's weight.  (The compressed weights are frozen: they have none.
+Forward-mode derivatives are refused.)
 
     y = rms_norm(x, weight)                       # norm
     y, s = rms_norm(x, weight, residual=r)        # s = x + r, y = norm of s
@@ -74,6 +75,15 @@ def _rows(t: "torch.Tensor", cols: int, what: str) -> Tuple["torch.Tensor", int]
 def _same_device(dev, what: str, t) -> None:
     if t is not None and t.device != dev:
         raise ValueError(f"{what} must be on {dev}, not on {t.device}")
+
+
+def _no_tangents(*tensors) -> None:
+    """Refuses forward-mode derivatives, which the outputs would lose (requires_grad
+    does not tell of them, and grad mode does not turn them off)."""
+    forward_ad = torch.autograd.forward_ad
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None
+                                              for t in tensors):
+        raise ValueError("the operators carry no forward-mode derivatives")
 
 
 def _check_outputs(*outs):
@@ -227,6 +237,7 @@ def rms_norm(x: "torch.Tensor", weight: Optional["torch.Tensor"] = None,  # noqa
     if torch is None:
         _import_torch()
     code, wcode = _check_norm(x, weight, residual, out, sum_out)
+    _no_tangents(x, weight, residual)
     if (x.requires_grad or (weight is not None and weight.requires_grad)
             or (residual is not None and residual.requires_grad)) and torch.is_grad_enabled():
         if out is not None or sum_out is not None or stream is not None:
@@ -361,6 +372,7 @@ def _product(ws, x, biases, activation, residual, out, out_dtype, stream):
     if torch is None:
         _import_torch()
     dev, act, out_dtype = _check_product(ws, x, biases, activation, residual, out, out_dtype)
+    _no_tangents(x, residual, *biases)
     if (x.requires_grad or (residual is not None and residual.requires_grad)
             or any(b is not None and b.requires_grad for b in biases)) and torch.is_grad_enabled():
         if out is not None or stream is not None:
