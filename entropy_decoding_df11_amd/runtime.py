@@ -184,7 +184,8 @@ def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5, cache: Opt
 
     With cache, the block's pair of paged keys and values, and step, x is
     (tokens, features) and the block attends over the cache (cached_attention;
-    no gradients); without them it has no attention mixing, as block_forward."""
+    no gradients), whose output of the cache's type is taken in x's; without them
+    it has no attention mixing, as block_forward."""
     import torch
     from .df11 import matmul_batch
 
@@ -205,7 +206,7 @@ def operator_block_forward(x, blk: DF11BlockBatch, eps: float = 1e-5, cache: Opt
     if cache is None:
         a = q + (k * v).repeat_interleave(q.shape[-1] // k.shape[-1], dim=-1)
     else:
-        a = cached_attention(q, k, v, cache, step)
+        a = cached_attention(q, k, v, cache, step).to(x.dtype)
     x = matmul_epilogue(w["o_proj"], a, residual=x)
     h = gated_matmul(w["gate_proj"], w["up_proj"], rms_norm(x, eps=eps))
     return matmul_epilogue(w["down_proj"], h, residual=x)
