@@ -957,7 +957,10 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
         p.head = 0;
         if (u == end) break;
         do {
-            if (++p.seq == a.b.n_seqs) return;  // (never: units are left)
+            if (++p.seq == a.b.n_seqs) {  // (never: units are left)
+                u = end;
+                break;
+            }
             p.s = shape_of(a, p.seq);
         } while (!p.s.tiles);
     }
@@ -1183,7 +1186,7 @@ int make_plan(const df11_kv_cache &c, const df11_kv_batch &b, uint32_t q_heads, 
     const uint64_t capacity = static_cast<uint64_t>(b.table_pages) * c.page_size;
     const uint64_t tiles = (static_cast<uint64_t>(b.n_tokens) * group + p.tile_rows - 1) / p.tile_rows + b.n_seqs;
     // (an upper bound of the tiles, at most twice as many)
-    const uint32_t uncut = df11::whole_places(few, tiles * c.heads, static_cast<uint32_t>(cus));
+    const uint32_t uncut = df11::whole_places(few, tiles * c.heads, static_cast<uint32_t>(cus), c.head_dim);
     p.step = df11::unit_places(capacity, few, uncut);
     // (a tile without a mask may count a unit for its own tokens beside the pages')
     p.extra = df11::extra_units(capacity, few, uncut, c.head_dim);

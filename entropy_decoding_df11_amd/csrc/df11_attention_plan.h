@@ -29,15 +29,18 @@ namespace df11 {
 constexpr uint32_t kFewStep = 256, kManyStep = 128;
 
 // Places of a sequence's pages up to which tiles are never cut: then a unit is a
-// whole tile, and no second kernel joins parts.  Measured in a graph, heads of
-// 128, whole against cut: one token of one sequence 15.9 and 17.0 us at 500
-// places, 20.4 and 16.7 at 960 (a call from Python saves 3 us more without the
-// second launch); 64 sequences 61.0 and 64.2 at 960; 16 trees of 16 tokens 27.6 and
-// 31.3 at 960, 45.9 and 41.4 at 1500; a tree of 32 of one sequence 28.5 and 22.3
-// at 500.  So it is the number of tiles, which fill the chip or not, that decides.
-constexpr uint32_t kMostWhole = 1024, kFewWhole = 768, kManyWhole = 128;
-constexpr uint32_t whole_places(bool few, uint64_t tiles, uint32_t workgroups) {
-    return tiles >= workgroups ? kMostWhole : few ? kFewWhole : kManyWhole;
+// whole tile, and no second kernel joins parts.  It is the number of tiles, which fill
+// the chip or not, that decides: 64 sequences of one token over 960 places 61.0 us
+// whole and 64.2 cut, 16 trees of 16 tokens 27.6 and 31.3 at 960, 45.9 and 41.4 at 1500; a
+// tree of 32 of one sequence 28.5 and 22.3 at 500.  Few tiles of few rows, by the time
+// that a place takes: one token of one sequence in a graph (from Python whole saves
+// about half a microsecond more), heads of 128 whole 13.8 us and cut 15.3 at 608 places,
+// 15.4 and 15.4 at 736, 15.7 and 15.7 at 800, 16.4 and 15.7 at 864; of 64 12.4 and 13.8 at
+// 1024; of 256 15.5 and 17.9 at 320, 18.7 and 18.7 at 480, 20.4 and 18.5 at 544.
+constexpr uint32_t kMostWhole = 1024, kManyWhole = 128;
+constexpr uint32_t few_whole(uint32_t dim) { return dim > 128u ? 448u : dim > 64u ? 768u : kMostWhole; }
+constexpr uint32_t whole_places(bool few, uint64_t tiles, uint32_t workgroups, uint32_t dim) {
+    return tiles >= workgroups ? kMostWhole : few ? few_whole(dim) : kManyWhole;
 }
 
 // Places of a unit, for pages of `capacity` places of which `whole` are never cut.
