@@ -363,7 +363,9 @@ struct Rows {
 
     // Scores to weights (in s, and rounded in w).  A weight past the room (infinite
     // while there is no reference) says that the reference has to move: then
-    // they are taken again, from the new one.
+    // they are taken again, from the new one, and from scores times c that are rounded
+    // as the reference's was: what a fused product keeps beside it may be many powers
+    // of two (from scores of 2^30 on), and the largest score's weight infinite.
     __device__ __forceinline__ void weigh(floatx4 (&s)[M][2], Vec (&w)[M]) {
         const T one = static_cast<T>(1.0f);
         floatx4 x[M][2];
@@ -378,6 +380,7 @@ struct Rows {
             moves |= !(largest(x[i]) <= kRoom<T>);
         }
         if (__ballot(moves)) {
+#pragma clang fp contract(off)
 #pragma unroll
             for (int i = 0; i < M; ++i) {
                 float top = largest(s[i]);
@@ -393,7 +396,7 @@ struct Rows {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][t][e] = exp2_fast(__builtin_fmaf(s[i][t][e], a.c, -base));
+                    for (int e = 0; e < 4; ++e) x[i][t][e] = exp2_fast(s[i][t][e] * a.c - base);
             }
         }
 #pragma unroll
