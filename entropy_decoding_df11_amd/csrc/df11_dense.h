@@ -43,6 +43,19 @@ struct DenseLoss {
 // the largest exponentials and their sums stay far from float's and BF16's range.
 constexpr float kRefRoom = 64.0f;
 
+// log2(e) in two floats.
+constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596303350001107901e-8f;
+
+// The exponent z log2(e) - r of a class, r whole: to 2^-24 for a logit of 100.  r was
+// rounded from z kLog2eHi; from logits of 2^24 on its last place is more than a whole
+// number (many powers of two from 2^30 on), and the difference is taken of products
+// that are rounded alike.
+__device__ __forceinline__ float class_exponent(float z, float r) {
+#pragma clang fp contract(off)
+    const float rounded = z * kLog2eHi - r;
+    return __builtin_fabsf(z) < 16777216.0f ? __builtin_fmaf(z, kLog2eLo, __builtin_fmaf(z, kLog2eHi, -r)) : rounded;
+}
+
 // One product.  R x C are a weight's rows and columns; tokens x K the left
 // operand, K = C forward and R backward, tokens x N the output.
 struct DenseCall {

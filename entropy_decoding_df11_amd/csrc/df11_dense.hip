@@ -258,8 +258,6 @@ struct LossRows {
     uint32_t rows, token0, col0, lane;
 
     __device__ __forceinline__ void run() const {
-        // log2(e) in two floats: a logit of 100 keeps its exponential to 2^-24.
-        constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596303350001107901e-8f;
         const df11::DenseLoss &l = a.loss;
         if (col0 >= a.n_out) return;
         const uint32_t c = 8u * (lane % 8u), first = l.first_class + col0 + c;
@@ -282,7 +280,7 @@ struct LossRows {
             }
 #pragma unroll
             for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
-            float ref = ceilf(top * kHi);
+            float ref = ceilf(top * df11::kLog2eHi);
             if constexpr (MODE == kDenseExp) {
                 const float known = l.ref[token];
                 if (ref <= known + df11::kRefRoom) ref = known;
@@ -291,7 +289,7 @@ struct LossRows {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                z[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], kLo, __builtin_fmaf(z[i], kHi, -base)));
+                z[i] = __builtin_amdgcn_exp2f(df11::class_exponent(z[i], base));
                 sum += z[i];
             }
 #pragma unroll

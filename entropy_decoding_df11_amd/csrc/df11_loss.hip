@@ -54,6 +54,7 @@
 
 namespace {
 
+using df11::kLog2eHi;
 using df11::kPartialTokens;
 using df11::Partials;
 using df11::PartialStream;
@@ -70,8 +71,6 @@ constexpr uint64_t kMaxRow = 1ull << 22;
 // has fewer than 2^32.
 constexpr uint32_t kMaxGradTokens = (1u << 24) - 1u;
 
-// log2(e) in two floats, and ln 2.
-constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596303350001107901e-8f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct SlotLossArgs {
@@ -105,7 +104,7 @@ __global__ __launch_bounds__(256) void df11_loss_slots_kernel(SlotLossArgs a) {
 #pragma unroll
         for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
         const float ref = ceilf(top * kLog2eHi), base = ref == -INFINITY ? 0.0f : ref;
-        float sum = __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2eLo, __builtin_fmaf(z, kLog2eHi, -base)));
+        float sum = __builtin_amdgcn_exp2f(df11::class_exponent(z, base));
 #pragma unroll
         for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
         if (lane == 0) {
