@@ -174,7 +174,8 @@ def append_kv(k: "torch.Tensor", v: "torch.Tensor", k_cache: "torch.Tensor", v_c
         _same_device(dev, "positions", positions)
     if needs and torch.is_grad_enabled():
         raise ValueError(_GRADIENTS)
-    _no_tangents(k, v, q, k_cache, v_cache, q_out, rotary)
+    if operators._forward_ad._current_level >= 0:
+        _no_tangents(k, v, q, k_cache, v_cache, q_out, rotary)
     out, = _run(dev, stream, _launch_append, k, v, q, k_cache, v_cache, page_table, starts, lengths, rotary, positions,
                 interleaved, q_out, code)
     torch.autograd.graph.increment_version((k_cache, v_cache) if q_out is None else (k_cache, v_cache, q_out))
@@ -251,7 +252,8 @@ def tree_attention(q: "torch.Tensor", k_cache: "torch.Tensor", v_cache: "torch.T
         given = _check_outputs(out)
     if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad) and torch.is_grad_enabled():
         raise ValueError(_GRADIENTS)
-    _no_tangents(q, k_cache, v_cache, out)
+    if operators._forward_ad._current_level >= 0:
+        _no_tangents(q, k_cache, v_cache, out)
     out, lse = _run(dev, stream, _launch_attention, q, k_cache, v_cache, page_table, starts, lengths, mask, scale, out,
                     return_lse, code)
     if given:

@@ -103,7 +103,8 @@ def linear_cross_entropy(w, x: "torch.Tensor", targets: "torch.Tensor", vocab: O
         operators._import_torch()
     torch = operators.torch
     dev, vocab = _check(w, x, targets, vocab, reduction)
-    _no_tangents(x)
+    if operators._forward_ad._current_level >= 0:
+        _no_tangents(x)
     if x.requires_grad and torch.is_grad_enabled():
         if stream is not None:
             raise ValueError("stream is for calls without gradients")

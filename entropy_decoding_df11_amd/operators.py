@@ -33,7 +33,7 @@ from . import _lib
 
 # torch, its types' codes and the autograd functions, filled in by the first
 # call (importing this package does not import torch).
-torch = None
+torch = _forward_ad = None
 _DTYPES = {}
 _FLOATS = ()
 _Norm = _Product = None
@@ -42,8 +42,9 @@ _MAX_ROWS = 1 << 30
 
 
 def _import_torch() -> None:
-    global torch, _FLOATS
+    global torch, _forward_ad, _FLOATS
     import torch as module
+    _forward_ad = module.autograd.forward_ad
     _DTYPES.update({module.bfloat16: _lib.BF16, module.float16: _lib.FP16, module.float32: _lib.FP32})
     _FLOATS = (module.bfloat16, module.float32)
     _make_functions(module)
@@ -79,10 +80,9 @@ def _same_device(dev, what: str, t) -> None:
 
 def _no_tangents(*tensors) -> None:
     """Refuses forward-mode derivatives, which the outputs would lose (requires_grad
-    does not tell of them, and grad mode does not turn them off)."""
-    forward_ad = torch.autograd.forward_ad
-    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None
-                                              for t in tensors):
+    does not tell of them, and grad mode does not turn them off).  Asked for inside
+    a dual level only, where alone there are any."""
+    if any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors):
         raise ValueError("the operators carry no forward-mode derivatives")
 
 
@@ -237,7 +237,8 @@ def rms_norm(x: "torch.Tensor", weight: Optional["torch.Tensor"] = None,  # noqa
     if torch is None:
         _import_torch()
     code, wcode = _check_norm(x, weight, residual, out, sum_out)
-    _no_tangents(x, weight, residual)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(x, weight, residual)
     if (x.requires_grad or (weight is not None and weight.requires_grad)
             or (residual is not None and residual.requires_grad)) and torch.is_grad_enabled():
         if out is not None or sum_out is not None or stream is not None:
@@ -372,7 +373,8 @@ def _product(ws, x, biases, activation, residual, out, out_dtype, stream):
     if torch is None:
         _import_torch()
     dev, act, out_dtype = _check_product(ws, x, biases, activation, residual, out, out_dtype)
-    _no_tangents(x, residual, *biases)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(x, residual, *biases)
     if (x.requires_grad or (residual is not None and residual.requires_grad)
             or any(b is not None and b.requires_grad for b in biases)) and torch.is_grad_enabled():
         if out is not None or stream is not None:
