@@ -15,6 +15,11 @@
 // most.  (Without the 2^7 a place 17 nats ahead left what others alike had added
 // off by 44%.)
 //
+// One rounding of a weight puts outputs off by 0.0020 to 0.0023 of their norm in BF16,
+// where rounding the result alone gives 0.0017.  A second product with the weights'
+// remainders would leave the latter: nothing slower for few rows, but prompts'
+// pieces 196 -> 237 us, the tree below 184 -> 231 and trees of a batch 47 -> 55.
+//
 // A query head's rows of one key head are the columns of the products, so that
 // all heads of a group read a place once:
 //   S^T = K Q^T    v_mfma_f32_16x16x32: lane l holds places 4 (l / 16) .. + 3 of
@@ -31,23 +36,24 @@
 // Up to 16 rows (few): memory is the bound.  K's operands come straight from
 // memory to registers, V's rows to LDS that each wave has to itself; waves take the
 // places of a step in turn and meet only at the end of a tile's run.  64 sequences of
-// one token over up to 8192 places each: 198 us, 5.1 TB/s of 1.01 GB.  With four
+// one token over up to 8192 places each: 197 us, 5.1 TB/s of 1.01 GB.  With four
 // waves and twice the workgroups 224.
 //
 // More rows: a wave with rows of its own needs all of K and V, so eight waves share
 // tiles of them in LDS (reading them from memory for each wave: 567 us for the tree
-// below, now 178).  A tree of 64 tokens over 131072 places, 256 rows to a key head:
-// 178 us, 3.0 TB/s and 0.77 PFLOP/s at once.  Two waves a SIMD, which the registers
-// allow, keep the matrix cores 37% busy: what is not overlapped is the softmax's
+// below, now 172).  A tree of 64 tokens over 131072 places, 256 rows to a key head:
+// 172 us, 3.1 TB/s and 0.80 PFLOP/s at once.  Two waves a SIMD, which the registers
+// allow, keep the matrix cores 40% busy: what is not overlapped is the softmax's
 // instructions between the two products.  (Wave priorities around the products, and
 // the scores of two blocks before their softmax: no faster.)
 //
-// One token over few places is a chain of latencies (lengths, pages, K, V, the
-// waves' sums): 17 us over 700 places, 10 over 16.
+// One token over few places is a chain of latencies (starts and lengths, pages, then K
+// and V of a block for each of the waves, three turns of them over 700 places, the waves'
+// sums): 17 us over 700 places, 10 over 16.
 //
 // Work is cut by df11_attention_plan.h; a tile that one workgroup does alone is
 // written at once, the parts of the others go to the workspace and a second
-// kernel joins them in order (6 to 11 us, 23 where prompts cut most tiles).
+// kernel joins them in order (5 to 12 us, 21 where prompts cut most tiles).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -908,7 +914,8 @@ __device__ __forceinline__ void for_each_part(const AttentionArgs &a, F f) {
         units = scan_units<THREADS>(a, at, units, shape, n, mine, s_part);
     }
     const bool none = units == 0 || units >= df11::kMaxUnits;
-    const uint32_t all = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(units)), runs = none ? 0u : df11::runs_of(all, a.workgroups);
+    const uint32_t all = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(units));
+    const uint32_t runs = none ? 0u : df11::runs_of(all, a.workgroups);
     // What the second kernel finds of a run: the tile that it begins and leaves.
     if (a.cut && blockIdx.x >= runs && threadIdx.x == 0) a.cut[blockIdx.x].last = 0;
     if (blockIdx.x >= runs) return;

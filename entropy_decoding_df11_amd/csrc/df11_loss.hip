@@ -30,13 +30,15 @@
 // into the workspace, and the dense product's epilogue makes them.
 //
 // The matrix cores bound it, and the decode for few tokens.  24 tokens through 32000 x
-// 4096: fused decode and product 110 us, slots' sums 14, tokens 5 (the floor, the
-// compressed head's bytes, 37).  1000 tokens through 128256 x 4096: decode 367 us,
-// product 860 to 1000 (1.05 to 1.22 PFLOP/s).  2048 tokens through 32000 x 4096 with the gradient: decode
-// 92, first references 28, logits and exponentials 460, their product with W 390 (1.2
-// to 1.4 PFLOP/s where the clocks hold), and all else 60.  The logits alone would
-// be 4 bytes a token and class, written once and read three times by the formulas
-// one by one: 8.3 and 7.9 ms.
+// 4096: fused decode and product 102 us, slots' sums 13, tokens 5 (the floor, the
+// compressed head's bytes, 37).  1000 tokens through 128256 x 4096: decode 353 us,
+// product 854 to 880 (1.2 PFLOP/s).  2048 tokens through 32000 x 4096 with the gradient:
+// decode 88, first references 28, logits and exponentials 460 (1.17 PFLOP/s), their
+// product with W 380 (1.41), and all else 60.  (Once the clocks have settled, after
+// some 100 passes; 5 to 15% more before.)  The logits alone would be 4 bytes a token and
+// class, written once and read three times by the formulas one by one: 8.4 and 8.0 ms.
+// The workspace has the decoded head, 2 bytes a weight: below in_features / 2 tokens
+// more than the logits would have.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
