@@ -369,9 +369,11 @@ struct Rows {
 
     // Scores to weights (in s, and rounded in w).  A weight past the room (infinite
     // while there is no reference) says that the reference has to move: then
-    // they are taken again, from the new one, and from scores times c that are rounded
-    // as the reference's was: what a fused product keeps beside it may be many powers
-    // of two (from scores of 2^30 on), and the largest score's weight infinite.
+    // they are taken again, from the new one.  What a fused product keeps of a score
+    // times c beside the reference, which was rounded, is the same for places of one
+    // score in all blocks; but of references from 2^24 on it is more than a power of two
+    // (from 2^31 on it makes the largest score's weight infinite): there, where scores
+    // no longer tell places apart, weights are taken from products rounded alike.
     __device__ __forceinline__ void weigh(floatx4 (&s)[M][2], Vec (&w)[M]) {
         const T one = static_cast<T>(1.0f);
         floatx4 x[M][2];
@@ -394,6 +396,7 @@ struct Rows {
                 const float to = fmaxf(ref[i], fmaxf(top, __shfl_xor(top, 32)) * a.c - kLead<T>);
                 const float f = weight_of(ref[i], to);
                 const float base = to == -INFINITY ? 0.0f : to;
+                const bool far = !(fabsf(base) < 16777216.0f);
                 ref[i] = to;
                 l[i] *= f;
                 total[i] *= f;
@@ -402,7 +405,10 @@ struct Rows {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][t][e] = exp2_fast(s[i][t][e] * a.c - base);
+                    for (int e = 0; e < 4; ++e) {
+                        const float rounded = s[i][t][e] * a.c - base;
+                        x[i][t][e] = exp2_fast(far ? rounded : __builtin_fmaf(s[i][t][e], a.c, -base));
+                    }
             }
         }
 #pragma unroll

@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from test_gpu_attention import Case  # noqa: E402
+from test_gpu_attention import E, Case  # noqa: E402
 
 
 def far(dtype):
@@ -69,3 +69,25 @@ def test_one_place_far_above(tokens, places, dtype):
         got = case.attend().cpu()
         value = case.v[case.table[0, one // case.page], one % case.page, 0]
         assert torch.equal(got, value.expand(got.shape))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens,places", [(1, 700), (1, 5000), (40, 3000), (70, 3000)])
+def test_large_scores_alike(tokens, places, dtype):
+    """Places of one score have one weight, whichever block they are in: the output is the values' mean.
+    (Weights are alike to the last bit, so that their rounding cancels: u of the result and the sums' n e are left.)"""
+    for score in (9e3, -9e3, 1.1e5, -1.3e5, 1.1e6, -1.7e6, 7.1e6, -1.1e7):
+        case = Case([places], [tokens], dtype, 4, 1, 64, page=16, seed=34)
+        p = torch.arange(places + tokens)
+        at = case.table[0].long()[p // case.page], p % case.page
+        case.q.zero_()
+        case.k[at] = 0
+        case.q[..., 0] = 8000
+        case.k[(*at, slice(None), 0)] = score / 1000  # (of a scale of 1/8)
+        case.upload()
+        got = case.attend().cpu().double()
+        v = case.v[at][:, 0].double()
+        for t in range(tokens):
+            mean, size = v[:places + t + 1].mean(0), v[:places + t + 1].abs().mean(0)
+            u = torch.finfo(dtype).eps / 2
+            assert bool(((got[t] - mean).abs() <= u * mean.abs() + 2 * (places + tokens) * E * size).all()), (score, t)
