@@ -11,12 +11,12 @@
 // steps; without one the later tiles see more, and a tile's steps are a bound
 // whose sums have a closed form: at most one step too many, and for a sequence's last
 // tile, which may not be full, as many more as a full one has of its own.  (With the
-// tiles of a step rounded down, as they were for groups that do not divide a tile's
-// rows, 10000 tokens of groups of 3 had 7021 steps for 4720: 4000 after 4000, three to
-// a key head, 402 us and now 355; 8000 after 100, five to a key head, 294 and 257.)  A tile counts some
-// units more, before its steps, for what it takes beside them (its queries, the
-// first loads that nothing hides, the end of its sums): a run that has only those
-// leaves the tile to the next one.
+// tiles that add a step rounded down to whole ones, groups of 3 counted 7021 steps for
+// 4720 in 10000 tokens: 4000 after 4000, three to a key head, 402 us against 355; 8000
+// after 100, five to a key head, 294 against 257.)  A tile counts some units more,
+// before its steps, for what it takes beside them (its queries, the first loads that
+// nothing hides, the end of its sums): a run that has only those leaves the tile to
+// the next one.
 #ifndef DF11_ATTENTION_PLAN_H
 #define DF11_ATTENTION_PLAN_H
 

@@ -661,8 +661,8 @@ int df11_matmul_epilogue_grad(const df11_device_stream *w, const df11_device_str
  *   loss = log(sum over v of exp(z_v)) - z_target
  *   grad = d loss / dx = sum over v of p_v W_v - W_target,  p = softmax(z)
  *   targets        n_tokens int64.  A token whose target is ignore_index has a
- *                  loss of zero and a gradient of minus zero; one whose target is no class
- *                  otherwise, NaN
+ *                  loss of zero and a gradient of minus zero; one whose target is
+ *                  no class otherwise, NaN
  *   loss           n_tokens floats
  *   total          a float, or NULL: the sum of loss over the tokens, divided by
  *                  their number if mean
@@ -832,11 +832,11 @@ int df11_append_kv(const df11_kv_cache *cache, const df11_kv_batch *batch, const
  *   lse          n_tokens x q_heads floats, or NULL: the natural logarithm of the
  *                sum of exp(scale q . k) over what the query sees
  *   mask         n_tokens x mask_cols bytes, mask_stride from token to token, or
- *                NULL (with mask_cols 0 any other address, of which nothing is
- *                read: no new token sees another or itself).  Every query sees the lengths[s] cached places of its
+ *                NULL.  Every query sees the lengths[s] cached places of its
  *                sequence; of the sequence's new tokens it sees the j-th if byte
  *                j of its row is not zero (none from mask_cols on), or without a
- *                mask those up to itself
+ *                mask those up to itself.  (With mask_cols 0 a mask is any address
+ *                but NULL, of which nothing is read)
  *   scale        positive, finite
  *   q_heads      a multiple of the cache's heads, at most 4096 */
 typedef struct df11_attention {
@@ -863,12 +863,12 @@ uint64_t df11_tree_attention_workspace(const df11_kv_cache *cache, const df11_kv
  * ones, a piece of a prompt) over a paged cache that already holds their keys
  * and values:
  *   out = sum over the visible places j of p_j v_j,  p = softmax(scale q . k_j)
- * Scores, the softmax's maximum and sum, and out's sums are float; p is rounded
+ * Scores, the softmax's maximum and sums, and out's sums are float; p is rounded
  * to the cache's type for its product with v (the matrix cores' operand type), and
- * out is divided by the sum of p as rounded (lse has it unrounded) and rounded once.  (That rounding is 2^-8 of p at
- * most in DF11_BF16 and 2^-11 in DF11_FP16, there also up to 2^-32 of the largest
- * score's p: over 2^21 places as much as the result's own.)  A query that sees nothing
- * gets zeros and an lse of minus infinity.  What a place holds reaches only the
+ * out is divided by the sum of p as rounded (lse has it unrounded) and rounded
+ * once.  (That rounding is 2^-8 of p at most in DF11_BF16 and 2^-11 in DF11_FP16,
+ * there also up to 2^-32 of the largest score's p: over 2^21 places as much as the
+ * result's own.)  A query that sees nothing gets zeros and an lse of minus infinity.  What a place holds reaches only the
  * queries that see it: an infinity or a NaN elsewhere in the cache does not.
  * Rows that belong to no sequence are left as they were.
  *   workspace    device, 256-byte aligned, df11_tree_attention_workspace bytes;
