@@ -181,7 +181,8 @@ extern "C" int df11_append_kv(const df11_kv_cache *c, const df11_kv_batch *b, co
     for (uint64_t *s : {&used.q_head_stride, &used.q_out_head_stride}) *s = kv_stride(used.q_heads, *s);
     const df11_append *a = &used;
     const uint32_t bytes = dtype_bytes(a->dtype), dim = c->head_dim, tokens = b->n_tokens;
-    if (!bytes || !a->q != !a->q_out || (a->q ? !a->q_heads || a->q_heads > kMaxKvHeads : a->q_heads != 0))
+    // (tensors without elements have no address, whatever their heads)
+    if (!bytes || !a->q != !a->q_out || (a->q ? !a->q_heads || a->q_heads > kMaxKvHeads : a->q_heads != 0 && tokens))
         return DF11_E_INVALID_ARG;
     if (a->rotary && (a->rotary_dims < 2 || a->rotary_dims % 2 || a->rotary_dims > dim || !aligned(a->rotary, 4) ||
                       a->rotary_rows > (1ull << 40) || a->interleaved > 1))
